@@ -53,7 +53,9 @@ typedef enum {
   TG_ERR_OUT_OF_MEMORY = -4
 } tg_status;
 
-typedef enum { TG_DTYPE_F32 = 0, TG_DTYPE_BF16 = 1 } tg_dtype;
+/* Logits are f32 or bf16; attention tensors bf16 or f16; a key-value cache
+ * bf16, f16 or e4m3 (8-bit floating point, finite values up to 448). */
+typedef enum { TG_DTYPE_F32 = 0, TG_DTYPE_BF16 = 1, TG_DTYPE_F16 = 2, TG_DTYPE_E4M3 = 3 } tg_dtype;
 typedef enum { TG_GREEDY = 0, TG_SAMPLE = 1 } tg_mode;
 
 /* Status-word bits (sticky until tg_clear_status). */
@@ -66,6 +68,7 @@ typedef enum { TG_GREEDY = 0, TG_SAMPLE = 1 } tg_mode;
  * out_match = -1.  Every other output of the call is valid. */
 #define TG_FLAG_TIMEOUT 0x8u
 #define TG_FLAG_BAD_STATE 0x10u              /* a row's processor state broke its layout; dropped */
+#define TG_FLAG_BAD_PAGE 0x20u               /* a page number outside the cache; its tokens were skipped */
 
 /* Largest vocabulary the kernels take. */
 #define TG_MAX_VOCAB (1 << 18)
@@ -410,6 +413,158 @@ tg_status tg_beam_step(const void* logits, int32_t num_prompts, int32_t num_beam
 /* Candidates a prompt keeps per beam step: max(2, 1 + eos ids) * num_beams,
  * or -1 for a NULL config or num_beams < 1. */
 int32_t tg_beam_keep(const tg_config* cfg, int32_t num_beams);
+
+/* ------------------------------------------------------------------------
+ * Attention over a paged key-value cache: what produces the hidden states
+ * whose logits tg_select and tg_verify read.  tg_cache_append writes new
+ * tokens into the cache (rotating queries and keys by their positions),
+ * tg_attend_step attends the last n tokens of every sequence over it (n = 1:
+ * a decode step; n = K + 1: the positions of a tg_verify step), and
+ * tg_attend_prompt attends whole prompts before they are read from a cache.
+ * ------------------------------------------------------------------------ */
+
+/* Largest head_dim (a multiple of 16), and most tokens per sequence of one
+ * tg_attend_step call. */
+#define TG_MAX_HEAD_DIM 128
+#define TG_MAX_STEP_TOKENS 32
+
+/* Order of the dimensions inside a page. */
+typedef enum {
+  TG_PAGES_TOKEN_HEAD = 0, /* [page_size, num_kv_heads, head_dim] */
+  TG_PAGES_HEAD_TOKEN = 1  /* [num_kv_heads, page_size, head_dim] */
+} tg_page_layout;
+
+/* Settings of the attention calls.  Host pointers; tg_attn_create copies what
+ * it needs.  tg_attn_params_init fills the defaults. */
+typedef struct tg_attn_params {
+  int32_t num_heads;     /* query heads H, a multiple of num_kv_heads */
+  int32_t num_kv_heads;  /* key and value heads G; head h reads key head h / (H / G) */
+  int32_t head_dim;      /* D, a multiple of 16, at most TG_MAX_HEAD_DIM */
+  tg_dtype dtype;        /* queries, keys, values and outputs: bf16 or f16 */
+  tg_dtype cache_dtype;  /* the cache's elements: dtype, or e4m3 */
+  int32_t page_size;     /* tokens per page, a power of two, 1 .. 1024 */
+  tg_page_layout page_layout;
+  float scale;           /* of the products q.k, > 0; 0 = 1 / sqrt(D) */
+  /* Rotation by position (tg_cache_append): pair i of the first rotary_dim
+   * elements of each head turns by position * inv_freq[i].  rotary_dim is a
+   * multiple of 16, at most head_dim; 0 = off.  The pair is (i, i +
+   * rotary_dim / 2), or (2i, 2i + 1) when rotary_interleaved is 1. */
+  int32_t rotary_dim;
+  int32_t rotary_interleaved;
+  const float* inv_freq; /* [rotary_dim / 2], finite */
+  /* What one unit of an e4m3 cache stands for, per key head [G], finite and
+   * > 0 (NULL: 1).  Other caches take NULL. */
+  const float* k_scales;
+  const float* v_scales;
+  int32_t max_step_tokens; /* largest n of tg_attend_step, 1 .. TG_MAX_STEP_TOKENS; 0 = 17 */
+} tg_attn_params;
+
+/* Opaque; holds the rotation's constants, the scales, a status word and the
+ * workspace in which tg_attend_step joins the parts of a long sequence (calls
+ * that share a tg_attn: in stream order, as with a tg_config). */
+typedef struct tg_attn tg_attn;
+
+void tg_attn_params_init(tg_attn_params* p, int32_t num_heads, int32_t num_kv_heads, int32_t head_dim);
+
+/* Validate *params and build the handle on the current device; the uploads
+ * are enqueued on `stream` and waited for.  Errors: TG_ERR_INVALID_ARGUMENT
+ * (a field out of range), TG_ERR_UNSUPPORTED (head_dim above TG_MAX_HEAD_DIM
+ * or no multiple of 16, rotary_dim no multiple of 16, a page size that is no
+ * power of two), TG_ERR_OUT_OF_MEMORY, TG_ERR_CUDA. */
+tg_status tg_attn_create(const tg_attn_params* params, tg_attn** out, tg_stream stream);
+tg_status tg_attn_destroy(tg_attn* cfg);
+
+/* The handle's sticky status bits (synchronous), and their reset.
+ * TG_FLAG_BAD_ROW: offsets or a length out of range, the sequence skipped;
+ * TG_FLAG_BAD_PAGE; TG_FLAG_TIMEOUT: a bounded wait ran out, the launch's
+ * outputs are not valid. */
+tg_status tg_attn_status_word(const tg_attn* cfg, uint32_t* flags);
+tg_status tg_attn_clear_status(const tg_attn* cfg);
+
+/* A paged cache as a call sees it.  Device pointers; the caller owns all of it. */
+typedef struct tg_cache {
+  void* k_pages;            /* num_pages pages, each laid out as page_layout says */
+  void* v_pages;
+  int64_t k_page_stride;    /* elements between pages (a multiple of 16 bytes) */
+  int64_t v_page_stride;
+  int32_t num_pages;
+  const int32_t* page_table; /* [batch, max_pages]: page t / page_size of row b holds its token t */
+  int64_t table_stride;     /* elements between rows of page_table */
+  int32_t max_pages;
+  const int32_t* kv_lens;   /* [batch]: tokens of each sequence, this call's included */
+  int32_t batch;
+} tg_cache;
+
+/*
+ * tg_cache_append -- rotate and store the new tokens of every sequence.
+ *
+ *  q, k, v      device, [tokens, H, D], [tokens, G, D], [tokens, G, D] in
+ *               dtype: the new tokens of all sequences back to back; rows
+ *               q_stride, k_stride, v_stride elements apart (multiples of 8;
+ *               a row's heads are contiguous; 16-byte aligned pointers).  q
+ *               may be NULL.
+ *  q_offsets    device int64 [batch + 1]: sequence b's new tokens are rows
+ *               q_offsets[b] .. q_offsets[b+1]; they are its last ones, so
+ *               the j-th of m gets position kv_lens[b] - m + j.
+ *  q_out        device [tokens, H, D] contiguous: the rotated queries (NULL
+ *               when q is; may be q itself when that is contiguous).
+ *  k_out        device [tokens, G, D] contiguous or NULL: the rotated keys.
+ *
+ * The angle's product is held to 2^-32 of a turn at any position; the
+ * rotation is computed in f32 and rounded once to each output's type.  An
+ * e4m3 cache holds value / scale, rounded to nearest and saturated at 448.
+ * Tokens of a page outside [0, num_pages) or past max_pages are left out of
+ * the cache (TG_FLAG_BAD_PAGE); a negative position or inconsistent offsets
+ * skip the token (TG_FLAG_BAD_ROW).
+ */
+tg_status tg_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                          int64_t v_stride, const int64_t* q_offsets, int32_t tokens, const tg_cache* cache,
+                          const tg_attn* cfg, void* q_out, void* k_out, tg_stream stream);
+
+/*
+ * tg_attend_step -- attention of the last n tokens of every sequence over the
+ * cache.
+ *
+ *  q            device, [batch, n, H, D] in dtype; token rows q_stride
+ *               elements apart (a multiple of 8; 16-byte aligned pointer).
+ *  n            tokens per sequence, 1 .. max_step_tokens.  Token j sees keys
+ *               0 .. kv_lens[b] - n + j.
+ *  out          device [batch, n, H, D] contiguous, dtype.
+ *  out_lse      device f32 [batch, n, H] or NULL: the natural logarithm of
+ *               the sum of exp(scale * q.k) over the keys seen.
+ *
+ * A token that sees no key (kv_lens[b] <= n - 1 - j, an empty sequence) gives
+ * 0 and -infinity.  Keys of a page outside [0, num_pages) are left out
+ * (TG_FLAG_BAD_PAGE); kv_lens[b] outside [0, max_pages * page_size] makes the
+ * sequence an empty one (TG_FLAG_BAD_ROW).  Softmax statistics and sums are
+ * f32; the weights are rounded to the 16-bit type of the products.  The keys
+ * of one sequence are split over the GPU and joined in a fixed order: equal
+ * inputs give equal bits.
+ */
+tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const tg_attn* cfg,
+                         void* out, float* out_lse, tg_stream stream);
+
+/*
+ * tg_attend_prompt -- attention of whole prompts, packed back to back.
+ *
+ *  q, k, v      device, [q_tokens, H, D], [kv_tokens, G, D] twice, in dtype;
+ *               rows *_stride elements apart (multiples of 8; 16-byte aligned
+ *               pointers; a row's heads are contiguous).
+ *  q_offsets    device int64 [batch + 1]: sequence b's queries.
+ *  kv_offsets   device int64 [batch + 1] or NULL (as q_offsets): its keys.
+ *  causal       1: query i of m sees keys 0 .. len - m + i of the sequence's
+ *               len (the queries are its last tokens; with more queries than
+ *               keys the first ones see none).  0: every query sees every key.
+ *  out, out_lse [q_tokens, H, D] contiguous and f32 [q_tokens, H] or NULL.
+ *
+ * A query that sees no key gives 0 and -infinity.  A sequence whose offsets
+ * decrease or leave the tensors is skipped (TG_FLAG_BAD_ROW), as are queries
+ * of no sequence.  Numerics as tg_attend_step.
+ */
+tg_status tg_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int64_t* q_offsets, const int64_t* kv_offsets, int32_t batch,
+                           int32_t q_tokens, int32_t kv_tokens, int32_t causal, const tg_attn* cfg, void* out,
+                           float* out_lse, tg_stream stream);
 
 /* A static, human-readable name of a status code. */
 const char* tg_status_string(tg_status s);

@@ -1,0 +1,197 @@
+// tg_cache_append: rotate the new tokens' queries and keys by their positions
+// and write keys and values into the pages of the cache.
+//
+// A pair (a, b) at position p turns by p * f_i radians:
+//   a' = a cos - b sin,  b' = b cos + a sin.
+// p * f_i is formed as a 64-bit fixed-point fraction of a turn: f_i / 2 pi is
+// stored as an integer t_i of 2^-64 turns, and p * t_i mod 2^64 drops whole
+// turns exactly, so a far position loses nothing; its top 32 bits give the
+// angle to 2^-32 of a turn and sincospi takes it from there.
+//
+// Bytes bound it: every element is read once and written once.
+#include "tg_attn.cuh"
+
+namespace tg {
+namespace {
+
+constexpr int kAppendThreads = 256;
+constexpr int kMaxTok = 8;  // tokens per CTA at most
+
+struct TokMeta {
+  int ok;          // the token belongs to a sequence and has a position
+  int page;        // its page, or -1: left out of the cache
+  int slot;
+  unsigned pos;
+};
+
+// The sequence that holds packed token t: the last b with off[b] <= t (bounded
+// whatever the offsets hold).
+__device__ __forceinline__ int find_seq(const int64_t* off, int batch, long long t) {
+  int lo = 0, hi = batch;  // invariant for sorted offsets: off[lo] <= t < off[hi]
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (off[mid] <= t) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+struct V8 { uint4 w; };
+
+template <bool F16>
+__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
+  const unsigned u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = unpack2<F16>(u[i]);
+    x[2 * i] = f.x;
+    x[2 * i + 1] = f.y;
+  }
+}
+template <bool F16>
+__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
+  return make_uint4(pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]), pack2<F16>(x[4], x[5]), pack2<F16>(x[6], x[7]));
+}
+__device__ __forceinline__ uint2 narrow8(const float (&x)[8], float inv) {
+  unsigned short h[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const float2 f = make_float2(x[2 * i] * inv, x[2 * i + 1] * inv);
+    h[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+  }
+  return make_uint2(h[0] | (static_cast<unsigned>(h[1]) << 16), h[2] | (static_cast<unsigned>(h[3]) << 16));
+}
+
+// One CTA: tpb tokens.  A unit of work is 16 elements of one head: two
+// 8-element vectors, which for rotated "halves" are the two partners.
+template <bool F16, bool Q8>
+__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c, const AppendArgs a, int tpb) {
+  __shared__ TokMeta meta[kMaxTok];
+  __shared__ float2 cs[kMaxTok][TG_MAX_HEAD_DIM / 2];
+  dep_wait();
+  const int t0 = blockIdx.x * tpb;
+  const int nt = min(tpb, a.tokens - t0);
+  if (threadIdx.x < nt) {
+    const long long t = t0 + threadIdx.x;
+    TokMeta m{0, -1, 0, 0u};
+    const int b = find_seq(a.off, a.c.batch, t);
+    const long long o0 = a.off[b], o1 = a.off[b + 1];
+    if (o0 <= t && t < o1) {
+      const long long pos = a.c.lens[b] - (o1 - t);
+      if (pos >= 0) {
+        m.ok = 1;
+        m.pos = static_cast<unsigned>(pos);
+        const int pi = m.pos >> c.page_shift;
+        m.slot = m.pos & (c.page_size - 1);
+        const int page = pi < a.c.max_pages ? a.c.table[b * a.c.table_stride + pi] : -1;
+        if (page >= 0 && page < a.c.num_pages) m.page = page;
+        else atomicOr(c.status, kAttnBadPage);
+      }
+    }
+    if (!m.ok) atomicOr(c.status, kAttnBadRow);
+    meta[threadIdx.x] = m;
+  }
+  __syncthreads();
+  const int half = c.rotary >> 1;
+  for (int i = threadIdx.x; i < nt * half; i += kAppendThreads) {
+    const int t = i / half, p = i - t * half;
+    const unsigned long long turn = c.turns[p] * meta[t].pos;
+    float sn, cn;
+    sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cn);
+    cs[t][p] = make_float2(cn, sn);
+  }
+  __syncthreads();
+
+  const int per_head = c.D >> 4;
+  const int heads = (a.q ? c.H : 0) + 2 * c.G;
+  const int units = heads * per_head;
+  const int rot_units = half >> 3;  // units of a head that turn
+  for (int i = threadIdx.x; i < nt * units; i += kAppendThreads) {
+    const int t = i / units, u = i - t * units;
+    const TokMeta m = meta[t];
+    if (!m.ok) continue;
+    int h = u / per_head;
+    const int part = u - h * per_head;
+    const long long row = t0 + t;
+    // q heads, then key heads, then value heads
+    const uint16_t* src;
+    int kind = 0, head = h;
+    if (!a.q) h += c.H;
+    if (h < c.H) { src = static_cast<const uint16_t*>(a.q) + row * a.qs + static_cast<long long>(h) * c.D; head = h; }
+    else if (h < c.H + c.G) { kind = 1; head = h - c.H; src = static_cast<const uint16_t*>(a.k) + row * a.ks + static_cast<long long>(head) * c.D; }
+    else { kind = 2; head = h - c.H - c.G; src = static_cast<const uint16_t*>(a.v) + row * a.vs + static_cast<long long>(head) * c.D; }
+    const bool turn = kind < 2 && part < rot_units;
+    const int e0 = turn && !c.inter ? part * 8 : part * 16;
+    const int e1 = turn && !c.inter ? e0 + half : e0 + 8;
+    const uint4 w0 = *reinterpret_cast<const uint4*>(src + e0), w1 = *reinterpret_cast<const uint4*>(src + e1);
+    float x[8], y[8];
+    widen<F16>(w0, x);
+    widen<F16>(w1, y);
+    if (turn) {
+      if (!c.inter) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 r = cs[t][e0 + j];
+          const float p = x[j], q = y[j];
+          x[j] = p * r.x - q * r.y;
+          y[j] = q * r.x + p * r.y;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 r = cs[t][(e0 >> 1) + j], r2 = cs[t][(e0 >> 1) + 4 + j];
+          const float p = x[2 * j], q = x[2 * j + 1], p2 = y[2 * j], q2 = y[2 * j + 1];
+          x[2 * j] = p * r.x - q * r.y;
+          x[2 * j + 1] = q * r.x + p * r.y;
+          y[2 * j] = p2 * r2.x - q2 * r2.y;
+          y[2 * j + 1] = q2 * r2.x + p2 * r2.y;
+        }
+      }
+    }
+    uint4 n0 = w0, n1 = w1;
+    if (turn) { n0 = narrow<F16>(x); n1 = narrow<F16>(y); }
+    if (kind == 0 || (kind == 1 && a.k_out)) {
+      uint16_t* dst = kind == 0 ? static_cast<uint16_t*>(a.q_out) + (row * c.H + head) * c.D
+                                : static_cast<uint16_t*>(a.k_out) + (row * c.G + head) * c.D;
+      *reinterpret_cast<uint4*>(dst + e0) = n0;
+      *reinterpret_cast<uint4*>(dst + e1) = n1;
+    }
+    if (kind > 0 && m.page >= 0) {
+      const long long at = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride) + m.slot * c.slot_stride +
+                           head * c.head_stride;
+      if constexpr (Q8) {
+        const float* sc = kind == 1 ? c.k_scale : c.v_scale;
+        const float inv = sc ? 1.0f / sc[head] : 1.0f;
+        uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
+        *reinterpret_cast<uint2*>(dst + e0) = narrow8(x, inv);
+        *reinterpret_cast<uint2*>(dst + e1) = narrow8(y, inv);
+      } else {
+        uint16_t* dst = static_cast<uint16_t*>(kind == 1 ? a.c.k : a.c.v) + at;
+        *reinterpret_cast<uint4*>(dst + e0) = n0;
+        *reinterpret_cast<uint4*>(dst + e1) = n1;
+      }
+    }
+  }
+}
+
+}  // namespace
+
+cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s) {
+  // One token per CTA while that does not fill the GPU; several share their
+  // page lookups and angles' latency when there are many.
+  const int tpb = max(1, min(kMaxTok, a.tokens / (4 * c.nsm)));
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((a.tokens + tpb - 1) / tpb);
+  cfg.blockDim = dim3(kAppendThreads);
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  const bool f16 = c.dtype == TG_DTYPE_F16, q8 = c.ctype == TG_DTYPE_E4M3;
+  auto k = f16 ? (q8 ? append_kernel<true, true> : append_kernel<true, false>)
+               : (q8 ? append_kernel<false, true> : append_kernel<false, false>);
+  return cudaLaunchKernelEx(&cfg, k, c, a, tpb);
+}
+
+}  // namespace tg

@@ -1,0 +1,185 @@
+// Shared declarations of the attention kernels (tg_append.cu, tg_step.cu,
+// tg_prompt.cu) and their C ABI (tg_attn_api.cu); internal to the library.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include "../../include/tg.h"
+
+namespace tg {
+
+// Status bits that the attention kernels raise (declared in tg_device.cuh for
+// the whole library; the values are include/tg.h's).
+constexpr unsigned kAttnBadRow = TG_FLAG_BAD_ROW;
+constexpr unsigned kAttnBadPage = TG_FLAG_BAD_PAGE;
+constexpr unsigned kAttnTimeout = TG_FLAG_TIMEOUT;
+
+// A handle's settings, passed to the kernels by value.
+struct AttnCfg {
+  int H, G, D, rep;        // query heads, key heads, head size, H / G
+  int dtype, ctype;        // tg_dtype of the tensors and of the cache
+  int page_size, page_shift;
+  long long slot_stride;   // elements between tokens of one head inside a page
+  long long head_stride;   // elements between heads inside a page
+  float scale;
+  int rotary, inter;
+  const unsigned long long* turns;  // [rotary / 2]: 2^64 * fraction of a turn per position
+  const float* k_scale;    // [G], or null
+  const float* v_scale;
+  unsigned* status;
+  int max_n;               // largest n of a step
+  int step_rows;           // rows of a workspace slot
+  int step_slots;          // workspace slots (two per CTA)
+  float* ws_o;             // [slots][step_rows][D]
+  float2* ws_ml;           // [slots][step_rows]: running maximum (base 2) and sum
+  unsigned* ws_count;      // [slots / 2]: parts of a split sequence that are done; zero between calls
+  int nsm;
+  int step_ctas[4];        // CTAs per SM of the step kernel's row variants
+};
+
+// The cache as a kernel sees it (tg_cache).
+struct CacheView {
+  void* k;
+  void* v;
+  long long k_page_stride, v_page_stride;
+  int num_pages;
+  const int32_t* table;
+  long long table_stride;
+  int max_pages;
+  const int32_t* lens;
+  int batch;
+};
+
+struct AppendArgs {
+  const void *q, *k, *v;
+  long long qs, ks, vs;
+  const int64_t* off;
+  int tokens;
+  CacheView c;
+  void *q_out, *k_out;
+};
+
+struct StepArgs {
+  const void* q;
+  long long qs;
+  int n;
+  CacheView c;
+  void* out;
+  float* lse;
+};
+
+struct PromptArgs {
+  const void *q, *k, *v;
+  long long qs, ks, vs;
+  const int64_t *qoff, *koff;
+  int batch, q_tokens, kv_tokens, causal;
+  void* out;
+  float* lse;
+};
+
+// Once per handle: shared-memory limits, and step_ctas.
+cudaError_t prepare_step(AttnCfg* c);
+cudaError_t prepare_prompt(const AttnCfg& c);
+cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
+cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
+// CTAs of the step kernel per SM at most: sizes the handle's workspace.
+constexpr int kStepCtasPerSm = 4;
+
+// ---------------------------------------------------------------------------
+// Device helpers
+// ---------------------------------------------------------------------------
+#ifdef __CUDACC__
+namespace {
+
+constexpr float kLog2E = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ unsigned sptr(const void* p) { return static_cast<unsigned>(__cvta_generic_to_shared(p)); }
+__device__ __forceinline__ void dep_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void dep_launch() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two f32 to two 16-bit values in one register (lo first), nearest even.
+template <bool F16>
+__device__ __forceinline__ unsigned pack2(float lo, float hi) {
+  if constexpr (F16) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&h);
+  } else {
+    const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const unsigned*>(&h);
+  }
+}
+template <bool F16>
+__device__ __forceinline__ float2 unpack2(unsigned w) {
+  if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
+  else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
+}
+// Two e4m3 values (low 16 bits of w) to two f16, exactly.
+__device__ __forceinline__ unsigned e4m3x2_to_f16x2(unsigned short w) {
+  unsigned h;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(w));
+  return h;
+}
+
+__device__ __forceinline__ void cp16(unsigned dst, const void* src, bool on) {
+  const int n = on ? 16 : 0;  // 0: the 16 bytes are filled with zeros, src is not read
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+__device__ __forceinline__ void ldsm4t(unsigned (&r)[4], unsigned addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+template <bool F16>
+__device__ __forceinline__ void mma16816(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// Byte offset of 16-byte chunk `c` of row `r` in a tile of rows of RB bytes
+// (64, 128 or 256).  Eight consecutive rows of one chunk column fall into
+// different banks: the chunk's number is exchanged by the row's low bits.
+template <int RB>
+__device__ __forceinline__ unsigned tile_at(int r, int c) {
+  if constexpr (RB == 64) {
+    const int line = r >> 1;
+    return line * 128 + ((((r & 1) << 2) | c) ^ (line & 3)) * 16;
+  } else {
+    return r * RB + (c ^ (r & 7)) * 16;
+  }
+}
+
+// Weights exp2(s - m) of f16 products are stored times 2^8: a weight 2^-33 of
+// the row's largest is still a (subnormal) f16 number, and the largest, 256,
+// is far below f16's end.  The sum carries the same factor.  bf16 has f32's
+// exponents and needs none.
+template <bool F16>
+constexpr float kWeightBias = F16 ? 8.0f : 0.0f;
+
+}  // namespace
+#endif
+
+}  // namespace tg

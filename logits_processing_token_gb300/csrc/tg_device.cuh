@@ -35,6 +35,7 @@ constexpr unsigned kFlagBadRow = 0x2u;
 constexpr unsigned kFlagSlow = 0x4u;
 constexpr unsigned kFlagTimeout = 0x8u;
 constexpr unsigned kFlagBadState = 0x10u;
+constexpr unsigned kFlagBadPage = 0x20u;
 constexpr int kMaxProcs = 8;           // the task's processors per config
 
 enum { kGreedy = 0, kSample = 1 };

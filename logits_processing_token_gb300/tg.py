@@ -9,7 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_uint32, c_uint64, c_void_p
+from ctypes import POINTER, c_char_p, c_float, c_int, c_int32, c_int64, c_uint32, c_uint64, c_void_p
 
 from . import _build
 
@@ -19,7 +19,7 @@ TG_ERR_UNSUPPORTED = -2
 TG_ERR_CUDA = -3
 TG_ERR_OUT_OF_MEMORY = -4
 
-TG_DTYPE_F32, TG_DTYPE_BF16 = 0, 1
+TG_DTYPE_F32, TG_DTYPE_BF16, TG_DTYPE_F16, TG_DTYPE_E4M3 = 0, 1, 2, 3
 TG_GREEDY, TG_SAMPLE = 0, 1
 
 TG_FLAG_HISTORY_ID_OUT_OF_RANGE = 0x1
@@ -27,17 +27,23 @@ TG_FLAG_BAD_ROW = 0x2
 TG_FLAG_SLOW_PATH = 0x4
 TG_FLAG_TIMEOUT = 0x8
 TG_FLAG_BAD_STATE = 0x10
+TG_FLAG_BAD_PAGE = 0x20
 TG_MAX_VOCAB = 1 << 18
 TG_PROC_BIAS, TG_PROC_SET = 0, 1
 TG_MAX_PROCESSORS = 8
 TG_MAX_STATE_COLS = 4096
+TG_MAX_HEAD_DIM = 128
+TG_MAX_STEP_TOKENS = 32
+TG_PAGES_TOKEN_HEAD, TG_PAGES_HEAD_TOKEN = 0, 1
 
 # Names of every entry point declared in include/tg.h.
 EXPORTS = ("tg_params_init", "tg_config_create", "tg_config_destroy", "tg_select", "tg_select_logprobs", "tg_verify",
            "tg_process", "tg_query_status", "tg_clear_status", "tg_next_num_candidates",
            "tg_status_string", "tg_verify_noalloc", "tg_beam_step", "tg_beam_keep",
            "tg_verify_history", "tg_select_state", "tg_process_state", "tg_set_wait_limit", "tg_status_word",
-           "tg_config_view", "tg_config_selection")
+           "tg_config_view", "tg_config_selection",
+           "tg_attn_params_init", "tg_attn_create", "tg_attn_destroy", "tg_attn_status_word", "tg_attn_clear_status",
+           "tg_cache_append", "tg_attend_step", "tg_attend_prompt")
 TG_NOALLOC_MAX_BATCH = 1024
 
 
@@ -79,6 +85,40 @@ class tg_params(ctypes.Structure):
         ("processor_kinds", POINTER(c_int32)),
         ("processor_sizes", POINTER(c_int32)),
         ("n_processors", c_int32),
+    ]
+
+
+class tg_attn_params(ctypes.Structure):
+    _fields_ = [
+        ("num_heads", c_int32),
+        ("num_kv_heads", c_int32),
+        ("head_dim", c_int32),
+        ("dtype", c_int),
+        ("cache_dtype", c_int),
+        ("page_size", c_int32),
+        ("page_layout", c_int),
+        ("scale", c_float),
+        ("rotary_dim", c_int32),
+        ("rotary_interleaved", c_int32),
+        ("inv_freq", POINTER(c_float)),
+        ("k_scales", POINTER(c_float)),
+        ("v_scales", POINTER(c_float)),
+        ("max_step_tokens", c_int32),
+    ]
+
+
+class tg_cache(ctypes.Structure):
+    _fields_ = [
+        ("k_pages", c_void_p),
+        ("v_pages", c_void_p),
+        ("k_page_stride", c_int64),
+        ("v_page_stride", c_int64),
+        ("num_pages", c_int32),
+        ("page_table", c_void_p),
+        ("table_stride", c_int64),
+        ("max_pages", c_int32),
+        ("kv_lens", c_void_p),
+        ("batch", c_int32),
     ]
 
 
@@ -137,6 +177,20 @@ def load_library(path: str | None = None):
     lib.tg_next_num_candidates.restype = c_int32
     lib.tg_status_string.argtypes = [c_int]
     lib.tg_status_string.restype = c_char_p
+    lib.tg_attn_params_init.argtypes = [POINTER(tg_attn_params), c_int32, c_int32, c_int32]
+    lib.tg_attn_params_init.restype = None
+    lib.tg_attn_create.argtypes = [POINTER(tg_attn_params), POINTER(c_void_p), c_void_p]
+    lib.tg_attn_destroy.argtypes = [c_void_p]
+    lib.tg_attn_status_word.argtypes = [c_void_p, POINTER(c_uint32)]
+    lib.tg_attn_clear_status.argtypes = [c_void_p]
+    lib.tg_cache_append.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
+                                    POINTER(tg_cache), c_void_p, c_void_p, c_void_p, c_void_p]
+    lib.tg_attend_step.argtypes = [c_void_p, c_int64, c_int32, POINTER(tg_cache), c_void_p, c_void_p, c_void_p, c_void_p]
+    lib.tg_attend_prompt.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int32,
+                                     c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
+    for fn in ("tg_attn_create", "tg_attn_destroy", "tg_attn_status_word", "tg_attn_clear_status", "tg_cache_append",
+               "tg_attend_step", "tg_attend_prompt"):
+        getattr(lib, fn).restype = c_int
     for fn in ("tg_config_create", "tg_config_destroy", "tg_select", "tg_select_logprobs", "tg_verify", "tg_process",
                "tg_query_status", "tg_clear_status"):
         getattr(lib, fn).restype = c_int
@@ -504,3 +558,208 @@ def tg_next_num_candidates(K: int, n_match: int, K_max: int) -> int:
 
 def tg_status_string(status: int) -> str:
     return status_string(status)
+
+
+_ATTN_DTYPES = {"bf16": TG_DTYPE_BF16, "f16": TG_DTYPE_F16, "e4m3": TG_DTYPE_E4M3}
+_PAGE_LAYOUTS = {"token": TG_PAGES_TOKEN_HEAD, "head": TG_PAGES_HEAD_TOKEN}
+
+
+def make_attn_params(num_heads, num_kv_heads, head_dim, dtype="bf16", cache_dtype=None, page_size=16,
+                     page_layout="token", scale=0.0, rotary_dim=0, rotary_interleaved=False, inv_freq=None,
+                     k_scales=None, v_scales=None, max_step_tokens=0):
+    """A filled tg_attn_params plus the ctypes arrays its pointers refer to."""
+    p = tg_attn_params()
+    load_library().tg_attn_params_init(ctypes.byref(p), int(num_heads), int(num_kv_heads), int(head_dim))
+    p.dtype = _ATTN_DTYPES[dtype] if isinstance(dtype, str) else int(dtype)
+    p.cache_dtype = p.dtype if cache_dtype is None else _ATTN_DTYPES[cache_dtype] if isinstance(cache_dtype, str) else int(cache_dtype)
+    p.page_size = int(page_size)
+    p.page_layout = _PAGE_LAYOUTS[page_layout] if isinstance(page_layout, str) else int(page_layout)
+    p.scale = float(scale or 0.0)
+    p.rotary_dim = int(rotary_dim)
+    p.rotary_interleaved = 1 if rotary_interleaved else 0
+    keep = []
+    for name, seq, n in (("inv_freq", inv_freq, p.rotary_dim // 2), ("k_scales", k_scales, p.num_kv_heads),
+                         ("v_scales", v_scales, p.num_kv_heads)):
+        if seq is None:
+            continue
+        seq = [float(x) for x in seq]
+        if len(seq) != n and not (name == "inv_freq" and n <= 0):
+            raise ValueError("%s holds %d values; the settings need %d" % (name, len(seq), n))
+        arr = (c_float * max(1, len(seq)))(*seq)
+        keep.append(arr)
+        setattr(p, name, ctypes.cast(arr, POINTER(c_float)))
+    p.max_step_tokens = int(max_step_tokens)
+    return p, keep
+
+
+class AttnConfig:
+    """Owns a tg_attn* (tg_attn_create / tg_attn_destroy); keyword arguments as make_attn_params."""
+
+    def __init__(self, stream=None, **params):
+        import torch
+        lib = load_library()
+        p, keep = make_attn_params(**params)
+        h = c_void_p()
+        self.handle = None
+        st = c_void_p(stream.cuda_stream) if stream is not None else None
+        _check("tg_attn_create", lib.tg_attn_create(ctypes.byref(p), ctypes.byref(h), st))
+        self.handle = h
+        del keep
+        types = {TG_DTYPE_BF16: torch.bfloat16, TG_DTYPE_F16: torch.float16, TG_DTYPE_E4M3: torch.float8_e4m3fn}
+        self.num_heads, self.num_kv_heads, self.head_dim = p.num_heads, p.num_kv_heads, p.head_dim
+        self.page_size, self.max_step_tokens = p.page_size, p.max_step_tokens or 17
+        self.dtype, self.cache_dtype = types[p.dtype], types[p.cache_dtype]
+        G, P, D = p.num_kv_heads, p.page_size, p.head_dim
+        self.page_shape = (P, G, D) if p.page_layout == TG_PAGES_TOKEN_HEAD else (G, P, D)
+
+    def close(self):
+        if self.handle:
+            load_library().tg_attn_destroy(self.handle)
+            self.handle = None
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _head_rows(t, name, heads, cfg):
+    """Pointer and row stride of a [.., heads, D] tensor whose heads are
+    contiguous and whose rows are evenly spaced."""
+    shape, stride = t.shape, t.stride()
+    D = cfg.head_dim
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != cfg.dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, cfg.dtype))
+    if shape[-2] != heads or shape[-1] != D:
+        raise ValueError("%s must end in [%d, %d], not %s" % (name, heads, D, tuple(shape[-2:])))
+    if (stride[-1] != 1 and D > 1) or (stride[-2] != D and heads > 1):
+        raise ValueError("%s: a row's heads must be contiguous" % name)
+    row = stride[-3] if shape[-3] > 1 else 0
+    if len(shape) == 4:  # [batch, n, heads, D]: one spacing for all rows
+        if row == 0:
+            row = stride[0] if shape[0] > 1 else 0
+        elif shape[0] > 1 and stride[0] != row * shape[1]:
+            raise ValueError("%s: its rows must be evenly spaced" % name)
+    return t.data_ptr(), row or heads * D
+
+
+def _whole(t, name, dtype, numel):
+    if t.dtype != dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    if t.numel() < numel:
+        raise ValueError("%s holds %d elements; the call needs %d" % (name, t.numel(), numel))
+    return t.data_ptr()
+
+
+def _cache(cfg, k_pages, v_pages, page_table, kv_lens):
+    """The tg_cache of a call."""
+    import torch
+    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
+        if not t.is_cuda:
+            raise ValueError("%s must be a CUDA tensor" % name)
+        if t.dtype != cfg.cache_dtype:
+            raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, cfg.cache_dtype))
+        s = t.shape
+        if len(s) != 4 or s[1:] != cfg.page_shape:
+            raise ValueError("%s must be [pages, %d, %d, %d], not %s" % ((name,) + cfg.page_shape + (tuple(s),)))
+        st, inner = t.stride(), cfg.page_shape[1] * cfg.head_dim
+        if st[3] != 1 or (st[2] != cfg.head_dim and s[2] > 1) or (st[1] != inner and s[1] > 1):
+            raise ValueError("%s: a page must be contiguous" % name)
+    pages = k_pages.shape[0]
+    if v_pages.shape[0] != pages:
+        raise ValueError("k_pages and v_pages must hold the same number of pages")
+    if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda:
+        raise ValueError("page_table must be a CUDA int32 tensor [batch, max_pages]")
+    B, most = page_table.shape
+    ts = page_table.stride()
+    if ts[1] != 1 and most > 1:
+        raise ValueError("page_table: a row must be contiguous")
+    whole = cfg.page_size * inner
+    return tg_cache(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.stride(0) if pages > 1 else whole,
+                    v_pages.stride(0) if pages > 1 else whole, pages, page_table.data_ptr(),
+                    ts[0] if B > 1 else most, most, _whole(kv_lens, "kv_lens", torch.int32, B), B)
+
+
+def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, q_out=None,
+                    k_out=None, stream=None):
+    """q [T, H, D] (or None), k and v [T, G, D]: the new tokens of all sequences, rows evenly spaced;
+    q_offsets int64 [B + 1]; kv_lens int32 [B], the new tokens included; page_table int32 [B, max_pages];
+    k_pages and v_pages [pages, page_size, G, D] or [pages, G, page_size, D] as the config says;
+    q_out [T, H, D] and k_out [T, G, D] (or None) take the rotated queries and keys."""
+    import torch
+    T, H, G, D = int(k.shape[0]), cfg.num_heads, cfg.num_kv_heads, cfg.head_dim
+    if k.dim() != 3 or v.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    if v.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k and v must hold the same number of tokens")
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out go together")
+    kp, ks = _head_rows(k, "k", G, cfg)
+    vp, vs = _head_rows(v, "v", G, cfg)
+    qp, qs = _head_rows(q, "q", H, cfg) if q is not None else (None, 0)
+    cache = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
+    st = load_library().tg_cache_append(
+        qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, cache.batch + 1), T, ctypes.byref(cache),
+        cfg.handle, _whole(q_out, "q_out", cfg.dtype, T * H * D) if q is not None else None,
+        _whole(k_out, "k_out", cfg.dtype, T * G * D) if k_out is not None else None, _stream(stream))
+    _check("tg_cache_append", st)
+
+
+def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, out, out_lse=None, stream=None):
+    """q and out [B, n, H, D]: the last n tokens of every sequence; out_lse f32 [B, n, H] or None; the cache's
+    tensors as tg_cache_append."""
+    import torch
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, n, heads, head_dim]")
+    B, n, H = int(q.shape[0]), int(q.shape[1]), cfg.num_heads
+    cache = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
+    if cache.batch != B:
+        raise ValueError("q holds %d sequences, page_table %d" % (B, cache.batch))
+    qp, qs = _head_rows(q, "q", H, cfg)
+    st = load_library().tg_attend_step(
+        qp, qs, n, ctypes.byref(cache), cfg.handle, _whole(out, "out", cfg.dtype, B * n * H * cfg.head_dim),
+        _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _stream(stream))
+    _check("tg_attend_step", st)
+    return out
+
+
+def tg_attend_prompt(q, k, v, q_offsets, kv_offsets, cfg: AttnConfig, out, out_lse=None, causal=True, stream=None):
+    """q and out [Tq, H, D], k and v [Tk, G, D]: sequences back to back, rows evenly spaced; q_offsets int64
+    [B + 1]; kv_offsets int64 [B + 1] or None (as q_offsets); out_lse f32 [Tq, H] or None."""
+    import torch
+    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
+        raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    Tq, Tk, H, G = int(q.shape[0]), int(k.shape[0]), cfg.num_heads, cfg.num_kv_heads
+    if v.shape[0] != Tk:
+        raise ValueError("k and v must hold the same number of tokens")
+    B = int(q_offsets.shape[0]) - 1
+    if B < 0:
+        raise ValueError("q_offsets must hold batch + 1 values")
+    qp, qs = _head_rows(q, "q", H, cfg)
+    kp, ks = _head_rows(k, "k", G, cfg)
+    vp, vs = _head_rows(v, "v", G, cfg)
+    st = load_library().tg_attend_prompt(
+        qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, B + 1),
+        _whole(kv_offsets, "kv_offsets", torch.int64, B + 1) if kv_offsets is not None else None, B, Tq, Tk,
+        1 if causal else 0, cfg.handle, _whole(out, "out", cfg.dtype, Tq * H * cfg.head_dim),
+        _whole(out_lse, "out_lse", torch.float32, Tq * H) if out_lse is not None else None, _stream(stream))
+    _check("tg_attend_prompt", st)
+    return out
+
+
+def tg_attn_status_word(cfg: AttnConfig) -> int:
+    """The handle's sticky status bits (synchronous)."""
+    f = c_uint32()
+    _check("tg_attn_status_word", load_library().tg_attn_status_word(cfg.handle, ctypes.byref(f)))
+    return int(f.value)
+
+
+def tg_attn_clear_status(cfg: AttnConfig):
+    _check("tg_attn_clear_status", load_library().tg_attn_clear_status(cfg.handle))
