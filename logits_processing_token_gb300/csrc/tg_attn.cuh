@@ -39,6 +39,8 @@ struct AttnCfg {
   unsigned* ws_count;      // [slots / 2]: parts of a split sequence that are done; zero between calls
   int nsm;
   int step_ctas[4];        // CTAs per SM of the step kernel's row variants
+  unsigned* prompt_count;  // [2]: next item and CTAs done of a prompt call; zero between calls
+  void* encode;            // the driver's tensor-map encoder (host)
 };
 
 // The cache as a kernel sees it (tg_cache).
@@ -83,7 +85,7 @@ struct PromptArgs {
 
 // Once per handle: shared-memory limits, and step_ctas.
 cudaError_t prepare_step(AttnCfg* c);
-cudaError_t prepare_prompt(const AttnCfg& c);
+cudaError_t prepare_prompt(AttnCfg* c);
 cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);

@@ -128,15 +128,15 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   cudaError_t e = cudaGetDevice(&cfg->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.nsm, cudaDevAttrMultiProcessorCount, cfg->device);
   if (e == cudaSuccess) e = tg::prepare_step(&d);
-  if (e == cudaSuccess) e = tg::prepare_prompt(d);
+  if (e == cudaSuccess) e = tg::prepare_prompt(&d);
   if (e != cudaSuccess) { delete cfg; return from_cuda(e); }
   // two slots per CTA of a step: the sequence it begins inside and the one it ends inside
   d.step_rows = std::min(128, (d.max_n * d.rep + 15) / 16 * 16);
   d.step_slots = 2 * tg::kStepCtasPerSm * d.nsm;
 
-  // [turns][k scales][v scales][counts][status] are uploaded; then the workspace
+  // [turns][k scales][v scales][counts][status, prompt counts] are uploaded; then the workspace
   const size_t o_turn = 0, o_ks = up16(o_turn + half * sizeof(unsigned long long)), o_vs = up16(o_ks + d.G * 4),
-               o_cnt = up16(o_vs + d.G * 4), o_st = up16(o_cnt + d.step_slots / 2 * 4), o_ml = up16(o_st + 4);
+               o_cnt = up16(o_vs + d.G * 4), o_st = up16(o_cnt + d.step_slots / 2 * 4), o_ml = up16(o_st + 12);
   const size_t rows = static_cast<size_t>(d.step_slots) * d.step_rows;
   const size_t o_o = up16(o_ml + rows * sizeof(float2)), bytes = o_o + rows * d.D * 4;
   unsigned char* host = new (std::nothrow) unsigned char[o_ml]();
@@ -166,6 +166,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.v_scale = p->v_scales ? reinterpret_cast<float*>(m + o_vs) : nullptr;
   d.ws_count = reinterpret_cast<unsigned*>(m + o_cnt);
   d.status = reinterpret_cast<unsigned*>(m + o_st);
+  d.prompt_count = d.status + 1;
   d.ws_ml = reinterpret_cast<float2*>(m + o_ml);
   d.ws_o = reinterpret_cast<float*>(m + o_o);
   *out = cfg;
@@ -191,7 +192,7 @@ tg_status tg_attn_clear_status(const tg_attn* cfg) {
   if (!cfg) return TG_ERR_INVALID_ARGUMENT;
   const tg_status st = check_device(cfg);
   if (st != TG_OK) return st;
-  cudaError_t e = cudaMemset(cfg->dev.status, 0, sizeof(uint32_t));
+  cudaError_t e = cudaMemset(cfg->dev.status, 0, 3 * sizeof(uint32_t));  // and the prompt's counts
   if (e == cudaSuccess) e = cudaMemset(cfg->dev.ws_count, 0, cfg->dev.step_slots / 2 * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   return from_cuda(e);

@@ -1,188 +1,636 @@
-// tg_attend_prompt: attention of whole prompts, packed back to back.
+// tg_attend_prompt: attention of whole prompts, packed back to back, on the
+// fifth-generation tensor cores.
 //
-// One CTA: 64 queries of one head; the keys pass in tiles of 64 with the
-// running maximum and sum of the softmax (tg_step.cu has the formulas), the
-// weights stay in registers as the second product's operand.  Causal tiles
-// past the diagonal are not visited.
+// For a row (a query of one head) and the keys in tiles of 128,
+//   s = c q.k,  o += 2^(s-r) v,  l += 2^(s-r),  result o / l,
+// where r is the row's reference: the running maximum, raised (and o, l scaled
+// down) only when a tile exceeds it by 2^6, which changes nothing in the
+// result and hardly ever happens after a row's first tiles.
+//
+// One CTA per SM takes items of 256 rows: two tiles of 128 rows, whose first
+// products S = Q K^T (shared memory x shared memory) and second products
+// O += P V (tensor memory x shared memory) alternate on the tensor core, so
+// that the softmax of one tile runs while the other tile's products do.
+// Rows of a tile are queries times `pack` heads of one key head, so the two
+// tiles see nearly the same keys and a causal tile is cut at 128 / pack queries.
+//   warps 0-3, 4-7   softmax of tile 0 and 1: one thread per row
+//   warp 8           issues the matrix instructions
+//   warp 9           takes items off a counter and issues the copies
+//   warps 10, 11     fill up the third group: it hands its registers to the
+//                    softmax, 256 x 208 + 128 x 88 = 384 x 168 as launched
+// Tensor memory: S0, S1 (128 columns each; P overwrites S as 16-bit pairs),
+// O0, O1 (128 columns each): all 512.
 #include <algorithm>
+#include <cuda.h>
 
 #include "tg_attn.cuh"
 
 namespace tg {
 namespace {
 
-constexpr int kQ = 64, kK = 64, kThr = 128;
+constexpr int kRowsT = 128;                 // rows of a tile
+constexpr int kKeys = 128;                  // keys of a tile
+constexpr int kThreadsP = 384;
+constexpr float kLazy = 6.0f;               // a row's reference may lag its maximum by 2^6
+constexpr unsigned long long kLimitP = 2000000000ull;  // bound of every wait, about 1 s of cycles
+constexpr int kBlock = 128 * 128;           // 128 rows of 64 elements: one swizzled block
+
+struct Item {
+  long long q_base, k_base;  // first packed rows of the sequence
+  int m_len, k_len;          // its queries and keys
+  int i0;                    // first query of the item
+  int hg;                    // head group
+  int n[2];                  // key tiles of the two row tiles
+  int keys[2];               // keys that the row tiles' last rows see
+  int valid;
+};
+
+constexpr int kMaxSlots = 10;
+struct Bars {
+  unsigned long long q_full, q_empty, kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], p_full[2], o_full[2],
+      item_full[2], item_empty[2], drain;
+  unsigned tmem;
+  int dead;
+  Item item[2];
+};
+
+template <int DP>
+struct Lay {
+  static constexpr int kTileB = DP / 64 * kBlock;          // bytes of a 128-row tile
+  static constexpr int kSlots = DP == 128 ? 5 : 10;        // K and V tiles in flight
+  static constexpr int kQ = 0, kKv = 2 * kTileB, kBars = kKv + kSlots * kTileB;
+  static constexpr int kSmem = kBars + static_cast<int>(sizeof(Bars)) + 1024;  // + alignment of the base
+};
+
+__device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sptr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sptr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
+  return ok != 0u;
+}
+// Bounded wait.  When the limit runs out (or another warp's did) the CTA is
+// dead: every role leaves its loop.
+__device__ __forceinline__ bool bar_wait(Bars* s, unsigned long long* b, unsigned parity, unsigned* status) {
+  if (bar_try(b, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (bar_try(b, parity)) return true;
+    if (*static_cast<volatile int*>(&s->dead)) return false;
+    if (static_cast<unsigned long long>(clock64() - t0) > kLimitP) {
+      *static_cast<volatile int*>(&s->dead) = 1;
+      atomicOr(status, kAttnTimeout);
+      return false;
+    }
+  }
+}
+__device__ __forceinline__ void drain_wait(unsigned long long* b, unsigned parity) {
+  const long long t0 = clock64();
+  while (!bar_try(b, parity) && static_cast<unsigned long long>(clock64() - t0) < kLimitP) {}
+}
+
+__device__ __forceinline__ void tma3(unsigned dst, const CUtensorMap* m, int x, int y, int z, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(sptr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, int y, int z, int w, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(sptr(bar)) : "memory");
+}
+
+// Shared-memory operand descriptors, 128-byte swizzle.  Q and K: rows of 64
+// elements of the summed dimension, groups of 8 rows 1,024 bytes apart.  V:
+// rows are keys (the summed dimension), 64-element blocks of the head
+// dimension one tile block apart.
+__device__ __forceinline__ unsigned long long desc(unsigned addr, unsigned lead, unsigned stride) {
+  return static_cast<unsigned long long>((addr >> 4) & 0x3fff) | (static_cast<unsigned long long>(lead >> 4) << 16) |
+         (static_cast<unsigned long long>(stride >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void mma_ss(unsigned d, unsigned long long a, unsigned long long b, unsigned idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+      "l"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(acc)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long long b, unsigned idesc, bool acc) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\ttcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+      "r"(a), "l"(b), "r"(idesc), "r"(static_cast<unsigned>(acc)) : "memory");
+}
+__device__ __forceinline__ void commit(unsigned long long* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sptr(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+#define TG_R8(a, i) "=r"(a[i]), "=r"(a[i + 1]), "=r"(a[i + 2]), "=r"(a[i + 3]), "=r"(a[i + 4]), "=r"(a[i + 5]), "=r"(a[i + 6]), "=r"(a[i + 7])
+#define TG_I8(a, i) "r"(a[i]), "r"(a[i + 1]), "r"(a[i + 2]), "r"(a[i + 3]), "r"(a[i + 4]), "r"(a[i + 5]), "r"(a[i + 6]), "r"(a[i + 7])
+// 32 columns of this warp's 32 lanes of tensor memory.
+__device__ __forceinline__ void tm_ld32(unsigned (&r)[32], unsigned addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      : TG_R8(r, 0), TG_R8(r, 8), TG_R8(r, 16), TG_R8(r, 24) : "r"(addr));
+}
+__device__ __forceinline__ void tm_st32(unsigned addr, const unsigned (&r)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,"
+      "%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr), TG_I8(r, 0), TG_I8(r, 8), TG_I8(r, 16), TG_I8(r, 24)
+      : "memory");
+}
+__device__ __forceinline__ void tm_ld16(unsigned (&r)[16], unsigned addr) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : TG_R8(r, 0), TG_R8(r, 8) : "r"(addr));
+}
+__device__ __forceinline__ void tm_st16(unsigned addr, const unsigned (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      TG_I8(r, 0), TG_I8(r, 8) : "memory");
+}
+// Keeps every use of loaded registers behind the wait.
+template <int N>
+__device__ __forceinline__ void tm_pin(unsigned (&r)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) asm volatile("" : "+r"(r[i]));
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
+
+struct PromptSetup {
+  int pack, pack_shift;  // heads of one key head in a row tile (a power of two), 128 / pack queries
+  int groups;            // H / pack
+  unsigned* counter;     // [0]: next item, [1]: CTAs done
+};
 
 template <int DP, bool F16>
-__global__ void __launch_bounds__(kThr) prompt_kernel(const AttnCfg c, const PromptArgs a) {
-  constexpr int RB = DP * 2, CPR = RB / 16, KS = DP / 16, MAT = kK * RB;
-  extern __shared__ __align__(128) unsigned char smem[];
-  __shared__ long long found[5];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, h = blockIdx.y, g = h / c.rep;
-  const int chunks = c.D >> 3;
-  for (int i = tid; i < 4 * kK * CPR; i += kThr)
-    if (i % CPR >= chunks)
-      *reinterpret_cast<uint4*>(smem + (i / CPR / kK) * MAT + tile_at<RB>(i / CPR % kK, i % CPR)) = make_uint4(0, 0, 0, 0);
-  dep_wait();
+__global__ void __launch_bounds__(kThreadsP, 1)
+prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const __grid_constant__ CUtensorMap mq,
+              const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using L = Lay<DP>;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (sptr(smem_raw) & 1023)) & 1023);
+  Bars* s = reinterpret_cast<Bars*>(smem + L::kBars);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
-    long long left = blockIdx.x;
-    found[0] = -1;
-    const int64_t* ko = a.koff ? a.koff : a.qoff;
-    for (int b = 0; b < a.batch; ++b) {
-      const long long q0 = a.qoff[b], q1 = a.qoff[b + 1], k0 = ko[b], k1 = ko[b + 1];
-      if (q0 < 0 || q1 < q0 || q1 > a.q_tokens || k0 < 0 || k1 < k0 || k1 > a.kv_tokens) {
-        if (blockIdx.x == 0 && h == 0) atomicOr(c.status, kAttnBadRow);
-        continue;
-      }
-      const long long t = (q1 - q0 + kQ - 1) / kQ;
-      if (left < t) {
-        found[0] = left; found[1] = q0; found[2] = q1 - q0; found[3] = k0; found[4] = k1 - k0;
-        if (blockIdx.x || h) break;
-        left = 1ll << 60;
-      }
-      left -= t;
+    bar_init(&s->q_full, 1);
+    bar_init(&s->q_empty, 1);
+    for (int i = 0; i < L::kSlots; ++i) { bar_init(&s->kv_full[i], 1); bar_init(&s->kv_empty[i], 1); }
+    for (int t = 0; t < 2; ++t) {
+      bar_init(&s->s_full[t], 1);
+      bar_init(&s->p_full[t], 4);
+      bar_init(&s->o_full[t], 1);
+      bar_init(&s->item_full[t], 1);
+      bar_init(&s->item_empty[t], 9);
     }
+    bar_init(&s->drain, 1);
+    s->dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sptr(&s->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
   }
   __syncthreads();
-  if (found[0] < 0) return;
-  const int i0 = static_cast<int>(found[0]) * kQ, m_len = static_cast<int>(found[2]), k_len = static_cast<int>(found[4]);
-  const long long q_base = found[1], k_base = found[3];
-  const int shift = k_len - m_len;  // query i sees keys 0 .. i + shift
-  const int k_end = a.causal ? min(k_len, min(i0 + kQ, m_len) + shift) : k_len;
-  const int tiles = k_end > 0 ? (k_end + kK - 1) / kK : 0;
+  fence_after();
+  const unsigned tmem = s->tmem;
+  dep_wait();
 
-  const auto issue = [&](int t) {
-    if (t < tiles) {
-      const unsigned ks = sptr(smem + (t & 1) * 2 * MAT), vs = ks + MAT;
-      for (int i = tid; i < kK * CPR; i += kThr) {
-        const int r = i / CPR, cc = i % CPR;
-        if (cc >= chunks) continue;
-        const bool on = t * kK + r < k_len;
-        const long long row = k_base + (on ? t * kK + r : 0);
-        cp16(ks + tile_at<RB>(r, cc), static_cast<const uint16_t*>(a.k) + row * a.ks + g * c.D + cc * 8, on);
-        cp16(vs + tile_at<RB>(r, cc), static_cast<const uint16_t*>(a.v) + row * a.vs + g * c.D + cc * 8, on);
-      }
-    }
-    cp_commit();
-  };
-  issue(0);
-  const int r0 = i0 + warp * 16 + (lane >> 2);
-  unsigned qf[KS][4];
-#pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    const int r = r0 + 8 * x;
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + (q_base + r) * a.qs + h * c.D + 2 * (lane & 3);
-#pragma unroll
-    for (int k = 0; k < KS; ++k) {
-      const bool on = r < m_len && 16 * k < c.D;
-      qf[k][x] = on ? *reinterpret_cast<const unsigned*>(q + 16 * k) : 0u;
-      qf[k][2 + x] = on ? *reinterpret_cast<const unsigned*>(q + 16 * k + 8) : 0u;
-    }
-  }
-  float o[KS * 2][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0, 0};
-#pragma unroll
-  for (int k = 0; k < KS * 2; ++k)
-#pragma unroll
-    for (int x = 0; x < 4; ++x) o[k][x] = 0.0f;
-  const float sc = c.scale * kLog2E;
-  const float bias = kWeightBias<F16>;
-  for (int t = 0; t < tiles; ++t) {
-    issue(t + 1);
-    cp_wait<1>();
-    __syncthreads();
-    const unsigned ks = sptr(smem + (t & 1) * 2 * MAT), vs = ks + MAT;
-    float s[8][4];
-#pragma unroll
-    for (int kg = 0; kg < 4; ++kg) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) s[2 * kg][x] = s[2 * kg + 1][x] = 0.0f;
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        unsigned r[4];
-        ldsm4(r, ks + tile_at<RB>(kg * 16 + ((lane >> 4) << 3) + (lane & 7), 2 * k + ((lane >> 3) & 1)));
-        mma16816<F16>(s[2 * kg], qf[k], r[0], r[1]);
-        mma16816<F16>(s[2 * kg + 1], qf[k], r[2], r[3]);
-      }
-    }
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int lim = a.causal ? min(k_len, r0 + 8 * x + shift + 1) : k_len;
-      float top = -INFINITY;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          float& v = s[i][2 * x + y];
-          v = t * kK + i * 8 + 2 * (lane & 3) + y < lim ? v * sc : -INFINITY;
-          top = fmaxf(top, v);
+  if (warp == 9) {
+    // ---- items and copies -------------------------------------------------
+    fewer_registers();
+    const int64_t* ko = a.koff ? a.koff : a.qoff;
+    int b0 = 0;               // sequences b0 .. b0 + 31 are looked at
+    long long base = 0;       // items before sequence b0
+    int slot = 0, it_n = 0;
+    unsigned kv_ph = 1, q_ph = 1;  // parities of the "empty" waits: the first ones pass
+    bool flagged = blockIdx.x != 0;
+    const unsigned kv0 = sptr(smem + L::kKv);
+    bool ok = true;
+    while (ok) {
+      long long want = 0;
+      if (lane == 0) want = atomicAdd(ps.counter, 1u);
+      want = __shfl_sync(~0u, want, 0);
+      Item item{};
+      while (b0 < a.batch) {
+        const int b = b0 + lane;
+        long long q0 = 0, m = 0, k0 = 0, kn = 0;
+        if (b < a.batch) {
+          q0 = a.qoff[b];
+          m = a.qoff[b + 1] - q0;
+          k0 = ko[b];
+          kn = ko[b + 1] - k0;
+          if (q0 < 0 || m < 0 || q0 + m > a.q_tokens || k0 < 0 || kn < 0 || k0 + kn > a.kv_tokens) {
+            if (!flagged) atomicOr(c.status, kAttnBadRow);
+            m = 0;
+          }
         }
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      top = fmaxf(top, m[x]);
-      const float base = top == -INFINITY ? 0.0f : top, f = ex2(m[x] - base);
-      m[x] = top;
-      l[x] *= f;
+        const long long blocks = ((m << ps.pack_shift) + 255) >> 8, mine = blocks * ps.groups;
+        long long upto = mine;
 #pragma unroll
-      for (int k = 0; k < KS * 2; ++k) {
-        o[k][2 * x] *= f;
-        o[k][2 * x + 1] *= f;
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-#pragma unroll
-        for (int y = 0; y < 2; ++y) {
-          s[i][2 * x + y] = ex2(s[i][2 * x + y] - base + bias);
-          l[x] += s[i][2 * x + y];
+        for (int d = 1; d < 32; d <<= 1) {
+          const long long v = __shfl_up_sync(~0u, upto, d);
+          if (lane >= d) upto += v;
         }
-    }
-#pragma unroll
-    for (int kg = 0; kg < 4; ++kg) {
-      const unsigned p[4] = {pack2<F16>(s[2 * kg][0], s[2 * kg][1]), pack2<F16>(s[2 * kg][2], s[2 * kg][3]),
-                             pack2<F16>(s[2 * kg + 1][0], s[2 * kg + 1][1]), pack2<F16>(s[2 * kg + 1][2], s[2 * kg + 1][3])};
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        unsigned r[4];
-        ldsm4t(r, vs + tile_at<RB>(kg * 16 + (lane & 15), 2 * k + (lane >> 4)));
-        mma16816<F16>(o[2 * k], p, r[0], r[1]);
-        mma16816<F16>(o[2 * k + 1], p, r[2], r[3]);
+        const unsigned hit = __ballot_sync(~0u, base + upto > want);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          const long long in = want - (base + upto - mine);  // of lane src
+          if (lane == src) {
+            const int blk = static_cast<int>(blocks - 1 - in / ps.groups);  // the longest first
+            item.q_base = q0;
+            item.k_base = k0;
+            item.m_len = static_cast<int>(m);
+            item.k_len = static_cast<int>(kn);
+            item.i0 = blk * (256 >> ps.pack_shift);
+            item.hg = static_cast<int>(in % ps.groups);
+            for (int t = 0; t < 2; ++t) {
+              const int first = item.i0 + (t * kRowsT >> ps.pack_shift);
+              const int last = min(item.i0 + ((t * kRowsT + kRowsT - 1) >> ps.pack_shift), item.m_len - 1);
+              int keys = a.causal ? min(item.k_len, last + 1 + item.k_len - item.m_len) : item.k_len;
+              if (first >= item.m_len || keys < 0) keys = 0;
+              item.keys[t] = keys;
+              item.n[t] = (keys + kKeys - 1) / kKeys;
+            }
+            item.valid = 1;
+          }
+          item.q_base = __shfl_sync(~0u, item.q_base, src);
+          item.k_base = __shfl_sync(~0u, item.k_base, src);
+          item.m_len = __shfl_sync(~0u, item.m_len, src);
+          item.k_len = __shfl_sync(~0u, item.k_len, src);
+          item.i0 = __shfl_sync(~0u, item.i0, src);
+          item.hg = __shfl_sync(~0u, item.hg, src);
+          for (int t = 0; t < 2; ++t) {
+            item.keys[t] = __shfl_sync(~0u, item.keys[t], src);
+            item.n[t] = __shfl_sync(~0u, item.n[t], src);
+          }
+          item.valid = 1;
+          break;
+        }
+        base += __shfl_sync(~0u, upto, 31);
+        b0 += 32;
+      }
+      const int is = it_n & 1;
+      ok = bar_wait(s, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c.status);
+      if (!ok) break;
+      if (lane == 0) {
+        s->item[is] = item;
+        bar_arrive(&s->item_full[is]);
+      }
+      ++it_n;
+      if (!item.valid) break;
+      const int n = max(item.n[0], item.n[1]);
+      if (n == 0) continue;
+      ok = bar_wait(s, &s->q_empty, q_ph, c.status);
+      if (!ok) break;
+      q_ph ^= 1;
+      if (lane == 0) {
+        const int tiles = item.n[1] > 0 ? 2 : 1;
+        bar_expect(&s->q_full, tiles * L::kTileB);
+        for (int t = 0; t < tiles; ++t)
+          for (int x = 0; x < DP / 64; ++x)
+            tma4(sptr(smem) + t * L::kTileB + x * kBlock, &mq, x * 64, 0, item.hg,
+                 static_cast<int>(item.q_base) + item.i0 + (t * kRowsT >> ps.pack_shift), &s->q_full);
+      }
+      const int g = (item.hg << ps.pack_shift) / c.rep;
+      for (int j = 0; j < n && ok; ++j) {
+        for (int w = 0; w < 2; ++w) {
+          ok = bar_wait(s, &s->kv_empty[slot], kv_ph, c.status);
+          if (!ok) break;
+          if (lane == 0) {
+            bar_expect(&s->kv_full[slot], L::kTileB);
+            for (int x = 0; x < DP / 64; ++x)
+              tma3(kv0 + slot * L::kTileB + x * kBlock, w ? &mv : &mk, x * 64, g,
+                   static_cast<int>(item.k_base) + j * kKeys, &s->kv_full[slot]);
+          }
+          if (++slot == L::kSlots) { slot = 0; kv_ph ^= 1; }
+        }
       }
     }
-    __syncthreads();
-  }
-  cp_wait<0>();
+    if (!ok && lane == 0) {
+      // a wait ran out: copies in flight land before the CTA's memory goes
+      for (int i = 0; i < L::kSlots; ++i) drain_wait(&s->kv_full[i], (i < slot ? kv_ph ^ 1 : kv_ph));
+      drain_wait(&s->q_full, q_ph);
+    }
+  } else if (warp == 8) {
+    // ---- matrix instructions ----------------------------------------------
+    fewer_registers();
+    const unsigned fmt = F16 ? 0u : 1u;
+    const unsigned id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | (8u << 24);
+    const unsigned id_pv = id0 | (1u << 16) | (static_cast<unsigned>(c.D >> 3) << 17);
+    const int ks = c.D >> 4;
+    const unsigned q0 = sptr(smem), kv0 = sptr(smem + L::kKv);
+    int slot = 0, it_n = 0;
+    unsigned kv_ph = 0, q_ph = 0, p_ph[2] = {0, 0};
+    bool ok = true;
+    while (ok) {
+      const int is = it_n & 1;
+      ok = bar_wait(s, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      if (!ok) break;
+      const int n0 = s->item[is].n[0], n1 = s->item[is].n[1], keys0 = s->item[is].keys[0], keys1 = s->item[is].keys[1];
+      const int k_len = s->item[is].k_len, valid = s->item[is].valid;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (!valid) break;
+      const int n = max(n0, n1);
+      if (n == 0) continue;
+      ok = bar_wait(s, &s->q_full, q_ph, c.status);
+      if (!ok) break;
+      q_ph ^= 1;
+      const auto next = [&]() {
+        if (++slot == L::kSlots) { slot = 0; kv_ph ^= 1; }
+      };
+      const auto nt = [&](int t) { return t ? n1 : n0; };
+      // keys of tile j that row tile t needs, in steps of 16
+      const auto width = [&](int t, int j) { return min(kKeys, ((t ? keys1 : keys0) - j * kKeys + 15) & ~15); };
+      const auto qk = [&](int t, int j, unsigned kaddr) {
+        if (lane == 0) {
+          const unsigned id = id0 | (static_cast<unsigned>(width(t, j) >> 3) << 17);
+          for (int k = 0; k < ks; ++k) {
+            const unsigned off = (k >> 2) * kBlock + (k & 3) * 32;
+            mma_ss(tmem + t * 128, desc(q0 + t * L::kTileB + off, 16, 1024), desc(kaddr + off, 16, 1024), id, k > 0);
+          }
+          commit(&s->s_full[t]);
+        }
+      };
+      const auto pv = [&](int t, int j, unsigned vaddr) {
+        if (lane == 0) {
+          const int steps = width(t, j) >> 4;
+          for (int k = 0; k < steps; ++k)
+            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, desc(vaddr + k * 2048, kBlock, 1024), id_pv, j > 0 || k > 0);
+          if (j + 1 == nt(t)) commit(&s->o_full[t]);
+        }
+      };
+      unsigned kslot = slot;
+      ok = bar_wait(s, &s->kv_full[slot], kv_ph, c.status);
+      if (!ok) break;
+      next();
+      fence_after();
+      for (int t = 0; t < 2; ++t)
+        if (nt(t) > 0) qk(t, 0, kv0 + kslot * L::kTileB);
+      if (lane == 0) {
+        commit(&s->kv_empty[kslot]);
+        if (n == 1) commit(&s->q_empty);
+      }
+      for (int j = 0; j < n && ok; ++j) {
+        const int vslot = slot;
+        const unsigned vaddr = kv0 + vslot * L::kTileB;
+        ok = bar_wait(s, &s->kv_full[vslot], kv_ph, c.status);
+        if (!ok) break;
+        next();
+        // rows behind the sequence's end are another sequence's: their weights
+        // are 0, but 0 x NaN is not, so what the products read of them is zeroed
+        const int end = k_len - j * kKeys;
+        if (end < kKeys) {
+          const int stop = min(kKeys, (end + 15) & ~15);
+          for (int i = lane; i < (stop - end) * (DP / 8); i += 32) {
+            const int r = end + i / (DP / 8), x = i % (DP / 8);
+            *reinterpret_cast<uint4*>(smem + L::kKv + vslot * L::kTileB + (x >> 3) * kBlock + r * 128 + (x & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+          __syncwarp();
+        }
+        const int kn = slot;
+        bool k_in = false;
+        for (int t = 0; t < 2 && ok; ++t) {
+          if (j < nt(t)) {
+            ok = bar_wait(s, &s->p_full[t], p_ph[t], c.status);
+            if (!ok) break;
+            p_ph[t] ^= 1;
+            fence_after();
+            pv(t, j, vaddr);
+          }
+          if (j + 1 < nt(t)) {
+            if (!k_in) {
+              ok = bar_wait(s, &s->kv_full[kn], kv_ph, c.status);
+              if (!ok) break;
+              k_in = true;
+              fence_after();
+            }
+            qk(t, j + 1, kv0 + kn * L::kTileB);
+          }
+        }
+        if (!ok) break;
+        if (lane == 0) {
+          commit(&s->kv_empty[vslot]);
+          if (k_in) commit(&s->kv_empty[kn]);
+          if (j + 2 == n) commit(&s->q_empty);
+        }
+        if (k_in) next();
+      }
+    }
+    if (!ok && lane == 0) {
+      commit(&s->drain);
+      drain_wait(&s->drain, 0);
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- softmax: one thread per row --------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    const int t = warp >> 2;
+    const int row = t * kRowsT + (tid & 127);
+    const unsigned lanes = static_cast<unsigned>(warp & 3) << 21;  // this warp's lanes of tensor memory
+    const unsigned ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    const float sc = c.scale * kLog2E;
+    constexpr float bias = kWeightBias<F16>;
+    int it_n = 0;
+    unsigned s_ph = 0, o_ph = 0;
+    bool ok = true;
+    while (ok) {
+      const int is = it_n & 1;
+      ok = bar_wait(s, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      if (!ok) break;
+      const Item it = s->item[is];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (!it.valid) break;
+      const int n = it.n[t];
+      const int i = it.i0 + (row >> ps.pack_shift);
+      const int head = (it.hg << ps.pack_shift) + (row & (ps.pack - 1));
+      const int lim = a.causal ? min(it.k_len, i + 1 + it.k_len - it.m_len) : it.k_len;
+      const int lim_w = __shfl_sync(~0u, lim, 0);  // the warp's smallest
+      float m = -INFINITY, l = 0.0f;
+      for (int j = 0; j < n; ++j) {
+        ok = bar_wait(s, &s->s_full[t], s_ph, c.status);
+        if (!ok) break;
+        s_ph ^= 1;
+        fence_after();
+        unsigned v[4][32];
 #pragma unroll
-  for (int x = 0; x < 2; ++x) {
-    l[x] += __shfl_xor_sync(~0u, l[x], 1);
-    l[x] += __shfl_xor_sync(~0u, l[x], 2);
-    const int r = r0 + 8 * x;
-    if (r >= m_len) continue;
-    const long long row = (q_base + r) * c.H + h;
-    const float f = l[x] > 0.0f ? 1.0f / l[x] : 0.0f;
+        for (int x = 0; x < 4; ++x) tm_ld32(v[x], ts + x * 32);
+        tm_wait_ld();
 #pragma unroll
-    for (int k = 0; k < KS * 2; ++k)
-      if (8 * k < c.D)
-        *reinterpret_cast<unsigned*>(static_cast<uint16_t*>(a.out) + row * c.D + 8 * k + 2 * (lane & 3)) =
-            pack2<F16>(o[k][2 * x] * f, o[k][2 * x + 1] * f);
-    if (a.lse && (lane & 3) == 0) a.lse[row] = l[x] > 0.0f ? (m[x] + log2f(l[x]) - bias) * kLn2 : -INFINITY;
+        for (int x = 0; x < 4; ++x) tm_pin(v[x]);
+        if (j * kKeys + kKeys > lim_w) {
+          const int rest = lim - j * kKeys;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (x * 32 + y >= rest) v[x][y] = 0xff800000u;  // -infinity
+        }
+        float top[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          top[x] = __uint_as_float(v[x][0]);
+#pragma unroll
+          for (int y = 1; y < 32; ++y) top[x] = fmaxf(top[x], __uint_as_float(v[x][y]));
+        }
+        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        const bool raise = mt > m + kLazy;
+        if (__any_sync(~0u, raise)) {
+          const float f = raise ? ex2(m - mt) : 1.0f;
+          if (raise) m = mt;
+          l *= f;
+          if (j > 0) {
+            for (int x = 0; x < c.D; x += 16) {
+              unsigned o[16];
+              tm_ld16(o, to + x);
+              tm_wait_ld();
+              tm_pin(o);
+#pragma unroll
+              for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+              tm_st16(to + x, o);
+            }
+          }
+        }
+        const float off = m == -INFINITY ? 0.0f : bias - m;
+        float sum[2] = {0.0f, 0.0f};
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          unsigned p[32];
+#pragma unroll
+          for (int y = 0; y < 32; ++y) {
+            const unsigned* src = &v[2 * x + (y >> 4)][(2 * y) & 31];
+            const float p0 = ex2(fmaf(__uint_as_float(src[0]), sc, off)), p1 = ex2(fmaf(__uint_as_float(src[1]), sc, off));
+            sum[0] += p0;
+            sum[1] += p1;
+            p[y] = pack2<F16>(p0, p1);
+          }
+          tm_st32(ts + x * 32, p);
+        }
+        l += sum[0] + sum[1];
+        tm_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&s->p_full[t]);
+      }
+      if (!ok) break;
+      const bool mine = i < it.m_len;
+      const long long at = (it.q_base + i) * c.H + head;
+      if (n > 0) {
+        ok = bar_wait(s, &s->o_full[t], o_ph, c.status);
+        if (!ok) break;
+        o_ph ^= 1;
+        fence_after();
+      }
+      const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
+      for (int x = 0; x < c.D; x += 16) {
+        unsigned o[16];
+        if (n > 0) {
+          tm_ld16(o, to + x);
+          tm_wait_ld();
+          tm_pin(o);
+        }
+        if (mine) {
+          unsigned w[8];
+#pragma unroll
+          for (int y = 0; y < 8; ++y)
+            w[y] = l == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at * c.D + x);
+          dst[0] = make_uint4(w[0], w[1], w[2], w[3]);
+          dst[1] = make_uint4(w[4], w[5], w[6], w[7]);
+        }
+      }
+      if (mine && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l) - bias) * kLn2;
+      fence_before();  // the reads of O come before the next item's products
+    }
+  } else {
+    fewer_registers();
   }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (tid == 0 && atomicAdd(ps.counter + 1, 1u) == gridDim.x - 1) {
+    ps.counter[0] = 0u;  // the last CTA leaves the counters at zero for the next call
+    ps.counter[1] = 0u;
+  }
+}
+
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool encode(void* fn, CUtensorMap* m, bool f16, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
+            const cuuint32_t* box) {
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return reinterpret_cast<EncodeFn>(fn)(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
+                                        const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int DP, bool F16>
 cudaError_t go(const AttnCfg& c, const PromptArgs* a, cudaStream_t s) {
   auto k = prompt_kernel<DP, F16>;
-  constexpr int smem = 4 * kK * DP * 2;
-  if (!a) return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  using L = Lay<DP>;
+  if (!a) return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  PromptSetup ps{};
+  ps.pack = 1;
+  while (ps.pack < kRowsT && c.rep % (2 * ps.pack) == 0) {
+    ps.pack *= 2;
+    ++ps.pack_shift;
+  }
+  ps.groups = c.H / ps.pack;
+  ps.counter = c.prompt_count;
+  const cuuint64_t D = c.D, e = 2;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(ps.pack), static_cast<cuuint64_t>(ps.groups),
+                                static_cast<cuuint64_t>(a->q_tokens)};
+    const cuuint64_t st[3] = {D * e, D * e * ps.pack, static_cast<cuuint64_t>(a->qs) * e};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(ps.pack), 1, static_cast<cuuint32_t>(kRowsT / ps.pack)};
+    if (!encode(c.encode, &mq, F16, a->q, 4, dims, st, box)) return cudaErrorInvalidValue;
+  }
+  for (int w = 0; w < 2; ++w) {
+    // without keys no copy is issued: any valid tensor will do
+    const bool none = a->kv_tokens == 0;
+    const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(none ? 1 : c.G), static_cast<cuuint64_t>(none ? 1 : a->kv_tokens)};
+    const cuuint64_t st[2] = {D * e, static_cast<cuuint64_t>(none ? a->qs : w ? a->vs : a->ks) * e};
+    const cuuint32_t box[3] = {64, 1, kKeys};
+    if (!encode(c.encode, w ? &mv : &mk, F16, none ? a->q : w ? a->v : a->k, 3, dims, st, box)) return cudaErrorInvalidValue;
+  }
+  // at most this many items; the grid is one CTA per SM
+  const long long items = (((static_cast<long long>(a->q_tokens) << ps.pack_shift) >> 8) + std::min(a->batch, a->q_tokens)) * ps.groups;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(a->q_tokens / kQ + std::min(a->batch, a->q_tokens), c.H);
-  cfg.blockDim = dim3(kThr);
-  cfg.dynamicSmemBytes = smem;
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(items, c.nsm)));
+  cfg.blockDim = dim3(kThreadsP);
+  cfg.dynamicSmemBytes = L::kSmem;
   cfg.stream = s;
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, k, c, *a);
+  return cudaLaunchKernelEx(&cfg, k, c, *a, ps, mq, mk, mv);
 }
 
 cudaError_t by_type(const AttnCfg& c, const PromptArgs* a, cudaStream_t s) {
@@ -192,7 +640,13 @@ cudaError_t by_type(const AttnCfg& c, const PromptArgs* a, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t prepare_prompt(const AttnCfg& c) { return by_type(c, nullptr, nullptr); }
+cudaError_t prepare_prompt(AttnCfg* c) {
+  cudaDriverEntryPointQueryResult found;
+  cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &c->encode, 12000, cudaEnableDefault, &found);
+  if (e != cudaSuccess) return e;
+  if (found != cudaDriverEntryPointSuccess || !c->encode) return cudaErrorNotSupported;
+  return by_type(*c, nullptr, nullptr);
+}
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s) { return by_type(c, &a, s); }
 
 }  // namespace tg
