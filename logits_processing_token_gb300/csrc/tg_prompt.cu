@@ -130,6 +130,14 @@ __device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned long lon
 __device__ __forceinline__ void commit(unsigned long long* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(sptr(bar)) : "memory");
 }
+// True in one thread of the warp, always the same: the compiler then knows that
+// the matrix instructions' operands are uniform (behind `lane == 0` it does
+// not, and every instruction took over 100 cycles to issue).
+__device__ __forceinline__ bool elect() {
+  unsigned p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0u;
+}
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
@@ -167,6 +175,32 @@ __device__ __forceinline__ void tm_pin(unsigned (&r)[N]) {
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+// Two f32 in one 64-bit register: one instruction for both.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(unsigned long long a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 88;"); }
 
 struct PromptSetup {
@@ -359,22 +393,28 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       // keys of tile j that row tile t needs, in steps of 16
       const auto width = [&](int t, int j) { return min(kKeys, ((t ? keys1 : keys0) - j * kKeys + 15) & ~15); };
       const auto qk = [&](int t, int j, unsigned kaddr) {
-        if (lane == 0) {
-          const unsigned id = id0 | (static_cast<unsigned>(width(t, j) >> 3) << 17);
-          for (int k = 0; k < ks; ++k) {
-            const unsigned off = (k >> 2) * kBlock + (k & 3) * 32;
-            mma_ss(tmem + t * 128, desc(q0 + t * L::kTileB + off, 16, 1024), desc(kaddr + off, 16, 1024), id, k > 0);
+        const unsigned id = id0 | (static_cast<unsigned>(width(t, j) >> 3) << 17);
+        const unsigned long long qd = desc(q0 + t * L::kTileB, 16, 1024), kd = desc(kaddr, 16, 1024);
+        if (elect()) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const unsigned off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+            if (k < ks) mma_ss(tmem + t * 128, qd + off, kd + off, id, k > 0);
           }
           commit(&s->s_full[t]);
         }
+        __syncwarp();
       };
       const auto pv = [&](int t, int j, unsigned vaddr) {
-        if (lane == 0) {
-          const int steps = width(t, j) >> 4;
-          for (int k = 0; k < steps; ++k)
-            mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, desc(vaddr + k * 2048, kBlock, 1024), id_pv, j > 0 || k > 0);
+        const int steps = width(t, j) >> 4;
+        const unsigned long long vd = desc(vaddr, kBlock, 1024);
+        if (elect()) {
+#pragma unroll
+          for (int k = 0; k < kKeys / 16; ++k)
+            if (k < steps) mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), id_pv, j > 0 || k > 0);
           if (j + 1 == nt(t)) commit(&s->o_full[t]);
         }
+        __syncwarp();
       };
       unsigned kslot = slot;
       ok = bar_wait(s, &s->kv_full[slot], kv_ph, c.status);
@@ -383,10 +423,11 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       fence_after();
       for (int t = 0; t < 2; ++t)
         if (nt(t) > 0) qk(t, 0, kv0 + kslot * L::kTileB);
-      if (lane == 0) {
+      if (elect()) {
         commit(&s->kv_empty[kslot]);
         if (n == 1) commit(&s->q_empty);
       }
+      __syncwarp();
       for (int j = 0; j < n && ok; ++j) {
         const int vslot = slot;
         const unsigned vaddr = kv0 + vslot * L::kTileB;
@@ -427,17 +468,21 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
           }
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (elect()) {
           commit(&s->kv_empty[vslot]);
           if (k_in) commit(&s->kv_empty[kn]);
           if (j + 2 == n) commit(&s->q_empty);
         }
+        __syncwarp();
         if (k_in) next();
       }
     }
-    if (!ok && lane == 0) {
-      commit(&s->drain);
-      drain_wait(&s->drain, 0);
+    if (!ok) {
+      __syncwarp();
+      if (elect()) {
+        commit(&s->drain);
+        drain_wait(&s->drain, 0);
+      }
     }
     __syncwarp();
   } else if (warp < 8) {
@@ -489,11 +534,11 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         float top[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          top[x] = __uint_as_float(v[x][0]);
+          top[x] = fmaxf(__uint_as_float(v[x][0]), __uint_as_float(v[x][1]));
 #pragma unroll
-          for (int y = 1; y < 32; ++y) top[x] = fmaxf(top[x], __uint_as_float(v[x][y]));
+          for (int y = 2; y < 32; y += 2) top[x] = max3(top[x], __uint_as_float(v[x][y]), __uint_as_float(v[x][y + 1]));
         }
-        const float mt = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * sc;
+        const float mt = max3(top[0], top[1], fmaxf(top[2], top[3])) * sc;
         const bool raise = mt > m + kLazy;
         if (__any_sync(~0u, raise)) {
           const float f = raise ? ex2(m - mt) : 1.0f;
@@ -512,25 +557,27 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
           }
         }
         const float off = m == -INFINITY ? 0.0f : bias - m;
-        float sum[2] = {0.0f, 0.0f};
+        const unsigned long long sc2 = pair(sc, sc), off2 = pair(off, off);
+        unsigned long long sum[2] = {0ull, 0ull};
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           unsigned p[32];
 #pragma unroll
           for (int y = 0; y < 32; ++y) {
             const unsigned* src = &v[2 * x + (y >> 4)][(2 * y) & 31];
-            const float p0 = ex2(fmaf(__uint_as_float(src[0]), sc, off)), p1 = ex2(fmaf(__uint_as_float(src[1]), sc, off));
-            sum[0] += p0;
-            sum[1] += p1;
+            const float2 e = unpair(fma2(pair(__uint_as_float(src[0]), __uint_as_float(src[1])), sc2, off2));
+            const float p0 = ex2(e.x), p1 = ex2(e.y);
+            sum[y & 1] = add2(sum[y & 1], pair(p0, p1));
             p[y] = pack2<F16>(p0, p1);
           }
           tm_st32(ts + x * 32, p);
         }
-        l += sum[0] + sum[1];
         tm_wait_st();
         fence_before();
         __syncwarp();
         if (lane == 0) bar_arrive(&s->p_full[t]);
+        const float2 l2 = unpair(add2(sum[0], sum[1]));
+        l += l2.x + l2.y;
       }
       if (!ok) break;
       const bool mine = i < it.m_len;
