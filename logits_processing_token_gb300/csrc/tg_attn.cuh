@@ -3,6 +3,7 @@
 #pragma once
 
 #include <cstdint>
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -23,6 +24,7 @@ struct AttnCfg {
   int H, G, D, rep;        // query heads, key heads, head size, H / G
   int dtype, ctype;        // tg_dtype of the tensors and of the cache
   int page_size, page_shift;
+  int token_major;         // a page is [tokens, heads, D], else [heads, tokens, D]
   long long slot_stride;   // elements between tokens of one head inside a page
   long long head_stride;   // elements between heads inside a page
   float scale;
@@ -91,6 +93,19 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
 // CTAs of the step kernel per SM at most: sizes the handle's workspace.
 constexpr int kStepCtasPerSm = 4;
+
+// A tensor map of `rank` dimensions (innermost first; strides in bytes from
+// dimension 1 on) through the driver's encoder; false when it refuses.
+typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
+                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline bool encode_map(void* fn, CUtensorMap* m, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* p, int rank,
+                       const cuuint64_t* dims, const cuuint64_t* strides, const cuuint32_t* box) {
+  const cuuint32_t one[4] = {1, 1, 1, 1};
+  return reinterpret_cast<EncodeFn>(fn)(m, type, rank, const_cast<void*>(p), dims, strides, box, one,
+                                        CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 // ---------------------------------------------------------------------------
 // Device helpers
@@ -172,6 +187,57 @@ __device__ __forceinline__ unsigned tile_at(int r, int c) {
   } else {
     return r * RB + (c ^ (r & 7)) * 16;
   }
+}
+
+// Barriers in shared memory.
+constexpr unsigned long long kAttnWaitLimit = 2000000000ull;  // bound of every wait, about 1 s of cycles
+__device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
+  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sptr(b)) : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes) {
+  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sptr(b)), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
+  return ok != 0u;
+}
+// Bounded wait.  When the limit runs out (or another warp's did) the CTA is
+// dead: every role leaves its loop.
+__device__ __forceinline__ bool bar_wait(int* dead, unsigned long long* b, unsigned parity, unsigned* status) {
+  if (bar_try(b, parity)) return true;
+  const long long t0 = clock64();
+  for (;;) {
+    if (bar_try(b, parity)) return true;
+    if (*static_cast<volatile int*>(dead)) return false;
+    if (static_cast<unsigned long long>(clock64() - t0) > kAttnWaitLimit) {
+      *static_cast<volatile int*>(dead) = 1;
+      atomicOr(status, kAttnTimeout);
+      return false;
+    }
+  }
+}
+// The wait for copies still in flight after that.
+__device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned parity) {
+  const long long t0 = clock64();
+  while (!bar_try(b, parity) && static_cast<unsigned long long>(clock64() - t0) < kAttnWaitLimit) {}
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+__device__ __forceinline__ void tma3(unsigned dst, const CUtensorMap* m, int x, int y, int z, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(sptr(bar)) : "memory");
+}
+__device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, int y, int z, int w, unsigned long long* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(sptr(bar)) : "memory");
 }
 
 // Weights exp2(s - m) of f16 products are stored times 2^8: a weight 2^-33 of

@@ -119,6 +119,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.page_size = p->page_size;
   while ((1 << d.page_shift) < d.page_size) ++d.page_shift;
   const bool token = p->page_layout == TG_PAGES_TOKEN_HEAD;
+  d.token_major = token;
   d.slot_stride = token ? static_cast<long long>(d.G) * d.D : d.D;
   d.head_stride = token ? d.D : static_cast<long long>(d.page_size) * d.D;
   d.scale = p->scale > 0.0f ? p->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d.D)));
@@ -127,8 +128,8 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.max_n = p->max_step_tokens ? p->max_step_tokens : 17;
   cudaError_t e = cudaGetDevice(&cfg->device);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.nsm, cudaDevAttrMultiProcessorCount, cfg->device);
-  if (e == cudaSuccess) e = tg::prepare_step(&d);
   if (e == cudaSuccess) e = tg::prepare_prompt(&d);
+  if (e == cudaSuccess) e = tg::prepare_step(&d);
   if (e != cudaSuccess) { delete cfg; return from_cuda(e); }
   // two slots per CTA of a step: the sequence it begins inside and the one it ends inside
   d.step_rows = std::min(128, (d.max_n * d.rep + 15) / 16 * 16);

@@ -21,7 +21,6 @@
 // Tensor memory: S0, S1 (128 columns each; P overwrites S as 16-bit pairs),
 // O0, O1 (128 columns each): all 512.
 #include <algorithm>
-#include <cuda.h>
 
 #include "tg_attn.cuh"
 
@@ -32,7 +31,6 @@ constexpr int kRowsT = 128;                 // rows of a tile
 constexpr int kKeys = 128;                  // keys of a tile
 constexpr int kThreadsP = 384;
 constexpr float kLazy = 6.0f;               // a row's reference may lag its maximum by 2^6
-constexpr unsigned long long kLimitP = 2000000000ull;  // bound of every wait, about 1 s of cycles
 constexpr int kBlock = 128 * 128;           // 128 rows of 64 elements: one swizzled block
 
 struct Item {
@@ -61,53 +59,6 @@ struct Lay {
   static constexpr int kQ = 0, kKv = 2 * kTileB, kBars = kKv + kSlots * kTileB;
   static constexpr int kSmem = kBars + static_cast<int>(sizeof(Bars)) + 1024;  // + alignment of the base
 };
-
-__device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
-  asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
-}
-__device__ __forceinline__ void bar_arrive(unsigned long long* b) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(sptr(b)) : "memory");
-}
-__device__ __forceinline__ void bar_expect(unsigned long long* b, unsigned bytes) {
-  asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(sptr(b)), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) {
-  unsigned ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
-  return ok != 0u;
-}
-// Bounded wait.  When the limit runs out (or another warp's did) the CTA is
-// dead: every role leaves its loop.
-__device__ __forceinline__ bool bar_wait(Bars* s, unsigned long long* b, unsigned parity, unsigned* status) {
-  if (bar_try(b, parity)) return true;
-  const long long t0 = clock64();
-  for (;;) {
-    if (bar_try(b, parity)) return true;
-    if (*static_cast<volatile int*>(&s->dead)) return false;
-    if (static_cast<unsigned long long>(clock64() - t0) > kLimitP) {
-      *static_cast<volatile int*>(&s->dead) = 1;
-      atomicOr(status, kAttnTimeout);
-      return false;
-    }
-  }
-}
-__device__ __forceinline__ void drain_wait(unsigned long long* b, unsigned parity) {
-  const long long t0 = clock64();
-  while (!bar_try(b, parity) && static_cast<unsigned long long>(clock64() - t0) < kLimitP) {}
-}
-
-__device__ __forceinline__ void tma3(unsigned dst, const CUtensorMap* m, int x, int y, int z, unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
-      "l"(m), "r"(x), "r"(y), "r"(z), "r"(sptr(bar)) : "memory");
-}
-__device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, int y, int z, int w, unsigned long long* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(sptr(bar)) : "memory");
-}
 
 // Shared-memory operand descriptors, 128-byte swizzle.  Q and K: rows of 64
 // elements of the summed dimension, groups of 8 rows 1,024 bytes apart.  V:
@@ -319,7 +270,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         b0 += 32;
       }
       const int is = it_n & 1;
-      ok = bar_wait(s, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c.status);
       if (!ok) break;
       if (lane == 0) {
         s->item[is] = item;
@@ -329,7 +280,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       if (!item.valid) break;
       const int n = max(item.n[0], item.n[1]);
       if (n == 0) continue;
-      ok = bar_wait(s, &s->q_empty, q_ph, c.status);
+      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c.status);
       if (!ok) break;
       q_ph ^= 1;
       if (lane == 0) {
@@ -343,7 +294,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       const int g = (item.hg << ps.pack_shift) / c.rep;
       for (int j = 0; j < n && ok; ++j) {
         for (int w = 0; w < 2; ++w) {
-          ok = bar_wait(s, &s->kv_empty[slot], kv_ph, c.status);
+          ok = bar_wait(&s->dead, &s->kv_empty[slot], kv_ph, c.status);
           if (!ok) break;
           if (lane == 0) {
             bar_expect(&s->kv_full[slot], L::kTileB);
@@ -357,8 +308,8 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     }
     if (!ok && lane == 0) {
       // a wait ran out: copies in flight land before the CTA's memory goes
-      for (int i = 0; i < L::kSlots; ++i) drain_wait(&s->kv_full[i], (i < slot ? kv_ph ^ 1 : kv_ph));
-      drain_wait(&s->q_full, q_ph);
+      for (int i = 0; i < L::kSlots; ++i) bar_drain(&s->kv_full[i], (i < slot ? kv_ph ^ 1 : kv_ph));
+      bar_drain(&s->q_full, q_ph);
     }
   } else if (warp == 8) {
     // ---- matrix instructions ----------------------------------------------
@@ -373,7 +324,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
-      ok = bar_wait(s, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
       if (!ok) break;
       const int n0 = s->item[is].n[0], n1 = s->item[is].n[1], keys0 = s->item[is].keys[0], keys1 = s->item[is].keys[1];
       const int k_len = s->item[is].k_len, valid = s->item[is].valid;
@@ -383,7 +334,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       if (!valid) break;
       const int n = max(n0, n1);
       if (n == 0) continue;
-      ok = bar_wait(s, &s->q_full, q_ph, c.status);
+      ok = bar_wait(&s->dead, &s->q_full, q_ph, c.status);
       if (!ok) break;
       q_ph ^= 1;
       const auto next = [&]() {
@@ -417,7 +368,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         __syncwarp();
       };
       unsigned kslot = slot;
-      ok = bar_wait(s, &s->kv_full[slot], kv_ph, c.status);
+      ok = bar_wait(&s->dead, &s->kv_full[slot], kv_ph, c.status);
       if (!ok) break;
       next();
       fence_after();
@@ -431,7 +382,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       for (int j = 0; j < n && ok; ++j) {
         const int vslot = slot;
         const unsigned vaddr = kv0 + vslot * L::kTileB;
-        ok = bar_wait(s, &s->kv_full[vslot], kv_ph, c.status);
+        ok = bar_wait(&s->dead, &s->kv_full[vslot], kv_ph, c.status);
         if (!ok) break;
         next();
         // rows behind the sequence's end are another sequence's: their weights
@@ -451,7 +402,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         bool k_in = false;
         for (int t = 0; t < 2 && ok; ++t) {
           if (j < nt(t)) {
-            ok = bar_wait(s, &s->p_full[t], p_ph[t], c.status);
+            ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c.status);
             if (!ok) break;
             p_ph[t] ^= 1;
             fence_after();
@@ -459,7 +410,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
           }
           if (j + 1 < nt(t)) {
             if (!k_in) {
-              ok = bar_wait(s, &s->kv_full[kn], kv_ph, c.status);
+              ok = bar_wait(&s->dead, &s->kv_full[kn], kv_ph, c.status);
               if (!ok) break;
               k_in = true;
               fence_after();
@@ -481,7 +432,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       __syncwarp();
       if (elect()) {
         commit(&s->drain);
-        drain_wait(&s->drain, 0);
+        bar_drain(&s->drain, 0);
       }
     }
     __syncwarp();
@@ -499,7 +450,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
-      ok = bar_wait(s, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
       if (!ok) break;
       const Item it = s->item[is];
       __syncwarp();
@@ -513,7 +464,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       const int lim_w = __shfl_sync(~0u, lim, 0);  // the warp's smallest
       float m = -INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j) {
-        ok = bar_wait(s, &s->s_full[t], s_ph, c.status);
+        ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c.status);
         if (!ok) break;
         s_ph ^= 1;
         fence_after();
@@ -583,7 +534,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       const bool mine = i < it.m_len;
       const long long at = (it.q_base + i) * c.H + head;
       if (n > 0) {
-        ok = bar_wait(s, &s->o_full[t], o_ph, c.status);
+        ok = bar_wait(&s->dead, &s->o_full[t], o_ph, c.status);
         if (!ok) break;
         o_ph ^= 1;
         fence_after();
@@ -622,19 +573,6 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
   }
 }
 
-typedef CUresult (*EncodeFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*,
-                             const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
-                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-bool encode(void* fn, CUtensorMap* m, bool f16, const void* p, int rank, const cuuint64_t* dims, const cuuint64_t* strides,
-            const cuuint32_t* box) {
-  const cuuint32_t one[4] = {1, 1, 1, 1};
-  return reinterpret_cast<EncodeFn>(fn)(m, f16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, rank,
-                                        const_cast<void*>(p), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 template <int DP, bool F16>
 cudaError_t go(const AttnCfg& c, const PromptArgs* a, cudaStream_t s) {
   auto k = prompt_kernel<DP, F16>;
@@ -649,13 +587,14 @@ cudaError_t go(const AttnCfg& c, const PromptArgs* a, cudaStream_t s) {
   ps.groups = c.H / ps.pack;
   ps.counter = c.prompt_count;
   const cuuint64_t D = c.D, e = 2;
+  const CUtensorMapDataType type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   CUtensorMap mq, mk, mv;
   {
     const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(ps.pack), static_cast<cuuint64_t>(ps.groups),
                                 static_cast<cuuint64_t>(a->q_tokens)};
     const cuuint64_t st[3] = {D * e, D * e * ps.pack, static_cast<cuuint64_t>(a->qs) * e};
     const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(ps.pack), 1, static_cast<cuuint32_t>(kRowsT / ps.pack)};
-    if (!encode(c.encode, &mq, F16, a->q, 4, dims, st, box)) return cudaErrorInvalidValue;
+    if (!encode_map(c.encode, &mq, type, CU_TENSOR_MAP_SWIZZLE_128B, a->q, 4, dims, st, box)) return cudaErrorInvalidValue;
   }
   for (int w = 0; w < 2; ++w) {
     // without keys no copy is issued: any valid tensor will do
@@ -663,7 +602,8 @@ cudaError_t go(const AttnCfg& c, const PromptArgs* a, cudaStream_t s) {
     const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(none ? 1 : c.G), static_cast<cuuint64_t>(none ? 1 : a->kv_tokens)};
     const cuuint64_t st[2] = {D * e, static_cast<cuuint64_t>(none ? a->qs : w ? a->vs : a->ks) * e};
     const cuuint32_t box[3] = {64, 1, kKeys};
-    if (!encode(c.encode, w ? &mv : &mk, F16, none ? a->q : w ? a->v : a->k, 3, dims, st, box)) return cudaErrorInvalidValue;
+    if (!encode_map(c.encode, w ? &mv : &mk, type, CU_TENSOR_MAP_SWIZZLE_128B, none ? a->q : w ? a->v : a->k, 3, dims, st, box))
+      return cudaErrorInvalidValue;
   }
   // at most this many items; the grid is one CTA per SM
   const long long items = (((static_cast<long long>(a->q_tokens) << ps.pack_shift) >> 8) + std::min(a->batch, a->q_tokens)) * ps.groups;

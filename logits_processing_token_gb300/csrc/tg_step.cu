@@ -8,12 +8,16 @@
 //   o' = o 2^(m-m') + sum 2^(s-m') v
 // (c holds the scale and log2 e), and parts join the same way.
 //
-// The work is cut into units of kTile keys of one (sequence, key head, row
+// The work is cut into units of KT keys of one (sequence, key head, row
 // tile), numbered in that order; CTA i of N takes units [U i / N, U (i+1) / N),
 // so every SM reads the same number of bytes whatever the lengths are.  A
 // (sequence, key head, row tile) that falls into several CTAs leaves its parts
 // in the handle's workspace, and the CTA that finishes last joins them in CTA
 // order: one launch, and the result does not depend on which was last.
+//
+// One warp looks up pages and issues the copies, a page's rows of one head at
+// a time, into a ring of stages; the other warps wait for a stage, take 16
+// rows and their share of its keys, and hand it back.
 #include <algorithm>
 
 #include "tg_attn.cuh"
@@ -21,73 +25,121 @@
 namespace tg {
 namespace {
 
-constexpr int kTile = 64;  // keys per unit
-
-struct Cursor {   // a place in the order of the units
-  int b, g, rt, tile;
-  int len, ntile;  // of sequence b
+// Everything about a unit that the computing warps need.
+struct Unit {
+  int b, g, rt, tile, len;
+  int any_bad;
+};
+struct UnitMeta {
+  Unit u;
+  unsigned bad[4];  // keys of the tile on pages that do not exist
 };
 
 // DP: head size padded to 64 or 128.  MF16: the products' type is f16 (an e4m3
 // cache is widened to f16, exactly), else bf16.  QF16: the tensors' type.
-// WM x WN warps: WM groups of 16 rows, each group's keys over WN warps.
-template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN, int ST>
+// WM x WN computing warps: WM groups of 16 rows, a tile's keys over WN warps.
+template <int DP, bool Q8, int WM, int WN>
 struct Shape {
-  static constexpr int kThreads = 32 * WM * WN;
+  static constexpr int kWarps = WM * WN;
+  static constexpr int kThreads = 32 * (kWarps + 1);
   static constexpr int kRows = 16 * WM;
-  static constexpr int kRB = DP * (Q8 ? 1 : 2);       // bytes of a key's row
-  static constexpr int kMat = kTile * kRB;            // a K or V tile
+  static constexpr int kRB = DP * (Q8 ? 1 : 2);           // bytes of a key's row
+  static constexpr int KT = kRB == 256 ? 64 : 128;        // keys of a unit
+  static constexpr int kMat = KT * kRB;                   // a K or V tile
   static constexpr int kStage = 2 * kMat;
-  static constexpr int kMerge = WN > 1 ? kRows * DP * 4 : 0;
-  static constexpr int kSmem = ST * kStage + kMerge + WN * kRows * 8 + (ST + 1) * 16 + 2 * kTile * 4 + 64 * 4;
+  static constexpr int kQRow = DP * 2 + 16;               // a query row, padded against bank conflicts
+  static constexpr int kQ = kRows * kQRow;
+  static constexpr int kMRow = DP + (Q8 ? 16 : 8);        // a row of sums, padded likewise
+  static constexpr int kMerge = WN > 1 ? WM * WN * 8 * kMRow * 4 : 0;
+  static constexpr int kHead = 1024;                      // barriers, metas, scan scratch
+  static constexpr int kML = WN * kRows * 8;
+  static constexpr int kFixed = kHead + 2 * kQ + kMerge + kML + 1024;
+  // two CTAs on an SM where four warps compute, one where eight do
+  static constexpr int kRoom = (kWarps > 4 ? 225 : 112) * 1024;
+  static constexpr int ST = (kRoom - kFixed) / kStage > 8 ? 8 : (kRoom - kFixed) / kStage;
+  static constexpr int kSmem = kFixed + ST * kStage;
+  static_assert(ST >= 2, "two stages at least");
 };
 
-template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN, int ST>
-__global__ void __launch_bounds__(32 * WM * WN)
-step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
-  using S = Shape<DP, MF16, QF16, Q8, WM, WN, ST>;
-  constexpr int NT = S::kThreads;
-  constexpr int KW = kTile / WN;    // keys of a tile per warp
-  constexpr int KS = DP / 16;       // 16-element slices of a head
-  extern __shared__ __align__(128) unsigned char smem[];
-  unsigned char* stage0 = smem;
-  float* merge = reinterpret_cast<float*>(smem + ST * S::kStage);
-  float2* wml = reinterpret_cast<float2*>(smem + ST * S::kStage + S::kMerge);   // [WN][rows]
-  unsigned* badw = reinterpret_cast<unsigned*>(wml + WN * S::kRows);            // [ST + 1][4]
-  int* ids = reinterpret_cast<int*>(badw + (ST + 1) * 4);                       // [2][kTile]
-  int* misc = ids + 2 * kTile;                                                  // scan scratch, broadcast values
+constexpr int kMaxStages = 8;
+struct Head {
+  unsigned long long full[kMaxStages], empty[kMaxStages], q_full[2], q_empty[2], meet;
+  int dead, last, first_b, first_in, first_len;
+  long long first_u;
+  long long wsum[16];
+  UnitMeta meta[kMaxStages];
+};
+static_assert(sizeof(Head) <= 1024, "");
+
+// Byte offset of 16-byte chunk c of key r in a tile: 128-byte rows (a 256-byte
+// row is two of them, one 64-element half behind the other) or 64-byte rows,
+// chunks exchanged as the tensor copies' swizzles do.
+template <int RB, int KT>
+__device__ __forceinline__ unsigned key_at(int r, int c) {
+  if constexpr (RB == 256) return (c >> 3) * (KT * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4);
+  else return tile_at<RB>(r, c);
+}
+
+template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN>
+__global__ void __launch_bounds__(32 * (WM * WN + 1), WM * WN > 4 ? 1 : 2)
+step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int box, const __grid_constant__ CUtensorMap mk,
+            const __grid_constant__ CUtensorMap mv) {
+  using S = Shape<DP, Q8, WM, WN>;
+  constexpr int NT = S::kThreads, NW = S::kWarps, KT = S::KT, ST = S::ST, RB = S::kRB;
+  constexpr int KW = KT / WN;    // keys of a tile per warp
+  constexpr int KS = DP / 16;    // 16-element slices of a head
+  constexpr int CPR = RB / 16;   // 16-byte chunks of a key's row
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (sptr(smem_raw) & 1023)) & 1023);
+  unsigned char* stages = smem;
+  Head* hd = reinterpret_cast<Head*>(smem + ST * S::kStage);
+  unsigned char* qbuf = smem + ST * S::kStage + S::kHead;
+  float* merge = reinterpret_cast<float*>(qbuf + 2 * S::kQ);
+  float2* wml = reinterpret_cast<float2*>(qbuf + 2 * S::kQ + S::kMerge);  // [WN][rows]
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int wm = warp % WM, wn = warp / WM;
   const int rows_all = a.n * c.rep;
-  const int chunks = (c.D * (Q8 ? 1 : 2)) >> 4;  // 16-byte chunks of a key's row that hold data
-  constexpr int CPR = S::kRB / 16;
+  const int chunks = (c.D * (Q8 ? 1 : 2)) >> 4;  // chunks of a key's row that hold data
+  const bool tensor_copies = box > 0;            // else the pages are too small for them
 
-  // chunks past the head size stay zero for the whole launch
-  if (chunks < CPR) {
-    for (int i = tid; i < ST * 2 * kTile * (CPR - chunks); i += NT) {
+  if (tid == 0) {
+    for (int i = 0; i < ST; ++i) {
+      bar_init(&hd->full[i], tensor_copies ? 1 : 33);
+      bar_init(&hd->empty[i], NW);
+    }
+    for (int i = 0; i < 2; ++i) {
+      bar_init(&hd->q_full[i], 1);
+      bar_init(&hd->q_empty[i], NW);
+    }
+    bar_init(&hd->meet, NW);
+    hd->dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // query rows and elements that do not exist stay zero, and so do elements
+  // past the head size where the copies do not fill them in
+  for (int i = tid; i < 2 * S::kQ / 16; i += NT) reinterpret_cast<uint4*>(qbuf)[i] = make_uint4(0, 0, 0, 0);
+  if (!tensor_copies && chunks < CPR) {
+    for (int i = tid; i < ST * 2 * KT * (CPR - chunks); i += NT) {
       const int r = i / (CPR - chunks), cc = chunks + i % (CPR - chunks);
-      *reinterpret_cast<uint4*>(stage0 + (r / kTile) * S::kMat + tile_at<S::kRB>(r % kTile, cc)) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(stages + (r / KT) * S::kMat + key_at<RB, KT>(r % KT, cc)) = make_uint4(0, 0, 0, 0);
     }
   }
+  fence_async();
   dep_wait();
 
   // ---- this CTA's units -------------------------------------------------
   const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
-  const auto seq_len = [&](int b) -> int {
-    const int l = a.c.lens[b];
-    return l >= 0 && l <= max_len ? l : 0;
-  };
-  const auto tiles_of = [](int len) { return len > 0 ? (len + kTile - 1) / kTile : 1; };
+  const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
+  const auto tiles_of = [](int len) { return len > 0 ? (len + KT - 1) / KT : 1; };
   const int per_tile = c.G * row_tiles;
-  const int bper = (a.c.batch + NT - 1) / NT;
+  const int bper = (a.c.batch + NT - 1) / NT, b_first = tid * bper;
   long long mine = 0;
-  for (int b = tid * bper; b < min(a.c.batch, (tid + 1) * bper); ++b) {
-    if (blockIdx.x == 0) {
-      const int l = a.c.lens[b];
-      if (l < 0 || l > max_len) atomicOr(c.status, kAttnBadRow);
-    }
-    mine += tiles_of(seq_len(b));
+  int len0 = 0;  // of this thread's first sequence
+  for (int b = b_first; b < min(a.c.batch, b_first + bper); ++b) {
+    const int raw = a.c.lens[b], l = checked(raw);
+    if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
+    if (b == b_first) len0 = l;
+    mine += tiles_of(l);
   }
   long long before = mine;
 #pragma unroll
@@ -95,128 +147,192 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
     const long long v = __shfl_up_sync(~0u, before, d);
     if (lane >= d) before += v;
   }
-  long long* wsum = reinterpret_cast<long long*>(misc);
-  if (lane == 31) wsum[warp] = before;
+  if (lane == 31) hd->wsum[warp] = before;
   __syncthreads();
   long long total = 0;
+#pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
-    if (w < warp) before += wsum[w];
-    total += wsum[w];
+    if (w < warp) before += hd->wsum[w];
+    total += hd->wsum[w];
   }
   before -= mine;  // key tiles of the sequences before this thread's
   const long long U = total * per_tile;
   const long long N = min(static_cast<long long>(gridDim.x), max(1ll, U / min_units));
   if (blockIdx.x >= N) return;
   const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
-  __syncthreads();
   if (mine > 0 && before * per_tile <= u0 && u0 < (before + mine) * per_tile) {
-    int b = tid * bper;
+    int b = b_first, l = len0;
     long long at = before;
-    for (;; ++b) {
-      const int t = tiles_of(seq_len(b));
+    for (;;) {
+      const int t = tiles_of(l);
       if ((at + t) * per_tile > u0) break;
       at += t;
+      l = checked(a.c.lens[++b]);
     }
-    misc[0] = b;
-    misc[1] = static_cast<int>(u0 - at * per_tile);
-    *reinterpret_cast<long long*>(misc + 2) = at * per_tile;
+    hd->first_b = b;
+    hd->first_len = l;
+    hd->first_in = static_cast<int>(u0 - at * per_tile);
   }
   __syncthreads();
-  Cursor cur;
-  cur.b = misc[0];
-  cur.len = seq_len(cur.b);
-  cur.ntile = tiles_of(cur.len);
-  cur.tile = misc[1] % cur.ntile;
-  cur.rt = misc[1] / cur.ntile % row_tiles;
-  cur.g = misc[1] / cur.ntile / row_tiles;
-  long long item_u = u0 - cur.tile;  // first unit of the current (sequence, head, row tile)
-  const auto advance = [&](Cursor& x) {
-    if (++x.tile < x.ntile) return;
-    x.tile = 0;
-    if (++x.rt < row_tiles) return;
-    x.rt = 0;
-    if (++x.g < c.G) return;
-    x.g = 0;
-    if (++x.b >= a.c.batch) return;
-    x.len = seq_len(x.b);
-    x.ntile = tiles_of(x.len);
-  };
-
-  // ---- the load pipeline ------------------------------------------------
   const int steps = static_cast<int>(u1 - u0);
-  Cursor ld = cur;    // next unit to load
-  Cursor idc = cur;   // next unit whose page numbers are fetched
-  int id_reg = -1;    // page number of this thread's key (tid < kTile), fetched one step ahead
-  bool id_in = false; // that key exists
-  const auto fetch_ids = [&](int step) {
-    if (tid < kTile && step < steps) {
-      const int key = idc.tile * kTile + tid;
-      id_in = key < idc.len;
-      id_reg = id_in ? __ldg(a.c.table + idc.b * a.c.table_stride + (key >> c.page_shift)) : -1;
-    }
-    if (step < steps) advance(idc);
-  };
-  const auto store_ids = [&](int step) {
-    if (tid < kTile && step < steps) {
-      const bool bad = id_in && (id_reg < 0 || id_reg >= a.c.num_pages);
-      if (bad) atomicOr(c.status, kAttnBadPage);
-      ids[(step & 1) * kTile + tid] = bad ? -1 : id_reg;
-      const unsigned w = __ballot_sync(~0u, bad);
-      if (lane == 0) badw[(step % (ST + 1)) * 4 + warp] = w;
-    }
-  };
-  const auto issue = [&](int step) {
-    if (step < steps) {
-      unsigned char* st = stage0 + (step % ST) * S::kStage;
-      const unsigned ks = sptr(st), vs = ks + S::kMat;
-      const int* id = ids + (step & 1) * kTile;
-      const long long head = ld.g * c.head_stride;
-#pragma unroll 4
-      for (int i = tid; i < kTile * CPR; i += NT) {
-        const int r = i / CPR, cc = i % CPR;
-        if (cc >= chunks) continue;
-        const int page = id[r];
-        const long long in = head + ((ld.tile * kTile + r) & (c.page_size - 1)) * c.slot_stride;
-        const long long pg = page < 0 ? 0 : page;
-        const unsigned at = tile_at<S::kRB>(r, cc);
-        constexpr int ES = Q8 ? 1 : 2;
-        cp16(ks + at, static_cast<const char*>(a.c.k) + (pg * a.c.k_page_stride + in) * ES + cc * 16, page >= 0);
-        cp16(vs + at, static_cast<const char*>(a.c.v) + (pg * a.c.v_page_stride + in) * ES + cc * 16, page >= 0);
-      }
-      advance(ld);
-    }
-    cp_commit();
-  };
-#pragma unroll
-  for (int s = 0; s < ST - 1; ++s) {
-    fetch_ids(s);
-    store_ids(s);
-    __syncthreads();
-    issue(s);
-  }
-  fetch_ids(ST - 1);
 
-  // ---- per item ----------------------------------------------------------
+  if (warp == NW) {
+    // ---- pages and copies ---------------------------------------------------
+    int b = hd->first_b, len = hd->first_len, nt = tiles_of(len);
+    int tile = hd->first_in % nt, rt = hd->first_in / nt % row_tiles, g = hd->first_in / nt / row_tiles;
+    int len_next = b + 1 < a.c.batch ? checked(a.c.lens[b + 1]) : 0;
+    const int R = tensor_copies ? box : 1;  // keys of one copy
+    const int shift = R == 1 ? 0 : 31 - __clz(R);
+    const auto entry = [&](int bb, int key, int ln) {  // the page of a key, -1 past the end
+      return key < ln ? __ldg(a.c.table + bb * a.c.table_stride + (key >> c.page_shift)) : -1;
+    };
+    // lane i: the page of copy i of the tile (of key i, 32 apart, without tensor copies)
+    int id = tensor_copies && lane < (KT >> shift) ? entry(b, tile * KT + (lane << shift), len) : -1;
+    int qs = 0;
+    unsigned q_ph = 1;
+    bool ok = true;
+    int i = 0;
+    for (; i < steps; ++i) {
+      const int st = i % ST;
+      const unsigned e_ph = ((i / ST) & 1) ^ 1;
+      if (i == 0 || tile == 0) {
+        // this item's queries: a row at a time into padded rows
+        ok = bar_wait(&hd->dead, &hd->q_empty[qs], q_ph, c.status);
+        if (!ok) break;
+        const int rows = min(S::kRows, rows_all - rt * S::kRows);
+        if (lane == 0) bar_expect(&hd->q_full[qs], rows * c.D * 2);
+        __syncwarp();
+        for (int r = lane; r < rows; r += 32) {
+          const int x = rt * S::kRows + r, j = x / c.rep;
+          const uint16_t* src = static_cast<const uint16_t*>(a.q) + (static_cast<long long>(b) * a.n + j) * a.qs +
+                                static_cast<long long>(g * c.rep + (x - j * c.rep)) * c.D;
+          asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           sptr(qbuf + qs * S::kQ + r * S::kQRow)),
+                       "l"(src), "r"(c.D * 2), "r"(sptr(&hd->q_full[qs])) : "memory");
+        }
+        if (++qs == 2) { qs = 0; q_ph ^= 1; }
+      }
+      // the following unit, and its pages while this one's stage is awaited
+      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nnt = nt;
+      if (ntile == nt) {
+        ntile = 0;
+        if (++nrt == row_tiles) {
+          nrt = 0;
+          if (++ng == c.G) {
+            ng = 0;
+            ++nb;
+            nlen = len_next;
+            nnt = tiles_of(nlen);
+            len_next = nb + 1 < a.c.batch ? checked(a.c.lens[nb + 1]) : 0;
+          }
+        }
+      }
+      const int id_next = tensor_copies && i + 1 < steps && lane < (KT >> shift) ? entry(nb, ntile * KT + (lane << shift), nlen) : -1;
+      ok = bar_wait(&hd->dead, &hd->empty[st], e_ph, c.status);
+      if (!ok) break;
+      const unsigned ks = sptr(stages + st * S::kStage), vs = ks + S::kMat;
+      if (tensor_copies) {
+        const int key = tile * KT + (lane << shift);
+        const bool in = lane < (KT >> shift) && key < len;
+        const bool bad = in && (id < 0 || id >= a.c.num_pages);
+        if (bad) atomicOr(c.status, kAttnBadPage);
+        const unsigned badm = __ballot_sync(~0u, bad);
+        const int copies = __popc(__ballot_sync(~0u, in && !bad));
+        if (lane < 4) {
+          // keys of bad pages, as bits of the tile's keys
+          unsigned w = 0;
+          if (badm)
+            for (int k = 0; k < 32; ++k)
+              if ((lane * 32 + k) < KT && ((badm >> ((lane * 32 + k) >> shift)) & 1)) w |= 1u << k;
+          hd->meta[st].bad[lane] = w;
+        }
+        if (lane == 0) {
+          hd->meta[st].u = Unit{b, g, rt, tile, len, badm != 0};
+        }
+        __syncwarp();
+        if (lane == 0) bar_expect(&hd->full[st], copies * R * RB * 2);
+        __syncwarp();
+        if (in && !bad) {
+          const int slot = key & (c.page_size - 1);
+          const int y = c.token_major ? g : slot, z = c.token_major ? slot : g;
+#pragma unroll
+          for (int x = 0; x < (RB == 256 ? 2 : 1); ++x) {
+            const unsigned at = (RB == 256 ? x * KT * 128 : 0) + (lane << shift) * (RB == 256 ? 128 : RB);
+            tma4(ks + at, &mk, x * 64, y, z, id, &hd->full[st]);
+            tma4(vs + at, &mv, x * 64, y, z, id, &hd->full[st]);
+          }
+        }
+      } else {
+        constexpr int ES = Q8 ? 1 : 2;
+        const long long head = g * c.head_stride;
+        unsigned any_bad = 0;
+        for (int k0 = 0; k0 < KT; k0 += 32) {
+          const int key = tile * KT + k0 + lane;
+          const int page = entry(b, key, len);
+          const bool bad = key < len && (page < 0 || page >= a.c.num_pages);
+          if (bad) atomicOr(c.status, kAttnBadPage);
+          const unsigned badm = __ballot_sync(~0u, bad);
+          any_bad |= badm;
+          if (lane == 0) hd->meta[st].bad[k0 >> 5] = badm;
+          const int good = bad ? -1 : page;
+          for (int k = 0; k < 32 * CPR; k += 32) {
+            const int r = (k + lane) / CPR, cc = (k + lane) % CPR;
+            const int pg = __shfl_sync(~0u, good, r);
+            if (cc >= chunks) continue;
+            const long long in = head + ((tile * KT + k0 + r) & (c.page_size - 1)) * c.slot_stride;
+            const long long p0 = pg < 0 ? 0 : pg;
+            const unsigned at = key_at<RB, KT>(k0 + r, cc);
+            cp16(ks + at, static_cast<const char*>(a.c.k) + (p0 * a.c.k_page_stride + in) * ES + cc * 16, pg >= 0);
+            cp16(vs + at, static_cast<const char*>(a.c.v) + (p0 * a.c.v_page_stride + in) * ES + cc * 16, pg >= 0);
+          }
+        }
+        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, tile, len, any_bad != 0};
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&hd->full[st]);
+      }
+      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; nt = nnt; id = id_next;
+    }
+    if (!ok) {
+      // a wait ran out: copies in flight land before the CTA's memory goes
+      for (int k = max(0, i - ST); k < i; ++k) bar_drain(&hd->full[k % ST], (k / ST) & 1);
+      for (int k = 0; k < 2; ++k) bar_drain(&hd->q_full[k], k < qs ? q_ph ^ 1 : q_ph);
+    }
+    return;
+  }
+
+  // ---- computing warps -----------------------------------------------------
+  const int wm = warp % WM, wn = warp / WM;
   unsigned qf[KS][4];
   float o[KS * 2][4];
   float m[2], l[2], rs[2];  // rows lane / 4 and lane / 4 + 8 of this warp's group
   int lim[2];               // keys that the row sees
   const int r0 = wm * 16 + (lane >> 2);
   const float bias = kWeightBias<MF16>;
+  Unit cur;
+  int qs = 0;
+  unsigned q_ph = 0, meet_ph = 0;
+  bool ok = true;
+  // All computing warps past this point.
+  const auto meet = [&]() {
+    __syncwarp();
+    if (lane == 0) bar_arrive(&hd->meet);
+    ok = bar_wait(&hd->dead, &hd->meet, meet_ph, c.status);
+    meet_ph ^= 1;
+    return ok;
+  };
 
   const auto begin_item = [&]() {
     const float sc = c.scale * kLog2E * (Q8 && c.k_scale ? c.k_scale[cur.g] : 1.0f);
+    const unsigned char* qb = qbuf + qs * S::kQ;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       const int r = cur.rt * S::kRows + r0 + 8 * h;
-      const bool on = r < rows_all;
-      const int j = on ? r / c.rep : 0, hd = on ? r - j * c.rep : 0;
-      lim[h] = on ? cur.len - a.n + j + 1 : 0;
+      lim[h] = r < rows_all ? cur.len - a.n + r / c.rep + 1 : 0;
       m[h] = -INFINITY;
       l[h] = 0.0f;
       rs[h] = sc;
-      const uint16_t* q = static_cast<const uint16_t*>(a.q) + (static_cast<long long>(cur.b) * a.n + j) * a.qs +
-                          static_cast<long long>(cur.g * c.rep + hd) * c.D;
+      const unsigned char* q = qb + (r0 + 8 * h) * S::kQRow;
       const int t = lane & 3;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -224,8 +340,8 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
         // e4m3 cache pairs (4t, 4t + 1) and (4t + 2, 4t + 3): the order in which
         // its keys' elements come out of shared memory (any order serves a sum)
         const int e = 16 * k + (Q8 ? 4 * t : 2 * t), f = Q8 ? e + 2 : e + 8;
-        qf[k][h] = on && 16 * k < c.D ? *reinterpret_cast<const unsigned*>(q + e) : 0u;
-        qf[k][2 + h] = on && 16 * k < c.D ? *reinterpret_cast<const unsigned*>(q + f) : 0u;
+        qf[k][h] = *reinterpret_cast<const unsigned*>(q + 2 * e);
+        qf[k][2 + h] = *reinterpret_cast<const unsigned*>(q + 2 * f);
       }
       if constexpr (MF16 && !QF16) {
         // bf16 queries to f16: a power of two per row brings the row's largest
@@ -258,117 +374,136 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
     for (int k = 0; k < KS * 2; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[k][i] = 0.0f;
+    __syncwarp();
+    if (lane == 0) bar_arrive(&hd->q_empty[qs]);
+    if (++qs == 2) { qs = 0; q_ph ^= 1; }
   };
 
-  const auto compute = [&](int step) {
-    const unsigned ks = sptr(stage0 + (step % ST) * S::kStage), vs = ks + S::kMat;
-    const int key0 = cur.tile * kTile + wn * KW;
-    if (key0 >= cur.len || cur.rt * S::kRows + wm * 16 >= rows_all) return;
-    float s[KW / 8][4];
+  const auto compute = [&](unsigned char* stage, const unsigned* bad) {
+    const unsigned ks = sptr(stage), vs = ks + S::kMat;
+    const int base = cur.tile * KT + wn * KW;
+    if (base >= cur.len || cur.rt * S::kRows + wm * 16 >= rows_all) return;
+    // Values of keys that do not exist are whatever their page holds, and
+    // 0 x NaN is not 0: zero them.
+    const int have = min(KW, cur.len - base);
+    if (have < KW || cur.any_bad) {
+      for (int i = lane; i < KW * CPR; i += 32) {
+        const int r = i / CPR, x = wn * KW + r;
+        if (r >= have || ((bad[x >> 5] >> (x & 31)) & 1))
+          *reinterpret_cast<uint4*>(stage + S::kMat + key_at<RB, KT>(x, i % CPR)) = make_uint4(0, 0, 0, 0);
+      }
+      fence_async();
+      __syncwarp();
+    }
+    // 32 keys at a time
+    constexpr int KC = KW < 32 ? KW : 32;
+#pragma unroll 1
+    for (int k0 = 0; k0 < KW; k0 += KC) {
+      const int at = wn * KW + k0;
+      if (cur.tile * KT + at >= cur.len) break;
+      float s[KC / 8][4];
 #pragma unroll
-    for (int i = 0; i < KW / 8; ++i)
+      for (int i = 0; i < KC / 8; ++i)
 #pragma unroll
-      for (int x = 0; x < 4; ++x) s[i][x] = 0.0f;
+        for (int x = 0; x < 4; ++x) s[i][x] = 0.0f;
 #pragma unroll
-    for (int kg = 0; kg < KW / 16; ++kg) {
-      const int row = wn * KW + kg * 16 + ((lane >> 4) << 3) + (lane & 7);
-      if constexpr (!Q8) {
+      for (int kg = 0; kg < KC / 16; ++kg) {
+        const int row = at + kg * 16 + ((lane >> 4) << 3) + (lane & 7);
+        if constexpr (!Q8) {
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          unsigned r[4];
-          ldsm4(r, ks + tile_at<S::kRB>(row, 2 * k + ((lane >> 3) & 1)));
-          mma16816<MF16>(s[2 * kg], qf[k], r[0], r[1]);
-          mma16816<MF16>(s[2 * kg + 1], qf[k], r[2], r[3]);
-        }
-      } else {
+          for (int k = 0; k < KS; ++k) {
+            unsigned r[4];
+            ldsm4(r, ks + key_at<RB, KT>(row, 2 * k + ((lane >> 3) & 1)));
+            mma16816<MF16>(s[2 * kg], qf[k], r[0], r[1]);
+            mma16816<MF16>(s[2 * kg + 1], qf[k], r[2], r[3]);
+          }
+        } else {
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          unsigned r[4];
-          ldsm4(r, ks + tile_at<S::kRB>(row, k + ((lane >> 3) & 1)));
+          for (int k = 0; k < KS; k += 2) {
+            unsigned r[4];
+            ldsm4(r, ks + key_at<RB, KT>(row, k + ((lane >> 3) & 1)));
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {  // slice k + x of both groups of 8 keys
-            mma16816<MF16>(s[2 * kg], qf[k + x], e4m3x2_to_f16x2(r[x] & 0xffff), e4m3x2_to_f16x2(r[x] >> 16));
-            mma16816<MF16>(s[2 * kg + 1], qf[k + x], e4m3x2_to_f16x2(r[2 + x] & 0xffff), e4m3x2_to_f16x2(r[2 + x] >> 16));
+            for (int x = 0; x < 2; ++x) {  // slice k + x of both groups of 8 keys
+              mma16816<MF16>(s[2 * kg], qf[k + x], e4m3x2_to_f16x2(r[x] & 0xffff), e4m3x2_to_f16x2(r[x] >> 16));
+              mma16816<MF16>(s[2 * kg + 1], qf[k + x], e4m3x2_to_f16x2(r[2 + x] & 0xffff), e4m3x2_to_f16x2(r[2 + x] >> 16));
+            }
           }
         }
       }
-    }
-    // mask: the end of what a row sees, and keys of bad pages
-    const unsigned* bw = badw + (step % (ST + 1)) * 4;
-    const unsigned long long bad = bw[0] | (static_cast<unsigned long long>(bw[1]) << 32);
-    if (key0 + KW > cur.len - a.n + 1 || bad) {
+      // mask: the end of what a row sees, and keys of bad pages
+      if (cur.tile * KT + at + KC > cur.len - a.n + 1 || cur.any_bad) {
+        const unsigned bw = bad[at >> 5] >> (at & 31);
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i)
+        for (int i = 0; i < KC / 8; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int in = wn * KW + i * 8 + 2 * (lane & 3) + (x & 1);
-          if (cur.tile * kTile + in >= lim[x >> 1] || ((bad >> in) & 1)) s[i][x] = -INFINITY;
-        }
-    }
-    float sub[2];
-    bool moved = false;
+          for (int x = 0; x < 4; ++x) {
+            const int in = i * 8 + 2 * (lane & 3) + (x & 1);
+            if (cur.tile * KT + at + in >= lim[x >> 1] || ((bw >> in) & 1)) s[i][x] = -INFINITY;
+          }
+      }
+      float sub[2];
+      bool moved = false;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      float top = -INFINITY;
+      for (int h = 0; h < 2; ++h) {
+        float top = -INFINITY;
 #pragma unroll
-      for (int i = 0; i < KW / 8; ++i) top = fmaxf(top, fmaxf(s[i][2 * h], s[i][2 * h + 1]));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-      top *= rs[h];
-      if (top > m[h]) {
-        const float f = ex2(m[h] - top);
-        l[h] *= f;
-        m[h] = top;
-        moved = true;
-        sub[h] = f;
-      } else {
+        for (int i = 0; i < KC / 8; ++i) top = fmaxf(top, fmaxf(s[i][2 * h], s[i][2 * h + 1]));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        top *= rs[h];
         sub[h] = 1.0f;
-      }
-    }
-    if (__any_sync(~0u, moved)) {
-#pragma unroll
-      for (int k = 0; k < KS * 2; ++k) {
-        o[k][0] *= sub[0];
-        o[k][1] *= sub[0];
-        o[k][2] *= sub[1];
-        o[k][3] *= sub[1];
-      }
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const float off = m[h] == -INFINITY ? 0.0f : m[h] - bias;
-#pragma unroll
-      for (int i = 0; i < KW / 8; ++i) {
-        s[i][2 * h] = ex2(fmaf(s[i][2 * h], rs[h], -off));
-        s[i][2 * h + 1] = ex2(fmaf(s[i][2 * h + 1], rs[h], -off));
-        l[h] += s[i][2 * h] + s[i][2 * h + 1];
-      }
-    }
-#pragma unroll
-    for (int kg = 0; kg < KW / 16; ++kg) {
-      const unsigned p[4] = {pack2<MF16>(s[2 * kg][0], s[2 * kg][1]), pack2<MF16>(s[2 * kg][2], s[2 * kg][3]),
-                             pack2<MF16>(s[2 * kg + 1][0], s[2 * kg + 1][1]), pack2<MF16>(s[2 * kg + 1][2], s[2 * kg + 1][3])};
-      const int row = wn * KW + kg * 16 + (lane & 15);
-      if constexpr (!Q8) {
-#pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          unsigned r[4];
-          ldsm4t(r, vs + tile_at<S::kRB>(row, 2 * k + (lane >> 4)));
-          mma16816<MF16>(o[2 * k], p, r[0], r[1]);
-          mma16816<MF16>(o[2 * k + 1], p, r[2], r[3]);
+        if (top > m[h]) {
+          sub[h] = ex2(m[h] - top);
+          l[h] *= sub[h];
+          m[h] = top;
+          moved = true;
         }
-      } else {
+      }
+      if (__any_sync(~0u, moved)) {
 #pragma unroll
-        for (int k = 0; k < KS; k += 2) {
-          unsigned r[4];
-          ldsm4t(r, vs + tile_at<S::kRB>(row, k + (lane >> 4)));
-          // a register holds values (2g, 2g + 1) of two keys: even and odd
-          // columns of a slice become the two products' columns
+        for (int k = 0; k < KS * 2; ++k) {
+          o[k][0] *= sub[0];
+          o[k][1] *= sub[0];
+          o[k][2] *= sub[1];
+          o[k][3] *= sub[1];
+        }
+      }
 #pragma unroll
-          for (int x = 0; x < 2; ++x) {
-            const unsigned u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
-            mma16816<MF16>(o[2 * (k + x)], p, e4m3x2_to_f16x2(u & 0xffff), e4m3x2_to_f16x2(w & 0xffff));
-            mma16816<MF16>(o[2 * (k + x) + 1], p, e4m3x2_to_f16x2(u >> 16), e4m3x2_to_f16x2(w >> 16));
+      for (int h = 0; h < 2; ++h) {
+        const float off = m[h] == -INFINITY ? 0.0f : m[h] - bias;
+#pragma unroll
+        for (int i = 0; i < KC / 8; ++i) {
+          s[i][2 * h] = ex2(fmaf(s[i][2 * h], rs[h], -off));
+          s[i][2 * h + 1] = ex2(fmaf(s[i][2 * h + 1], rs[h], -off));
+          l[h] += s[i][2 * h] + s[i][2 * h + 1];
+        }
+      }
+#pragma unroll
+      for (int kg = 0; kg < KC / 16; ++kg) {
+        const unsigned p[4] = {pack2<MF16>(s[2 * kg][0], s[2 * kg][1]), pack2<MF16>(s[2 * kg][2], s[2 * kg][3]),
+                               pack2<MF16>(s[2 * kg + 1][0], s[2 * kg + 1][1]), pack2<MF16>(s[2 * kg + 1][2], s[2 * kg + 1][3])};
+        const int row = at + kg * 16 + (lane & 15);
+        if constexpr (!Q8) {
+#pragma unroll
+          for (int k = 0; k < KS; ++k) {
+            unsigned r[4];
+            ldsm4t(r, vs + key_at<RB, KT>(row, 2 * k + (lane >> 4)));
+            mma16816<MF16>(o[2 * k], p, r[0], r[1]);
+            mma16816<MF16>(o[2 * k + 1], p, r[2], r[3]);
+          }
+        } else {
+#pragma unroll
+          for (int k = 0; k < KS; k += 2) {
+            unsigned r[4];
+            ldsm4t(r, vs + key_at<RB, KT>(row, k + (lane >> 4)));
+            // a register holds values (2g, 2g + 1) of two keys: even and odd
+            // columns of a slice become the two products' columns
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const unsigned u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
+              mma16816<MF16>(o[2 * (k + x)], p, e4m3x2_to_f16x2(u & 0xffff), e4m3x2_to_f16x2(w & 0xffff));
+              mma16816<MF16>(o[2 * (k + x) + 1], p, e4m3x2_to_f16x2(u >> 16), e4m3x2_to_f16x2(w >> 16));
+            }
           }
         }
       }
@@ -384,26 +519,28 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
     const int j = r / c.rep;
     return (static_cast<long long>(cur.b) * a.n + j) * c.H + cur.g * c.rep + (r - j * c.rep);
   };
-  const auto vscale = [&]() { return Q8 && c.v_scale ? c.v_scale[cur.g] : 1.0f; };
-  const auto put = [&](long long row, int d, float x) {
-    if constexpr (QF16) static_cast<__half*>(a.out)[row * c.D + d] = __float2half_rn(x);
-    else static_cast<__nv_bfloat16*>(a.out)[row * c.D + d] = __float2bfloat16_rn(x);
+  const auto put4 = [&](long long row, int d, float4 x) {
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + row * c.D + d) =
+        make_uint2(pack2<QF16>(x.x, x.y), pack2<QF16>(x.z, x.w));
   };
   const auto put_lse = [&](long long row, float mm, float ll) {
-    if (a.lse) a.lse[row] = ll > 0.0f ? (mm + log2f(ll) - bias) * kLn2 : -INFINITY;
+    if (a.lse) a.lse[row] = ll > 0.0f ? (mm + log2f(ll) - bias) * kLn2 : ll == 0.0f ? -INFINITY : ll;
   };
+  const auto factor = [&](float ll, float vs) { return ll == 0.0f ? 0.0f : vs / ll; };
 
   // The item's end in this CTA: join the warps, then write the result, or this
   // CTA's part of it.
-  const auto end_item = [&](long long u_end) {
-    const long long c0 = ((item_u + 1) * N - 1) / U;
-    const long long c1 = ((item_u + cur.ntile) * N - 1) / U;
+  const auto end_item = [&](long long u) {
+    const int nt = tiles_of(cur.len);
+    const long long item_u = u - cur.tile;
+    const long long c0 = ((item_u + 1) * N - 1) / U, c1 = ((item_u + nt) * N - 1) / U;
     const bool whole = c0 == c1;
-    const int slot = 2 * blockIdx.x + (item_u < u0 ? 0 : 1);
-    float* po = c.ws_o + static_cast<long long>(slot) * c.step_rows * c.D;
-    float2* pml = c.ws_ml + static_cast<long long>(slot) * c.step_rows;
+    const long long slot = 2ll * blockIdx.x + (item_u < u0 ? 0 : 1);
+    float* po = c.ws_o + slot * c.step_rows * c.D;
+    float2* pml = c.ws_ml + slot * c.step_rows;
     const int row_base = cur.rt * S::kRows;
     const int nrow = min(S::kRows, rows_all - row_base);
+    const float vs = Q8 && c.v_scale ? c.v_scale[cur.g] : 1.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
       l[h] += __shfl_xor_sync(~0u, l[h], 1);
@@ -414,79 +551,81 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
         wml[wn * S::kRows + r0] = make_float2(m[0], l[0]);
         wml[wn * S::kRows + r0 + 8] = make_float2(m[1], l[1]);
       }
-      __syncthreads();
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
+      if (!meet()) return;
+      for (int h = 0; h < 2; ++h) {  // rows 0 .. 7 of every group, then 8 .. 15
+        if (8 * h >= nrow) break;    // (uniform: later groups exist only when earlier ones are full)
         float mm = -INFINITY;
 #pragma unroll
         for (int w = 0; w < WN; ++w) mm = fmaxf(mm, wml[w * S::kRows + r0 + 8 * h].x);
-        const float f = m[h] == -INFINITY ? 0.0f : ex2(m[h] - mm);
-        float ll = 0.0f;
+        const float mh = h ? m[1] : m[0];
+        const float f = mh == -INFINITY ? 0.0f : ex2(mh - mm);
+        // merge: [warp][8 rows][kMRow]
+        float* mp = merge + (warp * 8 + (lane >> 2)) * S::kMRow;
 #pragma unroll
-        for (int w = 0; w < WN; ++w) {
-          const float2 x = wml[w * S::kRows + r0 + 8 * h];
-          ll += x.x == -INFINITY ? 0.0f : x.y * ex2(x.x - mm);
+        for (int k = 0; k < KS * 2; k += Q8 ? 2 : 1) {
+          const float x0 = f * (h ? o[k][2] : o[k][0]), x1 = f * (h ? o[k][3] : o[k][1]);
+          if constexpr (Q8) {
+            const float y0 = f * (h ? o[k + 1][2] : o[k + 1][0]), y1 = f * (h ? o[k + 1][3] : o[k + 1][1]);
+            *reinterpret_cast<float4*>(mp + col(k, 0)) = make_float4(x0, y0, x1, y1);
+          } else {
+            *reinterpret_cast<float2*>(mp + col(k, 0)) = make_float2(x0, x1);
+          }
         }
+        if (!meet()) return;
+        for (int i = tid; i < WM * 8 * (DP / 4); i += 32 * NW) {
+          const int rr = i / (DP / 4), d = (i % (DP / 4)) * 4, grp = rr >> 3;
+          const int r = grp * 16 + 8 * h + (rr & 7);
+          if (r >= nrow || d >= c.D) continue;
+          float4 acc = make_float4(0, 0, 0, 0);
+          float top = -INFINITY, ll = 0.0f;
 #pragma unroll
-        for (int k = 0; k < KS * 2; ++k) {
-          o[k][2 * h] *= f;
-          o[k][2 * h + 1] *= f;
-        }
-        m[h] = mm;
-        l[h] = ll;
-      }
-      // the groups add up in turn: a fixed order
-      for (int w = 0; w < WN; ++w) {
-        if (wn == w) {
+          for (int w = 0; w < WN; ++w) top = fmaxf(top, wml[w * S::kRows + r].x);
 #pragma unroll
-          for (int k = 0; k < KS * 2; ++k)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              float* p = merge + (r0 + 8 * (x >> 1)) * DP + col(k, x);
-              *p = w ? *p + o[k][x] : o[k][x];
-            }
+          for (int w = 0; w < WN; ++w) {  // a fixed order
+            const float2 y = wml[w * S::kRows + r];
+            ll += y.x == -INFINITY ? 0.0f : y.y * ex2(y.x - top);
+            const float4 v = *reinterpret_cast<const float4*>(merge + ((w * WM + grp) * 8 + (rr & 7)) * S::kMRow + d);
+            acc.x += v.x;
+            acc.y += v.y;
+            acc.z += v.z;
+            acc.w += v.w;
+          }
+          if (whole) {
+            const float ff = factor(ll, vs);
+            const long long row = out_row(row_base + r);
+            put4(row, d, make_float4(acc.x * ff, acc.y * ff, acc.z * ff, acc.w * ff));
+            if (d == 0) put_lse(row, top, ll);
+          } else {
+            *reinterpret_cast<float4*>(po + r * c.D + d) = acc;
+            if (d == 0) pml[r] = make_float2(top, ll);
+          }
         }
-        __syncthreads();
-      }
-      if (wn == 0 && (lane & 3) == 0) {
-        wml[r0] = make_float2(m[0], l[0]);
-        wml[r0 + 8] = make_float2(m[1], l[1]);
-      }
-      __syncthreads();
-      if (whole) {
-        const float vs = vscale();
-        for (int i = tid; i < nrow * c.D; i += NT) {
-          const int r = i / c.D, d = i - r * c.D;
-          const float ll = wml[r].y;
-          const long long row = out_row(row_base + r);
-          put(row, d, ll > 0.0f ? merge[r * DP + d] * vs / ll : 0.0f);
-          if (d == 0) put_lse(row, wml[r].x, ll);
-        }
-      } else {
-        for (int i = tid; i < nrow * c.D; i += NT) {
-          const int r = i / c.D, d = i - r * c.D;
-          po[r * c.D + d] = merge[r * DP + d];
-          if (d == 0) pml[r] = wml[r];
-        }
+        if (!meet()) return;
       }
     } else {
-      const float vs = vscale();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const int r = r0 + 8 * h;
         if (r < nrow) {
           const long long row = out_row(row_base + r);
-          const float f = whole ? (l[h] > 0.0f ? vs / l[h] : 0.0f) : 1.0f;
+          const float f = whole ? factor(l[h], vs) : 1.0f;
 #pragma unroll
-          for (int k = 0; k < KS * 2; ++k)
-#pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const int d = col(k, x);
+          for (int k = 0; k < KS * 2; ++k) {
+            if constexpr (!Q8) {
+              const int d = col(k, 0);
               if (d < c.D) {
-                if (whole) put(row, d, o[k][2 * h + x] * f);
-                else po[r * c.D + d] = o[k][2 * h + x];
+                if (whole) *reinterpret_cast<unsigned*>(static_cast<uint16_t*>(a.out) + row * c.D + d) = pack2<QF16>(o[k][2 * h] * f, o[k][2 * h + 1] * f);
+                else *reinterpret_cast<float2*>(po + r * c.D + d) = make_float2(o[k][2 * h], o[k][2 * h + 1]);
+              }
+            } else if (!(k & 1)) {  // columns 4t .. 4t + 3 of a slice are in accumulators k, k + 1
+              const int d = col(k, 0);
+              if (d < c.D) {
+                const float4 x = make_float4(o[k][2 * h] * f, o[k + 1][2 * h] * f, o[k][2 * h + 1] * f, o[k + 1][2 * h + 1] * f);
+                if (whole) put4(row, d, x);
+                else *reinterpret_cast<float4*>(po + r * c.D + d) = x;
               }
             }
+          }
           if ((lane & 3) == 0) {
             if (whole) put_lse(row, m[h], l[h]);
             else pml[r] = make_float2(m[h], l[h]);
@@ -494,82 +633,91 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units) {
         }
       }
     }
-    if (whole) {
-      if constexpr (WN > 1) __syncthreads();
-      return;
-    }
-    // the last CTA of the item joins its parts
+    if (whole) return;
+    // the last CTA of the item joins its parts, in their order
     __threadfence();
-    __syncthreads();
-    if (tid == 0) misc[0] = atomicAdd(c.ws_count + c0, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
-    __syncthreads();
-    if (misc[0]) {
+    if (!meet()) return;
+    if (tid == 0) hd->last = atomicAdd(c.ws_count + c0, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
+    if (!meet()) return;
+    if (hd->last) {
       __threadfence();
       if (tid == 0) c.ws_count[c0] = 0u;
       const int parts = static_cast<int>(c1 - c0) + 1;
       const auto slot_of = [&](int p) { return 2 * (c0 + p) + (p == 0 ? 1 : 0); };
-      const float vs = vscale();
-      for (int i = tid; i < nrow * (c.D >> 2); i += NT) {
+      for (int i = tid; i < nrow * (c.D >> 2); i += 32 * NW) {
         const int r = i / (c.D >> 2), d = (i - r * (c.D >> 2)) * 4;
-        float mm = -INFINITY;
-        for (int p = 0; p < parts; ++p) mm = fmaxf(mm, __ldcg(&c.ws_ml[slot_of(p) * c.step_rows + r]).x);
         float4 acc = make_float4(0, 0, 0, 0);
-        float ll = 0.0f;
-        for (int p = 0; p < parts; ++p) {
-          const float2 x = __ldcg(&c.ws_ml[slot_of(p) * c.step_rows + r]);
-          const float4 v = __ldcg(reinterpret_cast<const float4*>(c.ws_o + (slot_of(p) * c.step_rows + r) * c.D + d));
-          const float f = x.x == -INFINITY ? 0.0f : ex2(x.x - mm);
-          ll += f * x.y;
-          acc.x += f * v.x;
-          acc.y += f * v.y;
-          acc.z += f * v.z;
-          acc.w += f * v.w;
+        float mm = -INFINITY, ll = 0.0f;
+        for (int p0 = 0; p0 < parts; p0 += 8) {  // eight parts' reads in flight
+          float2 x[8];
+          float4 v[8];
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            const long long sl = slot_of(min(p0 + p, parts - 1)) * c.step_rows + r;
+            x[p] = __ldcg(&c.ws_ml[sl]);
+            v[p] = __ldcg(reinterpret_cast<const float4*>(c.ws_o + sl * c.D + d));
+          }
+          float top = mm;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            if (p0 + p >= parts) x[p].x = -INFINITY;
+            top = fmaxf(top, x[p].x);
+          }
+          const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - top);
+          ll *= f0;
+          acc.x *= f0;
+          acc.y *= f0;
+          acc.z *= f0;
+          acc.w *= f0;
+          mm = top;
+#pragma unroll
+          for (int p = 0; p < 8; ++p) {
+            if (x[p].x == -INFINITY) continue;
+            const float f = ex2(x[p].x - top);
+            ll += f * x[p].y;
+            acc.x += f * v[p].x;
+            acc.y += f * v[p].y;
+            acc.z += f * v[p].z;
+            acc.w += f * v[p].w;
+          }
         }
         const long long row = out_row(row_base + r);
-        const float f = ll > 0.0f ? vs / ll : 0.0f;
-        put(row, d, acc.x * f);
-        put(row, d + 1, acc.y * f);
-        put(row, d + 2, acc.z * f);
-        put(row, d + 3, acc.w * f);
+        const float f = factor(ll, vs);
+        put4(row, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
         if (d == 0) put_lse(row, mm, ll);
       }
     }
-    __syncthreads();
   };
 
-  begin_item();
   for (int i = 0; i < steps; ++i) {
-    cp_wait<ST - 2>();
-    store_ids(i + ST - 1);
-    __syncthreads();
-    issue(i + ST - 1);
-    fetch_ids(i + ST);
-    compute(i);
-    const bool last = cur.tile + 1 == cur.ntile;
-    if (last || i + 1 == steps) {
-      end_item(u0 + i + 1);
-      if (i + 1 < steps) {
-        item_u += cur.ntile;
-        advance(cur);
-        begin_item();
-      }
-    } else {
-      advance(cur);
+    const int st = i % ST;
+    ok = bar_wait(&hd->dead, &hd->full[st], (i / ST) & 1, c.status);
+    if (!ok) break;
+    cur = hd->meta[st].u;
+    if (i == 0 || cur.tile == 0) {
+      ok = bar_wait(&hd->dead, &hd->q_full[qs], q_ph, c.status);
+      if (!ok) break;
+      begin_item();
+    }
+    compute(stages + st * S::kStage, hd->meta[st].bad);
+    __syncwarp();
+    if (lane == 0) bar_arrive(&hd->empty[st]);
+    if (cur.tile + 1 == tiles_of(cur.len) || i + 1 == steps) {
+      end_item(u0 + i);
+      if (!ok) break;
     }
   }
-  cp_wait<0>();
 }
 
 // Row variants: groups of 16 rows, warps per group.  Up to 16 rows (a decode
 // step) four warps share a tile's keys; with more rows the warps take rows.
-constexpr int kStages = 3;
 #define TG_ROW_VARIANTS(X) X(0, 1, 4) X(1, 2, 2) X(2, 4, 1) X(3, 8, 1)
 int row_variant(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
 
 template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN>
 cudaError_t prepare_one(int* ctas) {
-  using S = Shape<DP, MF16, QF16, Q8, WM, WN, kStages>;
-  auto k = step_kernel<DP, MF16, QF16, Q8, WM, WN, kStages>;
+  using S = Shape<DP, Q8, WM, WN>;
+  auto k = step_kernel<DP, MF16, QF16, Q8, WM, WN>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
   if (e != cudaSuccess) return e;
   int occ = 0;
@@ -582,10 +730,27 @@ cudaError_t prepare_one(int* ctas) {
 
 template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN>
 cudaError_t launch_one(const AttnCfg& c, const StepArgs& a, int variant, cudaStream_t s) {
-  using S = Shape<DP, MF16, QF16, Q8, WM, WN, kStages>;
+  using S = Shape<DP, Q8, WM, WN>;
   const int row_tiles = (a.n * c.rep + S::kRows - 1) / S::kRows;
-  const long long tiles = ((static_cast<long long>(a.c.max_pages) << c.page_shift) + kTile - 1) / kTile;
+  const long long tiles = ((static_cast<long long>(a.c.max_pages) << c.page_shift) + S::KT - 1) / S::KT;
   const long long most = static_cast<long long>(a.c.batch) * c.G * row_tiles * std::max(1ll, tiles);
+  // Keys of one tensor copy: a page's, or a tile's.  Pages of fewer than 8
+  // tokens are copied row by row (a swizzled block has 8 rows).
+  const int box = c.page_size < 8 ? 0 : std::min(c.page_size, S::KT);
+  CUtensorMap mk{}, mv{};
+  if (box > 0) {
+    const cuuint64_t es = Q8 ? 1 : 2, D = c.D, P = c.page_size, G = c.G;
+    const bool token = c.token_major;
+    const cuuint64_t dims[4] = {D, token ? G : P, token ? P : G, static_cast<cuuint64_t>(a.c.num_pages)};
+    const cuuint32_t bx[4] = {static_cast<cuuint32_t>(std::min(DP, Q8 ? 128 : 64)), token ? 1u : static_cast<cuuint32_t>(box),
+                              token ? static_cast<cuuint32_t>(box) : 1u, 1};
+    const CUtensorMapDataType type = Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : QF16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    const CUtensorMapSwizzle sw = S::kRB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
+    for (int w = 0; w < 2; ++w) {
+      const cuuint64_t st[3] = {D * es, D * es * dims[1], static_cast<cuuint64_t>(w ? a.c.v_page_stride : a.c.k_page_stride) * es};
+      if (!encode_map(c.encode, w ? &mv : &mk, type, sw, w ? a.c.v : a.c.k, 4, dims, st, bx)) return cudaErrorInvalidValue;
+    }
+  }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(most, c.nsm * c.step_ctas[variant])));
   cfg.blockDim = dim3(S::kThreads);
@@ -596,7 +761,7 @@ cudaError_t launch_one(const AttnCfg& c, const StepArgs& a, int variant, cudaStr
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, Q8, WM, WN, kStages>, c, a, row_tiles, 2);
+  return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, Q8, WM, WN>, c, a, row_tiles, 2, box, mk, mv);
 }
 
 template <int DP, bool MF16, bool QF16, bool Q8>
