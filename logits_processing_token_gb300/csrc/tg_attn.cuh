@@ -40,7 +40,7 @@ struct AttnCfg {
   float2* ws_ml;           // [slots][step_rows]: running maximum (base 2) and sum
   unsigned* ws_count;      // [slots / 2]: parts of a split sequence that are done; zero between calls
   int nsm;
-  int step_ctas[4];        // CTAs per SM of the step kernel's row variants
+  int step_ctas[5];        // CTAs per SM of the step kernel's row variants
   unsigned* prompt_count;  // [2]: next item and CTAs done of a prompt call; zero between calls
   void* encode;            // the driver's tensor-map encoder (host)
 };
@@ -163,6 +163,12 @@ __device__ __forceinline__ void ldsm4(unsigned (&r)[4], unsigned addr) {
 __device__ __forceinline__ void ldsm4t(unsigned (&r)[4], unsigned addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
+// An 8 x 8 matrix of 16-bit values, a row over four lanes, transposed.
+__device__ __forceinline__ unsigned transposed(unsigned x) {
+  unsigned y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
 }
 template <bool F16>
 __device__ __forceinline__ void mma16816(float (&d)[4], const unsigned (&a)[4], unsigned b0, unsigned b1) {

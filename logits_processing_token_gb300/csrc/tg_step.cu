@@ -8,12 +8,13 @@
 //   o' = o 2^(m-m') + sum 2^(s-m') v
 // (c holds the scale and log2 e), and parts join the same way.
 //
-// The work is cut into units of KT keys of one (sequence, key head, row
-// tile), numbered in that order; CTA i of N takes units [U i / N, U (i+1) / N),
-// so every SM reads the same number of bytes whatever the lengths are.  A
-// (sequence, key head, row tile) that falls into several CTAs leaves its parts
-// in the handle's workspace, and the CTA that finishes last joins them in CTA
-// order: one launch, and the result does not depend on which was last.
+// The work is cut into units of KT keys of one item, a (sequence, key head, row
+// tile), numbered in that order; beginning and ending an item counts as
+// kItemCost units.  CTA i of N takes units [U i / N, U (i+1) / N), so every SM
+// has the same work whatever the lengths are.  An item that falls into several
+// CTAs leaves its parts in the handle's workspace, and the CTA that finishes
+// last joins them in CTA order: one launch, and the result does not depend on
+// which was last.
 //
 // One warp looks up pages and issues the copies, a page's rows of one head at
 // a time, into a ring of stages; the other warps wait for a stage, take 16
@@ -27,29 +28,42 @@ namespace {
 
 // Everything about a unit that the computing warps need.
 struct Unit {
-  int b, g, rt, tile, len;
+  int b, g, rt, tile, len;  // b < 0: no more units
   int any_bad;
+  int first, last;          // of its item in this CTA
+  long long base;           // the item's number of units before it
 };
 struct UnitMeta {
   Unit u;
   unsigned bad[4];  // keys of the tile on pages that do not exist
 };
+// Beginning and ending an item, in units (measured on 256 sequences of 1 to
+// 2,048 keys in e4m3: 140 us at 0, 110 at 1, 104 at 2).
+constexpr int kItemCost = 2;
 
+// Up to 8 rows (a decode step) the products are taken the other way round,
+// S^T = K Q^T and O^T = V^T P^T: the instruction's 16 rows are keys or head
+// elements then and its 8 columns are the rows, half the instructions of the
+// usual way, whose 16 rows would be half empty.  More rows go 16 to a warp.
+//
 // DP: head size padded to 64 or 128.  MF16: the products' type is f16 (an e4m3
 // cache is widened to f16, exactly), else bf16.  QF16: the tensors' type.
-// WM x WN computing warps: WM groups of 16 rows, a tile's keys over WN warps.
-template <int DP, bool Q8, int WM, int WN>
+// WM x WN computing warps: WM groups of 16 rows (WM = 0: one of 8), a tile's
+// keys over WN warps.
+template <int DP, bool Q8, int WMX, int WN>
 struct Shape {
+  static constexpr bool kT = WMX == 0;
+  static constexpr int WM = kT ? 1 : WMX;
   static constexpr int kWarps = WM * WN;
   static constexpr int kThreads = 32 * (kWarps + 1);
-  static constexpr int kRows = 16 * WM;
+  static constexpr int kRows = kT ? 8 : 16 * WM;
   static constexpr int kRB = DP * (Q8 ? 1 : 2);           // bytes of a key's row
   static constexpr int KT = kRB == 256 ? 64 : 128;        // keys of a unit
   static constexpr int kMat = KT * kRB;                   // a K or V tile
   static constexpr int kStage = 2 * kMat;
   static constexpr int kQRow = DP * 2 + 16;               // a query row, padded against bank conflicts
   static constexpr int kQ = kRows * kQRow;
-  static constexpr int kMRow = DP + (Q8 ? 16 : 8);        // a row of sums, padded likewise
+  static constexpr int kMRow = DP + (kT ? 4 : Q8 ? 16 : 8);        // a row of sums, padded likewise
   static constexpr int kMerge = WN > 1 ? WM * WN * 8 * kMRow * 4 : 0;
   static constexpr int kHead = 1024;                      // barriers, metas, scan scratch
   static constexpr int kML = WN * kRows * 8;
@@ -64,8 +78,8 @@ struct Shape {
 constexpr int kMaxStages = 8;
 struct Head {
   unsigned long long full[kMaxStages], empty[kMaxStages], q_full[2], q_empty[2], meet;
-  int dead, last, first_b, first_in, first_len;
-  long long first_u;
+  int dead, last, first_b, first_len;
+  long long first_in;
   long long wsum[16];
   UnitMeta meta[kMaxStages];
 };
@@ -80,11 +94,13 @@ __device__ __forceinline__ unsigned key_at(int r, int c) {
   else return tile_at<RB>(r, c);
 }
 
-template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN>
-__global__ void __launch_bounds__(32 * (WM * WN + 1), WM * WN > 4 ? 1 : 2)
+template <int DP, bool MF16, bool QF16, bool Q8, int WMX, int WN>
+__global__ void __launch_bounds__(32 * ((WMX ? WMX : 1) * WN + 1), WMX * WN > 4 ? 1 : 2)
 step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int box, const __grid_constant__ CUtensorMap mk,
             const __grid_constant__ CUtensorMap mv) {
-  using S = Shape<DP, Q8, WM, WN>;
+  using S = Shape<DP, Q8, WMX, WN>;
+  constexpr bool T = S::kT;
+  constexpr int WM = S::WM;
   constexpr int NT = S::kThreads, NW = S::kWarps, KT = S::KT, ST = S::ST, RB = S::kRB;
   constexpr int KW = KT / WN;    // keys of a tile per warp
   constexpr int KS = DP / 16;    // 16-element slices of a head
@@ -131,6 +147,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
   const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
   const auto tiles_of = [](int len) { return len > 0 ? (len + KT - 1) / KT : 1; };
+  const auto cost = [&](int len) { return tiles_of(len) + kItemCost; };
   const int per_tile = c.G * row_tiles;
   const int bper = (a.c.batch + NT - 1) / NT, b_first = tid * bper;
   long long mine = 0;
@@ -139,7 +156,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     const int raw = a.c.lens[b], l = checked(raw);
     if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
     if (b == b_first) len0 = l;
-    mine += tiles_of(l);
+    mine += cost(l);
   }
   long long before = mine;
 #pragma unroll
@@ -155,7 +172,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     if (w < warp) before += hd->wsum[w];
     total += hd->wsum[w];
   }
-  before -= mine;  // key tiles of the sequences before this thread's
+  before -= mine;  // units of one (head, row tile) of the sequences before this thread's
   const long long U = total * per_tile;
   const long long N = min(static_cast<long long>(gridDim.x), max(1ll, U / min_units));
   if (blockIdx.x >= N) return;
@@ -164,22 +181,24 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     int b = b_first, l = len0;
     long long at = before;
     for (;;) {
-      const int t = tiles_of(l);
+      const int t = cost(l);
       if ((at + t) * per_tile > u0) break;
       at += t;
       l = checked(a.c.lens[++b]);
     }
     hd->first_b = b;
     hd->first_len = l;
-    hd->first_in = static_cast<int>(u0 - at * per_tile);
+    hd->first_in = u0 - at * per_tile;
   }
   __syncthreads();
-  const int steps = static_cast<int>(u1 - u0);
-
   if (warp == NW) {
     // ---- pages and copies ---------------------------------------------------
     int b = hd->first_b, len = hd->first_len, nt = tiles_of(len);
-    int tile = hd->first_in % nt, rt = hd->first_in / nt % row_tiles, g = hd->first_in / nt / row_tiles;
+    const int skip = static_cast<int>(hd->first_in / cost(len));
+    int rt = skip % row_tiles, g = skip / row_tiles;
+    long long base = u0 - hd->first_in % cost(len);  // units before the item
+    // its tiles that are this CTA's: tile .. tend - 1
+    int tile = static_cast<int>(max(0ll, u0 - base - kItemCost)), tend = static_cast<int>(min(static_cast<long long>(nt), u1 - base - kItemCost));
     int len_next = b + 1 < a.c.batch ? checked(a.c.lens[b + 1]) : 0;
     const int R = tensor_copies ? box : 1;  // keys of one copy
     const int shift = R == 1 ? 0 : 31 - __clz(R);
@@ -190,12 +209,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     int id = tensor_copies && lane < (KT >> shift) ? entry(b, tile * KT + (lane << shift), len) : -1;
     int qs = 0;
     unsigned q_ph = 1;
-    bool ok = true;
+    bool ok = true, first = true;
     int i = 0;
-    for (; i < steps; ++i) {
+    for (; base + kItemCost < u1; ++i) {
       const int st = i % ST;
       const unsigned e_ph = ((i / ST) & 1) ^ 1;
-      if (i == 0 || tile == 0) {
+      if (first) {
         // this item's queries: a row at a time into padded rows
         ok = bar_wait(&hd->dead, &hd->q_empty[qs], q_ph, c.status);
         if (!ok) break;
@@ -213,9 +232,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         if (++qs == 2) { qs = 0; q_ph ^= 1; }
       }
       // the following unit, and its pages while this one's stage is awaited
-      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nnt = nt;
-      if (ntile == nt) {
+      const bool last = tile + 1 == tend;
+      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nnt = nt, ntend = tend;
+      long long nbase = base;
+      if (last) {
         ntile = 0;
+        nbase += nt + kItemCost;
         if (++nrt == row_tiles) {
           nrt = 0;
           if (++ng == c.G) {
@@ -226,8 +248,9 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             len_next = nb + 1 < a.c.batch ? checked(a.c.lens[nb + 1]) : 0;
           }
         }
+        ntend = static_cast<int>(min(static_cast<long long>(nnt), u1 - nbase - kItemCost));
       }
-      const int id_next = tensor_copies && i + 1 < steps && lane < (KT >> shift) ? entry(nb, ntile * KT + (lane << shift), nlen) : -1;
+      const int id_next = tensor_copies && nbase + kItemCost < u1 && lane < (KT >> shift) ? entry(nb, ntile * KT + (lane << shift), nlen) : -1;
       ok = bar_wait(&hd->dead, &hd->empty[st], e_ph, c.status);
       if (!ok) break;
       const unsigned ks = sptr(stages + st * S::kStage), vs = ks + S::kMat;
@@ -247,7 +270,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           hd->meta[st].bad[lane] = w;
         }
         if (lane == 0) {
-          hd->meta[st].u = Unit{b, g, rt, tile, len, badm != 0};
+          hd->meta[st].u = Unit{b, g, rt, tile, len, badm != 0, first, last, base};
         }
         __syncwarp();
         if (lane == 0) bar_expect(&hd->full[st], copies * R * RB * 2);
@@ -286,12 +309,24 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             cp16(vs + at, static_cast<const char*>(a.c.v) + (p0 * a.c.v_page_stride + in) * ES + cc * 16, pg >= 0);
           }
         }
-        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, tile, len, any_bad != 0};
+        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, tile, len, any_bad != 0, first, last, base};
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
         __syncwarp();
         if (lane == 0) bar_arrive(&hd->full[st]);
       }
-      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; nt = nnt; id = id_next;
+      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; nt = nnt; tend = ntend; base = nbase; id = id_next;
+      first = last;
+    }
+    if (ok) {
+      const int st = i % ST;  // the end
+      ok = bar_wait(&hd->dead, &hd->empty[st], ((i / ST) & 1) ^ 1, c.status);
+      if (ok) {
+        if (lane == 0) hd->meta[st].u.b = -1;
+        if (!tensor_copies)
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
+        __syncwarp();
+        if (lane == 0) bar_arrive(&hd->full[st]);
+      }
     }
     if (!ok) {
       // a wait ran out: copies in flight land before the CTA's memory goes
@@ -303,11 +338,13 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 
   // ---- computing warps -----------------------------------------------------
   const int wm = warp % WM, wn = warp / WM;
-  unsigned qf[KS][4];
-  float o[KS * 2][4];
-  float m[2], l[2], rs[2];  // rows lane / 4 and lane / 4 + 8 of this warp's group
+  constexpr int NO = T ? KS : KS * 2;
+  unsigned qf[KS][T ? 2 : 4];
+  float o[NO][4];
+  float m[2], l[2], rs[2];  // of two rows: lane / 4 and lane / 4 + 8 of this warp's 16, or 2 (lane % 4) and the next of 8
   int lim[2];               // keys that the row sees
-  const int r0 = wm * 16 + (lane >> 2);
+  const int r0 = T ? 2 * (lane & 3) : wm * 16 + (lane >> 2);
+  constexpr int RSTEP = T ? 1 : 8;
   const float bias = kWeightBias<MF16>;
   Unit cur;
   int qs = 0;
@@ -327,12 +364,16 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     const unsigned char* qb = qbuf + qs * S::kQ;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      const int r = cur.rt * S::kRows + r0 + 8 * h;
+      const int r = cur.rt * S::kRows + r0 + RSTEP * h;
       lim[h] = r < rows_all ? cur.len - a.n + r / c.rep + 1 : 0;
       m[h] = -INFINITY;
       l[h] = 0.0f;
       rs[h] = sc;
-      const unsigned char* q = qb + (r0 + 8 * h) * S::kQRow;
+    }
+#pragma unroll
+    for (int h = 0; h < (T ? 1 : 2); ++h) {
+      // as the second operand (T) a lane holds row lane / 4 alone
+      const unsigned char* q = qb + (T ? lane >> 2 : r0 + 8 * h) * S::kQRow;
       const int t = lane & 3;
 #pragma unroll
       for (int k = 0; k < KS; ++k) {
@@ -341,7 +382,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         // its keys' elements come out of shared memory (any order serves a sum)
         const int e = 16 * k + (Q8 ? 4 * t : 2 * t), f = Q8 ? e + 2 : e + 8;
         qf[k][h] = *reinterpret_cast<const unsigned*>(q + 2 * e);
-        qf[k][2 + h] = *reinterpret_cast<const unsigned*>(q + 2 * f);
+        qf[k][(T ? 1 : 2) + h] = *reinterpret_cast<const unsigned*>(q + 2 * f);
       }
       if constexpr (MF16 && !QF16) {
         // bf16 queries to f16: a power of two per row brings the row's largest
@@ -352,7 +393,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float2 v = unpack2<false>(qf[k][2 * x + h]);
+            const float2 v = unpack2<false>(qf[k][(T ? 1 : 2) * x + h]);
             top = fmaxf(top, fmaxf(fabsf(v.x), fabsf(v.y)));
           }
         top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
@@ -360,18 +401,24 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         const int e = top > 0.0f && top < INFINITY ? 14 - (static_cast<int>(__float_as_uint(top) >> 23) - 127) : 0;
         const int e1 = min(e, 120);  // of a subnormal largest value the rest stays
         const float up = __uint_as_float(static_cast<unsigned>(max(e1, -120) + 127) << 23);
-        rs[h] = sc / up;
+        const float down = sc / up;
+        if constexpr (T) {
+          rs[0] = __shfl_sync(~0u, down, r0 * 4);
+          rs[1] = __shfl_sync(~0u, down, r0 * 4 + 4);
+        } else {
+          rs[h] = down;
+        }
 #pragma unroll
         for (int k = 0; k < KS; ++k)
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            const float2 v = unpack2<false>(qf[k][2 * x + h]);
-            qf[k][2 * x + h] = pack2<true>(v.x * up, v.y * up);
+            const float2 v = unpack2<false>(qf[k][(T ? 1 : 2) * x + h]);
+            qf[k][(T ? 1 : 2) * x + h] = pack2<true>(v.x * up, v.y * up);
           }
       }
     }
 #pragma unroll
-    for (int k = 0; k < KS * 2; ++k)
+    for (int k = 0; k < NO; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[k][i] = 0.0f;
     __syncwarp();
@@ -401,31 +448,59 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     for (int k0 = 0; k0 < KW; k0 += KC) {
       const int at = wn * KW + k0;
       if (cur.tile * KT + at >= cur.len) break;
-      float s[KC / 8][4];
+      // Scores: s[i] of 8 keys (lane / 4 and 8 more rows), or, T, of 16 keys:
+      // keys lane / 4 and 8 more, columns the two rows.
+      constexpr int NS = T ? KC / 16 : KC / 8;
+      float s[NS][4];
 #pragma unroll
-      for (int i = 0; i < KC / 8; ++i)
+      for (int i = 0; i < NS; ++i)
 #pragma unroll
         for (int x = 0; x < 4; ++x) s[i][x] = 0.0f;
 #pragma unroll
       for (int kg = 0; kg < KC / 16; ++kg) {
-        const int row = at + kg * 16 + ((lane >> 4) << 3) + (lane & 7);
-        if constexpr (!Q8) {
+        if constexpr (T) {
+          const int row = at + kg * 16 + (lane & 15);
+          if constexpr (!Q8) {
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            unsigned r[4];
-            ldsm4(r, ks + key_at<RB, KT>(row, 2 * k + ((lane >> 3) & 1)));
-            mma16816<MF16>(s[2 * kg], qf[k], r[0], r[1]);
-            mma16816<MF16>(s[2 * kg + 1], qf[k], r[2], r[3]);
+            for (int k = 0; k < KS; ++k) {
+              unsigned r[4];
+              ldsm4(r, ks + key_at<RB, KT>(row, 2 * k + (lane >> 4)));
+              mma16816<MF16>(s[kg], r, qf[k][0], qf[k][1]);
+            }
+          } else {
+#pragma unroll
+            for (int k = 0; k < KS; k += 2) {
+              unsigned r[4];
+              ldsm4(r, ks + key_at<RB, KT>(row, k + (lane >> 4)));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const unsigned w[4] = {e4m3x2_to_f16x2(r[2 * x] & 0xffff), e4m3x2_to_f16x2(r[2 * x + 1] & 0xffff),
+                                       e4m3x2_to_f16x2(r[2 * x] >> 16), e4m3x2_to_f16x2(r[2 * x + 1] >> 16)};
+                mma16816<MF16>(s[kg], w, qf[k + x][0], qf[k + x][1]);
+              }
+            }
           }
+          continue;
         } else {
+          const int row = at + kg * 16 + ((lane >> 4) << 3) + (lane & 7);
+          if constexpr (!Q8) {
 #pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            unsigned r[4];
-            ldsm4(r, ks + key_at<RB, KT>(row, k + ((lane >> 3) & 1)));
+            for (int k = 0; k < KS; ++k) {
+              unsigned r[4];
+              ldsm4(r, ks + key_at<RB, KT>(row, 2 * k + ((lane >> 3) & 1)));
+              mma16816<MF16>(s[2 * kg], qf[k], r[0], r[1]);
+              mma16816<MF16>(s[2 * kg + 1], qf[k], r[2], r[3]);
+            }
+          } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {  // slice k + x of both groups of 8 keys
-              mma16816<MF16>(s[2 * kg], qf[k + x], e4m3x2_to_f16x2(r[x] & 0xffff), e4m3x2_to_f16x2(r[x] >> 16));
-              mma16816<MF16>(s[2 * kg + 1], qf[k + x], e4m3x2_to_f16x2(r[2 + x] & 0xffff), e4m3x2_to_f16x2(r[2 + x] >> 16));
+            for (int k = 0; k < KS; k += 2) {
+              unsigned r[4];
+              ldsm4(r, ks + key_at<RB, KT>(row, k + ((lane >> 3) & 1)));
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {  // slice k + x of both groups of 8 keys
+                mma16816<MF16>(s[2 * kg], qf[k + x], e4m3x2_to_f16x2(r[x] & 0xffff), e4m3x2_to_f16x2(r[x] >> 16));
+                mma16816<MF16>(s[2 * kg + 1], qf[k + x], e4m3x2_to_f16x2(r[2 + x] & 0xffff), e4m3x2_to_f16x2(r[2 + x] >> 16));
+              }
             }
           }
         }
@@ -434,22 +509,30 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       if (cur.tile * KT + at + KC > cur.len - a.n + 1 || cur.any_bad) {
         const unsigned bw = bad[at >> 5] >> (at & 31);
 #pragma unroll
-        for (int i = 0; i < KC / 8; ++i)
+        for (int i = 0; i < NS; ++i)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
-            const int in = i * 8 + 2 * (lane & 3) + (x & 1);
-            if (cur.tile * KT + at + in >= lim[x >> 1] || ((bw >> in) & 1)) s[i][x] = -INFINITY;
+            const int in = T ? i * 16 + (lane >> 2) + 8 * (x >> 1) : i * 8 + 2 * (lane & 3) + (x & 1);
+            if (cur.tile * KT + at + in >= lim[T ? x & 1 : x >> 1] || ((bw >> in) & 1)) s[i][x] = -INFINITY;
           }
       }
+      // element (h, y) of s[i]: row h of the two
+      const auto el = [](int h, int y) { return T ? 2 * y + h : 2 * h + y; };
       float sub[2];
       bool moved = false;
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float top = -INFINITY;
 #pragma unroll
-        for (int i = 0; i < KC / 8; ++i) top = fmaxf(top, fmaxf(s[i][2 * h], s[i][2 * h + 1]));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-        top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        for (int i = 0; i < NS; ++i) top = fmaxf(top, fmaxf(s[i][el(h, 0)], s[i][el(h, 1)]));
+        if constexpr (T) {
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
+        } else {
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
+          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
+        }
         top *= rs[h];
         sub[h] = 1.0f;
         if (top > m[h]) {
@@ -461,48 +544,78 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       }
       if (__any_sync(~0u, moved)) {
 #pragma unroll
-        for (int k = 0; k < KS * 2; ++k) {
-          o[k][0] *= sub[0];
-          o[k][1] *= sub[0];
-          o[k][2] *= sub[1];
-          o[k][3] *= sub[1];
-        }
+        for (int k = 0; k < NO; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) o[k][el(h, y)] *= sub[h];
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float off = m[h] == -INFINITY ? 0.0f : m[h] - bias;
 #pragma unroll
-        for (int i = 0; i < KC / 8; ++i) {
-          s[i][2 * h] = ex2(fmaf(s[i][2 * h], rs[h], -off));
-          s[i][2 * h + 1] = ex2(fmaf(s[i][2 * h + 1], rs[h], -off));
-          l[h] += s[i][2 * h] + s[i][2 * h + 1];
-        }
+        for (int i = 0; i < NS; ++i)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) {
+            float& x = s[i][el(h, y)];
+            x = ex2(fmaf(x, rs[h], -off));
+            l[h] += x;
+          }
       }
 #pragma unroll
       for (int kg = 0; kg < KC / 16; ++kg) {
-        const unsigned p[4] = {pack2<MF16>(s[2 * kg][0], s[2 * kg][1]), pack2<MF16>(s[2 * kg][2], s[2 * kg][3]),
-                               pack2<MF16>(s[2 * kg + 1][0], s[2 * kg + 1][1]), pack2<MF16>(s[2 * kg + 1][2], s[2 * kg + 1][3])};
-        const int row = at + kg * 16 + (lane & 15);
-        if constexpr (!Q8) {
+        const int row = at + kg * 16 + (T ? ((lane >> 4) << 3) + (lane & 7) : lane & 15);
+        if constexpr (T) {
+          // keys by rows to rows by keys: the second operand of V^T P^T
+          const unsigned b0 = transposed(pack2<MF16>(s[kg][0], s[kg][1])), b1 = transposed(pack2<MF16>(s[kg][2], s[kg][3]));
+          if constexpr (!Q8) {
 #pragma unroll
-          for (int k = 0; k < KS; ++k) {
-            unsigned r[4];
-            ldsm4t(r, vs + key_at<RB, KT>(row, 2 * k + (lane >> 4)));
-            mma16816<MF16>(o[2 * k], p, r[0], r[1]);
-            mma16816<MF16>(o[2 * k + 1], p, r[2], r[3]);
+            for (int k = 0; k < KS; ++k) {
+              unsigned r[4];
+              ldsm4t(r, vs + key_at<RB, KT>(row, 2 * k + ((lane >> 3) & 1)));
+              mma16816<MF16>(o[k], r, b0, b1);
+            }
+          } else {
+            const int row8 = at + kg * 16 + (lane & 15);
+#pragma unroll
+            for (int k = 0; k < KS; k += 2) {
+              unsigned r[4];
+              ldsm4t(r, vs + key_at<RB, KT>(row8, k + (lane >> 4)));
+              // a register holds elements (2g, 2g + 1) of two keys: the even ones
+              // become the instruction's rows 0 .. 7, the odd ones 8 .. 15
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const unsigned u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
+                const unsigned va[4] = {e4m3x2_to_f16x2(u & 0xffff), e4m3x2_to_f16x2(u >> 16), e4m3x2_to_f16x2(w & 0xffff),
+                                        e4m3x2_to_f16x2(w >> 16)};
+                mma16816<MF16>(o[k + x], va, b0, b1);
+              }
+            }
           }
         } else {
+          const unsigned p[4] = {pack2<MF16>(s[2 * kg][0], s[2 * kg][1]), pack2<MF16>(s[2 * kg][2], s[2 * kg][3]),
+                                 pack2<MF16>(s[2 * kg + 1][0], s[2 * kg + 1][1]), pack2<MF16>(s[2 * kg + 1][2], s[2 * kg + 1][3])};
+          if constexpr (!Q8) {
 #pragma unroll
-          for (int k = 0; k < KS; k += 2) {
-            unsigned r[4];
-            ldsm4t(r, vs + key_at<RB, KT>(row, k + (lane >> 4)));
-            // a register holds values (2g, 2g + 1) of two keys: even and odd
-            // columns of a slice become the two products' columns
+            for (int k = 0; k < KS; ++k) {
+              unsigned r[4];
+              ldsm4t(r, vs + key_at<RB, KT>(row, 2 * k + (lane >> 4)));
+              mma16816<MF16>(o[2 * k], p, r[0], r[1]);
+              mma16816<MF16>(o[2 * k + 1], p, r[2], r[3]);
+            }
+          } else {
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              const unsigned u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
-              mma16816<MF16>(o[2 * (k + x)], p, e4m3x2_to_f16x2(u & 0xffff), e4m3x2_to_f16x2(w & 0xffff));
-              mma16816<MF16>(o[2 * (k + x) + 1], p, e4m3x2_to_f16x2(u >> 16), e4m3x2_to_f16x2(w >> 16));
+            for (int k = 0; k < KS; k += 2) {
+              unsigned r[4];
+              ldsm4t(r, vs + key_at<RB, KT>(row, k + (lane >> 4)));
+              // a register holds values (2g, 2g + 1) of two keys: even and odd
+              // columns of a slice become the two products' columns
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const unsigned u = __byte_perm(r[2 * x], 0, 0x3120), w = __byte_perm(r[2 * x + 1], 0, 0x3120);
+                mma16816<MF16>(o[2 * (k + x)], p, e4m3x2_to_f16x2(u & 0xffff), e4m3x2_to_f16x2(w & 0xffff));
+                mma16816<MF16>(o[2 * (k + x) + 1], p, e4m3x2_to_f16x2(u >> 16), e4m3x2_to_f16x2(w >> 16));
+              }
             }
           }
         }
@@ -530,12 +643,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 
   // The item's end in this CTA: join the warps, then write the result, or this
   // CTA's part of it.
-  const auto end_item = [&](long long u) {
-    const int nt = tiles_of(cur.len);
-    const long long item_u = u - cur.tile;
-    const long long c0 = ((item_u + 1) * N - 1) / U, c1 = ((item_u + nt) * N - 1) / U;
+  const auto end_item = [&]() {
+    // the CTAs with the item's first and last tile
+    const long long tile0 = cur.base + kItemCost;
+    const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(cur.len)) * N - 1) / U;
     const bool whole = c0 == c1;
-    const long long slot = 2ll * blockIdx.x + (item_u < u0 ? 0 : 1);
+    const long long slot = 2ll * blockIdx.x + (tile0 < u0 ? 0 : 1);
     float* po = c.ws_o + slot * c.step_rows * c.D;
     float2* pml = c.ws_ml + slot * c.step_rows;
     const int row_base = cur.rt * S::kRows;
@@ -543,32 +656,58 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     const float vs = Q8 && c.v_scale ? c.v_scale[cur.g] : 1.0f;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-      l[h] += __shfl_xor_sync(~0u, l[h], 1);
-      l[h] += __shfl_xor_sync(~0u, l[h], 2);
+      if constexpr (T) {
+        l[h] += __shfl_xor_sync(~0u, l[h], 4);
+        l[h] += __shfl_xor_sync(~0u, l[h], 8);
+        l[h] += __shfl_xor_sync(~0u, l[h], 16);
+      } else {
+        l[h] += __shfl_xor_sync(~0u, l[h], 1);
+        l[h] += __shfl_xor_sync(~0u, l[h], 2);
+      }
     }
     if constexpr (WN > 1) {
-      if ((lane & 3) == 0) {
+      if (T ? lane < 4 : (lane & 3) == 0) {
         wml[wn * S::kRows + r0] = make_float2(m[0], l[0]);
-        wml[wn * S::kRows + r0 + 8] = make_float2(m[1], l[1]);
+        wml[wn * S::kRows + r0 + RSTEP] = make_float2(m[1], l[1]);
       }
       if (!meet()) return;
       for (int h = 0; h < 2; ++h) {  // rows 0 .. 7 of every group, then 8 .. 15
         if (8 * h >= nrow) break;    // (uniform: later groups exist only when earlier ones are full)
-        float mm = -INFINITY;
+        // merge: [warp][8 rows][kMRow], scaled to the common maximum
+        if constexpr (T) {
 #pragma unroll
-        for (int w = 0; w < WN; ++w) mm = fmaxf(mm, wml[w * S::kRows + r0 + 8 * h].x);
-        const float mh = h ? m[1] : m[0];
-        const float f = mh == -INFINITY ? 0.0f : ex2(mh - mm);
-        // merge: [warp][8 rows][kMRow]
-        float* mp = merge + (warp * 8 + (lane >> 2)) * S::kMRow;
+          for (int x = 0; x < 2; ++x) {
+            float mm = -INFINITY;
 #pragma unroll
-        for (int k = 0; k < KS * 2; k += Q8 ? 2 : 1) {
-          const float x0 = f * (h ? o[k][2] : o[k][0]), x1 = f * (h ? o[k][3] : o[k][1]);
-          if constexpr (Q8) {
-            const float y0 = f * (h ? o[k + 1][2] : o[k + 1][0]), y1 = f * (h ? o[k + 1][3] : o[k + 1][1]);
-            *reinterpret_cast<float4*>(mp + col(k, 0)) = make_float4(x0, y0, x1, y1);
-          } else {
-            *reinterpret_cast<float2*>(mp + col(k, 0)) = make_float2(x0, x1);
+            for (int w = 0; w < WN; ++w) mm = fmaxf(mm, wml[w * S::kRows + r0 + x].x);
+            const float f = m[x] == -INFINITY ? 0.0f : ex2(m[x] - mm);
+            float* mp = merge + (warp * 8 + r0 + x) * S::kMRow;
+#pragma unroll
+            for (int k = 0; k < NO; ++k) {
+              if constexpr (Q8) {
+                *reinterpret_cast<float2*>(mp + 16 * k + 2 * (lane >> 2)) = make_float2(f * o[k][x], f * o[k][2 + x]);
+              } else {
+                mp[16 * k + (lane >> 2)] = f * o[k][x];
+                mp[16 * k + 8 + (lane >> 2)] = f * o[k][2 + x];
+              }
+            }
+          }
+        } else {
+          float mm = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < WN; ++w) mm = fmaxf(mm, wml[w * S::kRows + r0 + 8 * h].x);
+          const float mh = h ? m[1] : m[0];
+          const float f = mh == -INFINITY ? 0.0f : ex2(mh - mm);
+          float* mp = merge + (warp * 8 + (lane >> 2)) * S::kMRow;
+#pragma unroll
+          for (int k = 0; k < NO; k += Q8 ? 2 : 1) {
+            const float x0 = f * (h ? o[k][2] : o[k][0]), x1 = f * (h ? o[k][3] : o[k][1]);
+            if constexpr (Q8) {
+              const float y0 = f * (h ? o[k + 1][2] : o[k + 1][0]), y1 = f * (h ? o[k + 1][3] : o[k + 1][1]);
+              *reinterpret_cast<float4*>(mp + col(k, 0)) = make_float4(x0, y0, x1, y1);
+            } else {
+              *reinterpret_cast<float2*>(mp + col(k, 0)) = make_float2(x0, x1);
+            }
           }
         }
         if (!meet()) return;
@@ -648,18 +787,19 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         const int r = i / (c.D >> 2), d = (i - r * (c.D >> 2)) * 4;
         float4 acc = make_float4(0, 0, 0, 0);
         float mm = -INFINITY, ll = 0.0f;
-        for (int p0 = 0; p0 < parts; p0 += 8) {  // eight parts' reads in flight
-          float2 x[8];
-          float4 v[8];
+        constexpr int PB = 16;  // parts whose reads are in flight
+        for (int p0 = 0; p0 < parts; p0 += PB) {
+          float2 x[PB];
+          float4 v[PB];
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
+          for (int p = 0; p < PB; ++p) {
             const long long sl = slot_of(min(p0 + p, parts - 1)) * c.step_rows + r;
             x[p] = __ldcg(&c.ws_ml[sl]);
             v[p] = __ldcg(reinterpret_cast<const float4*>(c.ws_o + sl * c.D + d));
           }
           float top = mm;
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
+          for (int p = 0; p < PB; ++p) {
             if (p0 + p >= parts) x[p].x = -INFINITY;
             top = fmaxf(top, x[p].x);
           }
@@ -671,7 +811,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           acc.w *= f0;
           mm = top;
 #pragma unroll
-          for (int p = 0; p < 8; ++p) {
+          for (int p = 0; p < PB; ++p) {
             if (x[p].x == -INFINITY) continue;
             const float f = ex2(x[p].x - top);
             ll += f * x[p].y;
@@ -689,12 +829,13 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     }
   };
 
-  for (int i = 0; i < steps; ++i) {
+  for (int i = 0;; ++i) {
     const int st = i % ST;
     ok = bar_wait(&hd->dead, &hd->full[st], (i / ST) & 1, c.status);
     if (!ok) break;
     cur = hd->meta[st].u;
-    if (i == 0 || cur.tile == 0) {
+    if (cur.b < 0) break;
+    if (cur.first) {
       ok = bar_wait(&hd->dead, &hd->q_full[qs], q_ph, c.status);
       if (!ok) break;
       begin_item();
@@ -702,17 +843,17 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     compute(stages + st * S::kStage, hd->meta[st].bad);
     __syncwarp();
     if (lane == 0) bar_arrive(&hd->empty[st]);
-    if (cur.tile + 1 == tiles_of(cur.len) || i + 1 == steps) {
-      end_item(u0 + i);
+    if (cur.last) {
+      end_item();
       if (!ok) break;
     }
   }
 }
 
-// Row variants: groups of 16 rows, warps per group.  Up to 16 rows (a decode
-// step) four warps share a tile's keys; with more rows the warps take rows.
-#define TG_ROW_VARIANTS(X) X(0, 1, 4) X(1, 2, 2) X(2, 4, 1) X(3, 8, 1)
-int row_variant(int rows) { return rows <= 16 ? 0 : rows <= 32 ? 1 : rows <= 64 ? 2 : 3; }
+// Row variants: groups of 16 rows (0: one of 8), warps per group.  Up to 16
+// rows four warps share a tile's keys; with more rows the warps take rows.
+#define TG_ROW_VARIANTS(X) X(0, 0, 4) X(1, 1, 4) X(2, 2, 2) X(3, 4, 1) X(4, 8, 1)
+int row_variant(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 3 : 4; }
 
 template <int DP, bool MF16, bool QF16, bool Q8, int WM, int WN>
 cudaError_t prepare_one(int* ctas) {
