@@ -624,29 +624,45 @@ class AttnConfig:
             pass
 
 
+# The attention calls run once or more per layer of a decode step: their checks
+# look at each tensor once and pass plain integers on.
+
+def _raw_stream(stream, t):
+    """The stream's handle: the given one's, or the current one of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    import torch
+    try:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    except AttributeError:
+        return torch.cuda.current_stream().cuda_stream
+
+
 def _head_rows(t, name, heads, cfg):
     """Pointer and row stride of a [.., heads, D] tensor whose heads are
     contiguous and whose rows are evenly spaced."""
-    shape, stride = t.shape, t.stride()
     D = cfg.head_dim
+    *lead, h, d = t.shape
+    *rows, sh, sd = t.stride()
     if not t.is_cuda:
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != cfg.dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, cfg.dtype))
-    if shape[-2] != heads or shape[-1] != D:
-        raise ValueError("%s must end in [%d, %d], not %s" % (name, heads, D, tuple(shape[-2:])))
-    if (stride[-1] != 1 and D > 1) or (stride[-2] != D and heads > 1):
+    if h != heads or d != D:
+        raise ValueError("%s must end in [%d, %d], not %s" % (name, heads, D, (h, d)))
+    if sd != 1 or (sh != D and heads > 1):
         raise ValueError("%s: a row's heads must be contiguous" % name)
-    row = stride[-3] if shape[-3] > 1 else 0
-    if len(shape) == 4:  # [batch, n, heads, D]: one spacing for all rows
+    row = rows[-1] if lead[-1] > 1 else 0
+    if len(lead) == 2:  # [batch, n, heads, D]: one spacing for all rows
         if row == 0:
-            row = stride[0] if shape[0] > 1 else 0
-        elif shape[0] > 1 and stride[0] != row * shape[1]:
+            row = rows[0] if lead[0] > 1 else 0
+        elif lead[0] > 1 and rows[0] != row * lead[1]:
             raise ValueError("%s: its rows must be evenly spaced" % name)
     return t.data_ptr(), row or heads * D
 
 
 def _whole(t, name, dtype, numel):
+    """Pointer of a contiguous tensor of at least numel elements."""
     if t.dtype != dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, dtype))
     if not t.is_cuda:
@@ -658,33 +674,36 @@ def _whole(t, name, dtype, numel):
     return t.data_ptr()
 
 
+def _pages(t, name, cfg):
+    """Pointer, page stride and number of pages."""
+    if not t.is_cuda:
+        raise ValueError("%s must be a CUDA tensor" % name)
+    if t.dtype != cfg.cache_dtype:
+        raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, cfg.cache_dtype))
+    n, x, y, D = (*t.shape, 0, 0, 0, 0)[:4]
+    if t.dim() != 4 or (x, y, D) != cfg.page_shape:
+        raise ValueError("%s must be [pages, %d, %d, %d], not %s" % ((name,) + cfg.page_shape + (tuple(t.shape),)))
+    sp, sx, sy, sd = t.stride()
+    if sd != 1 or (sy != D and y > 1) or (sx != y * D and x > 1):
+        raise ValueError("%s: a page must be contiguous" % name)
+    return t.data_ptr(), sp if n > 1 else x * y * D, n
+
+
 def _cache(cfg, k_pages, v_pages, page_table, kv_lens):
     """The tg_cache of a call."""
     import torch
-    for t, name in ((k_pages, "k_pages"), (v_pages, "v_pages")):
-        if not t.is_cuda:
-            raise ValueError("%s must be a CUDA tensor" % name)
-        if t.dtype != cfg.cache_dtype:
-            raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, cfg.cache_dtype))
-        s = t.shape
-        if len(s) != 4 or s[1:] != cfg.page_shape:
-            raise ValueError("%s must be [pages, %d, %d, %d], not %s" % ((name,) + cfg.page_shape + (tuple(s),)))
-        st, inner = t.stride(), cfg.page_shape[1] * cfg.head_dim
-        if st[3] != 1 or (st[2] != cfg.head_dim and s[2] > 1) or (st[1] != inner and s[1] > 1):
-            raise ValueError("%s: a page must be contiguous" % name)
-    pages = k_pages.shape[0]
-    if v_pages.shape[0] != pages:
+    kp, ks, pages = _pages(k_pages, "k_pages", cfg)
+    vp, vs, vpages = _pages(v_pages, "v_pages", cfg)
+    if vpages != pages:
         raise ValueError("k_pages and v_pages must hold the same number of pages")
     if page_table.dtype != torch.int32 or page_table.dim() != 2 or not page_table.is_cuda:
         raise ValueError("page_table must be a CUDA int32 tensor [batch, max_pages]")
     B, most = page_table.shape
-    ts = page_table.stride()
-    if ts[1] != 1 and most > 1:
+    row, one = page_table.stride()
+    if one != 1 and most > 1:
         raise ValueError("page_table: a row must be contiguous")
-    whole = cfg.page_size * inner
-    return tg_cache(k_pages.data_ptr(), v_pages.data_ptr(), k_pages.stride(0) if pages > 1 else whole,
-                    v_pages.stride(0) if pages > 1 else whole, pages, page_table.data_ptr(),
-                    ts[0] if B > 1 else most, most, _whole(kv_lens, "kv_lens", torch.int32, B), B)
+    return tg_cache(kp, vp, ks, vs, pages, page_table.data_ptr(), row if B > 1 else most, most,
+                    _whole(kv_lens, "kv_lens", torch.int32, B), B), B
 
 
 def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, q_out=None,
@@ -694,9 +713,10 @@ def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, c
     k_pages and v_pages [pages, page_size, G, D] or [pages, G, page_size, D] as the config says;
     q_out [T, H, D] and k_out [T, G, D] (or None) take the rotated queries and keys."""
     import torch
-    T, H, G, D = int(k.shape[0]), cfg.num_heads, cfg.num_kv_heads, cfg.head_dim
+    H, G, D = cfg.num_heads, cfg.num_kv_heads, cfg.head_dim
     if k.dim() != 3 or v.dim() != 3 or (q is not None and q.dim() != 3):
         raise ValueError("q, k and v must be [tokens, heads, head_dim]")
+    T = k.shape[0]
     if v.shape[0] != T or (q is not None and q.shape[0] != T):
         raise ValueError("q, k and v must hold the same number of tokens")
     if (q is None) != (q_out is None):
@@ -704,12 +724,13 @@ def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, c
     kp, ks = _head_rows(k, "k", G, cfg)
     vp, vs = _head_rows(v, "v", G, cfg)
     qp, qs = _head_rows(q, "q", H, cfg) if q is not None else (None, 0)
-    cache = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
-    st = load_library().tg_cache_append(
-        qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, cache.batch + 1), T, ctypes.byref(cache),
-        cfg.handle, _whole(q_out, "q_out", cfg.dtype, T * H * D) if q is not None else None,
-        _whole(k_out, "k_out", cfg.dtype, T * G * D) if k_out is not None else None, _stream(stream))
-    _check("tg_cache_append", st)
+    cache, B = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
+    st = _lib.tg_cache_append(
+        qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, B + 1), T, cache, cfg.handle,
+        _whole(q_out, "q_out", cfg.dtype, T * H * D) if q is not None else None,
+        _whole(k_out, "k_out", cfg.dtype, T * G * D) if k_out is not None else None, _raw_stream(stream, k))
+    if st:
+        _check("tg_cache_append", st)
 
 
 def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, out, out_lse=None, stream=None):
@@ -718,15 +739,16 @@ def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, ou
     import torch
     if q.dim() != 4:
         raise ValueError("q must be [batch, n, heads, head_dim]")
-    B, n, H = int(q.shape[0]), int(q.shape[1]), cfg.num_heads
-    cache = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
-    if cache.batch != B:
-        raise ValueError("q holds %d sequences, page_table %d" % (B, cache.batch))
-    qp, qs = _head_rows(q, "q", H, cfg)
-    st = load_library().tg_attend_step(
-        qp, qs, n, ctypes.byref(cache), cfg.handle, _whole(out, "out", cfg.dtype, B * n * H * cfg.head_dim),
-        _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _stream(stream))
-    _check("tg_attend_step", st)
+    B, n, H, D = q.shape
+    cache, rows = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
+    if rows != B:
+        raise ValueError("q holds %d sequences, page_table %d" % (B, rows))
+    qp, qs = _head_rows(q, "q", cfg.num_heads, cfg)
+    st = _lib.tg_attend_step(
+        qp, qs, n, cache, cfg.handle, _whole(out, "out", cfg.dtype, B * n * H * D),
+        _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _raw_stream(stream, q))
+    if st:
+        _check("tg_attend_step", st)
     return out
 
 
@@ -736,21 +758,22 @@ def tg_attend_prompt(q, k, v, q_offsets, kv_offsets, cfg: AttnConfig, out, out_l
     import torch
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [tokens, heads, head_dim]")
-    Tq, Tk, H, G = int(q.shape[0]), int(k.shape[0]), cfg.num_heads, cfg.num_kv_heads
+    Tq, Tk, H, G = q.shape[0], k.shape[0], cfg.num_heads, cfg.num_kv_heads
     if v.shape[0] != Tk:
         raise ValueError("k and v must hold the same number of tokens")
-    B = int(q_offsets.shape[0]) - 1
+    B = q_offsets.numel() - 1
     if B < 0:
         raise ValueError("q_offsets must hold batch + 1 values")
     qp, qs = _head_rows(q, "q", H, cfg)
     kp, ks = _head_rows(k, "k", G, cfg)
     vp, vs = _head_rows(v, "v", G, cfg)
-    st = load_library().tg_attend_prompt(
+    st = _lib.tg_attend_prompt(
         qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, B + 1),
         _whole(kv_offsets, "kv_offsets", torch.int64, B + 1) if kv_offsets is not None else None, B, Tq, Tk,
         1 if causal else 0, cfg.handle, _whole(out, "out", cfg.dtype, Tq * H * cfg.head_dim),
-        _whole(out_lse, "out_lse", torch.float32, Tq * H) if out_lse is not None else None, _stream(stream))
-    _check("tg_attend_prompt", st)
+        _whole(out_lse, "out_lse", torch.float32, Tq * H) if out_lse is not None else None, _raw_stream(stream, q))
+    if st:
+        _check("tg_attend_prompt", st)
     return out
 
 
