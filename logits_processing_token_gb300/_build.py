@@ -16,8 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtg.so")
-SOURCES = ["tg_kernels.cu", "tg_api.cu", "tg_beam.cu", "tg_attn_api.cu", "tg_append.cu", "tg_step.cu", "tg_prompt.cu"]
-HEADERS = ["tg_device.cuh", "tg_select_core.cuh", "tg_attn.cuh", os.path.join("..", "..", "include", "tg.h")]
+SOURCES = ["tg_kernels.cu", "tg_api.cu", "tg_beam.cu", "tg_attn_api.cu", "tg_append.cu", "tg_step.cu", "tg_wide.cu", "tg_prompt.cu"]
+HEADERS = ["tg_device.cuh", "tg_select_core.cuh", "tg_attn.cuh", "tg_mma5.cuh", os.path.join("..", "..", "include", "tg.h")]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2",

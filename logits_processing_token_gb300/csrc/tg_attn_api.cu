@@ -139,7 +139,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   const size_t o_turn = 0, o_ks = up16(o_turn + half * sizeof(unsigned long long)), o_vs = up16(o_ks + d.G * 4),
                o_cnt = up16(o_vs + d.G * 4), o_st = up16(o_cnt + d.step_slots / 2 * 4), o_ml = up16(o_st + 12);
   const size_t rows = static_cast<size_t>(d.step_slots) * d.step_rows;
-  const size_t o_o = up16(o_ml + rows * sizeof(float2)), bytes = o_o + rows * d.D * 4;
+  const size_t o_o = (o_ml + rows * sizeof(float2) + 255) / 256 * 256, bytes = o_o + rows * d.D * 4;  // 32-byte stores
   unsigned char* host = new (std::nothrow) unsigned char[o_ml]();
   if (!host) { delete cfg; return TG_ERR_OUT_OF_MEMORY; }
   for (int i = 0; i < half; ++i) {

@@ -931,10 +931,16 @@ cudaError_t by_type(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStre
 }  // namespace
 
 cudaError_t prepare_step(AttnCfg* c) {
+  const cudaError_t e = prepare_wide(*c);
+  if (e != cudaSuccess) return e;
   return c->D <= 64 ? by_type<64>(c, *c, nullptr, nullptr) : by_type<128>(c, *c, nullptr, nullptr);
 }
 
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
+  // More rows than a group of 16 over a 16-bit cache: the tensor-memory kernel.
+  // Its copies want pages of 8 tokens or more (a swizzled block has 8 rows), and
+  // a token's heads of one key head have to fit its 128 rows.
+  if (a.n * c.rep > 16 && c.ctype != TG_DTYPE_E4M3 && c.page_size >= 8 && c.rep <= 128) return launch_wide(c, a, s);
   return c.D <= 64 ? by_type<64>(nullptr, c, &a, s) : by_type<128>(nullptr, c, &a, s);
 }
 
