@@ -447,7 +447,7 @@ typedef struct tg_attn_params {
   float scale;           /* of the products q.k, > 0; 0 = 1 / sqrt(D) */
   /* Rotation by position (tg_cache_append): pair i of the first rotary_dim
    * elements of each head turns by position * inv_freq[i].  rotary_dim is a
-   * multiple of 16, at most head_dim; 0 = off.  The pair is (i, i +
+   * multiple of 8, at most head_dim; 0 = off.  The pair is (i, i +
    * rotary_dim / 2), or (2i, 2i + 1) when rotary_interleaved is 1. */
   int32_t rotary_dim;
   int32_t rotary_interleaved;
@@ -469,7 +469,7 @@ void tg_attn_params_init(tg_attn_params* p, int32_t num_heads, int32_t num_kv_he
 /* Validate *params and build the handle on the current device; the uploads
  * are enqueued on `stream` and waited for.  Errors: TG_ERR_INVALID_ARGUMENT
  * (a field out of range), TG_ERR_UNSUPPORTED (head_dim above TG_MAX_HEAD_DIM
- * or no multiple of 16, rotary_dim no multiple of 16, a page size that is no
+ * or no multiple of 16, rotary_dim no multiple of 8, a page size that is no
  * power of two), TG_ERR_OUT_OF_MEMORY, TG_ERR_CUDA. */
 tg_status tg_attn_create(const tg_attn_params* params, tg_attn** out, tg_stream stream);
 tg_status tg_attn_destroy(tg_attn* cfg);

@@ -35,35 +35,46 @@ __device__ __forceinline__ int find_seq(const int64_t* off, int batch, long long
   return lo;
 }
 
-struct V8 { uint4 w; };
+// W 16-bit elements of a head, in registers of two.
+template <int W>
+struct alignas(2 * W) Vec { unsigned w[W / 2]; };
 
-template <bool F16>
-__device__ __forceinline__ void widen(const uint4& w, float (&x)[8]) {
-  const unsigned u[4] = {w.x, w.y, w.z, w.w};
+template <bool F16, int W>
+__device__ __forceinline__ void widen(const Vec<W>& v, float (&x)[W]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<F16>(u[i]);
+  for (int i = 0; i < W / 2; ++i) {
+    const float2 f = unpack2<F16>(v.w[i]);
     x[2 * i] = f.x;
     x[2 * i + 1] = f.y;
   }
 }
-template <bool F16>
-__device__ __forceinline__ uint4 narrow(const float (&x)[8]) {
-  return make_uint4(pack2<F16>(x[0], x[1]), pack2<F16>(x[2], x[3]), pack2<F16>(x[4], x[5]), pack2<F16>(x[6], x[7]));
-}
-__device__ __forceinline__ uint2 narrow8(const float (&x)[8], float inv) {
-  unsigned short h[4];
+template <bool F16, int W>
+__device__ __forceinline__ Vec<W> narrow(const float (&x)[W]) {
+  Vec<W> v;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = make_float2(x[2 * i] * inv, x[2 * i + 1] * inv);
-    h[i] = __nv_cvt_float2_to_fp8x2(f, __NV_SATFINITE, __NV_E4M3);
+  for (int i = 0; i < W / 2; ++i) v.w[i] = pack2<F16>(x[2 * i], x[2 * i + 1]);
+  return v;
+}
+// As e4m3, x / scale.
+template <int W>
+struct alignas(W) Vec8 { unsigned w[W / 4]; };
+template <int W>
+__device__ __forceinline__ Vec8<W> narrow8(const float (&x)[W], float inv) {
+  Vec8<W> v;
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const unsigned lo = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i] * inv, x[4 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
+    const unsigned hi = __nv_cvt_float2_to_fp8x2(make_float2(x[4 * i + 2] * inv, x[4 * i + 3] * inv), __NV_SATFINITE, __NV_E4M3);
+    v.w[i] = lo | (hi << 16);
   }
-  return make_uint2(h[0] | (static_cast<unsigned>(h[1]) << 16), h[2] | (static_cast<unsigned>(h[3]) << 16));
+  return v;
 }
 
-// One CTA: tpb tokens.  A unit of work is 16 elements of one head: two
-// 8-element vectors, which for rotated "halves" are the two partners.
-template <bool F16, bool Q8>
+// One CTA: tpb tokens.  A unit of work is 2 W elements of one head: two vectors
+// of W, which for rotated "halves" are the two partners.  W is 8, or 4 where
+// half the rotated width is no multiple of 8 and the partners would straddle
+// 16-byte boundaries.
+template <bool F16, bool Q8, int W>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c, const AppendArgs a, int tpb) {
   __shared__ TokMeta meta[kMaxTok];
   __shared__ float2 cs[kMaxTok][TG_MAX_HEAD_DIM / 2];
@@ -101,10 +112,10 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
   }
   __syncthreads();
 
-  const int per_head = c.D >> 4;
+  const int per_head = c.D / (2 * W);
   const int heads = (a.q ? c.H : 0) + 2 * c.G;
   const int units = heads * per_head;
-  const int rot_units = half >> 3;  // units of a head that turn
+  const int rot_units = half / W;  // units of a head that turn
   for (int i = threadIdx.x; i < nt * units; i += kAppendThreads) {
     const int t = i / units, u = i - t * units;
     const TokMeta m = meta[t];
@@ -120,16 +131,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
     else if (h < c.H + c.G) { kind = 1; head = h - c.H; src = static_cast<const uint16_t*>(a.k) + row * a.ks + static_cast<long long>(head) * c.D; }
     else { kind = 2; head = h - c.H - c.G; src = static_cast<const uint16_t*>(a.v) + row * a.vs + static_cast<long long>(head) * c.D; }
     const bool turn = kind < 2 && part < rot_units;
-    const int e0 = turn && !c.inter ? part * 8 : part * 16;
-    const int e1 = turn && !c.inter ? e0 + half : e0 + 8;
-    const uint4 w0 = *reinterpret_cast<const uint4*>(src + e0), w1 = *reinterpret_cast<const uint4*>(src + e1);
-    float x[8], y[8];
-    widen<F16>(w0, x);
-    widen<F16>(w1, y);
+    const int e0 = turn && !c.inter ? part * W : part * 2 * W;
+    const int e1 = turn && !c.inter ? e0 + half : e0 + W;
+    const Vec<W> w0 = *reinterpret_cast<const Vec<W>*>(src + e0), w1 = *reinterpret_cast<const Vec<W>*>(src + e1);
+    float x[W], y[W];
+    widen<F16, W>(w0, x);
+    widen<F16, W>(w1, y);
     if (turn) {
       if (!c.inter) {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
+        for (int j = 0; j < W; ++j) {
           const float2 r = cs[t][e0 + j];
           const float p = x[j], q = y[j];
           x[j] = p * r.x - q * r.y;
@@ -137,8 +148,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 r = cs[t][(e0 >> 1) + j], r2 = cs[t][(e0 >> 1) + 4 + j];
+        for (int j = 0; j < W / 2; ++j) {
+          const float2 r = cs[t][(e0 >> 1) + j], r2 = cs[t][((e0 + W) >> 1) + j];
           const float p = x[2 * j], q = x[2 * j + 1], p2 = y[2 * j], q2 = y[2 * j + 1];
           x[2 * j] = p * r.x - q * r.y;
           x[2 * j + 1] = q * r.x + p * r.y;
@@ -147,13 +158,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
         }
       }
     }
-    uint4 n0 = w0, n1 = w1;
-    if (turn) { n0 = narrow<F16>(x); n1 = narrow<F16>(y); }
+    Vec<W> n0 = w0, n1 = w1;
+    if (turn) { n0 = narrow<F16, W>(x); n1 = narrow<F16, W>(y); }
     if (kind == 0 || (kind == 1 && a.k_out)) {
       uint16_t* dst = kind == 0 ? static_cast<uint16_t*>(a.q_out) + (row * c.H + head) * c.D
                                 : static_cast<uint16_t*>(a.k_out) + (row * c.G + head) * c.D;
-      *reinterpret_cast<uint4*>(dst + e0) = n0;
-      *reinterpret_cast<uint4*>(dst + e1) = n1;
+      *reinterpret_cast<Vec<W>*>(dst + e0) = n0;
+      *reinterpret_cast<Vec<W>*>(dst + e1) = n1;
     }
     if (kind > 0 && m.page >= 0) {
       const long long at = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride) + m.slot * c.slot_stride +
@@ -162,12 +173,12 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
         const float* sc = kind == 1 ? c.k_scale : c.v_scale;
         const float inv = sc ? 1.0f / sc[head] : 1.0f;
         uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
-        *reinterpret_cast<uint2*>(dst + e0) = narrow8(x, inv);
-        *reinterpret_cast<uint2*>(dst + e1) = narrow8(y, inv);
+        *reinterpret_cast<Vec8<W>*>(dst + e0) = narrow8<W>(x, inv);
+        *reinterpret_cast<Vec8<W>*>(dst + e1) = narrow8<W>(y, inv);
       } else {
         uint16_t* dst = static_cast<uint16_t*>(kind == 1 ? a.c.k : a.c.v) + at;
-        *reinterpret_cast<uint4*>(dst + e0) = n0;
-        *reinterpret_cast<uint4*>(dst + e1) = n1;
+        *reinterpret_cast<Vec<W>*>(dst + e0) = n0;
+        *reinterpret_cast<Vec<W>*>(dst + e1) = n1;
       }
     }
   }
@@ -189,8 +200,11 @@ cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s)
   cfg.attrs = at;
   cfg.numAttrs = 1;
   const bool f16 = c.dtype == TG_DTYPE_F16, q8 = c.ctype == TG_DTYPE_E4M3;
-  auto k = f16 ? (q8 ? append_kernel<true, true> : append_kernel<true, false>)
-               : (q8 ? append_kernel<false, true> : append_kernel<false, false>);
+  const bool narrow = (c.rotary >> 1) % 8 != 0;
+  auto k = narrow ? (f16 ? (q8 ? append_kernel<true, true, 4> : append_kernel<true, false, 4>)
+                         : (q8 ? append_kernel<false, true, 4> : append_kernel<false, false, 4>))
+                  : (f16 ? (q8 ? append_kernel<true, true, 8> : append_kernel<true, false, 8>)
+                         : (q8 ? append_kernel<false, true, 8> : append_kernel<false, false, 8>));
   return cudaLaunchKernelEx(&cfg, k, c, a, tpb);
 }
 

@@ -100,7 +100,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   if (p->max_step_tokens < 0 || p->max_step_tokens > TG_MAX_STEP_TOKENS) return TG_ERR_INVALID_ARGUMENT;
   if ((p->k_scales || p->v_scales) && p->cache_dtype != TG_DTYPE_E4M3) return TG_ERR_INVALID_ARGUMENT;
   if (!positive(p->k_scales, p->num_kv_heads) || !positive(p->v_scales, p->num_kv_heads)) return TG_ERR_INVALID_ARGUMENT;
-  if (p->head_dim > TG_MAX_HEAD_DIM || p->head_dim % 16 || p->rotary_dim % 16 || (p->page_size & (p->page_size - 1)))
+  if (p->head_dim > TG_MAX_HEAD_DIM || p->head_dim % 16 || p->rotary_dim % 8 || (p->page_size & (p->page_size - 1)))
     return TG_ERR_UNSUPPORTED;
   const int half = p->rotary_dim / 2;
   for (int i = 0; i < half; ++i)

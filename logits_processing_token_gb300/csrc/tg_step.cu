@@ -338,6 +338,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 
   // ---- computing warps -----------------------------------------------------
   const int wm = warp % WM, wn = warp / WM;
+  const int slices = c.D >> 4;  // slices that hold data (asked for in 16-bit tiles; in e4m3 ones the question costs 10 %)
   constexpr int NO = T ? KS : KS * 2;
   unsigned qf[KS][T ? 2 : 4];
   float o[NO][4];
@@ -463,6 +464,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           if constexpr (!Q8) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
+              if (k >= slices) break;
               unsigned r[4];
               ldsm4(r, ks + key_at<RB, KT>(row, 2 * k + (lane >> 4)));
               mma16816<MF16>(s[kg], r, qf[k][0], qf[k][1]);
@@ -486,6 +488,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           if constexpr (!Q8) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
+              if (k >= slices) break;
               unsigned r[4];
               ldsm4(r, ks + key_at<RB, KT>(row, 2 * k + ((lane >> 3) & 1)));
               mma16816<MF16>(s[2 * kg], qf[k], r[0], r[1]);
@@ -571,6 +574,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           if constexpr (!Q8) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
+              if (k >= slices) break;
               unsigned r[4];
               ldsm4t(r, vs + key_at<RB, KT>(row, 2 * k + ((lane >> 3) & 1)));
               mma16816<MF16>(o[k], r, b0, b1);
@@ -598,6 +602,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           if constexpr (!Q8) {
 #pragma unroll
             for (int k = 0; k < KS; ++k) {
+              if (k >= slices) break;
               unsigned r[4];
               ldsm4t(r, vs + key_at<RB, KT>(row, 2 * k + (lane >> 4)));
               mma16816<MF16>(o[2 * k], p, r[0], r[1]);
@@ -889,7 +894,8 @@ cudaError_t launch_one(const AttnCfg& c, const StepArgs& a, int variant, cudaStr
     const CUtensorMapSwizzle sw = S::kRB == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B;
     for (int w = 0; w < 2; ++w) {
       const cuuint64_t st[3] = {D * es, D * es * dims[1], static_cast<cuuint64_t>(w ? a.c.v_page_stride : a.c.k_page_stride) * es};
-      if (!encode_map(c.encode, w ? &mv : &mk, type, sw, w ? a.c.v : a.c.k, 4, dims, st, bx)) return cudaErrorInvalidValue;
+      if (!encode_map(c.encode, w ? &mv : &mk, type, sw, w ? a.c.v : a.c.k, 4, dims, st, bx, page_fetch(c, static_cast<int>(es))))
+        return cudaErrorInvalidValue;
     }
   }
   cudaLaunchConfig_t cfg{};
@@ -937,10 +943,11 @@ cudaError_t prepare_step(AttnCfg* c) {
 }
 
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
-  // More rows than a group of 16 over a 16-bit cache: the tensor-memory kernel.
+  // More rows than 8 over a 16-bit cache: the tensor-memory kernel (11 rows over
+  // 32 sequences of 330 to 1,430 keys: 66 us, 72 here; 24 rows: 70 us, 174 here).
   // Its copies want pages of 8 tokens or more (a swizzled block has 8 rows), and
   // a token's heads of one key head have to fit its 128 rows.
-  if (a.n * c.rep > 16 && c.ctype != TG_DTYPE_E4M3 && c.page_size >= 8 && c.rep <= 128) return launch_wide(c, a, s);
+  if (a.n * c.rep > 8 && c.ctype != TG_DTYPE_E4M3 && c.page_size >= 8 && c.rep <= 128) return launch_wide(c, a, s);
   return c.D <= 64 ? by_type<64>(nullptr, c, &a, s) : by_type<128>(nullptr, c, &a, s);
 }
 

@@ -543,7 +543,7 @@ cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
   const cuuint32_t box[4] = {64, token ? 1u : static_cast<cuuint32_t>(ws.box), token ? static_cast<cuuint32_t>(ws.box) : 1u, 1};
   for (int w = 0; w < 2; ++w) {
     const cuuint64_t st[3] = {D * 2, D * 2 * dims[1], static_cast<cuuint64_t>(w ? a->c.v_page_stride : a->c.k_page_stride) * 2};
-    if (!encode_map(c.encode, w ? &mv : &mk, type, CU_TENSOR_MAP_SWIZZLE_128B, w ? a->c.v : a->c.k, 4, dims, st, box))
+    if (!encode_map(c.encode, w ? &mv : &mk, type, CU_TENSOR_MAP_SWIZZLE_128B, w ? a->c.v : a->c.k, 4, dims, st, box, page_fetch(c, 2)))
       return cudaErrorInvalidValue;
   }
   const long long tiles = ((static_cast<long long>(a->c.max_pages) << c.page_shift) + kKeysW - 1) / kKeysW + kItemCostW;

@@ -46,7 +46,7 @@ GOOD = dict(num_heads=8, num_kv_heads=2, head_dim=64)
     (dict(dtype=0), False), (dict(dtype="e4m3"), False), (dict(cache_dtype="f16"), False),
     (dict(page_size=0), False), (dict(page_size=24), True), (dict(page_size=2048), False), (dict(page_layout=2), False),
     (dict(scale=-1.0), False), (dict(scale=float("nan")), False), (dict(scale=float("inf")), False),
-    (dict(rotary_dim=80, inv_freq=[0.1] * 40), False), (dict(rotary_dim=8, inv_freq=[0.1] * 4), True),
+    (dict(rotary_dim=80, inv_freq=[0.1] * 40), False), (dict(rotary_dim=12, inv_freq=[0.1] * 6), True),
     (dict(rotary_dim=32), False), (dict(rotary_dim=32, inv_freq=[float("inf")] * 16), False),
     (dict(rotary_dim=-16), False), (dict(max_step_tokens=33), False), (dict(max_step_tokens=-1), False),
     (dict(k_scales=[1.0, 1.0]), False), (dict(cache_dtype="e4m3", k_scales=[1.0, 0.0]), False),

@@ -14,6 +14,9 @@ CASES = [
     (4, 4, 64, "f16", "f16", 8, "head", 64, True, [3, 0, 17, 1], [3, 5, 40, 1]),
     (4, 1, 128, "bf16", "e4m3", 64, "head", 64, False, [100, 1], [130, 7]),
     (6, 2, 80, "f16", "e4m3", 1, "token", 48, True, [9, 30], [9, 300]),
+    (6, 2, 80, "f16", "f16", 32, "head", 40, False, [9, 30, 1], [9, 300, 70]),
+    (4, 4, 80, "bf16", "e4m3", 16, "token", 40, True, [3, 20], [3, 25]),
+    (3, 1, 16, "bf16", "e4m3", 16, "token", 8, False, [3, 20], [3, 25]),
     (2, 1, 96, "bf16", "bf16", 32, "token", 0, False, [5, 40], [50, 40]),
     (1, 1, 16, "f16", "f16", 2, "head", 16, False, [7], [9]),
     (40, 8, 128, "bf16", "bf16", 16, "token", 128, True, [700, 1, 2000], [700, 90, 5000]),
