@@ -16,6 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtg.so")
+BINDING = os.path.join(BUILD, "tg_binding.so")  # native argument marshalling of the attention calls
+BINDING_SOURCE = "tg_binding.cpp"
 SOURCES = ["tg_kernels.cu", "tg_api.cu", "tg_beam.cu", "tg_attn_api.cu", "tg_append.cu", "tg_step.cu", "tg_wide.cu", "tg_prompt.cu"]
 HEADERS = ["tg_device.cuh", "tg_select_core.cuh", "tg_attn.cuh", "tg_mma5.cuh", os.path.join("..", "..", "include", "tg.h")]
 
@@ -32,11 +34,32 @@ def nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + [os.path.join(CSRC, h) for h in HEADERS]
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
+    deps = [os.path.join(CSRC, s) for s in SOURCES + [BINDING_SOURCE]] + [os.path.join(CSRC, h) for h in HEADERS]
     return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+
+
+def build_binding() -> str:
+    """Compile the marshalling module against the installed PyTorch's headers (host code only)."""
+    import sysconfig
+
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc, lib = os.path.join(base, "include"), os.path.join(base, "lib")
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-fPIC", "-shared", "-std=c++17",
+           "-D_GLIBCXX_USE_CXX11_ABI=%d" % int(torch._C._GLIBCXX_USE_CXX11_ABI)]
+    cmd += ["-I" + d for d in (inc, os.path.join(inc, "torch", "csrc", "api", "include"), os.path.join(cuda, "include"),
+                               sysconfig.get_paths()["include"])]
+    cmd += [os.path.join(CSRC, BINDING_SOURCE), "-o", BINDING + ".tmp", "-L" + lib, "-ltorch_python", "-ltorch_cpu", "-lc10",
+            "-lc10_cuda", "-Wl,-rpath," + lib]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError("the compiler failed for %s:\n%s\n%s" % (BINDING_SOURCE, " ".join(cmd), r.stderr))
+    os.replace(BINDING + ".tmp", BINDING)
+    return BINDING
 
 
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
@@ -55,8 +78,10 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
             raise RuntimeError("nvcc failed for %s:\n%s\n%s" % (src, " ".join(cmd), r.stderr))
         return obj, r.stderr
 
-    with ThreadPoolExecutor(len(SOURCES)) as ex:
+    with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
+        binding = ex.submit(build_binding)
         results = list(ex.map(compile_one, SOURCES))
+        binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             sys.stderr.write(log)

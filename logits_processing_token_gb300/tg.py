@@ -123,6 +123,21 @@ class tg_cache(ctypes.Structure):
 
 
 _lib = None
+_binding = None
+
+
+def _load_binding():
+    """The native marshalling module (built beside libtg.so)."""
+    global _binding
+    if _binding is None:
+        import importlib.util
+        if not os.path.exists(_build.BINDING):
+            raise RuntimeError("tg_binding.so is not built (%s); run __graft_entry__.build()" % _build.BINDING)
+        spec = importlib.util.spec_from_file_location("tg_binding", _build.BINDING)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _binding = module
+    return _binding
 
 
 def library_path() -> str:
@@ -611,9 +626,12 @@ class AttnConfig:
         self.dtype, self.cache_dtype = types[p.dtype], types[p.cache_dtype]
         G, P, D = p.num_kv_heads, p.page_size, p.head_dim
         self.page_shape = (P, G, D) if p.page_layout == TG_PAGES_TOKEN_HEAD else (G, P, D)
+        calls = [ctypes.cast(f, c_void_p).value for f in (lib.tg_cache_append, lib.tg_attend_step, lib.tg_attend_prompt)]
+        self._native = _load_binding().make(h.value, p.num_heads, G, D, *self.page_shape[:2], p.dtype, p.cache_dtype, *calls)
 
     def close(self):
         if self.handle:
+            self._native = None
             load_library().tg_attn_destroy(self.handle)
             self.handle = None
 
@@ -624,19 +642,10 @@ class AttnConfig:
             pass
 
 
-# The attention calls run once or more per layer of a decode step: their checks
-# look at each tensor once and pass plain integers on.
-
-def _raw_stream(stream, t):
-    """The stream's handle: the given one's, or the current one of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    import torch
-    try:
-        return torch._C._cuda_getCurrentRawStream(t.get_device())
-    except AttributeError:
-        return torch.cuda.current_stream().cuda_stream
-
+# The attention calls run once or more per layer of a decode step: the native
+# module (csrc/tg_binding.cpp) checks and passes on a call whose tensors are as
+# they should be.  It returns None for any other, and the checks below then say
+# what is wrong with it.
 
 def _head_rows(t, name, heads, cfg):
     """Pointer and row stride of a [.., heads, D] tensor whose heads are
@@ -712,6 +721,12 @@ def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, c
     q_offsets int64 [B + 1]; kv_lens int32 [B], the new tokens included; page_table int32 [B, max_pages];
     k_pages and v_pages [pages, page_size, G, D] or [pages, G, page_size, D] as the config says;
     q_out [T, H, D] and k_out [T, G, D] (or None) take the rotated queries and keys."""
+    native = getattr(cfg, "_native", None)
+    if native is not None:
+        st = _binding.append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, native, q_out, k_out,
+                             None if stream is None else stream.cuda_stream)
+        if st is not None:
+            return _check("tg_cache_append", st)
     import torch
     H, G, D = cfg.num_heads, cfg.num_kv_heads, cfg.head_dim
     if k.dim() != 3 or v.dim() != 3 or (q is not None and q.dim() != 3):
@@ -728,14 +743,20 @@ def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, c
     st = _lib.tg_cache_append(
         qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, B + 1), T, cache, cfg.handle,
         _whole(q_out, "q_out", cfg.dtype, T * H * D) if q is not None else None,
-        _whole(k_out, "k_out", cfg.dtype, T * G * D) if k_out is not None else None, _raw_stream(stream, k))
-    if st:
-        _check("tg_cache_append", st)
+        _whole(k_out, "k_out", cfg.dtype, T * G * D) if k_out is not None else None, _stream(stream))
+    _check("tg_cache_append", st)
 
 
 def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, out, out_lse=None, stream=None):
     """q and out [B, n, H, D]: the last n tokens of every sequence; out_lse f32 [B, n, H] or None; the cache's
     tensors as tg_cache_append."""
+    native = getattr(cfg, "_native", None)
+    if native is not None:
+        st = _binding.step(q, kv_lens, page_table, k_pages, v_pages, native, out, out_lse,
+                           None if stream is None else stream.cuda_stream)
+        if st is not None:
+            _check("tg_attend_step", st)
+            return out
     import torch
     if q.dim() != 4:
         raise ValueError("q must be [batch, n, heads, head_dim]")
@@ -746,15 +767,21 @@ def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, ou
     qp, qs = _head_rows(q, "q", cfg.num_heads, cfg)
     st = _lib.tg_attend_step(
         qp, qs, n, cache, cfg.handle, _whole(out, "out", cfg.dtype, B * n * H * D),
-        _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _raw_stream(stream, q))
-    if st:
-        _check("tg_attend_step", st)
+        _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _stream(stream))
+    _check("tg_attend_step", st)
     return out
 
 
 def tg_attend_prompt(q, k, v, q_offsets, kv_offsets, cfg: AttnConfig, out, out_lse=None, causal=True, stream=None):
     """q and out [Tq, H, D], k and v [Tk, G, D]: sequences back to back, rows evenly spaced; q_offsets int64
     [B + 1]; kv_offsets int64 [B + 1] or None (as q_offsets); out_lse f32 [Tq, H] or None."""
+    native = getattr(cfg, "_native", None)
+    if native is not None:
+        st = _binding.prompt(q, k, v, q_offsets, kv_offsets, native, out, out_lse, causal,
+                             None if stream is None else stream.cuda_stream)
+        if st is not None:
+            _check("tg_attend_prompt", st)
+            return out
     import torch
     if q.dim() != 3 or k.dim() != 3 or v.dim() != 3:
         raise ValueError("q, k and v must be [tokens, heads, head_dim]")
@@ -771,9 +798,8 @@ def tg_attend_prompt(q, k, v, q_offsets, kv_offsets, cfg: AttnConfig, out, out_l
         qp, qs, kp, ks, vp, vs, _whole(q_offsets, "q_offsets", torch.int64, B + 1),
         _whole(kv_offsets, "kv_offsets", torch.int64, B + 1) if kv_offsets is not None else None, B, Tq, Tk,
         1 if causal else 0, cfg.handle, _whole(out, "out", cfg.dtype, Tq * H * cfg.head_dim),
-        _whole(out_lse, "out_lse", torch.float32, Tq * H) if out_lse is not None else None, _raw_stream(stream, q))
-    if st:
-        _check("tg_attend_prompt", st)
+        _whole(out_lse, "out_lse", torch.float32, Tq * H) if out_lse is not None else None, _stream(stream))
+    _check("tg_attend_prompt", st)
     return out
 
 

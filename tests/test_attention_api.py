@@ -163,3 +163,20 @@ def test_oracle_rotation_pins():
     f = [1.0, 0.3, 0.01, 0.002]
     dots = [float((A.rotate(q, [p + 5], f, False)[0] * A.rotate(k, [p], f, False)[0]).sum()) for p in (0, 17, 400)]
     assert np.allclose(dots, dots[0])
+
+
+def test_native_marshalling_leaves_refusals_to_the_checks():
+    # on tensors that are not on a GPU, or not tensors, the native module makes no call
+    import torch
+    from logits_processing_token_gb300 import tg as T
+    m = T._load_binding()
+    h = m.make(0, 4, 2, 64, 16, 2, tg.TG_DTYPE_BF16, tg.TG_DTYPE_BF16, 0, 0, 0)
+    bf = torch.bfloat16
+    q, kv, pages = torch.zeros(2, 1, 4, 64, dtype=bf), torch.zeros(2, 2, 64, dtype=bf), torch.zeros(3, 16, 2, 64, dtype=bf)
+    table, lens, off = torch.zeros(2, 2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(3, dtype=torch.int64)
+    assert m.step(q, lens, table, pages, pages, h, q, None, None) is None
+    assert m.append(None, kv, kv, off, lens, table, pages, pages, h, None, None, None) is None
+    assert m.prompt(q[0], kv, kv, off, None, h, q[0], None, True, None) is None
+    assert m.step(1, 2, 3, 4, 5, h, 6, 7, 8) is None
+    assert m.step(q, lens, table, pages, pages, "no handle", q, None, None) is None
+    assert m.step(q) is None
