@@ -64,9 +64,10 @@ struct Shape {
   static constexpr int kQRow = DP * 2 + 16;               // a query row, padded against bank conflicts
   static constexpr int kQ = kRows * kQRow;
   static constexpr int kMRow = DP + (kT ? 4 : Q8 ? 16 : 8);        // a row of sums, padded likewise
-  static constexpr int kMerge = WN > 1 ? WM * WN * 8 * kMRow * 4 : 0;
+  static constexpr int kMergeBufs = kT ? 2 : 1;           // (two: no wait before the next item's)
+  static constexpr int kMerge = WN > 1 ? kMergeBufs * WM * WN * 8 * kMRow * 4 : 0;
   static constexpr int kHead = 1024;                      // barriers, metas, scan scratch
-  static constexpr int kML = WN * kRows * 8;
+  static constexpr int kML = kMergeBufs * WN * kRows * 8;
   static constexpr int kFixed = kHead + 2 * kQ + kMerge + kML + 1024;
   // two CTAs on an SM where four warps compute, one where eight do
   static constexpr int kRoom = (kWarps > 4 ? 225 : 112) * 1024;
@@ -350,6 +351,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   Unit cur;
   int qs = 0;
   unsigned q_ph = 0, meet_ph = 0;
+  int buf = 0;  // merge buffer of the next item (T)
   bool ok = true;
   // All computing warps past this point.
   const auto meet = [&]() {
@@ -435,7 +437,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     // 0 x NaN is not 0: zero them.
     const int have = min(KW, cur.len - base);
     if (have < KW || cur.any_bad) {
-      for (int i = lane; i < KW * CPR; i += 32) {
+      for (int i = (cur.any_bad ? 0 : have * CPR) + lane; i < KW * CPR; i += 32) {
         const int r = i / CPR, x = wn * KW + r;
         if (r >= have || ((bad[x >> 5] >> (x & 31)) & 1))
           *reinterpret_cast<uint4*>(stage + S::kMat + key_at<RB, KT>(x, i % CPR)) = make_uint4(0, 0, 0, 0);
@@ -671,39 +673,39 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       }
     }
     if constexpr (WN > 1) {
+      float2* const ml = wml + buf * WN * S::kRows;
+      float* const sums = merge + buf * WM * WN * 8 * S::kMRow;
       if (T ? lane < 4 : (lane & 3) == 0) {
-        wml[wn * S::kRows + r0] = make_float2(m[0], l[0]);
-        wml[wn * S::kRows + r0 + RSTEP] = make_float2(m[1], l[1]);
+        ml[wn * S::kRows + r0] = make_float2(m[0], l[0]);
+        ml[wn * S::kRows + r0 + RSTEP] = make_float2(m[1], l[1]);
       }
-      if (!meet()) return;
+      if constexpr (!T) {
+        if (!meet()) return;
+      }
       for (int h = 0; h < 2; ++h) {  // rows 0 .. 7 of every group, then 8 .. 15
         if (8 * h >= nrow) break;    // (uniform: later groups exist only when earlier ones are full)
-        // merge: [warp][8 rows][kMRow], scaled to the common maximum
+        // sums: [warp][8 rows][kMRow]
         if constexpr (T) {
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
-            float mm = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < WN; ++w) mm = fmaxf(mm, wml[w * S::kRows + r0 + x].x);
-            const float f = m[x] == -INFINITY ? 0.0f : ex2(m[x] - mm);
-            float* mp = merge + (warp * 8 + r0 + x) * S::kMRow;
+            float* mp = sums + (warp * 8 + r0 + x) * S::kMRow;
 #pragma unroll
             for (int k = 0; k < NO; ++k) {
               if constexpr (Q8) {
-                *reinterpret_cast<float2*>(mp + 16 * k + 2 * (lane >> 2)) = make_float2(f * o[k][x], f * o[k][2 + x]);
+                *reinterpret_cast<float2*>(mp + 16 * k + 2 * (lane >> 2)) = make_float2(o[k][x], o[k][2 + x]);
               } else {
-                mp[16 * k + (lane >> 2)] = f * o[k][x];
-                mp[16 * k + 8 + (lane >> 2)] = f * o[k][2 + x];
+                mp[16 * k + (lane >> 2)] = o[k][x];
+                mp[16 * k + 8 + (lane >> 2)] = o[k][2 + x];
               }
             }
           }
         } else {
           float mm = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < WN; ++w) mm = fmaxf(mm, wml[w * S::kRows + r0 + 8 * h].x);
+          for (int w = 0; w < WN; ++w) mm = fmaxf(mm, ml[w * S::kRows + r0 + 8 * h].x);
           const float mh = h ? m[1] : m[0];
           const float f = mh == -INFINITY ? 0.0f : ex2(mh - mm);
-          float* mp = merge + (warp * 8 + (lane >> 2)) * S::kMRow;
+          float* mp = sums + (warp * 8 + (lane >> 2)) * S::kMRow;
 #pragma unroll
           for (int k = 0; k < NO; k += Q8 ? 2 : 1) {
             const float x0 = f * (h ? o[k][2] : o[k][0]), x1 = f * (h ? o[k][3] : o[k][1]);
@@ -723,16 +725,17 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           float4 acc = make_float4(0, 0, 0, 0);
           float top = -INFINITY, ll = 0.0f;
 #pragma unroll
-          for (int w = 0; w < WN; ++w) top = fmaxf(top, wml[w * S::kRows + r].x);
+          for (int w = 0; w < WN; ++w) top = fmaxf(top, ml[w * S::kRows + r].x);
 #pragma unroll
           for (int w = 0; w < WN; ++w) {  // a fixed order
-            const float2 y = wml[w * S::kRows + r];
-            ll += y.x == -INFINITY ? 0.0f : y.y * ex2(y.x - top);
-            const float4 v = *reinterpret_cast<const float4*>(merge + ((w * WM + grp) * 8 + (rr & 7)) * S::kMRow + d);
-            acc.x += v.x;
-            acc.y += v.y;
-            acc.z += v.z;
-            acc.w += v.w;
+            const float2 y = ml[w * S::kRows + r];
+            const float e = y.x == -INFINITY ? 0.0f : ex2(y.x - top), g = T ? e : 1.0f;  // (not T: scaled above)
+            ll += y.y * e;
+            const float4 v = *reinterpret_cast<const float4*>(sums + ((w * WM + grp) * 8 + (rr & 7)) * S::kMRow + d);
+            acc.x = fmaf(g, v.x, acc.x);
+            acc.y = fmaf(g, v.y, acc.y);
+            acc.z = fmaf(g, v.z, acc.z);
+            acc.w = fmaf(g, v.w, acc.w);
           }
           if (whole) {
             const float ff = factor(ll, vs);
@@ -744,8 +747,13 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             if (d == 0) pml[r] = make_float2(top, ll);
           }
         }
-        if (!meet()) return;
+        if constexpr (!T) {
+          if (!meet()) return;
+        }
       }
+      // The buffer after next is this one again: by then every warp has passed
+      // the next item's meeting, and so has read what it had to.
+      if constexpr (T) buf ^= 1;
     } else {
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -792,7 +800,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         const int r = i / (c.D >> 2), d = (i - r * (c.D >> 2)) * 4;
         float4 acc = make_float4(0, 0, 0, 0);
         float mm = -INFINITY, ll = 0.0f;
-        constexpr int PB = 16;  // parts whose reads are in flight
+        constexpr int PB = 8;  // parts whose reads are in flight
         for (int p0 = 0; p0 < parts; p0 += PB) {
           float2 x[PB];
           float4 v[PB];
