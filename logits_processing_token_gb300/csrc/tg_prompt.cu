@@ -17,8 +17,9 @@
 //   warps 0-3, 4-7   softmax of tile 0 and 1: one thread per row
 //   warp 8           issues the matrix instructions
 //   warp 9           takes items off a counter and issues the copies
-//   warps 10, 11     fill up the third group: it hands its registers to the
-//                    softmax, 256 x 208 + 128 x 88 = 384 x 168 as launched
+//   warps 10, 11     fill up the third group, which hands registers to the
+//                    softmax: 256 x 192 + 256 x 64 = 512 x 128 as launched
+//   warps 12-15      write the results, while the softmax is at the next item
 // Tensor memory: S0, S1 (128 columns each; P overwrites S as 16-bit pairs),
 // O0, O1 (128 columns each): all 512.
 #include <algorithm>
@@ -30,7 +31,7 @@ namespace {
 
 constexpr int kRowsT = 128;                 // rows of a tile
 constexpr int kKeys = 128;                  // keys of a tile
-constexpr int kThreadsP = 384;
+constexpr int kThreadsP = 512;
 
 struct Item {
   long long q_base, k_base;  // first packed rows of the sequence
@@ -44,11 +45,12 @@ struct Item {
 
 constexpr int kMaxSlots = 10;
 struct Bars {
-  unsigned long long q_full, q_empty, kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], p_full[2], o_full[2],
+  unsigned long long q_full, q_empty, kv_full[kMaxSlots], kv_empty[kMaxSlots], s_full[2], p_full[2], o_full[2], o_empty[2], l_full[2],
       item_full[2], item_empty[2], drain;
   unsigned tmem;
   int dead;
   Item item[2];
+  float inv[2][kRowsT];  // 1 / l of the rows, 0 where no key was seen
 };
 
 template <int DP>
@@ -84,7 +86,9 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       bar_init(&s->p_full[t], 4);
       bar_init(&s->o_full[t], 1);
       bar_init(&s->item_full[t], 1);
-      bar_init(&s->item_empty[t], 9);
+      bar_init(&s->o_empty[t], 4);
+      bar_init(&s->l_full[t], 4);
+      bar_init(&s->item_empty[t], 13);
     }
     bar_init(&s->drain, 1);
     s->dead = 0;
@@ -103,7 +107,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
 
   if (warp == 9) {
     // ---- items and copies -------------------------------------------------
-    fewer_registers();
+    registers_down<64>();
     const int64_t* ko = a.koff ? a.koff : a.qoff;
     int b0 = 0;               // sequences b0 .. b0 + 31 are looked at
     long long base = 0;       // items before sequence b0
@@ -219,14 +223,14 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     }
   } else if (warp == 8) {
     // ---- matrix instructions ----------------------------------------------
-    fewer_registers();
+    registers_down<64>();
     const unsigned fmt = F16 ? 0u : 1u;
     const unsigned id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | (8u << 24);
     const unsigned id_pv = id0 | (1u << 16) | (static_cast<unsigned>(c.D >> 3) << 17);
     const int ks = c.D >> 4;
     const unsigned q0 = sptr(smem), kv0 = sptr(smem + L::kKv);
     int slot = 0, it_n = 0;
-    unsigned kv_ph = 0, q_ph = 0, p_ph[2] = {0, 0};
+    unsigned kv_ph = 0, q_ph = 0, p_ph[2] = {0, 0}, e_ph[2] = {1, 1};
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
@@ -311,6 +315,11 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
             ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c.status);
             if (!ok) break;
             p_ph[t] ^= 1;
+            if (j == 0) {  // the sums of the item before have been read
+              ok = bar_wait(&s->dead, &s->o_empty[t], e_ph[t], c.status);
+              if (!ok) break;
+              e_ph[t] ^= 1;
+            }
             fence_after();
             pv(t, j, vaddr);
           }
@@ -344,7 +353,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: one thread per row --------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 192;");
     const int t = warp >> 2;
     const int row = t * kRowsT + (tid & 127);
     const unsigned lanes = static_cast<unsigned>(warp & 3) << 21;  // this warp's lanes of tensor memory
@@ -352,7 +361,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     const float sc = c.scale * kLog2E;
     constexpr float bias = kWeightBias<F16>;
     int it_n = 0;
-    unsigned s_ph = 0, o_ph = 0;
+    unsigned s_ph = 0, e_ph = 1;
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
@@ -381,12 +390,14 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
 #pragma unroll
         for (int x = 0; x < 4; ++x) tm_pin(v[x]);
         if (j * kKeys + kKeys > lim_w) {
-          const int rest = lim - j * kKeys;
+          const int rest = lim - j * kKeys;  // of the tile's keys, as bits per 32 (5 % of a short item over comparing each)
 #pragma unroll
-          for (int x = 0; x < 4; ++x)
+          for (int x = 0; x < 4; ++x) {
+            const unsigned off = rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x);
 #pragma unroll
             for (int y = 0; y < 32; ++y)
-              if (x * 32 + y >= rest) v[x][y] = 0xff800000u;  // -infinity
+              if (off & (1u << y)) v[x][y] = 0xff800000u;  // -infinity
+          }
         }
         softmax_tile<F16>(v, ts, to, c.D, sc, j > 0, m, l);
         tm_wait_st();
@@ -395,41 +406,82 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         if (lane == 0) bar_arrive(&s->p_full[t]);
       }
       if (!ok) break;
-      const bool mine = i < it.m_len;
-      const long long at = (it.q_base + i) * c.H + head;
+      if (i < it.m_len && a.lse)
+        a.lse[(it.q_base + i) * c.H + head] = l == 0.0f ? -INFINITY : (m + log2f(l) - bias) * kLn2;
       if (n > 0) {
-        ok = bar_wait(&s->dead, &s->o_full[t], o_ph, c.status);
+        // (the factors of the item before have been read when its sums have)
+        ok = bar_wait(&s->dead, &s->o_empty[t], e_ph, c.status);
         if (!ok) break;
-        o_ph ^= 1;
-        fence_after();
+        e_ph ^= 1;
+        s->inv[t][tid & 127] = l == 0.0f ? 0.0f : 1.0f / l;
+        __syncwarp();
+        if (lane == 0) bar_arrive(&s->l_full[t]);
       }
-      const float f = l > 0.0f || l != l ? 1.0f / l : 0.0f;
-      for (int x = 0; x < c.D; x += 16) {
-        unsigned o[16];
+    }
+  } else if (warp >= 12) {
+    // ---- results: one thread per row of each tile in turn --------------------
+    registers_down<64>();
+    const unsigned lanes = static_cast<unsigned>(warp & 3) << 21;
+    int it_n = 0;
+    unsigned o_ph[2] = {0, 0};
+    bool ok = true;
+    while (ok) {
+      const int is = it_n & 1;
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      if (!ok) break;
+      const Item* it = &s->item[is];
+      const int valid = it->valid, n0 = it->n[0], n1 = it->n[1], i0 = it->i0, m_len = it->m_len, hg = it->hg;
+      const long long q_base = it->q_base;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (!valid) break;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int n = t ? n1 : n0, row = t * kRowsT + (tid & 127);
+        const int i = i0 + (row >> ps.pack_shift), head = (hg << ps.pack_shift) + (row & (ps.pack - 1));
+        const bool mine = i < m_len;
+        const unsigned to = tmem + lanes + 256 + t * 128;
+        float f = 0.0f;
         if (n > 0) {
-          tm_ld16(o, to + x);
+          ok = bar_wait(&s->dead, &s->l_full[t], o_ph[t], c.status) && bar_wait(&s->dead, &s->o_full[t], o_ph[t], c.status);
+          if (!ok) break;
+          o_ph[t] ^= 1;
+          fence_after();
+          f = s->inv[t][tid & 127];
+        }
+        uint16_t* dst = static_cast<uint16_t*>(a.out) + ((q_base + i) * c.H + head) * c.D;
+#pragma unroll 1
+        for (int x = 0; x < c.D; x += 32) {
+          unsigned o[32];  // columns past the head size are read and not used
+          tm_ld32(o, to + x);
           tm_wait_ld();
           tm_pin(o);
-        }
-        if (mine) {
-          unsigned w[8];
+          if (!mine) continue;
 #pragma unroll
-          for (int y = 0; y < 8; ++y)
-            w[y] = l == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
-          uint16_t* dst = static_cast<uint16_t*>(a.out) + at * c.D + x;
-          if (ps.wide) {
-            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), TG_I8(w, 0) : "memory");
-          } else {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          for (int h = 0; h < 2; ++h) {
+            if (x + 16 * h >= c.D) break;
+            unsigned w[8];
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              w[y] = f == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[16 * h + 2 * y]) * f, __uint_as_float(o[16 * h + 2 * y + 1]) * f);
+            if (ps.wide) {
+              asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + x + 16 * h), TG_I8(w, 0) : "memory");
+            } else {
+              reinterpret_cast<uint4*>(dst + x + 16 * h)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+              reinterpret_cast<uint4*>(dst + x + 16 * h)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+            }
           }
         }
+        if (n > 0) {
+          fence_before();  // the reads of O come before the next item's products
+          __syncwarp();
+          if (lane == 0) bar_arrive(&s->o_empty[t]);
+        }
       }
-      if (mine && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l) - bias) * kLn2;
-      fence_before();  // the reads of O come before the next item's products
     }
   } else {
-    fewer_registers();
+    registers_down<64>();
   }
   fence_before();
   __syncthreads();

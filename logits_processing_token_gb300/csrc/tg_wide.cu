@@ -143,7 +143,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
 
   if (warp == 9) {
     // ---- items, pages and copies --------------------------------------------
-    fewer_registers();
+    registers_down<88>();
     int b = s->first_b, len = s->first_len, nt = tiles_of(len);
     const int skip = static_cast<int>(s->first_in / cost(len));
     int rt = skip % ws.row_tiles, pr = skip / ws.row_tiles;
@@ -243,7 +243,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     }
   } else if (warp == 8) {
     // ---- matrix instructions ----------------------------------------------
-    fewer_registers();
+    registers_down<88>();
     const unsigned fmt = F16 ? 0u : 1u;
     const unsigned id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | (8u << 24);
     const unsigned id_pv = id0 | (1u << 16) | (static_cast<unsigned>(c.D >> 3) << 17);
@@ -523,7 +523,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
     }
   } else {
-    fewer_registers();
+    registers_down<88>();
   }
   fence_before();
   __syncthreads();
