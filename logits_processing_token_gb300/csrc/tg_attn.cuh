@@ -93,7 +93,7 @@ cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s)
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
 cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, 16-bit cache
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
-// CTAs of the step kernel per SM at most: sizes the handle's workspace.
+// CTAs of the step kernel per SM at most (they size the handle's workspace).
 constexpr int kStepCtasPerSm = 4;
 
 // A tensor map of `rank` dimensions (innermost first; strides in bytes from

@@ -131,9 +131,10 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   if (e == cudaSuccess) e = tg::prepare_prompt(&d);
   if (e == cudaSuccess) e = tg::prepare_step(&d);
   if (e != cudaSuccess) { delete cfg; return from_cuda(e); }
-  // two slots per CTA of a step: the sequence it begins inside and the one it ends inside
+  // two slots per CTA of a step: the item it begins inside and the one it ends
+  // inside (the wide kernel: one CTA per SM, two items side by side)
   d.step_rows = std::min(128, (d.max_n * d.rep + 15) / 16 * 16);
-  d.step_slots = 2 * tg::kStepCtasPerSm * d.nsm;
+  d.step_slots = 2 * d.nsm * std::max(2, *std::max_element(d.step_ctas, d.step_ctas + 5));
 
   // [turns][k scales][v scales][counts][status, prompt counts] are uploaded; then the workspace
   const size_t o_turn = 0, o_ks = up16(o_turn + half * sizeof(unsigned long long)), o_vs = up16(o_ks + d.G * 4),
