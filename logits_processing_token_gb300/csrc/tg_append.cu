@@ -116,11 +116,13 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
   const int heads = (a.q ? c.H : 0) + 2 * c.G;
   const int units = heads * per_head;
   const int rot_units = half / W;  // units of a head that turn
-  for (int i = threadIdx.x; i < nt * units; i += kAppendThreads) {
-    const int t = i / units, u = i - t * units;
+  const unsigned inv_head = (1u << 20) / per_head + 1;  // u / per_head for u < 2^20 / per_head
+  for (int t = 0, u = threadIdx.x;; u += kAppendThreads) {
+    while (u >= units) { u -= units; ++t; }
+    if (t >= nt) break;
     const TokMeta m = meta[t];
     if (!m.ok) continue;
-    int h = u / per_head;
+    int h = static_cast<int>((u * inv_head) >> 20);
     const int part = u - h * per_head;
     const long long row = t0 + t;
     // q heads, then key heads, then value heads
@@ -170,8 +172,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
       const long long at = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride) + m.slot * c.slot_stride +
                            head * c.head_stride;
       if constexpr (Q8) {
-        const float* sc = kind == 1 ? c.k_scale : c.v_scale;
-        const float inv = sc ? 1.0f / sc[head] : 1.0f;
+        const float* sc = kind == 1 ? c.k_inv : c.v_inv;
+        const float inv = sc ? sc[head] : 1.0f;
         uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
         *reinterpret_cast<Vec8<W>*>(dst + e0) = narrow8<W>(x, inv);
         *reinterpret_cast<Vec8<W>*>(dst + e1) = narrow8<W>(y, inv);

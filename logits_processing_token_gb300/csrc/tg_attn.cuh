@@ -32,6 +32,8 @@ struct AttnCfg {
   const unsigned long long* turns;  // [rotary / 2]: 2^64 * fraction of a turn per position
   const float* k_scale;    // [G], or null
   const float* v_scale;
+  const float* k_inv;      // their reciprocals
+  const float* v_inv;
   unsigned* status;
   int max_n;               // largest n of a step
   int step_rows;           // rows of a workspace slot

@@ -951,11 +951,12 @@ cudaError_t prepare_step(AttnCfg* c) {
 }
 
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
-  // More rows than 8 over a 16-bit cache: the tensor-memory kernel (11 rows over
-  // 32 sequences of 330 to 1,430 keys: 66 us, 72 here; 24 rows: 70 us, 174 here).
+  // More rows than 16 over a 16-bit cache: the tensor-memory kernel (24 rows over
+  // 32 sequences: 70 us, 174 here; 11 rows: 66 us, 72 here, but 10 rows over 5
+  // short sequences 24 us, 12 here).
   // Its copies want pages of 8 tokens or more (a swizzled block has 8 rows), and
   // a token's heads of one key head have to fit its 128 rows.
-  if (a.n * c.rep > 8 && c.ctype != TG_DTYPE_E4M3 && c.page_size >= 8 && c.rep <= 128) return launch_wide(c, a, s);
+  if (a.n * c.rep > 16 && c.ctype != TG_DTYPE_E4M3 && c.page_size >= 8 && c.rep <= 128) return launch_wide(c, a, s);
   return c.D <= 64 ? by_type<64>(nullptr, c, &a, s) : by_type<128>(nullptr, c, &a, s);
 }
 
