@@ -15,7 +15,7 @@ namespace tg {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kMaxTok = 8;  // tokens per CTA at most
+constexpr int kMaxTok = 4;  // tokens per CTA at most (7,300 into an e4m3 cache: 23.9 us, 27.7 at 8; 13,800 in bf16: the same)
 
 struct TokMeta {
   int ok;          // the token belongs to a sequence and has a position
