@@ -294,11 +294,11 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           if (!ok) break;
           // Values of keys that do not exist are what the page or an earlier tile
           // holds; their weights are 0, but 0 x NaN is not: zero what is read.
-          const int end = len - j * kKeysW;
+          const int end = max(0, len - j * kKeysW);
           const unsigned any_bad = s->bad[meta][0] | s->bad[meta][1] | s->bad[meta][2] | s->bad[meta][3];
           if (end < kKeysW || any_bad) {
             const int stop = width(j);
-            for (int i = lane; i < stop * (DP / 8); i += 32) {
+            for (int i = (any_bad ? 0 : end * (DP / 8)) + lane; i < stop * (DP / 8); i += 32) {
               const int r = i / (DP / 8), x = i % (DP / 8);
               if (r >= end || ((s->bad[meta][r >> 5] >> (r & 31)) & 1))
                 *reinterpret_cast<uint4*>(smem + L::kKv + vs * L::kTileB + (x >> 3) * kBlock + r * 128 + (x & 7) * 16) =
