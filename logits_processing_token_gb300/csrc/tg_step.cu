@@ -16,6 +16,12 @@
 // last joins them in CTA order: one launch, and the result does not depend on
 // which was last.
 //
+// The copies bound it: 64 sequences of 0 to 4,096 keys (32 heads over 8, D 128,
+// bf16) 91.5 us, 5.9 TB/s, 87 % of the measured copy rate; 256 of 1 to 2,048 keys
+// in e4m3 100 us, 84 %; 5 of 20,000 to 40,000 keys of 16 heads of 64 113 us, 95 %.
+// One sequence of 4,001 keys takes 11.8 us: look-ups 3, two tiles 2, the part's
+// end 2, the join of 32 parts 3.
+//
 // One warp looks up pages and issues the copies, a page's rows of one head at
 // a time, into a ring of stages; the other warps wait for a stage, take 16
 // rows and their share of its keys, and hand it back.
