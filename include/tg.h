@@ -558,8 +558,11 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
  *  out, out_lse [q_tokens, H, D] contiguous and f32 [q_tokens, H] or NULL.
  *
  * A query that sees no key gives 0 and -infinity.  A sequence whose offsets
- * decrease or leave the tensors is skipped (TG_FLAG_BAD_ROW), as are queries
- * of no sequence.  Numerics as tg_attend_step.
+ * decrease or leave the tensors is skipped (TG_FLAG_BAD_ROW), its outputs left
+ * as they were, as are those of queries of no sequence.  What other sequences
+ * hold never reaches this one's results; a non-finite value that only later
+ * queries of the same sequence see may reach earlier ones (0 x NaN).  Numerics
+ * as tg_attend_step.
  */
 tg_status tg_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                            int64_t v_stride, const int64_t* q_offsets, const int64_t* kv_offsets, int32_t batch,

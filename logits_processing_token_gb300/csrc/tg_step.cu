@@ -46,6 +46,10 @@ struct UnitMeta {
 // Beginning and ending an item, in units (measured on 256 sequences of 1 to
 // 2,048 keys in e4m3: 140 us at 0, 110 at 1, 104 at 2).
 constexpr int kItemCost = 2;
+// CTAs per item at most, on average: more of them read faster and make the join
+// longer (one sequence of 100,000 keys of one head: 71 us at 304, 40 at 64, 45 at
+// 48; two of 12,000: 17, 15, 15).
+constexpr int kMostParts = 64;
 
 // Up to 8 rows (a decode step) the products are taken the other way round,
 // S^T = K Q^T and O^T = V^T P^T: the instruction's 16 rows are keys or head
@@ -181,7 +185,8 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   }
   before -= mine;  // units of one (head, row tile) of the sequences before this thread's
   const long long U = total * per_tile;
-  const long long N = min(static_cast<long long>(gridDim.x), max(1ll, U / min_units));
+  long long N = min(static_cast<long long>(gridDim.x), max(1ll, U / min_units));
+  N = min(N, static_cast<long long>(kMostParts) * a.c.batch * per_tile);
   if (blockIdx.x >= N) return;
   const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
   if (mine > 0 && before * per_tile <= u0 && u0 < (before + mine) * per_tile) {
