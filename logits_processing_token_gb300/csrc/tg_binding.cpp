@@ -61,12 +61,11 @@ inline int64_t rows(const at::Tensor* t, int64_t dims, int64_t heads, const Hand
   const auto s = t->sizes(), st = t->strides();
   const int64_t n = dims;
   if (s[n - 2] != heads || s[n - 1] != h->D || st[n - 1] != 1 || (heads > 1 && st[n - 2] != h->D)) return -1;
-  int64_t row = s[n - 3] > 1 ? st[n - 3] : 0;
-  if (dims == 4) {
-    if (row == 0) row = s[0] > 1 ? st[0] : 0;
-    else if (s[0] > 1 && st[0] != row * s[1]) return -1;
-  }
-  return row ? row : heads * h->D;
+  const int64_t inner = s[n - 3], outer = dims == 4 ? s[0] : 1;
+  if (inner == 0 || outer == 0 || (inner == 1 && outer == 1)) return heads * h->D;  // no row, or one
+  const int64_t row = inner > 1 ? st[n - 3] : st[0];
+  if (row == 0 || (inner > 1 && outer > 1 && st[0] != row * inner)) return -1;  // a broadcast row, or two spacings
+  return row;
 }
 
 inline bool whole(const at::Tensor* t, at::ScalarType type, int64_t numel) {

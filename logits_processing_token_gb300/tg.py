@@ -661,13 +661,14 @@ def _head_rows(t, name, heads, cfg):
         raise ValueError("%s must end in [%d, %d], not %s" % (name, heads, D, (h, d)))
     if sd != 1 or (sh != D and heads > 1):
         raise ValueError("%s: a row's heads must be contiguous" % name)
-    row = rows[-1] if lead[-1] > 1 else 0
-    if len(lead) == 2:  # [batch, n, heads, D]: one spacing for all rows
-        if row == 0:
-            row = rows[0] if lead[0] > 1 else 0
-        elif lead[0] > 1 and rows[0] != row * lead[1]:
-            raise ValueError("%s: its rows must be evenly spaced" % name)
-    return t.data_ptr(), row or heads * D
+    if min(lead) == 0 or max(lead) == 1:
+        return t.data_ptr(), heads * D  # no row, or one
+    row = rows[-1] if lead[-1] > 1 else rows[0]
+    if row == 0:
+        raise ValueError("%s: its rows are one broadcast row" % name)
+    if len(lead) == 2 and min(lead) > 1 and rows[0] != row * lead[1]:  # [batch, n, heads, D]: one spacing for all rows
+        raise ValueError("%s: its rows must be evenly spaced" % name)
+    return t.data_ptr(), row
 
 
 def _whole(t, name, dtype, numel):

@@ -180,3 +180,35 @@ def test_native_marshalling_leaves_refusals_to_the_checks():
     assert m.step(1, 2, 3, 4, 5, h, 6, 7, 8) is None
     assert m.step(q, lens, table, pages, pages, "no handle", q, None, None) is None
     assert m.step(q) is None
+
+
+def test_binding_refuses_broadcast_rows():
+    # a stride of 0 between rows: one row in memory, however many the shape says
+    import torch
+    cfg, F = _fake_cfg(), _FakeCuda
+    bf, i32 = torch.bfloat16, torch.int32
+    z = lambda *s: torch.zeros(*s, dtype=bf)  # noqa: E731
+    pages, table, lens = F(z(3, 16, 2, 64)), F(torch.zeros(3, 2, dtype=i32)), F(torch.zeros(3, dtype=i32))
+    off = F(torch.zeros(4, dtype=torch.int64))
+    q, kv = z(5, 4, 64), z(5, 2, 64)
+    good = dict(q=q, k=kv, v=kv)
+    for name, x in (("q", z(1, 4, 64).expand(5, 4, 64)), ("k", z(1, 2, 64).expand(5, 2, 64)), ("v", z(1, 2, 64).expand(5, 2, 64))):
+        t = {n: F(x if n == name else y) for n, y in good.items()}
+        with pytest.raises(ValueError, match="%s: its rows are one broadcast row" % name):
+            tg.tg_cache_append(t["q"], t["k"], t["v"], off, lens, table, pages, pages, cfg, F(q))
+        with pytest.raises(ValueError, match="%s: its rows are one broadcast row" % name):
+            tg.tg_attend_prompt(t["q"], t["k"], t["v"], off, None, cfg, F(q))
+    for x in (z(3, 1, 4, 64).expand(3, 17, 4, 64), z(1, 1, 4, 64).expand(3, 1, 4, 64), z(1, 1, 4, 64).expand(3, 5, 4, 64)):
+        with pytest.raises(ValueError, match="q: its rows are one broadcast row"):
+            tg.tg_attend_step(F(x), lens, table, pages, pages, cfg, F(z(*x.shape)))
+    # the rows of a sequence broadcast over the batch have two spacings
+    with pytest.raises(ValueError, match="evenly"):
+        tg.tg_attend_step(F(z(1, 5, 4, 64).expand(3, 5, 4, 64)), lens, table, pages, pages, cfg, F(z(3, 5, 4, 64)))
+    # one row alone has no spacing, whatever its strides say
+    rows = lambda x, heads: tg.tg._head_rows(F(x), "x", heads, cfg)[1]  # noqa: E731
+    with pytest.raises(ValueError, match="x: its rows are one broadcast row"):
+        rows(z(1, 1, 4, 64).expand(1, 5, 4, 64), 4)
+    assert rows(z(1, 4, 64).as_strided((1, 4, 64), (0, 64, 1)), 4) == 256
+    assert rows(z(1, 1, 4, 64).as_strided((1, 1, 4, 64), (0, 0, 64, 1)), 4) == 256
+    assert rows(z(0, 5, 4, 64), 4) == 256 and rows(z(3, 5, 4, 64), 4) == 256
+    assert rows(z(6, 6, 64)[::2, :4], 4) == 768 and rows(z(3, 1, 6, 64)[:, :, :4], 4) == 384

@@ -71,3 +71,25 @@ def test_a_closed_handle_is_refused(make):
     cfg.close()
     with pytest.raises(tg.TGError, match="INVALID_ARGUMENT"):
         tg.tg_attend_step(a["q"], a["lens"], a["table"], a["kp"], a["vp"], cfg, a["out"])
+
+
+def test_broadcast_rows_are_refused(make):
+    # one row in memory under a shape of many: nothing is launched
+    tg, torch, cfg, z, a = make
+    q, kv, off = z(5, 4, 64), z(5, 2, 64), torch.tensor([0, 2, 5], device="cuda")
+    out = z(5, 4, 64) + 7
+    wide = {"q": z(1, 4, 64).expand(5, 4, 64), "k": z(1, 2, 64).expand(5, 2, 64), "v": z(1, 2, 64).expand(5, 2, 64)}
+    for name, x in wide.items():
+        t = {"q": q, "k": kv, "v": kv, name: x}
+        with pytest.raises(ValueError, match="%s: its rows are one broadcast row" % name):
+            tg.tg_attend_prompt(t["q"], t["k"], t["v"], off, None, cfg, out)
+        with pytest.raises(ValueError, match="%s: its rows are one broadcast row" % name):
+            tg.tg_cache_append(t["q"], t["k"], t["v"], off, a["lens"], a["table"], a["kp"], a["vp"], cfg, out)
+    for x in (z(2, 1, 4, 64).expand(2, 3, 4, 64), z(1, 1, 4, 64).expand(2, 1, 4, 64), z(1, 1, 4, 64).expand(2, 3, 4, 64)):
+        with pytest.raises(ValueError, match="q: its rows are one broadcast row"):
+            tg.tg_attend_step(x, a["lens"], a["table"], a["kp"], a["vp"], cfg, z(2, 3, 4, 64))
+    torch.cuda.synchronize()
+    assert (out == 7).all() and tg.tg_attn_status_word(cfg) == 0
+    # a single row has no spacing
+    tg.tg_attend_prompt(z(1, 4, 64).as_strided((1, 4, 64), (0, 64, 1)), kv[:1], kv[:1], torch.tensor([0, 1], device="cuda"), None, cfg, out)
+    assert (out[0] == 0).all() and (out[1:] == 7).all()
