@@ -132,12 +132,14 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         long long q0 = 0, m = 0, k0 = 0, kn = 0;
         if (b < a.batch) {
           q0 = a.qoff[b];
-          m = a.qoff[b + 1] - q0;
           k0 = ko[b];
-          kn = ko[b + 1] - k0;
-          if (q0 < 0 || m < 0 || q0 + m > a.q_tokens || k0 < 0 || kn < 0 || k0 + kn > a.kv_tokens) {
-            if (!flagged) atomicOr(c.status, kAttnBadRow);
-            m = 0;
+          const long long q1 = a.qoff[b + 1], k1 = ko[b + 1];
+          // (no differences before the bounds hold: they could wrap)
+          if (q0 >= 0 && q1 >= q0 && q1 <= a.q_tokens && k0 >= 0 && k1 >= k0 && k1 <= a.kv_tokens) {
+            m = q1 - q0;
+            kn = k1 - k0;
+          } else if (!flagged) {
+            atomicOr(c.status, kAttnBadRow);
           }
         }
         const long long blocks = ((m << ps.pack_shift) + 255) >> 8, mine = blocks * ps.groups;

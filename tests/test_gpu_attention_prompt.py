@@ -151,3 +151,23 @@ def test_prompt_bad_offsets_are_flagged():
             assert torch.equal(out[:100], good[:100])
         else:
             assert torch.equal(out[100:], good[100:]) and (out[:100] == 7.0).all()
+
+
+def test_prompt_offsets_at_the_ends_of_64_bits():
+    # an end so far below its beginning that their difference wraps to a positive number
+    import torch
+    import logits_processing_token_gb300 as tg
+    nq, least = [100, 50, 80], -2 ** 63
+    cfg, q, k, v, qo, ko, out, lse = run_case(2, 1, 64, "f16", True, nq, None, seed=9)
+    good = out.clone()
+    for qb, kb in (([0, 100, least, 230], None), ([0, 100, 150, 230], [0, 100, least, 230]), ([5, least, 150, 230], None),
+                   ([0, 100, 2 ** 63 - 1, 230], None)):
+        out.fill_(7.0)
+        tg.tg_attend_prompt(q, k, v, ids(qb, np.int64), None if kb is None else ids(kb, np.int64), cfg, out, lse)
+        torch.cuda.synchronize()
+        assert tg.tg_attn_status_word(cfg) == tg.TG_FLAG_BAD_ROW
+        tg.tg_attn_clear_status(cfg)
+        if qb[0] == 0:
+            assert torch.equal(out[:100], good[:100]) and (out[100:] == 7.0).all()
+        else:
+            assert torch.equal(out[150:], good[150:]) and (out[:150] == 7.0).all()
