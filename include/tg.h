@@ -474,8 +474,9 @@ void tg_attn_params_init(tg_attn_params* p, int32_t num_heads, int32_t num_kv_he
 tg_status tg_attn_create(const tg_attn_params* params, tg_attn** out, tg_stream stream);
 tg_status tg_attn_destroy(tg_attn* cfg);
 
-/* The handle's sticky status bits (synchronous), and their reset.
- * TG_FLAG_BAD_ROW: offsets or a length out of range, the sequence skipped;
+/* The handle's sticky status bits, and their reset (which also clears the
+ * counts that calls keep in the handle).  Both wait for the calls in flight on
+ * every stream.  TG_FLAG_BAD_ROW: offsets or a length out of range, the sequence skipped;
  * TG_FLAG_BAD_PAGE; TG_FLAG_TIMEOUT: a bounded wait ran out, the launch's
  * outputs are not valid. */
 tg_status tg_attn_status_word(const tg_attn* cfg, uint32_t* flags);

@@ -193,14 +193,19 @@ tg_status tg_attn_status_word(const tg_attn* cfg, uint32_t* flags) {
   if (!cfg || !flags) return TG_ERR_INVALID_ARGUMENT;
   const tg_status st = check_device(cfg);
   if (st != TG_OK) return st;
-  return from_cuda(cudaMemcpy(flags, cfg->dev.status, sizeof(uint32_t), cudaMemcpyDeviceToHost));
+  // the copy's own stream does not wait for the others (streams may be non-blocking)
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemcpy(flags, cfg->dev.status, sizeof(uint32_t), cudaMemcpyDeviceToHost);
+  return from_cuda(e);
 }
 
 tg_status tg_attn_clear_status(const tg_attn* cfg) {
   if (!cfg) return TG_ERR_INVALID_ARGUMENT;
   const tg_status st = check_device(cfg);
   if (st != TG_OK) return st;
-  cudaError_t e = cudaMemset(cfg->dev.status, 0, 3 * sizeof(uint32_t));  // and the prompt's counts
+  // a call in flight uses the counts that are cleared here: it ends first
+  cudaError_t e = cudaDeviceSynchronize();
+  if (e == cudaSuccess) e = cudaMemset(cfg->dev.status, 0, 3 * sizeof(uint32_t));  // and the prompt's counts
   if (e == cudaSuccess) e = cudaMemset(cfg->dev.ws_count, 0, cfg->dev.step_slots / 2 * sizeof(unsigned));
   if (e == cudaSuccess) e = cudaDeviceSynchronize();
   return from_cuda(e);
