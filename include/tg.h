@@ -537,10 +537,14 @@ tg_status tg_cache_append(const void* q, int64_t q_stride, const void* k, int64_
  * A token that sees no key (kv_lens[b] <= n - 1 - j, an empty sequence) gives
  * 0 and -infinity.  Keys of a page outside [0, num_pages) are left out
  * (TG_FLAG_BAD_PAGE); kv_lens[b] outside [0, max_pages * page_size] makes the
- * sequence an empty one (TG_FLAG_BAD_ROW).  Softmax statistics and sums are
- * f32; the weights are rounded to the 16-bit type of the products.  The keys
- * of one sequence are split over the GPU and joined in a fixed order: equal
- * inputs give equal bits.
+ * sequence an empty one (TG_FLAG_BAD_ROW).  What other sequences hold, or a
+ * page behind the sequence's end, never reaches this one's results (the other
+ * sequences' lengths decide where its keys are split, and so how its sums
+ * round).  A non-finite value of one of the call's own n tokens may reach the
+ * tokens before it (0 x NaN), but none that sees no key.
+ * Softmax statistics and sums are f32; the weights are rounded to the 16-bit
+ * type of the products.  The keys of one sequence are split over the GPU and
+ * joined in a fixed order: equal inputs give equal bits.
  */
 tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const tg_attn* cfg,
                          void* out, float* out_lse, tg_stream stream);

@@ -657,7 +657,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   const auto put_lse = [&](long long row, float mm, float ll) {
     if (a.lse) a.lse[row] = ll > 0.0f ? (mm + log2f(ll) - bias) * kLn2 : ll == 0.0f ? -INFINITY : ll;
   };
-  const auto factor = [&](float ll, float vs) { return ll == 0.0f ? 0.0f : vs / ll; };
+  // A row's sums divided.  A row that saw no key gives 0 whatever the values that
+  // its weights of 0 met (0 x infinity is not 0).
+  const auto divided = [](float4 x, float ll, float vs) {
+    const float f = vs / ll;
+    return ll == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
+  };
 
   // The item's end in this CTA: join the warps, then write the result, or this
   // CTA's part of it.
@@ -749,9 +754,8 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             acc.w = fmaf(g, v.w, acc.w);
           }
           if (whole) {
-            const float ff = factor(ll, vs);
             const long long row = out_row(row_base + r);
-            put4(row, d, make_float4(acc.x * ff, acc.y * ff, acc.z * ff, acc.w * ff));
+            put4(row, d, divided(acc, ll, vs));
             if (d == 0) put_lse(row, top, ll);
           } else {
             *reinterpret_cast<float4*>(po + r * c.D + d) = acc;
@@ -771,20 +775,21 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         const int r = r0 + 8 * h;
         if (r < nrow) {
           const long long row = out_row(row_base + r);
-          const float f = whole ? factor(l[h], vs) : 1.0f;
+          const float f = vs / l[h];
+          const bool none = l[h] == 0.0f;
 #pragma unroll
           for (int k = 0; k < KS * 2; ++k) {
             if constexpr (!Q8) {
               const int d = col(k, 0);
               if (d < c.D) {
-                if (whole) *reinterpret_cast<unsigned*>(static_cast<uint16_t*>(a.out) + row * c.D + d) = pack2<QF16>(o[k][2 * h] * f, o[k][2 * h + 1] * f);
+                if (whole) *reinterpret_cast<unsigned*>(static_cast<uint16_t*>(a.out) + row * c.D + d) = none ? 0u : pack2<QF16>(o[k][2 * h] * f, o[k][2 * h + 1] * f);
                 else *reinterpret_cast<float2*>(po + r * c.D + d) = make_float2(o[k][2 * h], o[k][2 * h + 1]);
               }
             } else if (!(k & 1)) {  // columns 4t .. 4t + 3 of a slice are in accumulators k, k + 1
               const int d = col(k, 0);
               if (d < c.D) {
-                const float4 x = make_float4(o[k][2 * h] * f, o[k + 1][2 * h] * f, o[k][2 * h + 1] * f, o[k + 1][2 * h + 1] * f);
-                if (whole) put4(row, d, x);
+                const float4 x = make_float4(o[k][2 * h], o[k + 1][2 * h], o[k][2 * h + 1], o[k + 1][2 * h + 1]);
+                if (whole) put4(row, d, divided(x, l[h], vs));
                 else *reinterpret_cast<float4*>(po + r * c.D + d) = x;
               }
             }
@@ -846,8 +851,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           }
         }
         const long long row = out_row(row_base + r);
-        const float f = factor(ll, vs);
-        put4(row, d, make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f));
+        put4(row, d, divided(acc, ll, vs));
         if (d == 0) put_lse(row, mm, ll);
       }
     }

@@ -446,7 +446,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           float* dst = c.ws_o + mine_part * c.D + x;
           const unsigned* lo = o;
           const unsigned* hi = o + 8;
-          // (a row without keys so far: its sums are products of zeros)
+          // (a row without keys so far: products of zeros, that the join leaves out)
           asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), TG_I8(lo, 0) : "memory");
           asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 8), TG_I8(hi, 0) : "memory");
         }
@@ -494,6 +494,14 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
               const int r = min(r0 + y * step, rows - 1);
               v[w][y] = __ldcg(reinterpret_cast<const float4*>(src + r * c.D));
               x[w][y] = __ldcg(&c.ws_ml[sl + r]);
+            }
+          }
+          // a part in which a row saw no key adds nothing, whatever the values that its weights of 0 met
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+#pragma unroll
+            for (int y = 0; y < JP; ++y) {
+              if (x[w][y].y == 0.0f) v[w][y] = make_float4(0, 0, 0, 0);
             }
           }
           const bool both = p + 1 < parts;
