@@ -829,7 +829,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           float top = mm;
 #pragma unroll
           for (int p = 0; p < PB; ++p) {
-            if (p0 + p >= parts) x[p].x = -INFINITY;
+            if (p0 + p >= parts) x[p] = make_float2(-INFINITY, 0.0f);
             top = fmaxf(top, x[p].x);
           }
           const float f0 = mm == -INFINITY ? 0.0f : ex2(mm - top);
@@ -841,7 +841,8 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           mm = top;
 #pragma unroll
           for (int p = 0; p < PB; ++p) {
-            if (x[p].x == -INFINITY) continue;
+            // no key in this part (a part of NaN scores alone has no maximum either, but a sum)
+            if (x[p].y == 0.0f) continue;
             const float f = ex2(x[p].x - top);
             ll += f * x[p].y;
             acc.x += f * v[p].x;

@@ -1,4 +1,5 @@
-"""Infinities and NaN where a row of a step does not look, in every step kernel."""
+"""Infinities and NaN where a row of a step does not look, in every step kernel;
+and NaN where it does."""
 import numpy as np
 import pytest
 
@@ -59,3 +60,12 @@ def test_a_part_without_keys_does_not_touch_the_join():
     out, lse = step(4, n, "bf16", "bf16", 16, lens, values, G=2)
     assert torch.isfinite(out[0, :15].float()).all() and torch.isfinite(lse[0]).all()
     assert torch.isnan(out[0, 15:]).all()
+
+
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(map(str, c)))
+def test_nan_keys_that_are_seen_give_nan(case):
+    # of a short sequence, and of one whose parts several CTAs join
+    import torch
+    n = case[1]
+    out, lse = step(*case, [n, 40, 3000], lambda c: c.k.copy_(torch.full(c.k.shape, float("nan"), device="cuda").to(c.k.dtype)))
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
