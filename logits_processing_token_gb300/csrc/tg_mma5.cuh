@@ -114,7 +114,10 @@ constexpr float kMostSum = F16 ? 255.0f * 256.0f : 255.0f;
 // -infinity) to weights, stored as 16-bit pairs over the scores' first 64
 // columns at `ts`; the row's reference m and sum l, and its sums O at `to` when
 // the reference rises (has_sums: there are some).  The caller waits for the
-// stores.
+// stores.  A row that is no token's of this sequence (it holds a neighbour's
+// query) comes with m = +infinity: its weights are 0, and it has no vote on
+// whether the warp's rows search their maximum, whose reference, and so whose
+// rounding, would else depend on the neighbour.
 template <bool F16>
 __device__ __forceinline__ void softmax_tile(unsigned (&v)[4][32], unsigned ts, unsigned to, int D, float sc, bool has_sums,
                                              float& m, float& l) {
@@ -169,7 +172,7 @@ __device__ __forceinline__ void softmax_tile(unsigned (&v)[4][32], unsigned ts, 
     }
     const float2 l2 = unpair(add2(sum[0], sum[1]));
     tile_sum = l2.x + l2.y;
-    if (search || !__any_sync(~0u, !(tile_sum <= kMostSum<F16>))) break;
+    if (search || !__any_sync(~0u, tile_sum > kMostSum<F16>)) break;  // (a NaN stays one with any reference)
     search = true;
     tm_wait_st();
   }

@@ -385,7 +385,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       const int head = (it.hg << ps.pack_shift) + (row & (ps.pack - 1));
       const int lim = a.causal ? min(it.k_len, i + 1 + it.k_len - it.m_len) : it.k_len;
       const int lim_w = __shfl_sync(~0u, lim, 0);  // the warp's smallest
-      float m = -INFINITY, l = 0.0f;
+      float m = i < it.m_len ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j) {
         ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c.status);
         if (!ok) break;

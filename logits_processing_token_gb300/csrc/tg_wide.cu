@@ -372,10 +372,9 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       const int j0 = it.rt * ws.tpt + tok;  // token
       const bool real = tok < ws.tpt && j0 < a.n;
-      // rows that are no token's see what the others see: nothing of them is kept
       const int lim = real ? it.len - a.n + j0 + 1 : it.len;
       const int lim_w = it.len - a.n + 1;
-      float m = -INFINITY, l = 0.0f;
+      float m = real ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = it.t0; j < it.t1; ++j) {
         ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c.status);
         if (!ok) break;

@@ -171,3 +171,26 @@ def test_prompt_offsets_at_the_ends_of_64_bits():
             assert torch.equal(out[:100], good[:100]) and (out[100:] == 7.0).all()
         else:
             assert torch.equal(out[150:], good[150:]) and (out[:150] == 7.0).all()
+
+
+@pytest.mark.parametrize("H, G, D, typ, causal", [(2, 1, 128, "bf16", True), (4, 2, 64, "f16", True), (3, 3, 80, "bf16", False)])
+def test_prompt_bits_do_not_depend_on_the_neighbours(H, G, D, typ, causal):
+    # the rows behind a sequence's end in its last tile are the next one's queries
+    import torch
+    import logits_processing_token_gb300 as tg
+    nq = [700, 41, 333, 20, 505]
+    q, k, v, qo, ko = make(H, G, D, typ, nq, nq, 11)
+    at = np.concatenate([[0], np.cumsum(nq)])
+    cfg = tg.AttnConfig(num_heads=H, num_kv_heads=G, head_dim=D, dtype=typ)
+    out, lse = torch.empty_like(q.contiguous()), torch.empty(q.shape[:2], device="cuda")
+    tg.tg_attend_prompt(q, k, v, qo, None, cfg, out, lse, causal=causal)
+    for other in (30.0, float("nan"), 0.0):
+        q2, k2, v2 = q.clone(), k.clone(), v.clone()
+        for s in (1, 3):
+            for t in (q2, k2, v2):
+                t[at[s]:at[s + 1]] *= other
+        o2, z2 = torch.empty_like(out), torch.empty_like(lse)
+        tg.tg_attend_prompt(q2, k2, v2, qo, None, cfg, o2, z2, causal=causal)
+        for s in (0, 2, 4):
+            rows = slice(int(at[s]), int(at[s + 1]))
+            assert torch.equal(o2[rows], out[rows]) and torch.equal(z2[rows], lse[rows]), (other, s)

@@ -162,3 +162,27 @@ def test_step_offsets_past_32_bits():
     c = Cache([0], G, D, "bf16", P, "token", 0, fill=False)
     c.keys, c.values = [f64(kk)], [f64(vv)]
     check_attention((out, lse), step_reference(c, f64(q), 1, 1, 1 / np.sqrt(D), "bf16", "bf16", lens=np.array([L])))
+
+
+@pytest.mark.parametrize("rep, n, typ", [(5, 32, "bf16"), (6, 25, "f16")])
+def test_wide_step_bits_do_not_depend_on_the_neighbours(rep, n, typ):
+    # a row tile holds 128 / rep tokens: the last one's other rows are the next sequence's
+    import torch
+    import logits_processing_token_gb300 as tg
+    G, D, lens = 2, 128, [2000 + 7 * b for b in range(24)]
+    c = Cache(lens, G, D, typ, 16, "token", 14)
+    cfg = tg.AttnConfig(num_heads=G * rep, num_kv_heads=G, head_dim=D, dtype=typ, max_step_tokens=32)
+    q = (2 * torch.randn(len(lens), n, G * rep, D, generator=torch.Generator("cuda").manual_seed(15), device="cuda")).to(torch_types()[typ])
+    kl, table = ids(lens, np.int32), c.device_table()
+
+    def call(q):
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:3], device="cuda")
+        tg.tg_attend_step(q, kl, table, c.k, c.v, cfg, out, lse)
+        return out, lse
+
+    out, lse = call(q)
+    for other in (30.0, float("nan"), 0.0):
+        q2 = q.clone()
+        q2[1::2] *= other
+        o2, z2 = call(q2)
+        assert torch.equal(o2[::2], out[::2]) and torch.equal(z2[::2], lse[::2]), other
