@@ -513,7 +513,8 @@ typedef struct tg_cache {
  *
  * The angle's product is held to 2^-32 of a turn at any position; the
  * rotation is computed in f32 and rounded once to each output's type.  An
- * e4m3 cache holds value / scale, rounded to nearest and saturated at 448.
+ * e4m3 cache holds the f32 quotient value / scale, rounded to the nearest code
+ * (ties to even) and saturated at 448.
  * Tokens of a page outside [0, num_pages) or past max_pages are left out of
  * the cache (TG_FLAG_BAD_PAGE); a negative position or inconsistent offsets
  * skip the token (TG_FLAG_BAD_ROW).

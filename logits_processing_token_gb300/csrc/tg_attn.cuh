@@ -32,8 +32,8 @@ struct AttnCfg {
   const unsigned long long* turns;  // [rotary / 2]: 2^64 * fraction of a turn per position
   const float* k_scale;    // [G], or null
   const float* v_scale;
-  const float* k_inv;      // their reciprocals
-  const float* v_inv;
+  const float4* k_div;     // [G], or null: a scale times a power of two, in [2^-64, 2^64]; its reciprocal; the power; -
+  const float4* v_div;
   unsigned* status;
   int max_n;               // largest n of a step
   int step_rows;           // rows of a workspace slot

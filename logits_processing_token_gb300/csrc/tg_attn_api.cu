@@ -65,6 +65,13 @@ bool positive(const float* p, int n) {
   return true;
 }
 
+// What the append's division by a scale takes (AttnCfg::k_div).  With the scale
+// in [2^-64, 2^64] no reciprocal overflows and no residual that matters is rounded.
+float4 divisor(float scale) {
+  const float power = scale < 0x1p-64f ? 0x1p96f : scale > 0x1p64f ? 0x1p-96f : 1.0f, s = scale * power;
+  return make_float4(s, 1.0f / s, power, 0.0f);
+}
+
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 }  // namespace
@@ -136,9 +143,9 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.step_rows = std::min(128, (d.max_n * d.rep + 15) / 16 * 16);
   d.step_slots = 2 * d.nsm * std::max(2, *std::max_element(d.step_ctas, d.step_ctas + 5));
 
-  // [turns][k scales][v scales][their reciprocals][counts][status, prompt counts] are uploaded; then the workspace
+  // [turns][k scales][v scales][what division by them needs][counts][status, prompt counts] are uploaded; then the workspace
   const size_t o_turn = 0, o_ks = up16(o_turn + half * sizeof(unsigned long long)), o_vs = up16(o_ks + d.G * 4),
-               o_ki = up16(o_vs + d.G * 4), o_vi = up16(o_ki + d.G * 4), o_cnt = up16(o_vi + d.G * 4), o_st = up16(o_cnt + d.step_slots / 2 * 4), o_ml = up16(o_st + 12);
+               o_kd = up16(o_vs + d.G * 4), o_vd = o_kd + d.G * sizeof(float4), o_cnt = o_vd + d.G * sizeof(float4), o_st = up16(o_cnt + d.step_slots / 2 * 4), o_ml = up16(o_st + 12);
   const size_t rows = static_cast<size_t>(d.step_slots) * d.step_rows;
   const size_t o_o = (o_ml + rows * sizeof(float2) + 255) / 256 * 256, bytes = o_o + rows * d.D * 4;  // 32-byte stores
   unsigned char* host = new (std::nothrow) unsigned char[o_ml]();
@@ -156,8 +163,8 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   if (p->k_scales) std::memcpy(host + o_ks, p->k_scales, d.G * 4);
   if (p->v_scales) std::memcpy(host + o_vs, p->v_scales, d.G * 4);
   for (int g = 0; g < d.G; ++g) {
-    if (p->k_scales) reinterpret_cast<float*>(host + o_ki)[g] = 1.0f / p->k_scales[g];
-    if (p->v_scales) reinterpret_cast<float*>(host + o_vi)[g] = 1.0f / p->v_scales[g];
+    if (p->k_scales) reinterpret_cast<float4*>(host + o_kd)[g] = divisor(p->k_scales[g]);
+    if (p->v_scales) reinterpret_cast<float4*>(host + o_vd)[g] = divisor(p->v_scales[g]);
   }
   e = cudaMalloc(&cfg->dmem, bytes);
   if (e == cudaSuccess)
@@ -170,8 +177,8 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.turns = reinterpret_cast<unsigned long long*>(m + o_turn);
   d.k_scale = p->k_scales ? reinterpret_cast<float*>(m + o_ks) : nullptr;
   d.v_scale = p->v_scales ? reinterpret_cast<float*>(m + o_vs) : nullptr;
-  d.k_inv = p->k_scales ? reinterpret_cast<float*>(m + o_ki) : nullptr;
-  d.v_inv = p->v_scales ? reinterpret_cast<float*>(m + o_vi) : nullptr;
+  d.k_div = p->k_scales ? reinterpret_cast<float4*>(m + o_kd) : nullptr;
+  d.v_div = p->v_scales ? reinterpret_cast<float4*>(m + o_vd) : nullptr;
   d.ws_count = reinterpret_cast<unsigned*>(m + o_cnt);
   d.status = reinterpret_cast<unsigned*>(m + o_st);
   d.prompt_count = d.status + 1;

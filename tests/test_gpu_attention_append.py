@@ -139,3 +139,66 @@ def test_append_in_a_graph():
     g.replay()
     torch.cuda.synchronize()
     assert torch.equal(qo, q1) and torch.equal(kp.view(torch.uint8), want)
+
+
+def e4m3_case(scales, x):
+    """x [T, G, D] (exact in bf16) as keys and values of a head-major e4m3 cache with these scales; both pools as f32."""
+    import torch
+    import logits_processing_token_gb300 as tg
+    T, G, D = x.shape
+    cfg = tg.AttnConfig(num_heads=G, num_kv_heads=G, head_dim=D, cache_dtype="e4m3", page_size=16, page_layout="head",
+                        k_scales=scales, v_scales=scales)
+    kv = x.cuda().bfloat16()
+    assert torch.equal(kv.double().cpu().nan_to_num(), x.nan_to_num())
+    pages = -(-T // 16)
+    kp, vp = (torch.zeros(pages, G, 16, D, device="cuda").to(torch.float8_e4m3fn) for _ in range(2))
+    tg.tg_cache_append(None, kv, kv, ids([0, T], np.int64), ids([T], np.int32), ids(np.arange(pages)[None], np.int32), kp, vp, cfg)
+    assert tg.tg_attn_status_word(cfg) == 0
+    return [p.float().cpu().transpose(1, 2).reshape(-1, G, D)[:T] for p in (kp, vp)]
+
+
+def test_append_e4m3_ties_go_to_even():
+    # quotients halfway between two codes, with scales whose reciprocals are not exact
+    import torch
+    scales = [m / 64 for m in (3, 5, 6, 7)] + [0.1015625]  # 0.1015625 = 13 / 128
+    odd = torch.arange(17, 32, 2).double()                # 5 bits: the middle of two codes of 4 bits
+    t = torch.stack([torch.cat([odd, -odd]) * 2.0 ** e for e in range(-8, 3)])  # [T, 16]
+    x = t[:, None] * torch.tensor(scales).double()[None, :, None]
+    keep = x.bfloat16().double() == x                     # (13 times 5 bits can take 9)
+    x = torch.where(keep, x, torch.zeros_like(x))
+    want = torch.where(keep, t[:, None].expand_as(x), torch.zeros_like(x)).float().to(torch.float8_e4m3fn).float()
+    for got in e4m3_case(scales, x):
+        assert torch.equal(got, want)
+
+
+def test_append_e4m3_scales_at_the_ends_of_f32():
+    # a scale whose reciprocal is no f32 number, and one whose reciprocal is subnormal
+    import torch
+    tiny, huge = 2.0 ** -140, 3 * 2.0 ** 126
+    row = torch.tensor([0.0, -0.0, 1.0, -1.0, 2.0 ** -133, 2.0 ** 125, 3.0 * 2.0 ** -132, 0.5] * 2).double()
+    x = row[None, None].expand(3, 2, 16)
+    want = (x / torch.tensor([tiny, huge]).double()[:, None]).clamp(-448, 448).float().to(torch.float8_e4m3fn).float()
+    for got in e4m3_case([tiny, huge], x):
+        assert torch.equal(got, want)
+
+
+def test_append_e4m3_is_the_rounded_quotient_of_every_value():
+    # every bf16 number by many scales, against the division of f32 numbers, code by code
+    import torch
+    rng = np.random.default_rng(21)
+    scales = np.concatenate([[448.0, 1.0, 1.9999999, 1.0000001, 2.0 ** -64, 2.0 ** 64, 3.4e38, 2.0 ** -149],
+                             np.exp(rng.uniform(np.log(1e-3), np.log(10), 16)), 2.0 ** rng.uniform(-149, 127, 8)]).astype(np.float32)
+    every = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16)
+    x = every.double()[torch.isfinite(every)].view(-1, 1, 16).expand(-1, len(scales), 16)
+    s = torch.from_numpy(scales)[:, None]
+    want = (x.float() / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+    for got in e4m3_case(scales.tolist(), x):
+        assert torch.equal(got.to(torch.float8_e4m3fn).view(torch.uint8), want)
+
+
+def test_append_e4m3_saturates_infinities_and_keeps_nan():
+    import torch
+    inf = float("inf")
+    x = torch.tensor([inf, -inf, float("nan"), 1.0] * 4).double().view(1, 1, 16).expand(2, 3, 16)
+    for got in e4m3_case([0.5, 2.0 ** -100, 2.0 ** 100], x):
+        assert (got[..., 0::4] == 448).all() and (got[..., 1::4] == -448).all() and torch.isnan(got[..., 2::4]).all()
