@@ -271,11 +271,13 @@ tg_status tg_process(const void* logits, int32_t B, int32_t V, const int32_t* hi
 
 /*
  * tg_set_wait_limit -- testing.  The select and verify kernels give up a
- * wait on a bulk copy of logits after about one second (TG_FLAG_TIMEOUT);
- * this sets that limit to `cycles` SM cycles on the current device, for the
- * launches that follow (0 restores the default).  The wait for copies still
- * in flight after such an error keeps the full limit, so no copy outlives
- * its CTA.  Not for use while other calls run.  Errors: TG_ERR_CUDA.
+ * wait on a bulk copy of logits after about one second (TG_FLAG_TIMEOUT), and
+ * the attention kernels any of their waits; this sets that limit to `cycles`
+ * SM cycles on the current device (of the attention kernels: in the process),
+ * for the launches that follow (0 restores the default).  The wait for copies
+ * and matrix instructions still in flight after such an error keeps the full
+ * limit, so nothing outlives its CTA.  Not for use while other calls run.
+ * Errors: TG_ERR_CUDA.
  */
 tg_status tg_set_wait_limit(uint64_t cycles);
 
@@ -476,9 +478,11 @@ tg_status tg_attn_destroy(tg_attn* cfg);
 
 /* The handle's sticky status bits, and their reset (which also clears the
  * counts that calls keep in the handle).  Both wait for the calls in flight on
- * every stream.  TG_FLAG_BAD_ROW: offsets or a length out of range, the sequence skipped;
- * TG_FLAG_BAD_PAGE; TG_FLAG_TIMEOUT: a bounded wait ran out, the launch's
- * outputs are not valid. */
+ * every stream.
+ * TG_FLAG_BAD_ROW: offsets or a length out of range, the sequence skipped;
+ * TG_FLAG_BAD_PAGE; TG_FLAG_TIMEOUT: a bounded wait ran out.  The outputs of
+ * that launch, and of every later one until tg_attn_clear_status, are not valid
+ * (the launch may have left counts behind). */
 tg_status tg_attn_status_word(const tg_attn* cfg, uint32_t* flags);
 tg_status tg_attn_clear_status(const tg_attn* cfg);
 

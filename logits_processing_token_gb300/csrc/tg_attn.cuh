@@ -19,6 +19,8 @@ constexpr unsigned kAttnBadRow = TG_FLAG_BAD_ROW;
 constexpr unsigned kAttnBadPage = TG_FLAG_BAD_PAGE;
 constexpr unsigned kAttnTimeout = TG_FLAG_TIMEOUT;
 
+constexpr unsigned long long kAttnWaitLimit = 2000000000ull;  // bound of every wait, about 1 s of cycles
+
 // A handle's settings, passed to the kernels by value.
 struct AttnCfg {
   int H, G, D, rep;        // query heads, key heads, head size, H / G
@@ -44,6 +46,8 @@ struct AttnCfg {
   int nsm;
   int step_ctas[5];        // CTAs per SM of the step kernel's row variants
   unsigned* prompt_count;  // [2]: next item and CTAs done of a prompt call; zero between calls
+  unsigned long long wait_limit;  // of a launch, in cycles: kAttnWaitLimit, or a test's
+  int short_waits;                // a test's
   void* encode;            // the driver's tensor-map encoder (host)
 };
 
@@ -214,7 +218,6 @@ __device__ __forceinline__ unsigned tile_at(int r, int c) {
 }
 
 // Barriers in shared memory.
-constexpr unsigned long long kAttnWaitLimit = 2000000000ull;  // bound of every wait, about 1 s of cycles
 __device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
 }
@@ -231,22 +234,39 @@ __device__ __forceinline__ bool bar_try(unsigned long long* b, unsigned parity) 
       : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
   return ok != 0u;
 }
-// Bounded wait.  When the limit runs out (or another warp's did) the CTA is
-// dead: every role leaves its loop.
-__device__ __forceinline__ bool bar_wait(int* dead, unsigned long long* b, unsigned parity, unsigned* status) {
-  if (bar_try(b, parity)) return true;
+__device__ __forceinline__ bool bar_test(unsigned long long* b, unsigned parity) {
+  unsigned ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok) : "r"(sptr(b)), "r"(parity) : "memory");
+  return ok != 0u;
+}
+// Bounded wait of a whole warp.  When the limit runs out (or another warp's did)
+// the CTA is dead: every role leaves its loop.  What follows a wait are
+// instructions of the whole warp, so its lanes have to decide alike: they come
+// together first and then poll one word and one clock.  try_wait may suspend the
+// warp until the phase completes: with a limit that a test has shortened, a phase
+// that completes later than the limit has run out too.  (All of this costs the
+// prompt kernel up to 0.7 % over a constant limit; a vote of the lanes at every
+// wait cost 2 to 4 %.)
+__device__ __forceinline__ bool bar_wait(int* dead, unsigned long long* b, unsigned parity, const AttnCfg& c) {
+  __syncwarp();
+  if (bar_test(b, parity)) return true;
   const long long t0 = clock64();
   for (;;) {
-    if (bar_try(b, parity)) return true;
-    if (*static_cast<volatile int*>(dead)) return false;
-    if (static_cast<unsigned long long>(clock64() - t0) > kAttnWaitLimit) {
+    const bool done = bar_try(b, parity);
+    if (done && !c.short_waits) return true;
+    if (static_cast<unsigned long long>(clock64() - t0) > c.wait_limit) {
       *static_cast<volatile int*>(dead) = 1;
-      atomicOr(status, kAttnTimeout);
+      atomicOr(c.status, kAttnTimeout);
       return false;
     }
+    if (done) return true;
+    if (*static_cast<volatile int*>(dead)) return false;
   }
 }
-// The wait for copies still in flight after that.
+// The wait for copies and matrix instructions still in flight at a CTA's end,
+// always with the full limit.
 __device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned parity) {
   const long long t0 = clock64();
   while (!bar_try(b, parity) && static_cast<unsigned long long>(clock64() - t0) < kAttnWaitLimit) {}

@@ -2,11 +2,17 @@
 // the handle and the launches.  Every check that can be made on the host is
 // made here, before anything is enqueued.
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstring>
 #include <new>
 
 #include "tg_attn.cuh"
+
+namespace tg {
+std::atomic<unsigned long long> attn_wait_limit{kAttnWaitLimit};
+void set_attn_wait_limit(unsigned long long cycles) { attn_wait_limit = cycles ? cycles : kAttnWaitLimit; }
+}  // namespace tg
 
 struct tg_attn {
   tg::AttnCfg dev;
@@ -70,6 +76,14 @@ bool positive(const float* p, int n) {
 float4 divisor(float scale) {
   const float power = scale < 0x1p-64f ? 0x1p96f : scale > 0x1p64f ? 0x1p-96f : 1.0f, s = scale * power;
   return make_float4(s, 1.0f / s, power, 0.0f);
+}
+
+// The settings of one launch.
+tg::AttnCfg launch_cfg(const tg_attn* cfg) {
+  tg::AttnCfg d = cfg->dev;
+  d.wait_limit = tg::attn_wait_limit.load(std::memory_order_relaxed);
+  d.short_waits = d.wait_limit < tg::kAttnWaitLimit;
+  return d;
 }
 
 size_t up16(size_t n) { return (n + 15) / 16 * 16; }
@@ -261,7 +275,7 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
   a.c = view_of(cache);
   a.out = out;
   a.lse = out_lse;
-  return from_cuda(tg::launch_step(d, a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(tg::launch_step(launch_cfg(cfg), a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 tg_status tg_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -291,7 +305,7 @@ tg_status tg_attend_prompt(const void* q, int64_t q_stride, const void* k, int64
   a.causal = causal;
   a.out = out;
   a.lse = out_lse;
-  return from_cuda(tg::launch_prompt(d, a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(tg::launch_prompt(launch_cfg(cfg), a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 }  // extern "C"

@@ -1344,11 +1344,15 @@ cudaError_t select_occupancy(int dtype, bool verify, int smem, int* blocks_per_s
   return cudaSuccess;
 }
 
-// Testing: the select kernels' streaming waits give up after `cycles` SM
-// cycles (0: the default, about one second).
+void set_attn_wait_limit(unsigned long long cycles);  // tg_attn_api.cu
+
+// Testing: the select kernels' streaming waits and all waits of the attention
+// kernels give up after `cycles` SM cycles (0: the default, about one second).
 extern "C" tg_status tg_set_wait_limit(uint64_t cycles) {
   const unsigned long long v = cycles ? static_cast<unsigned long long>(cycles) : kWaitLimitCycles;
-  return cudaMemcpyToSymbol(g_wait_limit, &v, sizeof(v)) == cudaSuccess ? TG_OK : TG_ERR_CUDA;
+  if (cudaMemcpyToSymbol(g_wait_limit, &v, sizeof(v)) != cudaSuccess) return TG_ERR_CUDA;
+  set_attn_wait_limit(cycles);
+  return TG_OK;
 }
 
 #ifdef TG_DEBUG

@@ -188,7 +188,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         b0 += 32;
       }
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c);
       if (!ok) break;
       if (lane == 0) {
         s->item[is] = item;
@@ -198,7 +198,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       if (!item.valid) break;
       const int n = max(item.n[0], item.n[1]);
       if (n == 0) continue;
-      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c.status);
+      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c);
       if (!ok) break;
       q_ph ^= 1;
       if (lane == 0) {
@@ -212,7 +212,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       const int g = (item.hg << ps.pack_shift) / c.rep;
       for (int j = 0; j < n && ok; ++j) {
         for (int w = 0; w < 2; ++w) {
-          ok = bar_wait(&s->dead, &s->kv_empty[slot], kv_ph, c.status);
+          ok = bar_wait(&s->dead, &s->kv_empty[slot], kv_ph, c);
           if (!ok) break;
           if (lane == 0) {
             bar_expect(&s->kv_full[slot], L::kTileB);
@@ -224,8 +224,9 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         }
       }
     }
-    if (!ok && lane == 0) {
-      // a wait ran out: copies in flight land before the CTA's memory goes
+    if (lane == 0) {
+      // Copies in flight land before the CTA's memory goes: the other warps have seen
+      // them land, except when a wait ran out, theirs or this warp's.
       for (int i = 0; i < L::kSlots; ++i) bar_drain(&s->kv_full[i], (i < slot ? kv_ph ^ 1 : kv_ph));
       bar_drain(&s->q_full, q_ph);
     }
@@ -242,7 +243,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
       const int n0 = s->item[is].n[0], n1 = s->item[is].n[1], keys0 = s->item[is].keys[0], keys1 = s->item[is].keys[1];
       const int k_len = s->item[is].k_len, valid = s->item[is].valid;
@@ -252,7 +253,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       if (!valid) break;
       const int n = max(n0, n1);
       if (n == 0) continue;
-      ok = bar_wait(&s->dead, &s->q_full, q_ph, c.status);
+      ok = bar_wait(&s->dead, &s->q_full, q_ph, c);
       if (!ok) break;
       q_ph ^= 1;
       const auto next = [&]() {
@@ -286,7 +287,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         __syncwarp();
       };
       unsigned kslot = slot;
-      ok = bar_wait(&s->dead, &s->kv_full[slot], kv_ph, c.status);
+      ok = bar_wait(&s->dead, &s->kv_full[slot], kv_ph, c);
       if (!ok) break;
       next();
       fence_after();
@@ -300,7 +301,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       for (int j = 0; j < n && ok; ++j) {
         const int vslot = slot;
         const unsigned vaddr = kv0 + vslot * L::kTileB;
-        ok = bar_wait(&s->dead, &s->kv_full[vslot], kv_ph, c.status);
+        ok = bar_wait(&s->dead, &s->kv_full[vslot], kv_ph, c);
         if (!ok) break;
         next();
         // rows behind the sequence's end are another sequence's: their weights
@@ -320,11 +321,11 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         bool k_in = false;
         for (int t = 0; t < 2 && ok; ++t) {
           if (j < nt(t)) {
-            ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c.status);
+            ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c);
             if (!ok) break;
             p_ph[t] ^= 1;
             if (j == 0) {  // the sums of the item before have been read
-              ok = bar_wait(&s->dead, &s->o_empty[t], e_ph[t], c.status);
+              ok = bar_wait(&s->dead, &s->o_empty[t], e_ph[t], c);
               if (!ok) break;
               e_ph[t] ^= 1;
             }
@@ -333,7 +334,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
           }
           if (j + 1 < nt(t)) {
             if (!k_in) {
-              ok = bar_wait(&s->dead, &s->kv_full[kn], kv_ph, c.status);
+              ok = bar_wait(&s->dead, &s->kv_full[kn], kv_ph, c);
               if (!ok) break;
               k_in = true;
               fence_after();
@@ -351,13 +352,6 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         if (k_in) next();
       }
     }
-    if (!ok) {
-      __syncwarp();
-      if (elect()) {
-        commit(&s->drain);
-        bar_drain(&s->drain, 0);
-      }
-    }
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: one thread per row --------------------------------------
@@ -373,7 +367,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
       const Item it = s->item[is];
       __syncwarp();
@@ -387,7 +381,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
       const int lim_w = __shfl_sync(~0u, lim, 0);  // the warp's smallest
       float m = i < it.m_len ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = 0; j < n; ++j) {
-        ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c.status);
+        ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c);
         if (!ok) break;
         s_ph ^= 1;
         fence_after();
@@ -418,7 +412,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         a.lse[(it.q_base + i) * c.H + head] = l == 0.0f ? -INFINITY : (m + log2f(l) - bias) * kLn2;
       if (n > 0) {
         // (the factors of the item before have been read when its sums have)
-        ok = bar_wait(&s->dead, &s->o_empty[t], e_ph, c.status);
+        ok = bar_wait(&s->dead, &s->o_empty[t], e_ph, c);
         if (!ok) break;
         e_ph ^= 1;
         s->inv[t][tid & 127] = l == 0.0f ? 0.0f : 1.0f / l;
@@ -435,7 +429,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
     bool ok = true;
     while (ok) {
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
       const Item* it = &s->item[is];
       const int valid = it->valid, n0 = it->n[0], n1 = it->n[1], i0 = it->i0, m_len = it->m_len, hg = it->hg;
@@ -452,7 +446,7 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
         const unsigned to = tmem + lanes + 256 + t * 128;
         float f = 0.0f;
         if (n > 0) {
-          ok = bar_wait(&s->dead, &s->l_full[t], o_ph[t], c.status) && bar_wait(&s->dead, &s->o_full[t], o_ph[t], c.status);
+          ok = bar_wait(&s->dead, &s->l_full[t], o_ph[t], c) && bar_wait(&s->dead, &s->o_full[t], o_ph[t], c);
           if (!ok) break;
           o_ph[t] ^= 1;
           fence_after();
@@ -494,7 +488,18 @@ prompt_kernel(const AttnCfg c, const PromptArgs a, const PromptSetup ps, const _
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == 8) {
+    // After a wait that ran out, whichever warp's, matrix instructions may be in
+    // flight: they end before the tensor memory goes.
+    if (*static_cast<volatile int*>(&s->dead)) {
+      if (elect()) {
+        commit(&s->drain);
+        bar_drain(&s->drain, 0);
+      }
+      __syncwarp();
+    }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
   if (tid == 0 && atomicAdd(ps.counter + 1, 1u) == gridDim.x - 1) {
     ps.counter[0] = 0u;  // the last CTA leaves the counters at zero for the next call
     ps.counter[1] = 0u;

@@ -228,7 +228,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       const unsigned e_ph = ((i / ST) & 1) ^ 1;
       if (first) {
         // this item's queries: a row at a time into padded rows
-        ok = bar_wait(&hd->dead, &hd->q_empty[qs], q_ph, c.status);
+        ok = bar_wait(&hd->dead, &hd->q_empty[qs], q_ph, c);
         if (!ok) break;
         const int rows = min(S::kRows, rows_all - rt * S::kRows);
         if (lane == 0) bar_expect(&hd->q_full[qs], rows * c.D * 2);
@@ -263,7 +263,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         ntend = static_cast<int>(min(static_cast<long long>(nnt), u1 - nbase - kItemCost));
       }
       const int id_next = tensor_copies && nbase + kItemCost < u1 && lane < (KT >> shift) ? entry(nb, ntile * KT + (lane << shift), nlen) : -1;
-      ok = bar_wait(&hd->dead, &hd->empty[st], e_ph, c.status);
+      ok = bar_wait(&hd->dead, &hd->empty[st], e_ph, c);
       if (!ok) break;
       const unsigned ks = sptr(stages + st * S::kStage), vs = ks + S::kMat;
       if (tensor_copies) {
@@ -329,22 +329,23 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; nt = nnt; tend = ntend; base = nbase; id = id_next;
       first = last;
     }
+    int used = i;  // stages used: the units, and the end
     if (ok) {
       const int st = i % ST;  // the end
-      ok = bar_wait(&hd->dead, &hd->empty[st], ((i / ST) & 1) ^ 1, c.status);
+      ok = bar_wait(&hd->dead, &hd->empty[st], ((i / ST) & 1) ^ 1, c);
       if (ok) {
         if (lane == 0) hd->meta[st].u.b = -1;
         if (!tensor_copies)
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
         __syncwarp();
         if (lane == 0) bar_arrive(&hd->full[st]);
+        ++used;
       }
     }
-    if (!ok) {
-      // a wait ran out: copies in flight land before the CTA's memory goes
-      for (int k = max(0, i - ST); k < i; ++k) bar_drain(&hd->full[k % ST], (k / ST) & 1);
-      for (int k = 0; k < 2; ++k) bar_drain(&hd->q_full[k], k < qs ? q_ph ^ 1 : q_ph);
-    }
+    // Copies in flight land before the CTA's memory goes: the computing warps have
+    // seen them land, except when a wait ran out, theirs or this warp's.
+    for (int k = max(0, used - ST); k < used; ++k) bar_drain(&hd->full[k % ST], (k / ST) & 1);
+    for (int k = 0; k < 2; ++k) bar_drain(&hd->q_full[k], k < qs ? q_ph ^ 1 : q_ph);
     return;
   }
 
@@ -368,7 +369,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   const auto meet = [&]() {
     __syncwarp();
     if (lane == 0) bar_arrive(&hd->meet);
-    ok = bar_wait(&hd->dead, &hd->meet, meet_ph, c.status);
+    ok = bar_wait(&hd->dead, &hd->meet, meet_ph, c);
     meet_ph ^= 1;
     return ok;
   };
@@ -860,12 +861,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 
   for (int i = 0;; ++i) {
     const int st = i % ST;
-    ok = bar_wait(&hd->dead, &hd->full[st], (i / ST) & 1, c.status);
+    ok = bar_wait(&hd->dead, &hd->full[st], (i / ST) & 1, c);
     if (!ok) break;
     cur = hd->meta[st].u;
     if (cur.b < 0) break;
     if (cur.first) {
-      ok = bar_wait(&hd->dead, &hd->q_full[qs], q_ph, c.status);
+      ok = bar_wait(&hd->dead, &hd->q_full[qs], q_ph, c);
       if (!ok) break;
       begin_item();
     }

@@ -158,7 +158,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     for (;;) {
       const bool more = base + kItemCostW < u1;
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c);
       if (!ok) break;
       WItem it{-1, 0, 0, 0, 0, 0, 0, 0};
       if (more) {
@@ -182,7 +182,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         return lane < per && key < len ? __ldg(a.c.table + b * a.c.table_stride + (key >> c.page_shift)) : -1;
       };
       int id = entry(it.t0);
-      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c.status);
+      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c);
       if (!ok) break;
       q_ph ^= 1;
       if (lane == 0) {
@@ -203,7 +203,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         for (int w = 0; w < 2 && ok; ++w)
           for (int t = 0; t < it.nch; ++t) {
             const int st = slot_of(pos);
-            ok = bar_wait(&s->dead, &s->kv_empty[st], use_of(pos) ^ 1, c.status);
+            ok = bar_wait(&s->dead, &s->kv_empty[st], use_of(pos) ^ 1, c);
             if (!ok) break;
             if (w == 0 && t == 0 && lane < 4) {
               unsigned bits = 0;
@@ -238,11 +238,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         }
       }
     }
-    if (!ok) {
-      // a wait ran out: copies in flight land before the CTA's memory goes
-      for (unsigned k = pos > L::kSlots ? pos - L::kSlots : 0; k < pos; ++k) bar_drain(&s->kv_full[slot_of(k)], use_of(k));
-      bar_drain(&s->q_full, q_ph);
-    }
+    // Copies in flight land before the CTA's memory goes: the other warps have seen
+    // them land, except when a wait ran out, theirs or this warp's.
+    for (unsigned k = pos > L::kSlots ? pos - L::kSlots : 0; k < pos; ++k) bar_drain(&s->kv_full[slot_of(k)], use_of(k));
+    bar_drain(&s->q_full, q_ph);
   } else if (warp == 8) {
     // ---- matrix instructions ----------------------------------------------
     registers_down<88>();
@@ -256,20 +255,20 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     bool ok = true;
     for (;;) {
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
       const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len;
       __syncwarp();
       if (lane == 0) bar_arrive(&s->item_empty[is]);
       ++it_n;
       if (b < 0) break;
-      ok = bar_wait(&s->dead, &s->q_full, q_ph, c.status);
+      ok = bar_wait(&s->dead, &s->q_full, q_ph, c);
       if (!ok) break;
       q_ph ^= 1;
       // keys of a tile that there are, in steps of 16
       const auto width = [&](int j) { return max(16, min(kKeysW, (len - j * kKeysW + 15) & ~15)); };
       const auto qk = [&](int t, int j, unsigned at) {
-        ok = bar_wait(&s->dead, &s->kv_full[slot_of(at)], use_of(at), c.status);
+        ok = bar_wait(&s->dead, &s->kv_full[slot_of(at)], use_of(at), c);
         if (!ok) return;
         fence_after();
         const unsigned id = id0 | (static_cast<unsigned>(width(j) >> 3) << 17);
@@ -292,7 +291,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         __syncwarp();
         for (int t = 0; t < nch && ok; ++t) {
           const int vs = slot_of(vpos + t);
-          ok = bar_wait(&s->dead, &s->kv_full[vs], use_of(vpos + t), c.status);
+          ok = bar_wait(&s->dead, &s->kv_full[vs], use_of(vpos + t), c);
           if (!ok) break;
           // Values of keys that do not exist are what the page or an earlier tile
           // holds; their weights are 0, but 0 x NaN is not: zero what is read.
@@ -309,7 +308,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             fence_async();
             __syncwarp();
           }
-          ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c.status);
+          ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c);
           if (!ok) break;
           p_ph[t] ^= 1;
           fence_after();
@@ -330,13 +329,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       if (!ok) break;
     }
-    if (!ok) {
-      __syncwarp();
-      if (elect()) {
-        commit(&s->drain);
-        bar_drain(&s->drain, 0);
-      }
-    }
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: one thread per row --------------------------------------
@@ -353,13 +345,13 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     const auto meet = [&]() {  // the four warps of this tile past this point
       __syncwarp();
       if (lane == 0) bar_arrive(&s->meet[t]);
-      ok = bar_wait(&s->dead, &s->meet[t], meet_ph, c.status);
+      ok = bar_wait(&s->dead, &s->meet[t], meet_ph, c);
       meet_ph ^= 1;
       return ok;
     };
     for (;;) {
       const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c.status);
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
       const WItem it = s->item[is];
       __syncwarp();
@@ -376,7 +368,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const int lim_w = it.len - a.n + 1;
       float m = real ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = it.t0; j < it.t1; ++j) {
-        ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c.status);
+        ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c);
         if (!ok) break;
         s_ph ^= 1;
         fence_after();
@@ -406,7 +398,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         if (lane == 0) bar_arrive(&s->p_full[t]);
       }
       if (!ok) break;
-      ok = bar_wait(&s->dead, &s->o_full[t], o_ph, c.status);
+      ok = bar_wait(&s->dead, &s->o_full[t], o_ph, c);
       if (!ok) break;
       o_ph ^= 1;
       fence_after();
@@ -537,7 +529,18 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   fence_before();
   __syncthreads();
   fence_after();
-  if (warp == 8) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (warp == 8) {
+    // After a wait that ran out, whichever warp's, matrix instructions may be in
+    // flight: they end before the tensor memory goes.
+    if (*static_cast<volatile int*>(&s->dead)) {
+      if (elect()) {
+        commit(&s->drain);
+        bar_drain(&s->drain, 0);
+      }
+      __syncwarp();
+    }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
 }
 
 template <int DP, bool F16>

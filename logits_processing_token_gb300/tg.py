@@ -561,8 +561,8 @@ def tg_clear_status(cfg: Config):
 
 
 def tg_set_wait_limit(cycles: int):
-    """Testing: the select/verify kernels give up a bulk-copy wait after
-    ``cycles`` SM cycles (0 restores the default of about one second)."""
+    """Testing: the select/verify kernels give up a bulk-copy wait, and the attention kernels
+    any wait, after ``cycles`` SM cycles (0 restores the default of about one second)."""
     lib = load_library()
     _check("tg_set_wait_limit", lib.tg_set_wait_limit(int(cycles)))
 
