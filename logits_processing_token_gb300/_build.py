@@ -1,7 +1,10 @@
 """In-tree build of libtg.so with nvcc for sm_103a (no cmake, no torch extension).
 
 The library is plain CUDA C++ behind the C ABI of include/tg.h; it links the
-CUDA runtime statically, so it uses the same primary context as PyTorch.
+CUDA runtime statically, so it uses the same primary context as PyTorch.  It
+needs nvcc alone.  The marshalling module of the Python binding is compiled
+beside it where PyTorch and its headers are there; without it the binding's
+Python checks pass the attention calls on.
 """
 from __future__ import annotations
 
@@ -33,12 +36,35 @@ def nvcc() -> str:
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libtg")
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(BINDING):
+def _older(target: str, deps) -> bool:
+    """target is not there, or older than one of deps (names in CSRC)."""
+    if not os.path.exists(target):
         return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
-    deps = [os.path.join(CSRC, s) for s in SOURCES + [BINDING_SOURCE]] + [os.path.join(CSRC, h) for h in HEADERS]
-    return any(os.path.getmtime(d) > t for d in deps if os.path.exists(d))
+    t = os.path.getmtime(target)
+    return any(os.path.getmtime(d) > t for d in (os.path.join(CSRC, d) for d in deps) if os.path.exists(d))
+
+
+def _stale_library() -> bool:
+    return _older(LIB, SOURCES + HEADERS)
+
+
+def _binding_for() -> str | None:
+    """What a marshalling module has to be compiled for here; None without PyTorch."""
+    import sysconfig
+    try:
+        import torch
+    except ImportError:
+        return None
+    return "%s, torch %s" % (sysconfig.get_config_var("SOABI"), torch.__version__)
+
+
+def binding_current() -> bool:
+    """The marshalling module is there, and was compiled for this Python and PyTorch."""
+    try:
+        with open(BINDING + ".for") as f:
+            return os.path.exists(BINDING) and f.read() == _binding_for()
+    except OSError:
+        return False
 
 
 def build_binding() -> str:
@@ -59,14 +85,29 @@ def build_binding() -> str:
     if r.returncode != 0:
         raise RuntimeError("the compiler failed for %s:\n%s\n%s" % (BINDING_SOURCE, " ".join(cmd), r.stderr))
     os.replace(BINDING + ".tmp", BINDING)
+    with open(BINDING + ".for", "w") as f:
+        f.write(_binding_for())
     return BINDING
 
 
+def _try_binding() -> None:
+    """build_binding() where it can be; a failure is reported and leaves the library's build alone."""
+    if _binding_for() is None:
+        return
+    try:
+        build_binding()
+    except Exception as e:  # no compiler, no headers, a file that is not there
+        sys.stderr.write("tg_binding.so was not built; the attention calls take the binding's slower Python checks: %s\n" % e)
+
+
 def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) -> str:
-    """Compile libtg.so if a source changed; return its path."""
-    if not force and not _stale():
-        return LIB
+    """Compile libtg.so, and the marshalling module, if a source changed; return the library's path."""
     os.makedirs(BUILD, exist_ok=True)
+    binding = force or _older(BINDING, [BINDING_SOURCE, HEADERS[-1]]) or not binding_current()
+    if not force and not _stale_library():
+        if binding:
+            _try_binding()
+        return LIB
     cc = nvcc()
     extra = ["-Xptxas", "-v"] if ptxas_info else []
 
@@ -79,9 +120,9 @@ def build(force: bool = False, verbose: bool = False, ptxas_info: bool = False) 
         return obj, r.stderr
 
     with ThreadPoolExecutor(len(SOURCES) + 1) as ex:
-        binding = ex.submit(build_binding)
+        if binding:
+            ex.submit(_try_binding)
         results = list(ex.map(compile_one, SOURCES))
-        binding.result()
     if verbose or ptxas_info:
         for _, log in results:
             sys.stderr.write(log)

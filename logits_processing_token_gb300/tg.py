@@ -127,12 +127,15 @@ _binding = None
 
 
 def _load_binding():
-    """The native marshalling module (built beside libtg.so)."""
+    """The native marshalling module, or None where it is not built for this Python and PyTorch."""
     global _binding
     if _binding is None:
         import importlib.util
-        if not os.path.exists(_build.BINDING):
-            raise RuntimeError("tg_binding.so is not built (%s); run __graft_entry__.build()" % _build.BINDING)
+        import warnings
+        if not _build.binding_current():
+            warnings.warn("%s is not built for this Python and PyTorch (__graft_entry__.build() does); the attention calls take "
+                          "the slower Python checks" % _build.BINDING)
+            return None
         spec = importlib.util.spec_from_file_location("tg_binding", _build.BINDING)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
@@ -627,7 +630,8 @@ class AttnConfig:
         G, P, D = p.num_kv_heads, p.page_size, p.head_dim
         self.page_shape = (P, G, D) if p.page_layout == TG_PAGES_TOKEN_HEAD else (G, P, D)
         calls = [ctypes.cast(f, c_void_p).value for f in (lib.tg_cache_append, lib.tg_attend_step, lib.tg_attend_prompt)]
-        self._native = _load_binding().make(h.value, p.num_heads, G, D, *self.page_shape[:2], p.dtype, p.cache_dtype, *calls)
+        native = _load_binding()
+        self._native = native and native.make(h.value, p.num_heads, G, D, *self.page_shape[:2], p.dtype, p.cache_dtype, *calls)
 
     def close(self):
         if self.handle:
@@ -645,7 +649,7 @@ class AttnConfig:
 # The attention calls run once or more per layer of a decode step: the native
 # module (csrc/tg_binding.cpp) checks and passes on a call whose tensors are as
 # they should be.  It returns None for any other, and the checks below then say
-# what is wrong with it.
+# what is wrong with it (or, where the module is not built, pass the call on).
 
 def _head_rows(t, name, heads, cfg):
     """Pointer and row stride of a [.., heads, D] tensor whose heads are
