@@ -18,7 +18,7 @@ namespace tg {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kMaxTok = 4;  // tokens per CTA at most (7,300 into an e4m3 cache: 23.9 us, 27.7 at 8; 13,800 in bf16: the same)
+constexpr int kMaxTok = 4;  // tokens per CTA at most (7,300 into an e4m3 cache: 37.3 us, 42.6 at 8; 13,800 in bf16: 60.1, 60.6)
 
 struct TokMeta {
   int ok;          // the token belongs to a sequence and has a position
@@ -60,10 +60,10 @@ __device__ __forceinline__ Vec<W> narrow(const float (&x)[W]) {
 }
 // x / scale as f32, correctly rounded: the product with the rounded reciprocal,
 // then one step with its exact residual (Markstein, IBM J. Res. Dev. 34, 1990).
-// The product alone misses quotients halfway between two codes, and the
-// instruction sequence of a general division takes 5 % longer (7,300 tokens into
-// an e4m3 cache) and 0.4 us more for a single token.  d holds the scale brought
-// to [2^-64, 2^64] by a power of two, its reciprocal, and that power.
+// The product alone misses quotients halfway between two codes (7,300 tokens into
+// an e4m3 cache: 37.2 us, 37.7 so, and 38.6 with a general division, which also
+// costs a single token 0.4 us).  d holds the scale brought to [2^-64, 2^64] by a
+// power of two, its reciprocal, and that power.
 // Quotients of 2^32 and more, which saturate, and NaN skip the step, where an
 // infinity would become NaN; the residual's sign keeps -0.
 __device__ __forceinline__ float quotient(float x, const float4& d) {

@@ -20,10 +20,10 @@
 //   warps 10, 11     fill up the third group, which hands registers to the
 //                    softmax: 256 x 192 + 256 x 64 = 512 x 128 as launched
 //   warps 12-15      write the results, while the softmax is at the next item
-// One prompt of 16,384 tokens (32 heads over 8, D 128, bf16): 1.31 to 1.36 ms, 1.62
+// One prompt of 16,384 tokens (32 heads over 8, D 128, bf16): 1.32 to 1.37 ms, 1.61
 // to 1.67 PFLOP/s, 85 to 88 % of the measured cuBLAS rate, at the power limit.
-// 64 prompts of 1 to 2,048 tokens 630 to 656 us (65 %: an item's beginning and end
-// cost about two tiles).  What bounds a long item is the chain of one tile, scores
+// 64 prompts of 1 to 2,048 tokens 641 to 668 us (63 to 66 %: an item's beginning and
+// end cost about two tiles).  What bounds a long item is the chain of one tile, scores
 // 512 cycles, softmax about 1,000, second product 512, which the other tile's
 // products do not cover entirely.
 // Tensor memory: S0, S1 (128 columns each; P overwrites S as 16-bit pairs),

@@ -968,9 +968,9 @@ cudaError_t prepare_step(AttnCfg* c) {
 }
 
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
-  // More rows than 16 over a 16-bit cache: the tensor-memory kernel (24 rows over
-  // 32 sequences: 70 us, 174 here; 11 rows: 66 us, 72 here, but 10 rows over 5
-  // short sequences 24 us, 12 here).
+  // More rows than 16 over a 16-bit cache: the tensor-memory kernel (32 sequences
+  // of 256 to 4,096 keys: 16 rows 61.0 us here and 65.9 there, 20 rows 73.6 and 66.4;
+  // 5 of 50 to 500: 16 rows 14.8 and 15.5, 18 rows 17.5 and 15.9).
   // Its copies want pages of 8 tokens or more (a swizzled block has 8 rows), and
   // a token's heads of one key head have to fit its 128 rows.
   if (a.n * c.rep > 16 && c.ctype != TG_DTYPE_E4M3 && c.page_size >= 8 && c.rep <= 128) return launch_wide(c, a, s);
