@@ -54,8 +54,10 @@ typedef enum {
 } tg_status;
 
 /* Logits are f32 or bf16; attention tensors bf16 or f16; a key-value cache
- * bf16, f16 or e4m3 (8-bit floating point, finite values up to 448). */
-typedef enum { TG_DTYPE_F32 = 0, TG_DTYPE_BF16 = 1, TG_DTYPE_F16 = 2, TG_DTYPE_E4M3 = 3 } tg_dtype;
+ * bf16, f16, e4m3 (8-bit floating point, finite values up to 448) or i8 (whole
+ * numbers from -127 to 127, kept as bytes 128 higher, with a scale per token
+ * and key head that tg_cache_append computes). */
+typedef enum { TG_DTYPE_F32 = 0, TG_DTYPE_BF16 = 1, TG_DTYPE_F16 = 2, TG_DTYPE_E4M3 = 3, TG_DTYPE_I8 = 4 } tg_dtype;
 typedef enum { TG_GREEDY = 0, TG_SAMPLE = 1 } tg_mode;
 
 /* Status-word bits (sticky until tg_clear_status). */
@@ -421,8 +423,11 @@ int32_t tg_beam_keep(const tg_config* cfg, int32_t num_beams);
  * whose logits tg_select and tg_verify read.  tg_cache_append writes new
  * tokens into the cache (rotating queries and keys by their positions),
  * tg_attend_step attends the last n tokens of every sequence over it (n = 1:
- * a decode step; n = K + 1: the positions of a tg_verify step), and
- * tg_attend_prompt attends whole prompts before they are read from a cache.
+ * a decode step; n = K + 1: the positions of a tg_verify step),
+ * tg_attend_shared does so for sequences that have a prefix in common (the
+ * beams of tg_beam_step, several draws from one prompt), tg_attend_prompt
+ * attends whole prompts before they are read from a cache, and tg_cache_read
+ * reads a cache back as the packed keys and values that tg_attend_prompt takes.
  * ------------------------------------------------------------------------ */
 
 /* Largest head_dim (a multiple of 16), and most tokens per sequence of one
@@ -443,7 +448,7 @@ typedef struct tg_attn_params {
   int32_t num_kv_heads;  /* key and value heads G; head h reads key head h / (H / G) */
   int32_t head_dim;      /* D, a multiple of 16, at most TG_MAX_HEAD_DIM */
   tg_dtype dtype;        /* queries, keys, values and outputs: bf16 or f16 */
-  tg_dtype cache_dtype;  /* the cache's elements: dtype, or e4m3 */
+  tg_dtype cache_dtype;  /* the cache's elements: dtype, e4m3, or i8 */
   int32_t page_size;     /* tokens per page, a power of two, 1 .. 1024 */
   tg_page_layout page_layout;
   float scale;           /* of the products q.k, > 0; 0 = 1 / sqrt(D) */
@@ -459,6 +464,9 @@ typedef struct tg_attn_params {
   const float* k_scales;
   const float* v_scales;
   int32_t max_step_tokens; /* largest n of tg_attend_step, 1 .. TG_MAX_STEP_TOKENS; 0 = 17 */
+  /* Largest batch * n of tg_attend_shared (its workspace: num_heads *
+   * (head_dim + 2) f32 a token); 0 = the call is refused. */
+  int32_t max_shared_tokens;
 } tg_attn_params;
 
 /* Opaque; holds the rotation's constants, the scales, a status word and the
@@ -486,11 +494,15 @@ tg_status tg_attn_destroy(tg_attn* cfg);
 tg_status tg_attn_status_word(const tg_attn* cfg, uint32_t* flags);
 tg_status tg_attn_clear_status(const tg_attn* cfg);
 
-/* A paged cache as a call sees it.  Device pointers; the caller owns all of it. */
+/* A paged cache as a call sees it.  Device pointers; the caller owns all of it.
+ * A page of an i8 cache is its codes, laid out as page_layout says (a byte
+ * holds code + 128), and behind them its scales, f32 [num_kv_heads, page_size]:
+ * page_size * num_kv_heads * (head_dim + 4) bytes.  An element stands for code *
+ * scale. */
 typedef struct tg_cache {
   void* k_pages;            /* num_pages pages, each laid out as page_layout says */
   void* v_pages;
-  int64_t k_page_stride;    /* elements between pages (a multiple of 16 bytes) */
+  int64_t k_page_stride;    /* elements (i8: bytes) between pages (a multiple of 16 bytes) */
   int64_t v_page_stride;
   int32_t num_pages;
   const int32_t* page_table; /* [batch, max_pages]: page t / page_size of row b holds its token t */
@@ -518,7 +530,11 @@ typedef struct tg_cache {
  * The angle's product is held to 2^-32 of a turn at any position; the
  * rotation is computed in f32 and rounded once to each output's type.  An
  * e4m3 cache holds the f32 quotient value / scale, rounded to the nearest code
- * (ties to even) and saturated at 448.
+ * (ties to even) and saturated at 448.  An i8 cache takes, for each token and
+ * key head, scale = (largest magnitude) / 127 in f32, of the rotated key before
+ * any rounding or of the value, and the f32 quotient value / scale rounded to the
+ * nearest whole number; a head of zeros has a scale of 0, and one that holds an
+ * infinity or a NaN a scale of NaN: it reads back as NaN, the others as they are.
  * Tokens of a page outside [0, num_pages) or past max_pages are left out of
  * the cache (TG_FLAG_BAD_PAGE); a negative position or inconsistent offsets
  * skip the token (TG_FLAG_BAD_ROW).
@@ -526,6 +542,26 @@ typedef struct tg_cache {
 tg_status tg_cache_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                           int64_t v_stride, const int64_t* q_offsets, int32_t tokens, const tg_cache* cache,
                           const tg_attn* cfg, void* q_out, void* k_out, tg_stream stream);
+
+/*
+ * tg_cache_read -- the cache's keys and values of every sequence's last tokens,
+ * packed.
+ *
+ *  offsets      device int64 [batch + 1]: rows offsets[b] .. offsets[b+1] of the
+ *               outputs take the last offsets[b+1] - offsets[b] of sequence b's
+ *               kv_lens[b] tokens (all of them, or those of the q_offsets of a
+ *               tg_cache_append).
+ *  k, v         device, [tokens, G, D] in dtype (either may be NULL): rows k_stride,
+ *               v_stride elements apart (multiples of 8; 16-byte aligned pointers).
+ *
+ * A 16-bit cache is copied as it is; an 8-bit one gives code * scale (f32, the
+ * scale of the handle's key head or of the page), rounded once to dtype.
+ * A token on a page outside [0, num_pages) or past max_pages gives 0
+ * (TG_FLAG_BAD_PAGE).  Rows of no sequence, or of more tokens than kv_lens[b],
+ * are left as they were (TG_FLAG_BAD_ROW).
+ */
+tg_status tg_cache_read(const int64_t* offsets, int32_t tokens, const tg_cache* cache, const tg_attn* cfg, void* k,
+                        int64_t k_stride, void* v, int64_t v_stride, tg_stream stream);
 
 /*
  * tg_attend_step -- attention of the last n tokens of every sequence over the
@@ -553,6 +589,31 @@ tg_status tg_cache_append(const void* q, int64_t q_stride, const void* k, int64_
  */
 tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const tg_attn* cfg,
                          void* out, float* out_lse, tg_stream stream);
+
+/*
+ * tg_attend_shared -- tg_attend_step for sequences that have a prefix in common:
+ * the beams of a prompt, several draws from it, requests under one system prompt.
+ * What a group of them shares is read once for all of it.
+ *
+ *  group_offsets device int64 [groups + 1], group_offsets[0] = 0, not decreasing,
+ *               the last one at most batch: group i is sequences group_offsets[i]
+ *               .. group_offsets[i+1] - 1; the sequences behind the last group
+ *               share nothing.
+ *  prefix_lens  device int32 [groups]: tokens 0 .. prefix_lens[i] - 1 are the same
+ *               for all of the group's sequences.  Each sequence's row of the page
+ *               table names them, on pages that they share or on copies, and the
+ *               row of the group's first sequence does whatever its length; the
+ *               call may read them through either.
+ *
+ * batch * n is at most max_shared_tokens.  Other arguments, outputs and numerics
+ * as tg_attend_step, whose results these are up to the order of the sums: a sequence may
+ * be shorter than the prefix, or empty.  Offsets out of order or a prefix_lens[i]
+ * outside [0, max_pages * page_size] raise TG_FLAG_BAD_ROW, and nothing is shared
+ * in that call.  Calls that share a tg_attn share its workspace: in stream order.
+ */
+tg_status tg_attend_shared(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const int64_t* group_offsets,
+                           const int32_t* prefix_lens, int32_t groups, const tg_attn* cfg, void* out, float* out_lse,
+                           tg_stream stream);
 
 /*
  * tg_attend_prompt -- attention of whole prompts, packed back to back.

@@ -9,7 +9,7 @@ from .tg import (  # noqa: F401
     TG_PROC_SET, TG_SAMPLE, Config, TGError, load_library, make_params, tg_clear_status, tg_beam_keep, tg_beam_step,
     tg_next_num_candidates, tg_params, tg_process, tg_process_state, tg_query_status, tg_select, tg_select_state,
     tg_set_wait_limit, tg_status_string, tg_status_word, tg_verify, tg_verify_history,
-    TG_DTYPE_E4M3, TG_DTYPE_F16, TG_FLAG_BAD_PAGE, TG_MAX_HEAD_DIM, TG_MAX_STEP_TOKENS, TG_PAGES_HEAD_TOKEN,
-    TG_PAGES_TOKEN_HEAD, AttnConfig, make_attn_params, tg_attend_prompt, tg_attend_step, tg_attn_clear_status,
-    tg_attn_params, tg_attn_status_word, tg_cache, tg_cache_append,
+    TG_DTYPE_E4M3, TG_DTYPE_F16, TG_DTYPE_I8, TG_FLAG_BAD_PAGE, TG_MAX_HEAD_DIM, TG_MAX_STEP_TOKENS, TG_PAGES_HEAD_TOKEN,
+    TG_PAGES_TOKEN_HEAD, AttnConfig, make_attn_params, tg_attend_prompt, tg_attend_shared, tg_attend_step,
+    tg_attn_clear_status, tg_attn_params, tg_attn_status_word, tg_cache, tg_cache_append, tg_cache_read,
 )

@@ -12,31 +12,15 @@
 // 32 + 2 x 8 heads of 128 in bf16: 60.9 us, 6.0 TB/s, 89 % of the measured copy
 // rate).  A few tokens are bound by the launch and one chain of dependent reads,
 // offsets, length, page (one token 3.4 us a pass, 256 tokens 4.8 us).
-#include "tg_attn.cuh"
+#include <type_traits>
+
+#include "tg_tokens.cuh"
 
 namespace tg {
 namespace {
 
 constexpr int kAppendThreads = 256;
 constexpr int kMaxTok = 4;  // tokens per CTA at most (7,300 into an e4m3 cache: 37.3 us, 42.6 at 8; 13,800 in bf16: 60.1, 60.6)
-
-struct TokMeta {
-  int ok;          // the token belongs to a sequence and has a position
-  int page;        // its page, or -1: left out of the cache
-  int slot;
-  unsigned pos;
-};
-
-// The sequence that holds packed token t: the last b with off[b] <= t (bounded
-// whatever the offsets hold).
-__device__ __forceinline__ int find_seq(const int64_t* off, int batch, long long t) {
-  int lo = 0, hi = batch;  // invariant for sorted offsets: off[lo] <= t < off[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (off[mid] <= t) lo = mid; else hi = mid;
-  }
-  return lo;
-}
 
 // W 16-bit elements of a head, in registers of two.
 template <int W>
@@ -86,37 +70,39 @@ __device__ __forceinline__ Vec8<W> narrow8(const float (&x)[W], const float4& d)
   return v;
 }
 
+// What quotient() takes of an i8 head's scale (0: every quotient 0).
+__device__ __forceinline__ float4 divisor(float scale) {
+  const float power = scale < 0x1p-64f ? 0x1p96f : scale > 0x1p64f ? 0x1p-96f : 1.0f, s = scale * power;
+  return make_float4(s, s > 0.0f ? __frcp_rn(s) : 0.0f, power, 0.0f);
+}
+// As i8: the quotient by the scale to the nearest whole number (ties to even:
+// 1.5 2^23 has an f32's last bit where ones are), plus 128.
+template <int W>
+__device__ __forceinline__ Vec8<W> narrow_i8(const float (&x)[W], const float4& d, bool fine) {
+  Vec8<W> v;
+  const auto one = [&](int i) {
+    return __float_as_uint(fminf(fmaxf(fine ? quotient(x[i], d) : 0.0f, -127.0f), 127.0f) + (0x1.8p23f + 128.0f));
+  };
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i)
+    v.w[i] = __byte_perm(__byte_perm(one(4 * i), one(4 * i + 1), 0x0040), __byte_perm(one(4 * i + 2), one(4 * i + 3), 0x0040), 0x5410);
+  return v;
+}
+
 // One CTA: tpb tokens.  A unit of work is 2 W elements of one head: two vectors
 // of W, which for rotated "halves" are the two partners.  W is 8, or 4 where
 // half the rotated width is no multiple of 8 and the partners would straddle
 // 16-byte boundaries.
-template <bool F16, bool Q8, int W>
+// CK: kC16, kE4M3, or kI8, where the lanes of a head (their number rounded up to a
+// power of two) find its largest magnitude together.
+template <bool F16, int CK, int W>
 __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c, const AppendArgs a, int tpb) {
   __shared__ TokMeta meta[kMaxTok];
   __shared__ float2 cs[kMaxTok][TG_MAX_HEAD_DIM / 2];
   dep_wait();
   const int t0 = blockIdx.x * tpb;
   const int nt = min(tpb, a.tokens - t0);
-  if (threadIdx.x < nt) {
-    const long long t = t0 + threadIdx.x;
-    TokMeta m{0, -1, 0, 0u};
-    const int b = find_seq(a.off, a.c.batch, t);
-    const long long o0 = a.off[b], o1 = a.off[b + 1];
-    if (o0 <= t && t < o1) {
-      const long long pos = a.c.lens[b] - (o1 - t);
-      if (pos >= 0) {
-        m.ok = 1;
-        m.pos = static_cast<unsigned>(pos);
-        const int pi = m.pos >> c.page_shift;
-        m.slot = m.pos & (c.page_size - 1);
-        const int page = pi < a.c.max_pages ? a.c.table[b * a.c.table_stride + pi] : -1;
-        if (page >= 0 && page < a.c.num_pages) m.page = page;
-        else atomicOr(c.status, kAttnBadPage);
-      }
-    }
-    if (!m.ok) atomicOr(c.status, kAttnBadRow);
-    meta[threadIdx.x] = m;
-  }
+  if (threadIdx.x < nt) meta[threadIdx.x] = look_up(c, a.c, a.off, t0 + threadIdx.x);
   __syncthreads();
   const int half = c.rotary >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kAppendThreads) {
@@ -128,18 +114,21 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
   }
   __syncthreads();
 
-  const int per_head = c.D / (2 * W);
+  constexpr bool I8 = CK == kI8;
+  const int parts = c.D / (2 * W);  // units of a head
+  const int per_head = I8 ? 1 << (32 - __clz(parts - 1)) : parts;
   const int heads = (a.q ? c.H : 0) + 2 * c.G;
   const int units = heads * per_head;
   const int rot_units = half / W;  // units of a head that turn
   const unsigned inv_head = (1u << 20) / per_head + 1;  // u / per_head for u < 2^20 / per_head
   for (int t = 0, u = threadIdx.x;; u += kAppendThreads) {
     while (u >= units) { u -= units; ++t; }
-    if (t >= nt) break;
-    const TokMeta m = meta[t];
-    if (!m.ok) continue;
+    if (I8 ? !__any_sync(~0u, t < nt) : t >= nt) break;  // (i8: a warp stays together)
+    const TokMeta m = meta[min(t, nt - 1)];
+    if (!I8 && !m.ok) continue;
     int h = static_cast<int>((u * inv_head) >> 20);
     const int part = u - h * per_head;
+    const bool on = !I8 || (t < nt && m.ok && part < parts);
     const long long row = t0 + t;
     // q heads, then key heads, then value heads
     const uint16_t* src;
@@ -148,10 +137,14 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
     if (h < c.H) { src = static_cast<const uint16_t*>(a.q) + row * a.qs + static_cast<long long>(h) * c.D; head = h; }
     else if (h < c.H + c.G) { kind = 1; head = h - c.H; src = static_cast<const uint16_t*>(a.k) + row * a.ks + static_cast<long long>(head) * c.D; }
     else { kind = 2; head = h - c.H - c.G; src = static_cast<const uint16_t*>(a.v) + row * a.vs + static_cast<long long>(head) * c.D; }
-    const bool turn = kind < 2 && part < rot_units;
+    const bool turn = on && kind < 2 && part < rot_units;
     const int e0 = turn && !c.inter ? part * W : part * 2 * W;
     const int e1 = turn && !c.inter ? e0 + half : e0 + W;
-    const Vec<W> w0 = *reinterpret_cast<const Vec<W>*>(src + e0), w1 = *reinterpret_cast<const Vec<W>*>(src + e1);
+    Vec<W> w0{}, w1{};
+    if (on) {
+      w0 = *reinterpret_cast<const Vec<W>*>(src + e0);
+      w1 = *reinterpret_cast<const Vec<W>*>(src + e1);
+    }
     float x[W], y[W];
     widen<F16, W>(w0, x);
     widen<F16, W>(w1, y);
@@ -178,16 +171,35 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
     }
     Vec<W> n0 = w0, n1 = w1;
     if (turn) { n0 = narrow<F16, W>(x); n1 = narrow<F16, W>(y); }
-    if (kind == 0 || (kind == 1 && a.k_out)) {
+    if (on && (kind == 0 || (kind == 1 && a.k_out))) {
       uint16_t* dst = kind == 0 ? static_cast<uint16_t*>(a.q_out) + (row * c.H + head) * c.D
                                 : static_cast<uint16_t*>(a.k_out) + (row * c.G + head) * c.D;
       *reinterpret_cast<Vec<W>*>(dst + e0) = n0;
       *reinterpret_cast<Vec<W>*>(dst + e1) = n1;
     }
+    if constexpr (I8) {
+      // the largest magnitude, as bits: above every number's are infinity's and NaN's
+      unsigned top = 0u;
+#pragma unroll
+      for (int j = 0; j < W; ++j) top = max(top, max(__float_as_uint(x[j]) & 0x7fffffffu, __float_as_uint(y[j]) & 0x7fffffffu));
+      for (int d = 1; d < per_head; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
+      if (on && kind > 0 && m.page >= 0) {
+        const bool fine = top < 0x7f800000u;
+        const float scale = fine ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7fc00000u);
+        const float4 d = divisor(scale);
+        const long long page = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride);
+        uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + page;
+        if (part == 0) *reinterpret_cast<float*>(dst + c.scale_at + (head * c.page_size + m.slot) * 4) = scale;
+        dst += m.slot * c.slot_stride + head * c.head_stride;
+        *reinterpret_cast<Vec8<W>*>(dst + e0) = narrow_i8<W>(x, d, fine);
+        *reinterpret_cast<Vec8<W>*>(dst + e1) = narrow_i8<W>(y, d, fine);
+      }
+      continue;
+    }
     if (kind > 0 && m.page >= 0) {
       const long long at = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride) + m.slot * c.slot_stride +
                            head * c.head_stride;
-      if constexpr (Q8) {
+      if constexpr (CK == kE4M3) {
         const float4* dv = kind == 1 ? c.k_div : c.v_div;
         const float4 d = dv ? dv[head] : make_float4(1.0f, 1.0f, 1.0f, 0.0f);
         uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + at;
@@ -217,12 +229,14 @@ cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s)
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  const bool f16 = c.dtype == TG_DTYPE_F16, q8 = c.ctype == TG_DTYPE_E4M3;
-  const bool narrow = (c.rotary >> 1) % 8 != 0;
-  auto k = narrow ? (f16 ? (q8 ? append_kernel<true, true, 4> : append_kernel<true, false, 4>)
-                         : (q8 ? append_kernel<false, true, 4> : append_kernel<false, false, 4>))
-                  : (f16 ? (q8 ? append_kernel<true, true, 8> : append_kernel<true, false, 8>)
-                         : (q8 ? append_kernel<false, true, 8> : append_kernel<false, false, 8>));
+  const bool f16 = c.dtype == TG_DTYPE_F16, narrow = (c.rotary >> 1) % 8 != 0;
+  const auto pick = [&](auto ck) {
+    constexpr int CK = decltype(ck)::value;
+    return narrow ? (f16 ? append_kernel<true, CK, 4> : append_kernel<false, CK, 4>)
+                  : (f16 ? append_kernel<true, CK, 8> : append_kernel<false, CK, 8>);
+  };
+  auto k = c.ctype == TG_DTYPE_E4M3 ? pick(std::integral_constant<int, kE4M3>()) : c.ctype == TG_DTYPE_I8 ? pick(std::integral_constant<int, kI8>())
+                                                                                                        : pick(std::integral_constant<int, kC16>());
   return cudaLaunchKernelEx(&cfg, k, c, a, tpb);
 }
 

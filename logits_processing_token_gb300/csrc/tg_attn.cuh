@@ -36,6 +36,7 @@ struct AttnCfg {
   const float* v_scale;
   const float4* k_div;     // [G], or null: a scale times a power of two, in [2^-64, 2^64]; its reciprocal; the power; -
   const float4* v_div;
+  int scale_at;            // i8: where a page's scales begin, in bytes
   unsigned* status;
   int max_n;               // largest n of a step
   int step_rows;           // rows of a workspace slot
@@ -45,6 +46,7 @@ struct AttnCfg {
   unsigned* ws_count;      // [slots / 2]: parts of a split sequence that are done; zero between calls
   int nsm;
   int step_ctas[5];        // CTAs per SM of the step kernel's row variants
+  int max_shared;          // largest batch * n of a shared call
   unsigned* prompt_count;  // [2]: next item and CTAs done of a prompt call; zero between calls
   unsigned long long wait_limit;  // of a launch, in cycles: kAttnWaitLimit, or a test's
   int short_waits;                // a test's
@@ -82,6 +84,14 @@ struct StepArgs {
   float* lse;
 };
 
+struct ReadArgs {
+  const int64_t* off;
+  int tokens;
+  CacheView c;
+  void *k, *v;
+  long long ks, vs;
+};
+
 struct PromptArgs {
   const void *q, *k, *v;
   long long qs, ks, vs;
@@ -96,7 +106,10 @@ cudaError_t prepare_step(AttnCfg* c);
 cudaError_t prepare_prompt(AttnCfg* c);
 cudaError_t prepare_wide(const AttnCfg& c);
 cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s);
+cudaError_t launch_read(const AttnCfg& c, const ReadArgs& a, cudaStream_t s);
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
+cudaError_t step_e4m3(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
+cudaError_t step_i8(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, 16-bit cache
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
 // CTAs of the step kernel per SM at most (they size the handle's workspace).
@@ -163,6 +176,9 @@ __device__ __forceinline__ float2 unpack2(unsigned w) {
   if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
   else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
+// What a cache's elements are: 16 bits, or 8 that are widened to f16, exactly.
+constexpr int kC16 = 0, kE4M3 = TG_DTYPE_E4M3, kI8 = TG_DTYPE_I8;
+
 // Two e4m3 values (low 16 bits of w) to two f16, exactly.
 __device__ __forceinline__ unsigned e4m3x2_to_f16x2(unsigned short w) {
   unsigned h;
@@ -170,6 +186,32 @@ __device__ __forceinline__ unsigned e4m3x2_to_f16x2(unsigned short w) {
   return h;
 }
 
+// Two bytes of an i8 cache (code + 128), picked by the low digits of SEL, to two
+// f16, exactly: behind the byte 0x64 a byte u reads 1024 + u.
+template <unsigned SEL>
+__device__ __forceinline__ unsigned i8x2_to_f16x2(unsigned w) {
+  const unsigned h = __byte_perm(w, 0x64646464u, SEL | 0x4040u), less = 0x64806480u;  // 1024 + 128
+  const __half2 d = __hsub2(*reinterpret_cast<const __half2*>(&h), *reinterpret_cast<const __half2*>(&less));
+  return *reinterpret_cast<const unsigned*>(&d);
+}
+// Bytes (0, 1), (2, 3), (0, 2), (1, 3) of four elements as two f16.
+template <int CK>
+__device__ __forceinline__ unsigned low2(unsigned w) { return CK == kI8 ? i8x2_to_f16x2<0x0100>(w) : e4m3x2_to_f16x2(w & 0xffff); }
+template <int CK>
+__device__ __forceinline__ unsigned high2(unsigned w) { return CK == kI8 ? i8x2_to_f16x2<0x0302>(w) : e4m3x2_to_f16x2(w >> 16); }
+template <int CK>
+__device__ __forceinline__ unsigned even2(unsigned w) {
+  return CK == kI8 ? i8x2_to_f16x2<0x0200>(w) : e4m3x2_to_f16x2(__byte_perm(w, 0, 0x3120) & 0xffff);
+}
+template <int CK>
+__device__ __forceinline__ unsigned odd2(unsigned w) {
+  return CK == kI8 ? i8x2_to_f16x2<0x0301>(w) : e4m3x2_to_f16x2(__byte_perm(w, 0, 0x3120) >> 16);
+}
+
+__device__ __forceinline__ void cp4(unsigned dst, const void* src, bool on) {
+  const int n = on ? 4 : 0;
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+}
 __device__ __forceinline__ void cp16(unsigned dst, const void* src, bool on) {
   const int n = on ? 16 : 0;  // 0: the 16 bytes are filled with zeros, src is not read
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -273,6 +315,10 @@ __device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned parity
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
+__device__ __forceinline__ void bulk(unsigned dst, const void* src, unsigned bytes, unsigned long long* bar) {
+  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
+               "r"(sptr(bar)) : "memory");
+}
 __device__ __forceinline__ void tma3(unsigned dst, const CUtensorMap* m, int x, int y, int z, unsigned long long* bar) {
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),

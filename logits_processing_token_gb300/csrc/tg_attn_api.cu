@@ -42,8 +42,8 @@ bool rows_ok(const void* p, int64_t stride, int64_t row) {
 }
 
 bool cache_ok(const tg_cache* c, const tg::AttnCfg& d) {
-  const int per16 = d.ctype == TG_DTYPE_E4M3 ? 16 : 8;
-  const int64_t page = static_cast<int64_t>(d.page_size) * d.G * d.D;
+  const int per16 = d.ctype == d.dtype ? 8 : 16;
+  const int64_t page = static_cast<int64_t>(d.page_size) * d.G * (d.D + (d.ctype == TG_DTYPE_I8 ? 4 : 0));
   return c->k_pages && c->v_pages && aligned16(c->k_pages) && aligned16(c->v_pages) && c->num_pages >= 1 &&
          c->k_page_stride >= page && c->v_page_stride >= page && c->k_page_stride % per16 == 0 &&
          c->v_page_stride % per16 == 0 && c->page_table && c->max_pages >= 1 && c->table_stride >= c->max_pages &&
@@ -111,7 +111,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
       p->head_dim < 1)
     return TG_ERR_INVALID_ARGUMENT;
   if (p->dtype != TG_DTYPE_BF16 && p->dtype != TG_DTYPE_F16) return TG_ERR_INVALID_ARGUMENT;
-  if (p->cache_dtype != p->dtype && p->cache_dtype != TG_DTYPE_E4M3) return TG_ERR_INVALID_ARGUMENT;
+  if (p->cache_dtype != p->dtype && p->cache_dtype != TG_DTYPE_E4M3 && p->cache_dtype != TG_DTYPE_I8) return TG_ERR_INVALID_ARGUMENT;
   if (p->page_size < 1 || p->page_size > 1024) return TG_ERR_INVALID_ARGUMENT;
   if (p->page_layout != TG_PAGES_TOKEN_HEAD && p->page_layout != TG_PAGES_HEAD_TOKEN) return TG_ERR_INVALID_ARGUMENT;
   if (!(p->scale >= 0.0f) || !std::isfinite(p->scale)) return TG_ERR_INVALID_ARGUMENT;
@@ -119,6 +119,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
     return TG_ERR_INVALID_ARGUMENT;
   if (p->rotary_dim > 0 && !p->inv_freq) return TG_ERR_INVALID_ARGUMENT;
   if (p->max_step_tokens < 0 || p->max_step_tokens > TG_MAX_STEP_TOKENS) return TG_ERR_INVALID_ARGUMENT;
+  if (p->max_shared_tokens < 0) return TG_ERR_INVALID_ARGUMENT;
   if ((p->k_scales || p->v_scales) && p->cache_dtype != TG_DTYPE_E4M3) return TG_ERR_INVALID_ARGUMENT;
   if (!positive(p->k_scales, p->num_kv_heads) || !positive(p->v_scales, p->num_kv_heads)) return TG_ERR_INVALID_ARGUMENT;
   if (p->head_dim > TG_MAX_HEAD_DIM || p->head_dim % 16 || p->rotary_dim % 8 || (p->page_size & (p->page_size - 1)))
@@ -143,6 +144,8 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.token_major = token;
   d.slot_stride = token ? static_cast<long long>(d.G) * d.D : d.D;
   d.head_stride = token ? d.D : static_cast<long long>(d.page_size) * d.D;
+  d.scale_at = d.page_size * d.G * d.D;  // (at most 1,024 x 1,024 x 128: 2^27)
+  d.max_shared = p->max_shared_tokens;
   d.scale = p->scale > 0.0f ? p->scale : static_cast<float>(1.0 / std::sqrt(static_cast<double>(d.D)));
   d.rotary = p->rotary_dim;
   d.inter = p->rotary_interleaved;
@@ -258,6 +261,37 @@ tg_status tg_cache_append(const void* q, int64_t q_stride, const void* k, int64_
   a.q_out = q_out;
   a.k_out = k_out;
   return from_cuda(tg::launch_append(d, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tg_cache_read(const int64_t* offsets, int32_t tokens, const tg_cache* cache, const tg_attn* cfg, void* k,
+                        int64_t k_stride, void* v, int64_t v_stride, tg_stream stream) {
+  if (!cfg || !cache || tokens < 0 || cache->batch < 0) return TG_ERR_INVALID_ARGUMENT;
+  if (tokens == 0 || cache->batch == 0) return TG_OK;
+  const tg::AttnCfg& d = cfg->dev;
+  if (!offsets || !cache_ok(cache, d) || (!k && !v)) return TG_ERR_INVALID_ARGUMENT;
+  if ((k && !rows_ok(k, k_stride, d.G * d.D)) || (v && !rows_ok(v, v_stride, d.G * d.D))) return TG_ERR_INVALID_ARGUMENT;
+  const tg_status st = check_device(cfg);
+  if (st != TG_OK) return st;
+  tg::ReadArgs a{};
+  a.off = offsets;
+  a.tokens = tokens;
+  a.c = view_of(cache);
+  a.k = k;
+  a.v = v;
+  a.ks = k_stride;
+  a.vs = v_stride;
+  return from_cuda(tg::launch_read(d, a, reinterpret_cast<cudaStream_t>(stream)));
+}
+
+tg_status tg_attend_shared(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const int64_t* group_offsets,
+                           const int32_t* prefix_lens, int32_t groups, const tg_attn* cfg, void* out, float* out_lse,
+                           tg_stream stream) {
+  if (!cfg || !cache || n < 1 || n > cfg->dev.max_n || cache->batch < 0 || groups < 0) return TG_ERR_INVALID_ARGUMENT;
+  if (cache->batch == 0) return TG_OK;
+  const tg::AttnCfg& d = cfg->dev;
+  if (static_cast<int64_t>(cache->batch) * n > d.max_shared || (groups > 0 && (!group_offsets || !prefix_lens)))
+    return TG_ERR_INVALID_ARGUMENT;
+  return tg_attend_step(q, q_stride, n, cache, cfg, out, out_lse, stream);
 }
 
 tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const tg_attn* cfg,

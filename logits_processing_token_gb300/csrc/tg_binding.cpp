@@ -20,16 +20,21 @@ namespace {
 typedef tg_status (*AppendFn)(const void*, int64_t, const void*, int64_t, const void*, int64_t, const int64_t*, int32_t,
                               const tg_cache*, const tg_attn*, void*, void*, tg_stream);
 typedef tg_status (*StepFn)(const void*, int64_t, int32_t, const tg_cache*, const tg_attn*, void*, float*, tg_stream);
+typedef tg_status (*ReadFn)(const int64_t*, int32_t, const tg_cache*, const tg_attn*, void*, int64_t, void*, int64_t, tg_stream);
+typedef tg_status (*SharedFn)(const void*, int64_t, int32_t, const tg_cache*, const int64_t*, const int32_t*, int32_t, const tg_attn*,
+                              void*, float*, tg_stream);
 typedef tg_status (*PromptFn)(const void*, int64_t, const void*, int64_t, const void*, int64_t, const int64_t*,
                               const int64_t*, int32_t, int32_t, int32_t, int32_t, const tg_attn*, void*, float*, tg_stream);
 
 // What a handle's tensors must look like (make()).
 struct Handle {
   const tg_attn* cfg;
-  int64_t H, G, D, p1, p2;  // a page is [p1, p2, D]
+  int64_t H, G, D, p1, p2;  // a page is [p1, p2, D], of an i8 cache p1 bytes
   at::ScalarType type, cache;
   AppendFn append;
+  ReadFn read;
   StepFn step;
+  SharedFn shared;
   PromptFn prompt;
 };
 
@@ -38,17 +43,18 @@ const char* kName = "tg_attention_handle";
 void drop(PyObject* capsule) { delete static_cast<Handle*>(PyCapsule_GetPointer(capsule, kName)); }
 
 at::ScalarType scalar(long code) {
-  return code == TG_DTYPE_BF16 ? at::kBFloat16 : code == TG_DTYPE_F16 ? at::kHalf : at::kFloat8_e4m3fn;
+  return code == TG_DTYPE_BF16 ? at::kBFloat16 : code == TG_DTYPE_F16 ? at::kHalf : code == TG_DTYPE_I8 ? at::kByte : at::kFloat8_e4m3fn;
 }
 
-// make(handle, H, G, D, p1, p2, dtype, cache_dtype, append, step, prompt): addresses as integers
+// make(handle, H, G, D, p1, p2, dtype, cache_dtype, append, step, prompt[, read, shared]): addresses as integers
 PyObject* make(PyObject*, PyObject* args) {
-  unsigned long long h, fa, fs, fp;
+  unsigned long long h, fa, fs, fp, fr = 0, fh = 0;
   long long H, G, D, p1, p2;
   long dt, ct;
-  if (!PyArg_ParseTuple(args, "KLLLLLllKKK", &h, &H, &G, &D, &p1, &p2, &dt, &ct, &fa, &fs, &fp)) return nullptr;
+  if (!PyArg_ParseTuple(args, "KLLLLLllKKK|KK", &h, &H, &G, &D, &p1, &p2, &dt, &ct, &fa, &fs, &fp, &fr, &fh)) return nullptr;
   auto* x = new (std::nothrow) Handle{reinterpret_cast<const tg_attn*>(h), H, G, D, p1, p2, scalar(dt), scalar(ct),
-                       reinterpret_cast<AppendFn>(fa), reinterpret_cast<StepFn>(fs), reinterpret_cast<PromptFn>(fp)};
+                       reinterpret_cast<AppendFn>(fa), reinterpret_cast<ReadFn>(fr), reinterpret_cast<StepFn>(fs),
+                       reinterpret_cast<SharedFn>(fh), reinterpret_cast<PromptFn>(fp)};
   if (!x) return PyErr_NoMemory();
   return PyCapsule_New(x, kName, drop);
 }
@@ -73,7 +79,13 @@ inline bool whole(const at::Tensor* t, at::ScalarType type, int64_t numel) {
 }
 
 inline bool pages(const at::Tensor* t, const Handle* h, int64_t* stride) {
-  if (!t || t->dim() != 4 || !t->is_cuda() || t->scalar_type() != h->cache) return false;
+  if (!t || !t->is_cuda() || t->scalar_type() != h->cache) return false;
+  if (h->cache == at::kByte) {
+    if (t->dim() != 2 || t->size(1) < h->p1 || t->stride(1) != 1) return false;
+    *stride = t->size(0) > 1 ? t->stride(0) : (t->size(1) + 15) / 16 * 16;
+    return true;
+  }
+  if (t->dim() != 4) return false;
   const auto s = t->sizes(), st = t->strides();
   if (s[1] != h->p1 || s[2] != h->p2 || s[3] != h->D || st[3] != 1 || (h->p2 > 1 && st[2] != h->D) ||
       (h->p1 > 1 && st[1] != h->p2 * h->D))
@@ -174,6 +186,56 @@ PyObject* step(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   Py_RETURN_NONE;
 }
 
+// read(offsets, kv_lens, page_table, k_pages, v_pages, handle, k, v, stream)
+PyObject* read(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  const Handle* h = n == 9 ? handle(a[5]) : nullptr;
+  if (!h || !h->read) Py_RETURN_NONE;
+  const at::Tensor* t[2] = {nullptr, nullptr};
+  int64_t stride[2] = {0, 0}, T = -1;
+  for (int w = 0; w < 2; ++w) {
+    if (a[6 + w] == Py_None) continue;
+    t[w] = tensor(a[6 + w]);
+    stride[w] = rows(t[w], 3, h->G, h);
+    if (stride[w] < 0 || (T >= 0 && t[w]->size(0) != T)) Py_RETURN_NONE;
+    T = t[w]->size(0);
+  }
+  const at::Tensor* off = tensor(a[0]);
+  tg_cache c;
+  tg_stream s;
+  if (T < 0 || T > kInt32 || !cache(a[1], a[2], a[3], a[4], h, &c) || !whole(off, at::kLong, c.batch + 1ll) ||
+      !stream_of(a[8], off, &s))
+    Py_RETURN_NONE;
+  return PyLong_FromLong(h->read(static_cast<const int64_t*>(off->data_ptr()), static_cast<int32_t>(T), &c, h->cfg,
+                                 t[0] ? t[0]->data_ptr() : nullptr, stride[0], t[1] ? t[1]->data_ptr() : nullptr, stride[1], s));
+} catch (...) {  // a tensor without storage
+  Py_RETURN_NONE;
+}
+
+// shared(q, kv_lens, page_table, k_pages, v_pages, group_offsets, prefix_lens, handle, out, out_lse, stream)
+PyObject* shared(PyObject*, PyObject* const* a, Py_ssize_t n) try {
+  const Handle* h = n == 11 ? handle(a[7]) : nullptr;
+  if (!h || !h->shared) Py_RETURN_NONE;
+  const at::Tensor *q = tensor(a[0]), *go = tensor(a[5]), *pl = tensor(a[6]), *out = tensor(a[8]), *lse = nullptr;
+  const int64_t qs = rows(q, 4, h->H, h);
+  tg_cache c;
+  tg_stream s;
+  if (qs < 0 || !cache(a[1], a[2], a[3], a[4], h, &c) || q->size(0) != c.batch || q->size(1) > kInt32) Py_RETURN_NONE;
+  const int64_t all = q->size(0) * q->size(1) * h->H, groups = pl ? pl->numel() : 0;
+  if (groups > kInt32 || !whole(pl, at::kInt, groups) || !whole(go, at::kLong, groups + 1) || !whole(out, h->type, all * h->D))
+    Py_RETURN_NONE;
+  if (a[9] != Py_None) {
+    lse = tensor(a[9]);
+    if (!whole(lse, at::kFloat, all)) Py_RETURN_NONE;
+  }
+  if (!stream_of(a[10], q, &s)) Py_RETURN_NONE;
+  return PyLong_FromLong(h->shared(q->data_ptr(), qs, static_cast<int32_t>(q->size(1)), &c,
+                                   static_cast<const int64_t*>(go->data_ptr()), static_cast<const int32_t*>(pl->data_ptr()),
+                                   static_cast<int32_t>(groups), h->cfg, out->data_ptr(),
+                                   lse ? static_cast<float*>(lse->data_ptr()) : nullptr, s));
+} catch (...) {  // a tensor without storage
+  Py_RETURN_NONE;
+}
+
 // prompt(q, k, v, q_offsets, kv_offsets, handle, out, out_lse, causal, stream)
 PyObject* prompt(PyObject*, PyObject* const* a, Py_ssize_t n) try {
   const Handle* h = n == 10 ? handle(a[5]) : nullptr;
@@ -209,6 +271,8 @@ PyMethodDef kMethods[] = {
     {"make", make, METH_VARARGS, "A handle for the calls below."},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(append)), METH_FASTCALL, "tg_cache_append, or None."},
     {"step", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(step)), METH_FASTCALL, "tg_attend_step, or None."},
+    {"read", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(read)), METH_FASTCALL, "tg_cache_read, or None."},
+    {"shared", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(shared)), METH_FASTCALL, "tg_attend_shared, or None."},
     {"prompt", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prompt)), METH_FASTCALL, "tg_attend_prompt, or None."},
     {nullptr, nullptr, 0, nullptr}};
 

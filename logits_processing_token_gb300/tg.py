@@ -19,7 +19,7 @@ TG_ERR_UNSUPPORTED = -2
 TG_ERR_CUDA = -3
 TG_ERR_OUT_OF_MEMORY = -4
 
-TG_DTYPE_F32, TG_DTYPE_BF16, TG_DTYPE_F16, TG_DTYPE_E4M3 = 0, 1, 2, 3
+TG_DTYPE_F32, TG_DTYPE_BF16, TG_DTYPE_F16, TG_DTYPE_E4M3, TG_DTYPE_I8 = 0, 1, 2, 3, 4
 TG_GREEDY, TG_SAMPLE = 0, 1
 
 TG_FLAG_HISTORY_ID_OUT_OF_RANGE = 0x1
@@ -43,7 +43,7 @@ EXPORTS = ("tg_params_init", "tg_config_create", "tg_config_destroy", "tg_select
            "tg_verify_history", "tg_select_state", "tg_process_state", "tg_set_wait_limit", "tg_status_word",
            "tg_config_view", "tg_config_selection",
            "tg_attn_params_init", "tg_attn_create", "tg_attn_destroy", "tg_attn_status_word", "tg_attn_clear_status",
-           "tg_cache_append", "tg_attend_step", "tg_attend_prompt")
+           "tg_cache_append", "tg_cache_read", "tg_attend_step", "tg_attend_shared", "tg_attend_prompt")
 TG_NOALLOC_MAX_BATCH = 1024
 
 
@@ -104,6 +104,7 @@ class tg_attn_params(ctypes.Structure):
         ("k_scales", POINTER(c_float)),
         ("v_scales", POINTER(c_float)),
         ("max_step_tokens", c_int32),
+        ("max_shared_tokens", c_int32),
     ]
 
 
@@ -204,10 +205,13 @@ def load_library(path: str | None = None):
     lib.tg_cache_append.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int32,
                                     POINTER(tg_cache), c_void_p, c_void_p, c_void_p, c_void_p]
     lib.tg_attend_step.argtypes = [c_void_p, c_int64, c_int32, POINTER(tg_cache), c_void_p, c_void_p, c_void_p, c_void_p]
+    lib.tg_cache_read.argtypes = [c_void_p, c_int32, POINTER(tg_cache), c_void_p, c_void_p, c_int64, c_void_p, c_int64, c_void_p]
+    lib.tg_attend_shared.argtypes = [c_void_p, c_int64, c_int32, POINTER(tg_cache), c_void_p, c_void_p, c_int32, c_void_p,
+                                     c_void_p, c_void_p, c_void_p]
     lib.tg_attend_prompt.argtypes = [c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_int64, c_void_p, c_void_p, c_int32,
                                      c_int32, c_int32, c_int32, c_void_p, c_void_p, c_void_p, c_void_p]
     for fn in ("tg_attn_create", "tg_attn_destroy", "tg_attn_status_word", "tg_attn_clear_status", "tg_cache_append",
-               "tg_attend_step", "tg_attend_prompt"):
+               "tg_cache_read", "tg_attend_step", "tg_attend_shared", "tg_attend_prompt"):
         getattr(lib, fn).restype = c_int
     for fn in ("tg_config_create", "tg_config_destroy", "tg_select", "tg_select_logprobs", "tg_verify", "tg_process",
                "tg_query_status", "tg_clear_status"):
@@ -578,13 +582,13 @@ def tg_status_string(status: int) -> str:
     return status_string(status)
 
 
-_ATTN_DTYPES = {"bf16": TG_DTYPE_BF16, "f16": TG_DTYPE_F16, "e4m3": TG_DTYPE_E4M3}
+_ATTN_DTYPES = {"bf16": TG_DTYPE_BF16, "f16": TG_DTYPE_F16, "e4m3": TG_DTYPE_E4M3, "i8": TG_DTYPE_I8}
 _PAGE_LAYOUTS = {"token": TG_PAGES_TOKEN_HEAD, "head": TG_PAGES_HEAD_TOKEN}
 
 
 def make_attn_params(num_heads, num_kv_heads, head_dim, dtype="bf16", cache_dtype=None, page_size=16,
                      page_layout="token", scale=0.0, rotary_dim=0, rotary_interleaved=False, inv_freq=None,
-                     k_scales=None, v_scales=None, max_step_tokens=0):
+                     k_scales=None, v_scales=None, max_step_tokens=0, max_shared_tokens=0):
     """A filled tg_attn_params plus the ctypes arrays its pointers refer to."""
     p = tg_attn_params()
     load_library().tg_attn_params_init(ctypes.byref(p), int(num_heads), int(num_kv_heads), int(head_dim))
@@ -607,11 +611,15 @@ def make_attn_params(num_heads, num_kv_heads, head_dim, dtype="bf16", cache_dtyp
         keep.append(arr)
         setattr(p, name, ctypes.cast(arr, POINTER(c_float)))
     p.max_step_tokens = int(max_step_tokens)
+    p.max_shared_tokens = int(max_shared_tokens)
     return p, keep
 
 
 class AttnConfig:
-    """Owns a tg_attn* (tg_attn_create / tg_attn_destroy); keyword arguments as make_attn_params."""
+    """Owns a tg_attn* (tg_attn_create / tg_attn_destroy); keyword arguments as make_attn_params.
+
+    page_shape is the shape of a page; page_bytes what a page takes, up to the next 16 bytes.  An i8 cache's pages are
+    rows of page_bytes (or more) of a uint8 tensor: codes, then scales (include/tg.h)."""
 
     def __init__(self, stream=None, **params):
         import torch
@@ -623,15 +631,23 @@ class AttnConfig:
         _check("tg_attn_create", lib.tg_attn_create(ctypes.byref(p), ctypes.byref(h), st))
         self.handle = h
         del keep
-        types = {TG_DTYPE_BF16: torch.bfloat16, TG_DTYPE_F16: torch.float16, TG_DTYPE_E4M3: torch.float8_e4m3fn}
+        types = {TG_DTYPE_BF16: torch.bfloat16, TG_DTYPE_F16: torch.float16, TG_DTYPE_E4M3: torch.float8_e4m3fn,
+                 TG_DTYPE_I8: torch.uint8}
         self.num_heads, self.num_kv_heads, self.head_dim = p.num_heads, p.num_kv_heads, p.head_dim
         self.page_size, self.max_step_tokens = p.page_size, p.max_step_tokens or 17
         self.dtype, self.cache_dtype = types[p.dtype], types[p.cache_dtype]
         G, P, D = p.num_kv_heads, p.page_size, p.head_dim
         self.page_shape = (P, G, D) if p.page_layout == TG_PAGES_TOKEN_HEAD else (G, P, D)
-        calls = [ctypes.cast(f, c_void_p).value for f in (lib.tg_cache_append, lib.tg_attend_step, lib.tg_attend_prompt)]
+        self.max_shared_tokens = p.max_shared_tokens
+        i8 = p.cache_dtype == TG_DTYPE_I8
+        self.page_bytes = -(-P * G * (D * self.cache_dtype.itemsize + (4 if i8 else 0)) // 16) * 16
+        if i8:
+            self.page_shape = (P * G * (D + 4),)
+        calls = [ctypes.cast(f, c_void_p).value for f in (lib.tg_cache_append, lib.tg_attend_step, lib.tg_attend_prompt,
+                                                          lib.tg_cache_read, lib.tg_attend_shared)]
         native = _load_binding()
-        self._native = native and native.make(h.value, p.num_heads, G, D, *self.page_shape[:2], p.dtype, p.cache_dtype, *calls)
+        page = (self.page_shape + (0,))[:2]
+        self._native = native and native.make(h.value, p.num_heads, G, D, *page, p.dtype, p.cache_dtype, *calls)
 
     def close(self):
         if self.handle:
@@ -694,6 +710,13 @@ def _pages(t, name, cfg):
         raise ValueError("%s must be a CUDA tensor" % name)
     if t.dtype != cfg.cache_dtype:
         raise ValueError("%s has dtype %s, expected %s" % (name, t.dtype, cfg.cache_dtype))
+    if len(cfg.page_shape) == 1:  # i8: rows of bytes
+        if t.dim() != 2 or t.shape[1] < cfg.page_shape[0]:
+            raise ValueError("%s must be [pages, %d bytes or more], not %s" % (name, cfg.page_shape[0], tuple(t.shape)))
+        if t.stride(1) != 1:
+            raise ValueError("%s: a page must be contiguous" % name)
+        n, size = t.shape
+        return t.data_ptr(), t.stride(0) if n > 1 else -(-size // 16) * 16, n
     n, x, y, D = (*t.shape, 0, 0, 0, 0)[:4]
     if t.dim() != 4 or (x, y, D) != cfg.page_shape:
         raise ValueError("%s must be [pages, %d, %d, %d], not %s" % ((name,) + cfg.page_shape + (tuple(t.shape),)))
@@ -724,7 +747,7 @@ def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, c
                     k_out=None, stream=None):
     """q [T, H, D] (or None), k and v [T, G, D]: the new tokens of all sequences, rows evenly spaced;
     q_offsets int64 [B + 1]; kv_lens int32 [B], the new tokens included; page_table int32 [B, max_pages];
-    k_pages and v_pages [pages, page_size, G, D] or [pages, G, page_size, D] as the config says;
+    k_pages and v_pages [pages, page_size, G, D] or [pages, G, page_size, D] as the config says (i8: uint8 [pages, page_bytes]);
     q_out [T, H, D] and k_out [T, G, D] (or None) take the rotated queries and keys."""
     native = getattr(cfg, "_native", None)
     if native is not None:
@@ -752,6 +775,31 @@ def tg_cache_append(q, k, v, q_offsets, kv_lens, page_table, k_pages, v_pages, c
     _check("tg_cache_append", st)
 
 
+def tg_cache_read(offsets, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, k=None, v=None, stream=None):
+    """k and v [T, G, D] (or None), rows evenly spaced: the last offsets[b + 1] - offsets[b] tokens of every sequence b
+    as the cache holds them; offsets int64 [B + 1]; the cache's tensors as tg_cache_append."""
+    native = getattr(cfg, "_native", None)
+    if native is not None:
+        st = _binding.read(offsets, kv_lens, page_table, k_pages, v_pages, native, k, v,
+                           None if stream is None else stream.cuda_stream)
+        if st is not None:
+            return _check("tg_cache_read", st)
+    import torch
+    G = cfg.num_kv_heads
+    if k is None and v is None:
+        raise ValueError("k or v is required")
+    if any(t is not None and t.dim() != 3 for t in (k, v)):
+        raise ValueError("k and v must be [tokens, heads, head_dim]")
+    T = (v if k is None else k).shape[0]
+    if v is not None and v.shape[0] != T:
+        raise ValueError("k and v must hold the same number of tokens")
+    kp, ks = _head_rows(k, "k", G, cfg) if k is not None else (None, 0)
+    vp, vs = _head_rows(v, "v", G, cfg) if v is not None else (None, 0)
+    cache, B = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
+    st = _lib.tg_cache_read(_whole(offsets, "offsets", torch.int64, B + 1), T, cache, cfg.handle, kp, ks, vp, vs, _stream(stream))
+    _check("tg_cache_read", st)
+
+
 def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, out, out_lse=None, stream=None):
     """q and out [B, n, H, D]: the last n tokens of every sequence; out_lse f32 [B, n, H] or None; the cache's
     tensors as tg_cache_append."""
@@ -774,6 +822,36 @@ def tg_attend_step(q, kv_lens, page_table, k_pages, v_pages, cfg: AttnConfig, ou
         qp, qs, n, cache, cfg.handle, _whole(out, "out", cfg.dtype, B * n * H * D),
         _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _stream(stream))
     _check("tg_attend_step", st)
+    return out
+
+
+def tg_attend_shared(q, kv_lens, page_table, k_pages, v_pages, group_offsets, prefix_lens, cfg: AttnConfig, out, out_lse=None,
+                     stream=None):
+    """tg_attend_step for sequences that have a prefix in common: group_offsets int64 [groups + 1], group i is sequences
+    group_offsets[i] .. group_offsets[i + 1] - 1; prefix_lens int32 [groups], the tokens that all of them begin with."""
+    native = getattr(cfg, "_native", None)
+    if native is not None:
+        st = _binding.shared(q, kv_lens, page_table, k_pages, v_pages, group_offsets, prefix_lens, native, out, out_lse,
+                             None if stream is None else stream.cuda_stream)
+        if st is not None:
+            _check("tg_attend_shared", st)
+            return out
+    import torch
+    if q.dim() != 4:
+        raise ValueError("q must be [batch, n, heads, head_dim]")
+    B, n, H, D = q.shape
+    if B * n > cfg.max_shared_tokens:
+        raise ValueError("q holds %d tokens, the config's max_shared_tokens is %d" % (B * n, cfg.max_shared_tokens))
+    cache, rows = _cache(cfg, k_pages, v_pages, page_table, kv_lens)
+    if rows != B:
+        raise ValueError("q holds %d sequences, page_table %d" % (B, rows))
+    groups = prefix_lens.numel()
+    qp, qs = _head_rows(q, "q", cfg.num_heads, cfg)
+    st = _lib.tg_attend_shared(
+        qp, qs, n, cache, _whole(group_offsets, "group_offsets", torch.int64, groups + 1),
+        _whole(prefix_lens, "prefix_lens", torch.int32, groups), groups, cfg.handle, _whole(out, "out", cfg.dtype, B * n * H * D),
+        _whole(out_lse, "out_lse", torch.float32, B * n * H) if out_lse is not None else None, _stream(stream))
+    _check("tg_attend_shared", st)
     return out
 
 
