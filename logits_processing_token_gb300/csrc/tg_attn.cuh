@@ -43,6 +43,12 @@ struct AttnCfg {
   int step_slots;          // workspace slots (two per CTA)
   float* ws_o;             // [slots][step_rows][D]
   float2* ws_ml;           // [slots][step_rows]: running maximum (base 2) and sum
+  int* ws_start;           // [max_shared]: keys of a sequence that its group's prefix pass took
+  int4* ws_pre;            // [max_shared][pairs of key heads]: where that pass left a token's sums (PrefixAt)
+  float* ws_pre_o;         // [max_shared][H][D]: sums of prefixes that one CTA had whole
+  float2* ws_pre_ml;       // [max_shared][H]: reference (base 2) and sum
+  float* ws_part_o;        // [4 x CTAs][kPrefixRows][D]: parts of the others
+  float2* ws_part_ml;
   unsigned* ws_count;      // [slots / 2]: parts of a split sequence that are done; zero between calls
   int nsm;
   int step_ctas[5];        // CTAs per SM of the step kernel's row variants
@@ -82,6 +88,12 @@ struct StepArgs {
   CacheView c;
   void* out;
   float* lse;
+  // a shared call's two passes: prefixes for whole groups (prefix), then each
+  // sequence's own keys (own), joined with its group's
+  int prefix, own;
+  const int64_t* goff;
+  const int32_t* plens;
+  int groups;
 };
 
 struct ReadArgs {
@@ -105,13 +117,18 @@ struct PromptArgs {
 cudaError_t prepare_step(AttnCfg* c);
 cudaError_t prepare_prompt(AttnCfg* c);
 cudaError_t prepare_wide(const AttnCfg& c);
+// by kind of cache; a null: prepare
+cudaError_t wide_e4m3(const AttnCfg& c, const StepArgs* a, cudaStream_t s);
+cudaError_t wide_i8(const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_read(const AttnCfg& c, const ReadArgs& a, cudaStream_t s);
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
+cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
 cudaError_t step_e4m3(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t step_i8(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, 16-bit cache
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
+constexpr int kPrefixRows = 128;  // of a part of a shared call's prefix
 // CTAs of the step kernel per SM at most (they size the handle's workspace).
 constexpr int kStepCtasPerSm = 4;
 
@@ -259,6 +276,21 @@ __device__ __forceinline__ unsigned tile_at(int r, int c) {
   }
 }
 
+// Two bytes of an i8 cache, or of an e4m3 one, to two bf16, exactly.  Bytes u of
+// code + 128 behind 0x43: without u's top bit 128 + (u & 127), from which 256 goes,
+// or 128 where that bit was set.
+template <int CK, unsigned SEL>
+__device__ __forceinline__ unsigned bytes_to_bf16x2(unsigned w) {
+  if constexpr (CK == kI8) {
+    const unsigned y = __byte_perm(w, 0x43434343u, SEL | 0x4040u), x = y & 0xff7fff7fu, less = (y & 0x00800080u) ^ 0x43804380u;
+    const __nv_bfloat162 d = __hsub2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&less));
+    return *reinterpret_cast<const unsigned*>(&d);
+  } else {
+    const float2 f = unpack2<true>(e4m3x2_to_f16x2(SEL == 0x0100 ? w & 0xffff : w >> 16));
+    return pack2<false>(f.x, f.y);
+  }
+}
+
 // Barriers in shared memory.
 __device__ __forceinline__ void bar_init(unsigned long long* b, unsigned n) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(sptr(b)), "r"(n) : "memory");
@@ -328,6 +360,58 @@ __device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, 
   asm volatile(
       "cp.async.bulk.tensor.4d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(sptr(bar)) : "memory");
+}
+
+// What a shared call's prefix pass left for one token and key head: the parts of
+// its group's item and the token's rows in it.
+struct PrefixAt {
+  int c0, parts, row;  // first CTA; how many (0: no prefix, 1: in ws_pre_o); the token's first row of the tile
+};
+__device__ __forceinline__ PrefixAt prefix_at(const AttnCfg& c, long long token, int g) {
+  const int4 x = __ldcg(c.ws_pre + token * ((c.G + 1) >> 1) + (g >> 1));
+  return PrefixAt{x.x, x.y, x.z};
+}
+// A part's rows in the workspace of tg_wide.cuh: by CTA, whether the item began in
+// it, and which of the two key heads.
+__device__ __forceinline__ long long wide_part(int slot_rows, long long cta, int begun, int t) {
+  return ((2 * cta + begun) * 2 + t) * slot_rows;
+}
+// Joins a row's sums with its group's prefix: acc, four columns from d, weights'
+// reference ref (base 2; a weight is 2^(score - ref)) and sum l.
+__device__ __forceinline__ void join_prefix(const AttnCfg& c, const PrefixAt& at, long long token, int h, int d, float4& acc,
+                                            float& ref, float& l) {
+  constexpr int PB = 8;  // parts whose reads are in flight
+  const int g = h / c.rep;
+  for (int p0 = 0; p0 < at.parts; p0 += PB) {
+    float2 x[PB];
+    float4 v[PB];
+#pragma unroll
+    for (int p = 0; p < PB; ++p) {
+      const int q = min(p0 + p, at.parts - 1);
+      const long long sl = wide_part(kPrefixRows, at.c0 + q, q == 0, g & 1) + at.row + (h - g * c.rep);
+      const long long row = token * c.H + h;
+      x[p] = at.parts == 1 ? __ldcg(c.ws_pre_ml + row) : __ldcg(c.ws_part_ml + sl);
+      v[p] = __ldcg(reinterpret_cast<const float4*>((at.parts == 1 ? c.ws_pre_o + row * c.D : c.ws_part_o + sl * c.D) + d));
+    }
+    float top = l == 0.0f ? -INFINITY : ref;
+#pragma unroll
+    for (int p = 0; p < PB; ++p)
+      if (p0 + p < at.parts && x[p].y != 0.0f) top = fmaxf(top, x[p].x);
+    const float f = l == 0.0f ? 0.0f : ex2(ref - top);
+    l *= f;
+    acc = l == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
+    ref = top;
+#pragma unroll
+    for (int p = 0; p < PB; ++p) {
+      if (p0 + p >= at.parts || x[p].y == 0.0f) continue;  // (a part in which the row saw no key)
+      const float e = ex2(x[p].x - top);
+      l += x[p].y * e;
+      acc.x += v[p].x * e;
+      acc.y += v[p].y * e;
+      acc.z += v[p].z * e;
+      acc.w += v[p].w * e;
+    }
+  }
 }
 
 // Weights exp2(s - m) of f16 products are stored times 2^8: a weight 2^-33 of

@@ -65,6 +65,17 @@ tg::CacheView view_of(const tg_cache* c) {
   return v;
 }
 
+tg::StepArgs step_args(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, void* out, float* out_lse) {
+  tg::StepArgs a{};
+  a.q = q;
+  a.qs = q_stride;
+  a.n = n;
+  a.c = view_of(cache);
+  a.out = out;
+  a.lse = out_lse;
+  return a;
+}
+
 bool positive(const float* p, int n) {
   for (int i = 0; p && i < n; ++i)
     if (!(p[i] > 0.0f) || !std::isfinite(p[i])) return false;
@@ -164,7 +175,13 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   const size_t o_turn = 0, o_ks = up16(o_turn + half * sizeof(unsigned long long)), o_vs = up16(o_ks + d.G * 4),
                o_kd = up16(o_vs + d.G * 4), o_vd = o_kd + d.G * sizeof(float4), o_cnt = o_vd + d.G * sizeof(float4), o_st = up16(o_cnt + d.step_slots / 2 * 4), o_ml = up16(o_st + 12);
   const size_t rows = static_cast<size_t>(d.step_slots) * d.step_rows;
-  const size_t o_o = (o_ml + rows * sizeof(float2) + 255) / 256 * 256, bytes = o_o + rows * d.D * 4;  // 32-byte stores
+  const auto up256 = [](size_t n) { return (n + 255) / 256 * 256; };  // 32-byte stores
+  const size_t o_o = up256(o_ml + rows * sizeof(float2));
+  // a shared call's: where each sequence's own keys begin, where its prefix's sums are, and those
+  const size_t shared = d.max_shared, part_rows = shared ? static_cast<size_t>(4) * d.nsm * tg::kPrefixRows : 0;
+  const size_t o_start = up256(o_o + rows * d.D * 4), o_pre = up256(o_start + shared * 4),
+               o_pml = up256(o_pre + shared * ((d.G + 1) / 2) * sizeof(int4)), o_po = up256(o_pml + shared * d.H * sizeof(float2)),
+               o_tml = up256(o_po + shared * d.H * d.D * 4), o_to = up256(o_tml + part_rows * sizeof(float2)), bytes = o_to + part_rows * d.D * 4;
   unsigned char* host = new (std::nothrow) unsigned char[o_ml]();
   if (!host) { delete cfg; return TG_ERR_OUT_OF_MEMORY; }
   for (int i = 0; i < half; ++i) {
@@ -186,6 +203,9 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   e = cudaMalloc(&cfg->dmem, bytes);
   if (e == cudaSuccess)
     e = cudaMemcpyAsync(cfg->dmem, host, o_ml, cudaMemcpyHostToDevice, reinterpret_cast<cudaStream_t>(stream));
+  // (what no pass has written yet names no part)
+  if (e == cudaSuccess && shared)
+    e = cudaMemsetAsync(static_cast<unsigned char*>(cfg->dmem) + o_start, 0, o_pml - o_start, reinterpret_cast<cudaStream_t>(stream));
   const cudaError_t e2 = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = e2;
   delete[] host;
@@ -201,6 +221,12 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.prompt_count = d.status + 1;
   d.ws_ml = reinterpret_cast<float2*>(m + o_ml);
   d.ws_o = reinterpret_cast<float*>(m + o_o);
+  d.ws_start = reinterpret_cast<int*>(m + o_start);
+  d.ws_pre = reinterpret_cast<int4*>(m + o_pre);
+  d.ws_pre_ml = reinterpret_cast<float2*>(m + o_pml);
+  d.ws_pre_o = reinterpret_cast<float*>(m + o_po);
+  d.ws_part_ml = reinterpret_cast<float2*>(m + o_tml);
+  d.ws_part_o = reinterpret_cast<float*>(m + o_to);
   *out = cfg;
   return TG_OK;
 }
@@ -291,7 +317,14 @@ tg_status tg_attend_shared(const void* q, int64_t q_stride, int32_t n, const tg_
   const tg::AttnCfg& d = cfg->dev;
   if (static_cast<int64_t>(cache->batch) * n > d.max_shared || (groups > 0 && (!group_offsets || !prefix_lens)))
     return TG_ERR_INVALID_ARGUMENT;
-  return tg_attend_step(q, q_stride, n, cache, cfg, out, out_lse, stream);
+  if (!rows_ok(q, q_stride, d.H * d.D) || !cache_ok(cache, d) || !out || !aligned16(out)) return TG_ERR_INVALID_ARGUMENT;
+  const tg_status st = check_device(cfg);
+  if (st != TG_OK) return st;
+  tg::StepArgs a = step_args(q, q_stride, n, cache, out, out_lse);
+  a.goff = group_offsets;
+  a.plens = prefix_lens;
+  a.groups = groups;
+  return from_cuda(tg::launch_shared(launch_cfg(cfg), a, reinterpret_cast<cudaStream_t>(stream)));
 }
 
 tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const tg_attn* cfg,
@@ -302,14 +335,7 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
   if (!rows_ok(q, q_stride, d.H * d.D) || !cache_ok(cache, d) || !out || !aligned16(out)) return TG_ERR_INVALID_ARGUMENT;
   const tg_status st = check_device(cfg);
   if (st != TG_OK) return st;
-  tg::StepArgs a{};
-  a.q = q;
-  a.qs = q_stride;
-  a.n = n;
-  a.c = view_of(cache);
-  a.out = out;
-  a.lse = out_lse;
-  return from_cuda(tg::launch_step(launch_cfg(cfg), a, reinterpret_cast<cudaStream_t>(stream)));
+  return from_cuda(tg::launch_step(launch_cfg(cfg), step_args(q, q_stride, n, cache, out, out_lse), reinterpret_cast<cudaStream_t>(stream)));
 }
 
 tg_status tg_attend_prompt(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,

@@ -39,7 +39,8 @@ namespace {
 
 // Everything about a unit that the computing warps need.
 struct Unit {
-  int b, g, rt, tile, len;  // b < 0: no more units
+  int b, g, rt, key0, len;  // b < 0: no more units; key0: its first key
+  int from;                 // its sequence's first key: 0, or behind a shared prefix
   int any_bad;
   int first, last;          // of its item in this CTA
   long long base;           // the item's number of units before it
@@ -98,7 +99,7 @@ struct Shape {
 constexpr int kMaxStages = 8;
 struct Head {
   unsigned long long full[kMaxStages], empty[kMaxStages], q_full[2], q_empty[2], meet;
-  int dead, last, first_b, first_len;
+  int dead, last, first_b, first_len, first_from;
   long long first_in;
   long long wsum[16];
   UnitMeta meta[kMaxStages];
@@ -114,7 +115,9 @@ __device__ __forceinline__ unsigned key_at(int r, int c) {
   else return tile_at<RB>(r, c);
 }
 
-template <int DP, bool MF16, bool QF16, int CK, int WMX, int WN>
+// OWN: the second pass of a shared call, over each sequence's keys behind its
+// group's prefix.
+template <int DP, bool MF16, bool QF16, int CK, int WMX, int WN, bool OWN>
 __global__ void __launch_bounds__(32 * ((WMX ? WMX : 1) * WN + 1), WMX * WN > 4 ? 1 : 2)
 step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int box, const __grid_constant__ CUtensorMap mk,
             const __grid_constant__ CUtensorMap mv) {
@@ -166,17 +169,19 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   // ---- this CTA's units -------------------------------------------------
   const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
   const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
-  const auto tiles_of = [](int len) { return len > 0 ? (len + KT - 1) / KT : 1; };
-  const auto cost = [&](int len) { return tiles_of(len) + kItemCost; };
+  const auto from_of = [&](int b, int l) { return OWN ? min(c.ws_start[b], l) : 0; };  // keys of the group's prefix
+  const auto tiles_of = [](int keys) { return keys > 0 ? (keys + KT - 1) / KT : 1; };
+  const auto cost = [&](int keys) { return tiles_of(keys) + kItemCost; };
   const int per_tile = c.G * row_tiles;
   const int bper = (a.c.batch + NT - 1) / NT, b_first = tid * bper;
   long long mine = 0;
-  int len0 = 0;  // of this thread's first sequence
+  int len0 = 0, from0 = 0;  // of this thread's first sequence
   for (int b = b_first; b < min(a.c.batch, b_first + bper); ++b) {
     const int raw = a.c.lens[b], l = checked(raw);
     if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
-    if (b == b_first) len0 = l;
-    mine += cost(l);
+    const int f = from_of(b, l);
+    if (b == b_first) { len0 = l; from0 = f; }
+    mine += cost(l - f);
   }
   long long before = mine;
 #pragma unroll
@@ -199,35 +204,38 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   if (blockIdx.x >= N) return;
   const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
   if (mine > 0 && before * per_tile <= u0 && u0 < (before + mine) * per_tile) {
-    int b = b_first, l = len0;
+    int b = b_first, l = len0, f = from0;
     long long at = before;
     for (;;) {
-      const int t = cost(l);
+      const int t = cost(l - f);
       if ((at + t) * per_tile > u0) break;
       at += t;
       l = checked(a.c.lens[++b]);
+      f = from_of(b, l);
     }
     hd->first_b = b;
     hd->first_len = l;
+    hd->first_from = f;
     hd->first_in = u0 - at * per_tile;
   }
   __syncthreads();
   if (warp == NW) {
     // ---- pages and copies ---------------------------------------------------
-    int b = hd->first_b, len = hd->first_len, nt = tiles_of(len);
-    const int skip = static_cast<int>(hd->first_in / cost(len));
+    int b = hd->first_b, len = hd->first_len, from = hd->first_from, nt = tiles_of(len - from);
+    const int skip = static_cast<int>(hd->first_in / cost(len - from));
     int rt = skip % row_tiles, g = skip / row_tiles;
-    long long base = u0 - hd->first_in % cost(len);  // units before the item
+    long long base = u0 - hd->first_in % cost(len - from);  // units before the item
     // its tiles that are this CTA's: tile .. tend - 1
     int tile = static_cast<int>(max(0ll, u0 - base - kItemCost)), tend = static_cast<int>(min(static_cast<long long>(nt), u1 - base - kItemCost));
     int len_next = b + 1 < a.c.batch ? checked(a.c.lens[b + 1]) : 0;
+    int from_next = b + 1 < a.c.batch ? from_of(b + 1, len_next) : 0;
     const int R = tensor_copies ? box : 1;  // keys of one copy
     const int shift = R == 1 ? 0 : 31 - __clz(R);
     const auto entry = [&](int bb, int key, int ln) {  // the page of a key, -1 past the end
       return key < ln ? __ldg(a.c.table + bb * a.c.table_stride + (key >> c.page_shift)) : -1;
     };
     // lane i: the page of copy i of the tile (of key i, 32 apart, without tensor copies)
-    int id = tensor_copies && lane < (KT >> shift) ? entry(b, tile * KT + (lane << shift), len) : -1;
+    int id = tensor_copies && lane < (KT >> shift) ? entry(b, from + tile * KT + (lane << shift), len) : -1;
     int qs = 0;
     unsigned q_ph = 1;
     bool ok = true, first = true;
@@ -252,7 +260,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       }
       // the following unit, and its pages while this one's stage is awaited
       const bool last = tile + 1 == tend;
-      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nnt = nt, ntend = tend;
+      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nfrom = from, nnt = nt, ntend = tend;
       long long nbase = base;
       if (last) {
         ntile = 0;
@@ -263,18 +271,20 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             ng = 0;
             ++nb;
             nlen = len_next;
-            nnt = tiles_of(nlen);
+            nfrom = from_next;
+            nnt = tiles_of(nlen - nfrom);
             len_next = nb + 1 < a.c.batch ? checked(a.c.lens[nb + 1]) : 0;
+            from_next = nb + 1 < a.c.batch ? from_of(nb + 1, len_next) : 0;
           }
         }
         ntend = static_cast<int>(min(static_cast<long long>(nnt), u1 - nbase - kItemCost));
       }
-      const int id_next = tensor_copies && nbase + kItemCost < u1 && lane < (KT >> shift) ? entry(nb, ntile * KT + (lane << shift), nlen) : -1;
+      const int id_next = tensor_copies && nbase + kItemCost < u1 && lane < (KT >> shift) ? entry(nb, nfrom + ntile * KT + (lane << shift), nlen) : -1;
       ok = bar_wait(&hd->dead, &hd->empty[st], e_ph, c);
       if (!ok) break;
       const unsigned ks = sptr(stages + st * S::kStage), vs = ks + S::kMat;
       if (tensor_copies) {
-        const int key = tile * KT + (lane << shift);
+        const int key = from + tile * KT + (lane << shift);
         const bool in = lane < (KT >> shift) && key < len;
         const bool bad = in && (id < 0 || id >= a.c.num_pages);
         if (bad) atomicOr(c.status, kAttnBadPage);
@@ -289,7 +299,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           hd->meta[st].bad[lane] = w;
         }
         if (lane == 0) {
-          hd->meta[st].u = Unit{b, g, rt, tile, len, badm != 0, first, last, base};
+          hd->meta[st].u = Unit{b, g, rt, from + tile * KT, len, from, badm != 0, first, last, base};
         }
         __syncwarp();
         if (lane == 0) bar_expect(&hd->full[st], copies * R * 2 * (RB + (I8 ? 4 : 0)));
@@ -315,7 +325,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         const long long head = g * c.head_stride;
         unsigned any_bad = 0;
         for (int k0 = 0; k0 < KT; k0 += 32) {
-          const int key = tile * KT + k0 + lane;
+          const int key = from + tile * KT + k0 + lane;
           const int page = entry(b, key, len);
           const bool bad = key < len && (page < 0 || page >= a.c.num_pages);
           if (bad) atomicOr(c.status, kAttnBadPage);
@@ -334,19 +344,19 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             const int r = (k + lane) / CPR, cc = (k + lane) % CPR;
             const int pg = __shfl_sync(~0u, good, r);
             if (cc >= chunks) continue;
-            const long long in = head + ((tile * KT + k0 + r) & (c.page_size - 1)) * c.slot_stride;
+            const long long in = head + ((from + tile * KT + k0 + r) & (c.page_size - 1)) * c.slot_stride;
             const long long p0 = pg < 0 ? 0 : pg;
             const unsigned at = key_at<RB, KT>(k0 + r, cc);
             cp16(ks + at, static_cast<const char*>(a.c.k) + (p0 * a.c.k_page_stride + in) * ES + cc * 16, pg >= 0);
             cp16(vs + at, static_cast<const char*>(a.c.v) + (p0 * a.c.v_page_stride + in) * ES + cc * 16, pg >= 0);
           }
         }
-        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, tile, len, any_bad != 0, first, last, base};
+        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, from + tile * KT, len, from, any_bad != 0, first, last, base};
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
         __syncwarp();
         if (lane == 0) bar_arrive(&hd->full[st]);
       }
-      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; nt = nnt; tend = ntend; base = nbase; id = id_next;
+      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; from = nfrom; nt = nnt; tend = ntend; base = nbase; id = id_next;
       first = last;
     }
     int used = i;  // stages used: the units, and the end
@@ -465,7 +475,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 
   const auto compute = [&](unsigned char* stage, const unsigned* bad) {
     const unsigned ks = sptr(stage), vs = ks + S::kMat;
-    const int base = cur.tile * KT + wn * KW;
+    const int base = cur.key0 + wn * KW;
     if (base >= cur.len || cur.rt * S::kRows + wm * 16 >= rows_all) return;
     // Values of keys that do not exist are whatever their page holds, and
     // 0 x NaN is not 0: zero them.
@@ -493,7 +503,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 #pragma unroll 1
     for (int k0 = 0; k0 < KW; k0 += KC) {
       const int at = wn * KW + k0;
-      if (cur.tile * KT + at >= cur.len) break;
+      if (cur.key0 + at >= cur.len) break;
       // Scores: s[i] of 8 keys (lane / 4 and 8 more rows), or, T, of 16 keys:
       // keys lane / 4 and 8 more, columns the two rows.
       constexpr int NS = T ? KC / 16 : KC / 8;
@@ -579,14 +589,14 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           }
       }
       // mask: the end of what a row sees, and keys of bad pages
-      if (cur.tile * KT + at + KC > cur.len - a.n + 1 || cur.any_bad) {
+      if (cur.key0 + at + KC > cur.len - a.n + 1 || cur.any_bad) {
         const unsigned bw = bad[at >> 5] >> (at & 31);
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
           for (int x = 0; x < 4; ++x) {
             const int in = T ? i * 16 + (lane >> 2) + 8 * (x >> 1) : i * 8 + 2 * (lane & 3) + (x & 1);
-            if (cur.tile * KT + at + in >= lim[T ? x & 1 : x >> 1] || ((bw >> in) & 1)) s[i][x] = -INFINITY;
+            if (cur.key0 + at + in >= lim[T ? x & 1 : x >> 1] || ((bw >> in) & 1)) s[i][x] = -INFINITY;
           }
       }
       float sub[2];
@@ -719,12 +729,29 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     return ll == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
   };
 
+  // A finished row's four columns from d: joined with the group's prefix, if there
+  // is one, divided, and written.
+  const auto put_row = [&](int r, int d, float4 x, float mm, float ll, float vs) {
+    const long long row = out_row(r);
+    if (OWN && cur.from > 0) {
+      const long long token = static_cast<long long>(cur.b) * a.n + r / c.rep;
+      const PrefixAt at = prefix_at(c, token, cur.g);
+      float ref = mm - bias;
+      x = make_float4(x.x * vs, x.y * vs, x.z * vs, x.w * vs);
+      join_prefix(c, at, token, cur.g * c.rep + r % c.rep, d, x, ref, ll);
+      mm = ref + bias;
+      vs = 1.0f;
+    }
+    put4(row, d, divided(x, ll, vs));
+    if (d == 0) put_lse(row, mm, ll);
+  };
+
   // The item's end in this CTA: join the warps, then write the result, or this
   // CTA's part of it.
   const auto end_item = [&]() {
     // the CTAs with the item's first and last tile
     const long long tile0 = cur.base + kItemCost;
-    const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(cur.len)) * N - 1) / U;
+    const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(cur.len - cur.from)) * N - 1) / U;
     const bool whole = c0 == c1;
     const long long slot = 2ll * blockIdx.x + (tile0 < u0 ? 0 : 1);
     float* po = c.ws_o + slot * c.step_rows * c.D;
@@ -815,9 +842,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             acc.w = fmaf(g, v.w, acc.w);
           }
           if (whole) {
-            const long long row = out_row(row_base + r);
-            put4(row, d, divided(acc, ll, vs));
-            if (d == 0) put_lse(row, top, ll);
+            put_row(row_base + r, d, acc, top, ll, vs);
           } else {
             *reinterpret_cast<float4*>(po + r * c.D + d) = acc;
             if (d == 0) pml[r] = make_float2(top, ll);
@@ -912,9 +937,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             acc.w += f * v[p].w;
           }
         }
-        const long long row = out_row(row_base + r);
-        put4(row, d, divided(acc, ll, vs));
-        if (d == 0) put_lse(row, mm, ll);
+        put_row(row_base + r, d, acc, mm, ll, vs);
       }
     }
   };
@@ -948,8 +971,12 @@ int row_variant(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ?
 template <int DP, bool MF16, bool QF16, int CK, int WM, int WN>
 cudaError_t prepare_one(int* ctas) {
   using S = Shape<DP, CK, WM, WN>;
-  auto k = step_kernel<DP, MF16, QF16, CK, WM, WN>;
+  auto k = step_kernel<DP, MF16, QF16, CK, WM, WN, false>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  if constexpr (WM < 2) {
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(step_kernel<DP, MF16, QF16, CK, WM, WN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+  }
   if (e != cudaSuccess) return e;
   int occ = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, S::kThreads, S::kSmem);
@@ -994,7 +1021,10 @@ cudaError_t launch_one(const AttnCfg& c, const StepArgs& a, int variant, cudaStr
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, CK, WM, WN>, c, a, row_tiles, 2, box, mk, mv);
+  if constexpr (WM < 2) {  // (more than 16 rows of a shared call: tg_wide.cuh)
+    if (a.own) return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, CK, WM, WN, true>, c, a, row_tiles, 2, box, mk, mv);
+  }
+  return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, CK, WM, WN, false>, c, a, row_tiles, 2, box, mk, mv);
 }
 
 template <int DP, bool MF16, bool QF16, int CK>

@@ -1,0 +1,888 @@
+// tg_attend_step with many rows (several new tokens of every sequence, as in a
+// verify step), and the prefixes of tg_attend_shared, whose rows are those of all
+// of a group's sequences, on the fifth-generation tensor cores.
+//
+// The split over the GPU, the parts and their join are those of tg_step.cu, the
+// matrix instructions and the softmax those of tg_prompt.cu.  A tile is 128
+// keys of one (sequence, key head) against up to 128 rows, whole tokens times
+// the query heads that share the key head; two key heads of a sequence go side
+// by side, so that the softmax of one runs while the other's products do.
+// With 68 rows the warp-wide instructions of tg_step.cu take four times as long
+// as the copies (32 sequences of 256 to 4,096 keys, 17 tokens: 177 us); here the
+// copies bound the stream, 50 us of 74 (floor 42), and the look-ups at the
+// beginning (5) and the joins at the end (10) do the rest.
+//
+// An 8-bit cache is copied as it is into stages of its own, and six warps widen
+// each tile, exactly, into one that the matrix instructions read: keys to the
+// queries' type, values to f16, as the weights are.  The scales of an i8 cache enter
+// in the softmax: a score times its key's, a weight times its value's relative to
+// about the largest so far (a power of f16's range apart would be lost), by which
+// the sums are multiplied at the end.
+//
+// A prefix item is a (group, key head, row tile): the tokens of the group's
+// sequences are neighbours in q.  Its parts are not joined here but where each
+// sequence's own keys are (join_prefix): those rows are spread over the GPU.
+//
+// One translation unit per kind of cache (tg_wide.cu, tg_wide_e4m3.cu,
+// tg_wide_i8.cu); internal to the library.
+#pragma once
+
+#include <algorithm>
+
+#include "tg_mma5.cuh"
+
+namespace tg {
+namespace {
+
+constexpr int kKeysW = 128;
+constexpr int kItemCostW = 2;   // beginning and ending an item, in tiles
+
+struct WItem {
+  int b, pair, rt, len;  // b: sequence or group, < 0: no more; len: where its keys end
+  int from;              // and begin
+  int tok0, toks;        // its first row's token in q, and the tokens from there on
+  int t0, t1;            // its tiles that are this CTA's
+  int nch;               // key heads side by side: 2, or 1 at the end of an odd number
+  long long base;        // units before it
+};
+
+// An entry of the work, a sequence or a group: where its keys end and begin, its
+// tokens in q, its row tiles.
+struct Entry {
+  int len, from, tok, toks, row_tiles;
+};
+
+constexpr int kSlotsMaxW = 10, kMetas = 8;
+struct WBars {
+  unsigned long long q_full, q_empty, kv_full[kSlotsMaxW], kv_empty[kSlotsMaxW], raw_full[kSlotsMaxW], raw_empty[kSlotsMaxW],
+      s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
+  unsigned tmem;
+  int dead, last[2], first_b;
+  Entry first;
+  long long first_in, wsum[16];
+  WItem item[2];
+  unsigned bad[kMetas][4];  // by tile, round the ring: keys on pages that do not exist
+  float2 fac[kMetas][2];    // i8, by tile and key head: what the sums shrink by first; the scale the values are relative to
+};
+
+// Warps 0 to 7: softmax, one warpgroup per key head; 8: matrix instructions; 9:
+// items and copies; an 8-bit cache: 10 to 15 widen.
+// Registers of the softmax's two warpgroups, the third and the fourth: their
+// threads times these are what the block is launched with (8-bit: 128 each).
+template <int DP, int CK>
+struct WLay {
+  static constexpr bool Q8 = CK != kC16;
+  static constexpr int kThreads = Q8 ? 512 : 384;
+  static constexpr int kRegSoftmax = Q8 ? 192 : 208, kRegThird = Q8 ? 72 : 88, kRegFourth = 56;
+  static constexpr int kWideners = Q8 ? 6 : 0;
+  static constexpr int kTileB = DP / 64 * kBlock;
+  static constexpr int kSlots = Q8 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
+  static constexpr int kRawB = kKeysW * DP;                       // a tile as the cache has it
+  static constexpr int kRaw = Q8 ? (DP == 128 ? 3 : 6) : 0;
+  // A tile's scales are read until its products are done.  By then at most kRaw +
+  // kSlots pieces (keys or values of one key head, two a tile at least) are past it.
+  static constexpr int kScaleTiles = DP == 128 ? 4 : 8;
+  static_assert(2 * kScaleTiles - kRaw - kSlots >= 1 && kScaleTiles <= kMetas, "");
+  static constexpr int kScaleB = CK == kI8 ? kScaleTiles * 2 * 2 * kKeysW * 4 : 0;  // [tile][head][keys, values][128]
+  static constexpr int kKv = 2 * kTileB, kRawAt = kKv + kSlots * kTileB, kScaleAt = kRawAt + kRaw * kRawB, kBars = kScaleAt + kScaleB;
+  static constexpr int kSmem = kBars + static_cast<int>(sizeof(WBars)) + 1024;
+  static_assert(kSmem <= 227 * 1024, "");
+};
+
+struct WSetup {
+  int tpt;        // tokens of a row tile
+  int row_tiles;  // (of a sequence; of a group: by its size)
+  int pairs;      // of key heads
+  int box;        // keys of one copy
+  int wide;       // outputs 32-byte aligned
+};
+
+// Sixteen 8-bit elements to 16 bits.
+template <int CK, bool F16>
+__device__ __forceinline__ void widen16(const uint4& r, unsigned (&w)[8]) {
+  const unsigned in[4] = {r.x, r.y, r.z, r.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[2 * i] = F16 ? low2<CK>(in[i]) : bytes_to_bf16x2<CK, 0x0100>(in[i]);
+    w[2 * i + 1] = F16 ? high2<CK>(in[i]) : bytes_to_bf16x2<CK, 0x0302>(in[i]);
+  }
+}
+
+// What a launch does: a step; a shared call's prefixes of groups; each sequence's own
+// keys behind them.
+enum Pass { kStepPass, kPrefixPass, kOwnPass };
+
+// F16: the tensors' type is f16, else bf16.
+template <int DP, bool F16, int CK, Pass PASS>
+__global__ void __launch_bounds__(WLay<DP, CK>::kThreads, 1)
+wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_constant__ CUtensorMap mq,
+            const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
+  using L = WLay<DP, CK>;
+  constexpr bool Q8 = L::Q8, I8 = CK == kI8;
+  constexpr bool SHARED = PASS == kPrefixPass, OWN = PASS == kOwnPass;
+  constexpr bool PF16 = Q8 || F16;  // the weights' type, and the values'
+  constexpr int NT = L::kThreads;
+  extern __shared__ unsigned char smem_raw[];
+  unsigned char* smem = smem_raw + ((1024 - (sptr(smem_raw) & 1023)) & 1023);
+  WBars* s = reinterpret_cast<WBars*>(smem + L::kBars);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    bar_init(&s->q_full, 1);
+    bar_init(&s->q_empty, 1);
+    for (int i = 0; i < L::kSlots; ++i) { bar_init(&s->kv_full[i], Q8 ? L::kWideners : 1); bar_init(&s->kv_empty[i], 1); }
+    for (int i = 0; i < L::kRaw; ++i) { bar_init(&s->raw_full[i], 1); bar_init(&s->raw_empty[i], L::kWideners); }
+    for (int t = 0; t < 2; ++t) {
+      bar_init(&s->s_full[t], 1);
+      bar_init(&s->p_full[t], 4);
+      bar_init(&s->o_full[t], 1);
+      bar_init(&s->item_full[t], 1);
+      bar_init(&s->item_empty[t], 9 + L::kWideners);
+      bar_init(&s->meet[t], 4);
+    }
+    bar_init(&s->drain, 1);
+    s->dead = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  // rows past the tokens are never written: zero scores, and nothing of them is read
+  for (int i = tid; i < 2 * L::kTileB / 16; i += NT) reinterpret_cast<uint4*>(smem)[i] = make_uint4(0, 0, 0, 0);
+  fence_async();
+  dep_wait();
+
+  // ---- this CTA's units, as in tg_step.cu --------------------------------
+  const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
+  const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
+  const auto tiles_of = [](int keys) { return keys > 0 ? (keys + kKeysW - 1) / kKeysW : 1; };
+  const auto entry_of = [&](int b) {
+    if constexpr (SHARED) {
+      const long long s0 = a.goff[b], s1 = a.goff[b + 1];
+      // a group of one shares nothing; a prefix is taken up to a whole copy
+      const int keys = s1 - s0 > 1 ? a.plens[b] & ~(ws.box - 1) : 0;
+      const int toks = static_cast<int>(s1 - s0) * a.n;
+      return Entry{keys, 0, static_cast<int>(s0) * a.n, toks, (toks + ws.tpt - 1) / ws.tpt};
+    } else {
+      const int l = checked(a.c.lens[b]);
+      return Entry{l, OWN ? min(c.ws_start[b], l) : 0, b * a.n, a.n, ws.row_tiles};
+    }
+  };
+  // A sequence takes part in its group's prefix when all its tokens see all of it.
+  const auto takes_part = [&](int b, int keys) { return checked(a.c.lens[b]) - a.n + 1 >= keys; };
+  // its units
+  const auto cost = [&](const Entry& e) {
+    if (SHARED && e.len == 0) return 0ll;
+    return static_cast<long long>(tiles_of(e.len - e.from) + kItemCostW) * (ws.pairs * e.row_tiles);
+  };
+  const int entries = SHARED ? a.groups : a.c.batch;
+  const int bper = (entries + NT - 1) / NT, b_first = tid * bper, b_end = min(entries, b_first + bper);
+  if constexpr (SHARED) {
+    // groups in order and inside the batch, prefixes inside the table; else none is shared
+    bool fine = tid > 0 || entries == 0 || a.goff[0] == 0;
+    for (int b = b_first; b < b_end; ++b) {
+      const long long s0 = a.goff[b], s1 = a.goff[b + 1];
+      fine = fine && s0 >= 0 && s0 <= s1 && s1 <= a.c.batch && a.plens[b] >= 0 && a.plens[b] <= max_len;
+    }
+    fine = __syncthreads_and(fine);
+    if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(c.status, kAttnBadRow);
+    // what is left to each sequence itself begins here
+    const long long behind = fine && entries > 0 ? a.goff[entries] : 0;
+    for (long long b = behind + blockIdx.x * NT + tid; b < a.c.batch; b += static_cast<long long>(gridDim.x) * NT) c.ws_start[b] = 0;
+    if (!fine) return;
+    for (int i = blockIdx.x; i < entries; i += gridDim.x) {
+      const Entry e = entry_of(i);
+      const int s0 = static_cast<int>(a.goff[i]), s1 = static_cast<int>(a.goff[i + 1]);
+      for (int b = s0 + tid; b < s1; b += NT) c.ws_start[b] = takes_part(b, e.len) ? e.len : 0;
+    }
+  }
+  long long mine = 0;
+  Entry e0{};
+  for (int b = b_first; b < b_end; ++b) {
+    const Entry e = entry_of(b);
+    if (!SHARED && blockIdx.x == 0 && checked(a.c.lens[b]) != a.c.lens[b]) atomicOr(c.status, kAttnBadRow);
+    if (b == b_first) e0 = e;
+    mine += cost(e);
+  }
+  long long before = mine;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const long long v = __shfl_up_sync(~0u, before, d);
+    if (lane >= d) before += v;
+  }
+  if (lane == 31) s->wsum[warp] = before;
+  __syncthreads();
+  long long U = 0;
+#pragma unroll
+  for (int w = 0; w < NT / 32; ++w) {
+    if (w < warp) before += s->wsum[w];
+    U += s->wsum[w];
+  }
+  before -= mine;
+  const long long N = min(static_cast<long long>(gridDim.x), max(1ll, U / 2));
+  if (blockIdx.x >= N || U == 0) return;
+  const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
+  if (mine > 0 && before <= u0 && u0 < before + mine) {
+    int b = b_first;
+    Entry e = e0;
+    long long at = before;
+    for (;;) {
+      const long long t = cost(e);
+      if (at + t > u0) break;
+      at += t;
+      e = entry_of(++b);
+    }
+    s->first_b = b;
+    s->first = e;
+    s->first_in = u0 - at;
+  }
+  if (warp == 8) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sptr(&s->tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    fence_before();
+  }
+  __syncthreads();
+  fence_after();
+  const unsigned tmem = s->tmem;
+  // where a ring position is, and the parity of its use
+  const auto slot_of = [](unsigned pos) { return pos % L::kSlots; };
+  const auto use_of = [](unsigned pos) { return (pos / L::kSlots) & 1u; };
+
+  // and of an 8-bit tile's
+  const auto raw_of = [](unsigned pos) { return pos % max(1, L::kRaw); };
+  const auto raw_use = [](unsigned pos) { return (pos / max(1, L::kRaw)) & 1u; };
+
+  if (warp == 9) {
+    // ---- items, pages and copies --------------------------------------------
+    registers_down<L::kRegThird>();
+    int b = s->first_b;
+    Entry e = s->first;
+    int nt = tiles_of(e.len - e.from);
+    const long long in = s->first_in;
+    const int skip = static_cast<int>(in / (nt + kItemCostW));
+    int rt = skip % e.row_tiles, pr = skip / e.row_tiles;
+    long long base = u0 - in % (nt + kItemCostW);
+    const int shift = 31 - __clz(ws.box), per = kKeysW >> shift;  // copies of a tile
+    const unsigned kv0 = sptr(smem + (Q8 ? L::kRawAt : L::kKv));
+    unsigned pos = 0, q_ph = 1;
+    int it_n = 0, meta = 0;
+    bool ok = true;
+    for (;;) {
+      const bool more = base + kItemCostW < u1;
+      const int is = it_n & 1;
+      ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c);
+      if (!ok) break;
+      WItem it{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+      if (more) {
+        it.b = b;
+        it.pair = pr;
+        it.rt = rt;
+        it.len = e.len;
+        it.from = e.from;
+        it.tok0 = e.tok + rt * ws.tpt;
+        it.toks = e.toks - rt * ws.tpt;
+        it.t0 = static_cast<int>(max(0ll, u0 - base - kItemCostW));
+        it.t1 = static_cast<int>(min(static_cast<long long>(nt), u1 - base - kItemCostW));
+        it.nch = min(2, c.G - 2 * pr);
+        it.base = base;
+      }
+      if (lane == 0) {
+        s->item[is] = it;
+        bar_arrive(&s->item_full[is]);
+      }
+      ++it_n;
+      if (!more) break;
+      // the row of the page table: the sequence's, or that of the group's first one
+      const int32_t* const table = a.c.table + (SHARED ? a.goff[b] : b) * a.c.table_stride;
+      const auto page_of = [&](int tile) {
+        const int key = e.from + tile * kKeysW + (lane << shift);
+        return lane < per && key < e.len ? __ldg(table + (key >> c.page_shift)) : -1;
+      };
+      int id = page_of(it.t0);
+      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c);
+      if (!ok) break;
+      q_ph ^= 1;
+      if (lane == 0) {
+        const int rows = (SHARED ? ws.tpt : min(a.n, ws.tpt)) * c.rep;
+        bar_expect(&s->q_full, it.nch * (DP / 64) * rows * 128);
+        for (int t = 0; t < it.nch; ++t)
+          for (int x = 0; x < DP / 64; ++x)
+            tma4(sptr(smem) + t * L::kTileB + x * kBlock, &mq, x * 64, 0, 2 * pr + t, it.tok0, &s->q_full);
+      }
+      for (int j = it.t0; j < it.t1 && ok; ++j) {
+        const int key = e.from + j * kKeysW + (lane << shift);
+        const bool in = lane < per && key < e.len, bad = in && (id < 0 || id >= a.c.num_pages);
+        if (bad) atomicOr(c.status, kAttnBadPage);
+        const unsigned badm = __ballot_sync(~0u, bad);
+        const int copies = __popc(__ballot_sync(~0u, in && !bad));
+        const int id_next = j + 1 < it.t1 ? page_of(j + 1) : -1;
+        const int slot = key & (c.page_size - 1);
+        for (int w = 0; w < 2 && ok; ++w)
+          for (int t = 0; t < it.nch; ++t) {
+            const int st = Q8 ? raw_of(pos) : slot_of(pos);
+            unsigned long long* const full = Q8 ? &s->raw_full[st] : &s->kv_full[st];
+            ok = bar_wait(&s->dead, Q8 ? &s->raw_empty[st] : &s->kv_empty[st], (Q8 ? raw_use(pos) : use_of(pos)) ^ 1, c);
+            if (!ok) break;
+            if (w == 0 && t == 0 && lane < 4) {
+              unsigned bits = 0;
+              if (badm)
+                for (int k = 0; k < 32; ++k)
+                  if ((badm >> ((lane * 32 + k) >> shift)) & 1) bits |= 1u << k;
+              s->bad[meta][lane] = bits;
+            }
+            __syncwarp();
+            if (lane == 0) bar_expect(full, copies * ws.box * (Q8 ? DP + (I8 && w == 0 ? 8 : 0) : (DP / 64) * 128));
+            __syncwarp();
+            if (in && !bad) {
+              const int g = 2 * pr + t;
+              const int y = c.token_major ? g : slot, z = c.token_major ? slot : g;
+              if constexpr (Q8) {
+                tma4(kv0 + st * L::kRawB + (lane << shift) * DP, w ? &mv : &mk, 0, y, z, id, full);
+                if (I8 && w == 0) {  // the scales, the values' too, come with the keys
+                  const int at = c.scale_at + (g * c.page_size + slot) * 4;
+                  const unsigned to = sptr(smem + L::kScaleAt) + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4) + (lane << shift) * 4;
+                  bulk(to, static_cast<const char*>(a.c.k) + id * a.c.k_page_stride + at, ws.box * 4, full);
+                  bulk(to + kKeysW * 4, static_cast<const char*>(a.c.v) + id * a.c.v_page_stride + at, ws.box * 4, full);
+                }
+              } else {
+                for (int x = 0; x < DP / 64; ++x)
+                  tma4(kv0 + st * L::kTileB + x * kBlock + (lane << shift) * 128, w ? &mv : &mk, x * 64, y, z, id, full);
+              }
+            }
+            ++pos;
+          }
+        meta = (meta + 1) % kMetas;
+        id = id_next;
+      }
+      if (!ok) break;
+      base += nt + kItemCostW;
+      if (++rt == e.row_tiles) {
+        rt = 0;
+        if (++pr == ws.pairs) {
+          pr = 0;
+          e = Entry{0, 0, 0, 0, 1};
+          while (++b < entries) {  // (groups that share nothing are no work)
+            e = entry_of(b);
+            if (!SHARED || e.len > 0) break;
+          }
+          nt = tiles_of(e.len - e.from);
+        }
+      }
+    }
+    // Copies in flight land before the CTA's memory goes: the other warps have seen
+    // them land, except when a wait ran out, theirs or this warp's.
+    constexpr unsigned ring = Q8 ? L::kRaw : L::kSlots;
+    for (unsigned k = pos > ring ? pos - ring : 0; k < pos; ++k)
+      bar_drain(Q8 ? &s->raw_full[raw_of(k)] : &s->kv_full[slot_of(k)], Q8 ? raw_use(k) : use_of(k));
+    bar_drain(&s->q_full, q_ph);
+  } else if (warp == 8) {
+    // ---- matrix instructions ----------------------------------------------
+    registers_down<L::kRegThird>();
+    const unsigned fmt = F16 ? 0u : 1u, fmt_pv = PF16 ? 0u : 1u;
+    const unsigned id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | (8u << 24);
+    const unsigned id_pv = (1u << 4) | (fmt_pv << 7) | (fmt_pv << 10) | (8u << 24) | (1u << 16) | (static_cast<unsigned>(c.D >> 3) << 17);
+    const int ks = c.D >> 4;
+    const unsigned q0 = sptr(smem), kv0 = sptr(smem + L::kKv);
+    unsigned pos = 0, q_ph = 0, p_ph[2] = {0, 0};
+    int it_n = 0, meta = 0;
+    bool ok = true;
+    for (;;) {
+      const int is = it_n & 1;
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
+      if (!ok) break;
+      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len - s->item[is].from;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (b < 0) break;
+      ok = bar_wait(&s->dead, &s->q_full, q_ph, c);
+      if (!ok) break;
+      q_ph ^= 1;
+      // keys of a tile that there are, in steps of 16
+      const auto width = [&](int j) { return max(16, min(kKeysW, (len - j * kKeysW + 15) & ~15)); };
+      const auto qk = [&](int t, int j, unsigned at) {
+        ok = bar_wait(&s->dead, &s->kv_full[slot_of(at)], use_of(at), c);
+        if (!ok) return;
+        fence_after();
+        const unsigned id = id0 | (static_cast<unsigned>(width(j) >> 3) << 17);
+        const unsigned long long qd = desc(q0 + t * L::kTileB, 16, 1024), kd = desc(kv0 + slot_of(at) * L::kTileB, 16, 1024);
+        if (elect()) {
+#pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            const unsigned off = ((k >> 2) * kBlock + (k & 3) * 32) >> 4;
+            if (k < ks) mma_ss(tmem + t * 128, qd + off, kd + off, id, k > 0);
+          }
+          commit(&s->s_full[t]);
+          commit(&s->kv_empty[slot_of(at)]);
+        }
+        __syncwarp();
+      };
+      for (int t = 0; t < nch && ok; ++t) qk(t, t0, pos + t);
+      for (int j = t0; j < t1 && ok; ++j) {
+        const unsigned vpos = pos + nch, next = pos + 2 * nch;
+        if (j + 1 == t1 && elect()) commit(&s->q_empty);
+        __syncwarp();
+        for (int t = 0; t < nch && ok; ++t) {
+          const int vs = slot_of(vpos + t);
+          ok = bar_wait(&s->dead, &s->kv_full[vs], use_of(vpos + t), c);
+          if (!ok) break;
+          // Values of keys that do not exist are what the page or an earlier tile
+          // holds; their weights are 0, but 0 x NaN is not: zero what is read.
+          // (Of an 8-bit tile the widening warps do.)
+          const int end = max(0, len - j * kKeysW);
+          const unsigned any_bad = Q8 ? 0u : s->bad[meta][0] | s->bad[meta][1] | s->bad[meta][2] | s->bad[meta][3];
+          if (!Q8 && (end < kKeysW || any_bad)) {
+            const int stop = width(j);
+            for (int i = (any_bad ? 0 : end * (DP / 8)) + lane; i < stop * (DP / 8); i += 32) {
+              const int r = i / (DP / 8), x = i % (DP / 8);
+              if (r >= end || ((s->bad[meta][r >> 5] >> (r & 31)) & 1))
+                *reinterpret_cast<uint4*>(smem + L::kKv + vs * L::kTileB + (x >> 3) * kBlock + r * 128 + (x & 7) * 16) =
+                    make_uint4(0, 0, 0, 0);
+            }
+            fence_async();
+            __syncwarp();
+          }
+          ok = bar_wait(&s->dead, &s->p_full[t], p_ph[t], c);
+          if (!ok) break;
+          p_ph[t] ^= 1;
+          fence_after();
+          const int steps = width(j) >> 4;
+          const unsigned long long vd = desc(kv0 + vs * L::kTileB, kBlock, 1024);
+          if (elect()) {
+#pragma unroll
+            for (int k = 0; k < kKeysW / 16; ++k)
+              if (k < steps) mma_ts(tmem + 256 + t * 128, tmem + t * 128 + k * 8, vd + k * (2048 >> 4), id_pv, j > t0 || k > 0);
+            if (j + 1 == t1) commit(&s->o_full[t]);
+            commit(&s->kv_empty[vs]);
+          }
+          __syncwarp();
+          if (j + 1 < t1) qk(t, j + 1, next + t);
+        }
+        pos = next;
+        meta = (meta + 1) % kMetas;
+      }
+      if (!ok) break;
+    }
+    __syncwarp();
+  } else if (Q8 && warp >= 10) {
+    // ---- 8-bit tiles to 16 bits --------------------------------------------
+    if (warp < 12) registers_down<L::kRegThird>();
+    else registers_down<L::kRegFourth>();
+    constexpr int CPR = DP / 16;  // vectors of a key's row
+    const int wt = tid - 320;     // of the widening warps' threads
+    unsigned pos = 0;
+    int it_n = 0, meta = 0;
+    bool ok = true;
+    for (;;) {
+      const int is = it_n & 1;
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
+      if (!ok) break;
+      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len - s->item[is].from;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (b < 0) break;
+      float vmax[2] = {0.0f, 0.0f};  // (warp 10)
+      for (int j = t0; j < t1 && ok; ++j) {
+        const int end = max(0, min(kKeysW, len - j * kKeysW)), stop = max(16, (end + 15) & ~15);
+        for (int w = 0; w < 2 && ok; ++w)
+          for (int t = 0; t < nch; ++t) {
+            const int rs = raw_of(pos), st = slot_of(pos);
+            ok = bar_wait(&s->dead, &s->raw_full[rs], raw_use(pos), c);
+            if (!ok) break;
+            ok = bar_wait(&s->dead, &s->kv_empty[st], use_of(pos) ^ 1, c);
+            if (!ok) break;
+            const unsigned* bad = s->bad[meta];
+            const unsigned any_bad = bad[0] | bad[1] | bad[2] | bad[3];
+            if (I8 && w == 0 && warp == 10) {
+              // The values' scales relative to about the largest so far; those of keys
+              // that do not exist, which may be anything, 0.
+              float4* const vs = reinterpret_cast<float4*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4)) + kKeysW / 4 + lane;
+              const float4 x = *vs;
+              float f[4] = {x.x, x.y, x.z, x.w};
+              unsigned top = 0u;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int key = 4 * lane + k;
+                if (key >= end || ((bad[key >> 5] >> (key & 31)) & 1)) f[k] = 0.0f;
+                const unsigned u = __float_as_uint(f[k]);
+                if (u < 0x7f800000u) top = max(top, u);
+              }
+              const float most = __uint_as_float(__reduce_max_sync(~0u, top));
+              float& vm = t ? vmax[1] : vmax[0];
+              float shrink = 1.0f;
+              if (most > 4.0f * vm || vm == 0.0f) {  // (rarely more than once: twice the largest leaves room for 8 times it)
+                const float now = fmaxf(2.0f * most, 0x1p-100f);
+                shrink = vm / now;
+                vm = now;
+              }
+              const float inv = 1.0f / vm;
+              *vs = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+              if (lane == 0) s->fac[meta][t] = make_float2(shrink, vm);
+            }
+            const uint4* const src = reinterpret_cast<const uint4*>(smem + L::kRawAt + rs * L::kRawB);
+            unsigned char* const dst = smem + L::kKv + st * L::kTileB;
+            // vector i of a row: chunks 2 i and 2 i + 1, in an order in which eight lanes meet different banks
+#pragma unroll 2
+            for (int u = wt; u < stop * CPR; u += 32 * L::kWideners) {
+              const int r = u / CPR, i = u % CPR;
+              unsigned y[8];
+              if (w == 0) widen16<CK, F16>(src[u], y);
+              else widen16<CK, true>(src[u], y);
+              if (w == 1 && (r >= end || (any_bad && ((bad[r >> 5] >> (r & 31)) & 1)))) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = 0u;  // (0 x NaN is not 0)
+              }
+              unsigned char* const to = dst + (i >> 2) * kBlock + r * 128;
+              const int ch = (2 * i) & 7, sw = (i >> 2) & 1;
+              const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+              *reinterpret_cast<uint4*>(to + (((ch + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
+              *reinterpret_cast<uint4*>(to + (((ch + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0) {
+              bar_arrive(&s->kv_full[st]);
+              bar_arrive(&s->raw_empty[rs]);
+            }
+            ++pos;
+          }
+        meta = (meta + 1) % kMetas;
+      }
+      if (!ok) break;
+    }
+    __syncwarp();
+  } else if (warp < 8) {
+    // ---- softmax: one thread per row --------------------------------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegSoftmax));
+    const int t = warp >> 2, row = tid & 127;
+    const unsigned lanes = static_cast<unsigned>(warp & 3) << 21;  // this warp's lanes of tensor memory
+    const unsigned ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
+    constexpr float bias = kBias<PF16, I8>;
+    const int tok = row / c.rep, head = row - tok * c.rep;
+    int it_n = 0, meta = 0;
+    unsigned s_ph = 0, o_ph = 0, meet_ph = 0;
+    bool ok = true;
+    const auto meet = [&]() {  // the four warps of this tile past this point
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->meet[t]);
+      ok = bar_wait(&s->dead, &s->meet[t], meet_ph, c);
+      meet_ph ^= 1;
+      return ok;
+    };
+    for (;;) {
+      const int is = it_n & 1;
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
+      if (!ok) break;
+      const WItem it = s->item[is];
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (it.b < 0) break;
+      if (t >= it.nch) {
+        meta = (meta + it.t1 - it.t0) % kMetas;
+        continue;
+      }
+      const int g = 2 * it.pair + t;
+      const bool real = tok < ws.tpt && tok < it.toks && (!SHARED || takes_part((it.tok0 + tok) / a.n, it.len));
+      const float sc = c.scale * kLog2E * (CK == kE4M3 && c.k_scale ? c.k_scale[g] : 1.0f);
+      // keys that the row sees, and the fewest that any does
+      const int lim_w = it.len - it.from - (SHARED ? 0 : a.n - 1);
+      const int lim = SHARED || !real ? it.len - it.from : lim_w + (a.n - it.toks + tok);
+      float vmax = 1.0f;
+      float m = real ? -INFINITY : INFINITY, l = 0.0f;
+      for (int j = it.t0; j < it.t1; ++j) {
+        ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c);
+        if (!ok) break;
+        s_ph ^= 1;
+        fence_after();
+        unsigned v[4][32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tm_ld32(v[x], ts + x * 32);
+        tm_wait_ld();
+#pragma unroll
+        for (int x = 0; x < 4; ++x) tm_pin(v[x]);
+        const float* const scales = reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4));
+        float shrink = 1.0f;
+        if constexpr (I8) {
+          const float2 f = s->fac[meta][t];
+          shrink = f.x;
+          vmax = f.y;
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+#pragma unroll
+            for (int y = 0; y < 32; y += 4) {
+              const float4 k = *reinterpret_cast<const float4*>(scales + x * 32 + y);
+              const float2 p = unpair(mul2(pair(__uint_as_float(v[x][y]), __uint_as_float(v[x][y + 1])), pair(k.x, k.y)));
+              const float2 q = unpair(mul2(pair(__uint_as_float(v[x][y + 2]), __uint_as_float(v[x][y + 3])), pair(k.z, k.w)));
+              v[x][y] = __float_as_uint(p.x);
+              v[x][y + 1] = __float_as_uint(p.y);
+              v[x][y + 2] = __float_as_uint(q.x);
+              v[x][y + 3] = __float_as_uint(q.y);
+            }
+        }
+        const unsigned* bad = s->bad[meta];
+        const unsigned any_bad = bad[0] | bad[1] | bad[2] | bad[3];
+        if ((j + 1) * kKeysW > lim_w || any_bad) {
+          const int rest = lim - j * kKeysW;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const unsigned off = bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
+#pragma unroll
+            for (int y = 0; y < 32; ++y)
+              if (off & (1u << y)) v[x][y] = 0xff800000u;  // -infinity
+          }
+        }
+        meta = (meta + 1) % kMetas;
+        softmax_tile<PF16, I8>(v, ts, to, c.D, sc, j > it.t0, m, l, scales + kKeysW, shrink);
+        tm_wait_st();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) bar_arrive(&s->p_full[t]);
+      }
+      if (!ok) break;
+      ok = bar_wait(&s->dead, &s->o_full[t], o_ph, c);
+      if (!ok) break;
+      o_ph ^= 1;
+      fence_after();
+      // the CTAs with the item's first and last tile
+      const long long tile0 = it.base + kItemCostW;
+      const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(it.len - it.from)) * N - 1) / U;
+      const bool whole = c0 == c1;
+      const long long token = it.tok0 + tok, at = token * c.H + g * c.rep + head;
+      const long long mine_part = wide_part(SHARED ? kPrefixRows : c.step_rows, blockIdx.x, tile0 < u0 ? 0 : 1, t) + row;
+      // what the values' sums stand for
+      const float vs = I8 ? vmax : CK == kE4M3 && c.v_scale ? c.v_scale[g] : 1.0f;
+      const bool to_out = !SHARED && whole;
+      const float f = !to_out ? vs : l == 0.0f ? 0.0f : vs / l;
+      const PrefixAt pre = OWN && real && it.from > 0 ? prefix_at(c, token, g) : PrefixAt{0, 0, 0};
+      float* const parts_to = !SHARED ? c.ws_o + mine_part * c.D : whole ? c.ws_pre_o + at * c.D : c.ws_part_o + mine_part * c.D;
+      float ref = m - bias, sum = l;
+#pragma unroll 1
+      for (int x = 0; x < c.D; x += 16) {
+        unsigned o[16];
+        tm_ld16(o, to + x);
+        tm_wait_ld();
+        tm_pin(o);
+        if (!real) continue;
+        if (to_out) {
+          unsigned w[8];
+          if (OWN && pre.parts > 0) {
+#pragma unroll
+            for (int y = 0; y < 4; ++y) {
+              float4 acc = make_float4(__uint_as_float(o[4 * y]) * vs, __uint_as_float(o[4 * y + 1]) * vs, __uint_as_float(o[4 * y + 2]) * vs, __uint_as_float(o[4 * y + 3]) * vs);
+              ref = m - bias;
+              sum = l;
+              join_prefix(c, pre, token, g * c.rep + head, x + 4 * y, acc, ref, sum);
+              const float e = sum == 0.0f ? 0.0f : 1.0f / sum;
+              w[2 * y] = sum == 0.0f ? 0u : pack2<F16>(acc.x * e, acc.y * e);
+              w[2 * y + 1] = sum == 0.0f ? 0u : pack2<F16>(acc.z * e, acc.w * e);
+            }
+          } else {
+#pragma unroll
+            for (int y = 0; y < 8; ++y)
+              w[y] = l == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
+          }
+          uint16_t* dst = static_cast<uint16_t*>(a.out) + at * c.D + x;
+          if (ws.wide) {
+            asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), TG_I8(w, 0) : "memory");
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+          }
+        } else {
+          float* dst = parts_to + x;
+          if constexpr (Q8) {
+#pragma unroll
+            for (int y = 0; y < 16; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+          }
+          const unsigned* lo = o;
+          const unsigned* hi = o + 8;
+          // (a row without keys so far: products of zeros, that the join leaves out)
+          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), TG_I8(lo, 0) : "memory");
+          asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst + 8), TG_I8(hi, 0) : "memory");
+        }
+      }
+      fence_before();  // the reads of O come before the next item's products
+      if constexpr (SHARED) {
+        // joined with each sequence's own keys
+        if (real) {
+          *(whole ? c.ws_pre_ml + at : c.ws_part_ml + mine_part) = make_float2(m - bias, l);
+          if (head == 0 && t == 0 && blockIdx.x == c0)
+            c.ws_pre[token * ws.pairs + it.pair] = make_int4(static_cast<int>(c0), static_cast<int>(c1 - c0) + 1, row, 0);  // PrefixAt
+        }
+        continue;
+      }
+      if (whole) {
+        if (real && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (OWN && pre.parts > 0 ? ref + log2f(sum) : m + log2f(l) - bias) * kLn2;
+        continue;
+      }
+      if (real) c.ws_ml[mine_part] = make_float2(m, l);
+      // the last CTA of the item joins its parts, in their order
+      __threadfence();
+      if (!meet()) break;
+      if (row == 0) s->last[t] = atomicAdd(c.ws_count + 2 * c0 + t, 1u) == static_cast<unsigned>(c1 - c0) ? 1 : 0;
+      if (!meet()) break;
+      if (!s->last[t]) continue;
+      __threadfence();
+      if (row == 0) c.ws_count[2 * c0 + t] = 0u;
+      const int parts = static_cast<int>(c1 - c0) + 1, rows = min(ws.tpt, it.toks) * c.rep;
+      // A thread keeps four columns and takes every step-th row, eight rows and
+      // two parts at a time, because the join waits for reads (68 rows of three
+      // parts: 14 us with four reads under way, 9 with sixteen).
+      constexpr int JP = 8;
+      const int per_row = c.D >> 2, step = 128 / per_row, r_first = row / per_row, d = (row - r_first * per_row) * 4;
+      const unsigned inv_rep = 65536u / c.rep + 1;  // r / rep for r < 128
+      for (int r0 = r_first < step ? r_first : rows; r0 < rows; r0 += step * JP) {
+        float4 acc[JP];
+        float mm[JP], ll[JP];
+#pragma unroll
+        for (int y = 0; y < JP; ++y) {
+          acc[y] = make_float4(0, 0, 0, 0);
+          mm[y] = -INFINITY;
+          ll[y] = 0.0f;
+        }
+        for (int p = 0; p < parts; p += 2) {
+          float4 v[2][JP];
+          float2 x[2][JP];
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            const int q = min(p + w, parts - 1);
+            const long long sl = wide_part(c.step_rows, c0 + q, q == 0, t);
+            const float* src = c.ws_o + sl * c.D + d;
+#pragma unroll
+            for (int y = 0; y < JP; ++y) {
+              const int r = min(r0 + y * step, rows - 1);
+              v[w][y] = __ldcg(reinterpret_cast<const float4*>(src + r * c.D));
+              x[w][y] = __ldcg(&c.ws_ml[sl + r]);
+            }
+          }
+          // a part in which a row saw no key adds nothing, whatever the values that its weights of 0 met
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+#pragma unroll
+            for (int y = 0; y < JP; ++y) {
+              if (x[w][y].y == 0.0f) v[w][y] = make_float4(0, 0, 0, 0);
+            }
+          }
+          const bool both = p + 1 < parts;
+#pragma unroll
+          for (int y = 0; y < JP; ++y) {
+            if (!both) x[1][y].x = -INFINITY;
+            const float top = fmaxf(mm[y], fmaxf(x[0][y].x, x[1][y].x));
+            const float z = top == -INFINITY ? 0.0f : top;  // no key so far: factors of 0
+            const float f = ex2(mm[y] - z), e = ex2(x[0][y].x - z), g = ex2(x[1][y].x - z);
+            ll[y] = ll[y] * f + x[0][y].y * e + (both ? x[1][y].y * g : 0.0f);
+            acc[y].x = acc[y].x * f + v[0][y].x * e + v[1][y].x * g;
+            acc[y].y = acc[y].y * f + v[0][y].y * e + v[1][y].y * g;
+            acc[y].z = acc[y].z * f + v[0][y].z * e + v[1][y].z * g;
+            acc[y].w = acc[y].w * f + v[0][y].w * e + v[1][y].w * g;
+            mm[y] = top;
+          }
+        }
+        const long long first = static_cast<long long>(it.tok0) * c.H + g * c.rep;
+#pragma unroll
+        for (int y = 0; y < JP; ++y) {
+          const int r = r0 + y * step;
+          if (r >= rows) break;
+          const int tk = (r * inv_rep) >> 16;
+          const long long to_row = first + r + static_cast<long long>(tk) * (c.H - c.rep);
+          float ref = mm[y];
+          if (OWN && it.from > 0) {
+            ref -= bias;
+            const PrefixAt pre = prefix_at(c, it.tok0 + tk, g);
+            join_prefix(c, pre, it.tok0 + tk, g * c.rep + r - tk * c.rep, d, acc[y], ref, ll[y]);
+            ref += bias;
+          }
+          const float e = ll[y] == 0.0f ? 0.0f : 1.0f / ll[y];
+          *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to_row * c.D + d) =
+              make_uint2(pack2<F16>(acc[y].x * e, acc[y].y * e), pack2<F16>(acc[y].z * e, acc[y].w * e));
+          if (d == 0 && a.lse) a.lse[to_row] = ll[y] == 0.0f ? -INFINITY : (ref + log2f(ll[y]) - bias) * kLn2;
+        }
+      }
+    }
+  } else {
+    registers_down<L::kRegThird>();
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == 8) {
+    // After a wait that ran out, whichever warp's, matrix instructions may be in
+    // flight: they end before the tensor memory goes.
+    if (*static_cast<volatile int*>(&s->dead)) {
+      if (elect()) {
+        commit(&s->drain);
+        bar_drain(&s->drain, 0);
+      }
+      __syncwarp();
+    }
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  }
+}
+
+template <int DP, bool F16, int CK, Pass PASS>
+cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
+  constexpr bool SHARED = PASS == kPrefixPass;
+  auto k = wide_kernel<DP, F16, CK, PASS>;
+  using L = WLay<DP, CK>;
+  if (!a) {
+    // the warpgroups' registers come out of what the block is launched with
+    cudaFuncAttributes at{};
+    const cudaError_t e = cudaFuncGetAttributes(&at, k);
+    if (e != cudaSuccess) return e;
+    if ((at.numRegs + 7) / 8 * 8 * L::kThreads < 256 * L::kRegSoftmax + 128 * L::kRegThird + (L::Q8 ? 128 * L::kRegFourth : 0))
+      return cudaErrorInvalidConfiguration;
+    return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
+  }
+  WSetup ws{};
+  ws.tpt = 128 / c.rep;
+  ws.row_tiles = (a->n + ws.tpt - 1) / ws.tpt;
+  ws.pairs = (c.G + 1) / 2;
+  ws.box = std::min(c.page_size, kKeysW);
+  ws.wide = (reinterpret_cast<uintptr_t>(a->out) & 31) == 0;
+  const CUtensorMapDataType type = F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const cuuint64_t D = c.D, P = c.page_size, G = c.G, rep = c.rep, es = L::Q8 ? 1 : 2;
+  CUtensorMap mq, mk, mv;
+  {
+    const cuuint64_t dims[4] = {D, rep, G, static_cast<cuuint64_t>(a->c.batch) * a->n};
+    const cuuint64_t st[3] = {D * 2, D * 2 * rep, static_cast<cuuint64_t>(a->qs) * 2};
+    const cuuint32_t box[4] = {64, static_cast<cuuint32_t>(rep), 1, static_cast<cuuint32_t>(SHARED ? ws.tpt : std::min(a->n, ws.tpt))};
+    if (!encode_map(c.encode, &mq, type, CU_TENSOR_MAP_SWIZZLE_128B, a->q, 4, dims, st, box)) return cudaErrorInvalidValue;
+  }
+  const bool token = c.token_major;
+  const cuuint64_t dims[4] = {D, token ? G : P, token ? P : G, static_cast<cuuint64_t>(a->c.num_pages)};
+  const cuuint32_t box[4] = {L::Q8 ? DP : 64, token ? 1u : static_cast<cuuint32_t>(ws.box), token ? static_cast<cuuint32_t>(ws.box) : 1u, 1};
+  for (int w = 0; w < 2; ++w) {
+    const cuuint64_t st[3] = {D * es, D * es * dims[1], static_cast<cuuint64_t>(w ? a->c.v_page_stride : a->c.k_page_stride) * es};
+    if (!encode_map(c.encode, w ? &mv : &mk, L::Q8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : type, L::Q8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
+                    w ? a->c.v : a->c.k, 4, dims, st, box, page_fetch(c, static_cast<int>(es))))
+      return cudaErrorInvalidValue;
+  }
+  const long long tiles = ((static_cast<long long>(a->c.max_pages) << c.page_shift) + kKeysW - 1) / kKeysW + kItemCostW;
+  const long long most = SHARED ? c.nsm : (static_cast<long long>(a->c.batch) * ws.pairs * ws.row_tiles * tiles + 1) / 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(std::min<long long>(most, c.nsm)));
+  cfg.blockDim = dim3(L::kThreads);
+  cfg.dynamicSmemBytes = L::kSmem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, k, c, *a, ws, mq, mk, mv);
+}
+
+template <int DP, bool F16, int CK>
+cudaError_t by_pass(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
+  if (a) return a->prefix ? go<DP, F16, CK, kPrefixPass>(c, a, s) : a->own ? go<DP, F16, CK, kOwnPass>(c, a, s) : go<DP, F16, CK, kStepPass>(c, a, s);
+  cudaError_t e = go<DP, F16, CK, kStepPass>(c, a, s);
+  if (e == cudaSuccess) e = go<DP, F16, CK, kPrefixPass>(c, a, s);
+  return e != cudaSuccess ? e : go<DP, F16, CK, kOwnPass>(c, a, s);
+}
+
+template <int CK>
+cudaError_t wide_by_type(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
+  if (c.D <= 64) return c.dtype == TG_DTYPE_F16 ? by_pass<64, true, CK>(c, a, s) : by_pass<64, false, CK>(c, a, s);
+  return c.dtype == TG_DTYPE_F16 ? by_pass<128, true, CK>(c, a, s) : by_pass<128, false, CK>(c, a, s);
+}
+
+}  // namespace
+}  // namespace tg

@@ -66,13 +66,56 @@ class I8Cache(Cache):
 
 
 def i8_reference(cache, q, n, rep, scale, kind, lens=None):
-    """step_reference, for weights that are rounded to f16 relative to the largest scale of a value: a weight below
-    f16's normal numbers is off by half a step of 2^-33 of the largest, times the largest value of the head."""
+    """step_reference, for weights that are rounded to f16 relative to a scale of at most twice the largest of a value
+    so far, the largest weight being at least 2^6 of such a unit (tensor memory kernel; 2^8 and the largest itself in the
+    other): a weight below f16's normal numbers is off by half its smallest step, 2^-25, so by 2^-25 2^-6 times a value of
+    at most twice the largest of the head, 2^-30 of that."""
     o, tol, z, ztol = step_reference(cache, q, n, rep, scale, kind, "f16", lens=lens)
     lens = cache.lens if lens is None else lens
     for b in range(q.shape[0]):
         for h in range(q.shape[2]):
             v = cache.values[b][:, h // rep]
             if v.size:
-                tol[b, :, h] += min(int(lens[b]), len(v)) * 2.0 ** -33 * np.abs(v).max()
+                tol[b, :, h] += min(int(lens[b]), len(v)) * 2.0 ** -30 * np.abs(v).max()
     return o, tol, z, ztol
+
+
+def _tokens(cache, pool, b, pos, heads, dim):
+    """Views of a pool and the indices of sequence b's tokens at pos: [(view, index), ..]."""
+    page, slot = ids(cache.table[b][pos // cache.page], np.int64), ids(pos % cache.page, np.int64)
+    import torch
+    token = cache.layout == "token"
+    if cache.kind == "i8":
+        codes, scales = parts(pool, heads, dim, cache.page, cache.layout)
+        return [(codes, (page, slot) if token else (page, slice(None), slot)), (scales, (page, slice(None), slot))]
+    raw = pool.view(torch.uint8) if cache.kind == "e4m3" else pool
+    return [(raw, (page, slot) if token else (page, slice(None), slot))]
+
+
+def shared_cache(kind, members, prefix, lens, heads, dim, page, layout, seed, copies=False, **more):
+    """A cache whose sequences begin, group by group, with the group's prefix: on the same pages as far as those are
+    whole (copies: on pages of their own), behind that on their own. The first row of a group's table holds the whole
+    prefix whatever its length."""
+    lens = np.asarray(lens)
+    first = np.repeat(np.concatenate([[0], np.cumsum(members)[:-1]]).astype(int), members)
+    pre = np.repeat(np.asarray(prefix), members)
+    alloc = np.where(first == np.arange(len(lens)), np.maximum(lens, pre), lens)
+    alloc = np.where(np.repeat(members, members) == 1, lens, alloc)
+    c = I8Cache(alloc, heads, dim, page, layout, seed, **more) if kind == "i8" else Cache(alloc, heads, dim, kind, page, layout, seed)
+    for b in range(len(lens)):
+        a, p = first[b], min(int(pre[b]), int(lens[b]))
+        if a != b and p > 0:
+            whole = 0 if copies else int(pre[b]) // page if lens[b] >= pre[b] // page * page else p // page
+            pos = np.arange(whole * page, p)
+            for pool in (c.k, c.v):
+                for (view, src), (_, dst) in zip(_tokens(c, pool, a, pos, heads, dim), _tokens(c, pool, b, pos, heads, dim)):
+                    if len(pos):
+                        view[dst] = view[src]
+            c.table[b, :whole] = c.table[a, :whole]
+            for x in (c.keys, c.values):
+                x[b][:p] = x[a][:p]
+    c.lens = lens
+    for x in (c.keys, c.values):
+        for b, n in enumerate(lens):
+            x[b] = x[b][:n]
+    return c
