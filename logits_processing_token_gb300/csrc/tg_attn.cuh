@@ -234,6 +234,7 @@ __device__ __forceinline__ void cp16(unsigned dst, const void* src, bool on) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void cp_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 template <int N>
 __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
@@ -347,9 +348,10 @@ __device__ __forceinline__ void bar_drain(unsigned long long* b, unsigned parity
 }
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
-__device__ __forceinline__ void bulk(unsigned dst, const void* src, unsigned bytes, unsigned long long* bar) {
-  asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst), "l"(src), "r"(bytes),
-               "r"(sptr(bar)) : "memory");
+// This thread's arrival, once all of its cp.async so far have landed (counted when
+// the barrier was initialised).
+__device__ __forceinline__ void bar_arrive_copied(unsigned long long* b) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(b)) : "memory");
 }
 __device__ __forceinline__ void tma3(unsigned dst, const CUtensorMap* m, int x, int y, int z, unsigned long long* bar) {
   asm volatile(
@@ -367,10 +369,10 @@ __device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, 
 struct PrefixAt {
   int c0, parts, row;  // first CTA; how many (0: no prefix, 1: in ws_pre_o); the token's first row of the tile
 };
-__device__ __forceinline__ PrefixAt prefix_at(const AttnCfg& c, long long token, int g) {
-  const int4 x = __ldcg(c.ws_pre + token * ((c.G + 1) >> 1) + (g >> 1));
-  return PrefixAt{x.x, x.y, x.z};
+__device__ __forceinline__ const int4* prefix_entry(const AttnCfg& c, long long token, int g) {
+  return c.ws_pre + token * ((c.G + 1) >> 1) + (g >> 1);
 }
+__device__ __forceinline__ PrefixAt prefix_at(const int4& x) { return PrefixAt{x.x, x.y, x.z}; }
 // A part's rows in the workspace of tg_wide.cuh: by CTA, whether the item began in
 // it, and which of the two key heads.
 __device__ __forceinline__ long long wide_part(int slot_rows, long long cta, int begun, int t) {

@@ -115,14 +115,6 @@ __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.
 template <bool F16>
 constexpr float kMostSum = F16 ? 255.0f * 256.0f : 255.0f;
 
-// With parts (an i8 cache: the scales of a tile's values relative to about the
-// largest, at most 4) the f16 weights are multiplied by them: a bias of 6, so that
-// none passes f16's end.
-template <bool F16, bool PARTS>
-constexpr float kBias = PARTS ? 6.0f : kWeightBias<F16>;
-template <bool F16, bool PARTS>
-constexpr float kMost = PARTS ? 255.0f * 64.0f : kMostSum<F16>;
-
 // The row's sums times a factor.
 __device__ __forceinline__ void scale_sums(unsigned to, int D, float f) {
   for (int x = 0; x < D; x += 16) {
@@ -143,17 +135,11 @@ __device__ __forceinline__ void scale_sums(unsigned to, int D, float f) {
 // stores.  A row that is no token's of this sequence (it holds a neighbour's
 // query) comes with m = +infinity: its weights are 0, and it has no vote on
 // whether the warp's rows search their maximum, whose reference, and so whose
-// rounding, would else depend on the neighbour.  part: of each key, what its weight
-// is multiplied by once it is summed (in shared memory); shrink: what the sums so
-// far are multiplied by first, the same for every row.
-template <bool F16, bool PARTS = false>
+// rounding, would else depend on the neighbour.
+template <bool F16>
 __device__ __forceinline__ void softmax_tile(unsigned (&v)[4][32], unsigned ts, unsigned to, int D, float sc, bool has_sums,
-                                             float& m, float& l, const float* part = nullptr, float shrink = 1.0f) {
-  constexpr float bias = kBias<F16, PARTS>;
-  if (PARTS && has_sums && shrink != 1.0f) {
-    scale_sums(to, D, shrink);
-    tm_wait_st();
-  }
+                                             float& m, float& l) {
+  constexpr float bias = kWeightBias<F16>;
   // The weights are taken against the row's reference as it stands; no
   // maximum is searched while their sum stays below 2^8, so none of them
   // can be too large.  (The first tile, and a tile that exceeds it, take
@@ -188,18 +174,13 @@ __device__ __forceinline__ void softmax_tile(unsigned (&v)[4][32], unsigned ts, 
         const float2 e = unpair(fma2(pair(__uint_as_float(src[0]), __uint_as_float(src[1])), sc2, off2));
         const float p0 = ex2(e.x), p1 = ex2(e.y);
         sum[y & 1] = add2(sum[y & 1], pair(p0, p1));
-        if constexpr (PARTS) {
-          const float2 f = *reinterpret_cast<const float2*>(part + x * 64 + 2 * y);
-          p[y] = pack2<F16>(p0 * f.x, p1 * f.y);
-        } else {
-          p[y] = pack2<F16>(p0, p1);
-        }
+        p[y] = pack2<F16>(p0, p1);
       }
       tm_st32(ts + x * 32, p);
     }
     const float2 l2 = unpair(add2(sum[0], sum[1]));
     tile_sum = l2.x + l2.y;
-    if (search || !__any_sync(~0u, tile_sum > (kMost<F16, PARTS>))) break;  // (a NaN stays one with any reference)
+    if (search || !__any_sync(~0u, tile_sum > kMostSum<F16>)) break;  // (a NaN stays one with any reference)
     search = true;
     tm_wait_st();
   }

@@ -86,7 +86,7 @@ struct Shape {
   static constexpr int kMRow = DP + (kT ? 4 : Q8 ? 16 : 8);        // a row of sums, padded likewise
   static constexpr int kMergeBufs = kT ? 2 : 1;           // (two: no wait before the next item's)
   static constexpr int kMerge = WN > 1 ? kMergeBufs * WM * WN * 8 * kMRow * 4 : 0;
-  static constexpr int kHead = 1024;                      // barriers, metas, scan scratch
+  static constexpr int kHead = 1536;                      // barriers, metas, scan scratch
   static constexpr int kML = kMergeBufs * WN * kRows * 8;
   static constexpr int kFixed = kHead + 2 * kQ + kMerge + kML + 1024;
   // two CTAs on an SM where four warps compute, one where eight do
@@ -103,8 +103,9 @@ struct Head {
   long long first_in;
   long long wsum[16];
   UnitMeta meta[kMaxStages];
+  int4 pre[2][16];  // of an item's tokens: where the group's prefix left their sums
 };
-static_assert(sizeof(Head) <= 1024, "");
+static_assert(sizeof(Head) <= 1536, "");
 
 // Byte offset of 16-byte chunk c of key r in a tile: 128-byte rows (a 256-byte
 // row is two of them, one 64-element half behind the other) or 64-byte rows,
@@ -140,14 +141,18 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   const int rows_all = a.n * c.rep;
   const int chunks = (c.D * (Q8 ? 1 : 2)) >> 4;  // chunks of a key's row that hold data
   const bool tensor_copies = box > 0;            // else the pages are too small for them
+  // copies that lanes make themselves: small ones.  (A bulk copy of a row of
+  // queries or a page's scales takes 0.2 us, one after the other: 32 sequences of
+  // 17 tokens over an i8 cache in pages of 16 took 123 us so.)
+  const bool lane_copies = I8 || !tensor_copies;
 
   if (tid == 0) {
     for (int i = 0; i < ST; ++i) {
-      bar_init(&hd->full[i], tensor_copies ? 1 : 33);
+      bar_init(&hd->full[i], lane_copies ? 33 : 1);
       bar_init(&hd->empty[i], NW);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&hd->q_full[i], 1);
+      bar_init(&hd->q_full[i], 32);
       bar_init(&hd->q_empty[i], NW);
     }
     bar_init(&hd->meet, NW);
@@ -247,15 +252,15 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         // this item's queries: a row at a time into padded rows
         ok = bar_wait(&hd->dead, &hd->q_empty[qs], q_ph, c);
         if (!ok) break;
-        const int rows = min(S::kRows, rows_all - rt * S::kRows);
-        if (lane == 0) bar_expect(&hd->q_full[qs], rows * c.D * 2);
-        __syncwarp();
-        for (int r = lane; r < rows; r += 32) {
-          const int x = rt * S::kRows + r, j = x / c.rep;
+        const int rows = min(S::kRows, rows_all - rt * S::kRows), vecs = c.D >> 3;
+        for (int y = lane; y < rows * vecs; y += 32) {
+          const int r = y / vecs, x = rt * S::kRows + r, j = x / c.rep;
           const uint16_t* src = static_cast<const uint16_t*>(a.q) + (static_cast<long long>(b) * a.n + j) * a.qs +
-                                static_cast<long long>(g * c.rep + (x - j * c.rep)) * c.D;
-          bulk(sptr(qbuf + qs * S::kQ + r * S::kQRow), src, c.D * 2, &hd->q_full[qs]);
+                                static_cast<long long>(g * c.rep + (x - j * c.rep)) * c.D + (y - r * vecs) * 8;
+          cp16(sptr(qbuf + qs * S::kQ + r * S::kQRow + (y - r * vecs) * 16), src, true);
         }
+        if (OWN && from > 0 && lane < a.n) cp16(sptr(&hd->pre[qs][lane]), prefix_entry(c, static_cast<long long>(b) * a.n + lane, g), true);
+        bar_arrive_copied(&hd->q_full[qs]);
         if (++qs == 2) { qs = 0; q_ph ^= 1; }
       }
       // the following unit, and its pages while this one's stage is awaited
@@ -302,8 +307,18 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           hd->meta[st].u = Unit{b, g, rt, from + tile * KT, len, from, badm != 0, first, last, base};
         }
         __syncwarp();
-        if (lane == 0) bar_expect(&hd->full[st], copies * R * 2 * (RB + (I8 ? 4 : 0)));
+        if (lane == 0) bar_expect(&hd->full[st], copies * R * RB * 2);
         __syncwarp();
+        if constexpr (I8) {
+          // scales, four keys a lane (a copy's keys are 8 at least, so of one page)
+          const int k4 = tile * KT + 4 * lane + from, page = __shfl_sync(~0u, id, (4 * lane) >> shift);
+          const bool have = k4 < len && page >= 0 && page < a.c.num_pages;
+          const long long p0 = have ? page : 0;
+          const int at = c.scale_at + (g * c.page_size + (k4 & (c.page_size - 1))) * 4;
+          cp16(vs + S::kMat + lane * 16, static_cast<const char*>(a.c.k) + p0 * a.c.k_page_stride + at, have);
+          cp16(vs + S::kMat + S::kScales + lane * 16, static_cast<const char*>(a.c.v) + p0 * a.c.v_page_stride + at, have);
+          bar_arrive_copied(&hd->full[st]);
+        }
         if (in && !bad) {
           const int slot = key & (c.page_size - 1);
           const int y = c.token_major ? g : slot, z = c.token_major ? slot : g;
@@ -312,12 +327,6 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             const unsigned at = (RB == 256 ? x * KT * 128 : 0) + (lane << shift) * (RB == 256 ? 128 : RB);
             tma4(ks + at, &mk, x * 64, y, z, id, &hd->full[st]);
             tma4(vs + at, &mv, x * 64, y, z, id, &hd->full[st]);
-          }
-          if constexpr (I8) {
-            const unsigned at = vs + S::kMat + (lane << shift) * 4;
-            const int from = c.scale_at + (g * c.page_size + slot) * 4;
-            bulk(at, static_cast<const char*>(a.c.k) + id * a.c.k_page_stride + from, R * 4, &hd->full[st]);
-            bulk(at + S::kScales, static_cast<const char*>(a.c.v) + id * a.c.v_page_stride + from, R * 4, &hd->full[st]);
           }
         }
       } else {
@@ -352,7 +361,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           }
         }
         if (lane == 0) hd->meta[st].u = Unit{b, g, rt, from + tile * KT, len, from, any_bad != 0, first, last, base};
-        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
+        bar_arrive_copied(&hd->full[st]);
         __syncwarp();
         if (lane == 0) bar_arrive(&hd->full[st]);
       }
@@ -365,8 +374,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       ok = bar_wait(&hd->dead, &hd->empty[st], ((i / ST) & 1) ^ 1, c);
       if (ok) {
         if (lane == 0) hd->meta[st].u.b = -1;
-        if (!tensor_copies)
-          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(sptr(&hd->full[st])) : "memory");
+        if (lane_copies) bar_arrive_copied(&hd->full[st]);
         __syncwarp();
         if (lane == 0) bar_arrive(&hd->full[st]);
         ++used;
@@ -394,6 +402,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   Unit cur;
   int qs = 0;
   unsigned q_ph = 0, meet_ph = 0;
+  int pq = 0;  // the item's places of hd->pre
   int buf = 0;  // merge buffer of the next item (T)
   bool ok = true;
   // All computing warps past this point.
@@ -468,8 +477,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     for (int k = 0; k < NO; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[k][i] = 0.0f;
-    __syncwarp();
-    if (lane == 0) bar_arrive(&hd->q_empty[qs]);
+    if constexpr (OWN) {
+      pq = qs;  // (its queries' places are handed back when the item ends)
+    } else {
+      __syncwarp();
+      if (lane == 0) bar_arrive(&hd->q_empty[qs]);
+    }
     if (++qs == 2) { qs = 0; q_ph ^= 1; }
   };
 
@@ -735,7 +748,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     const long long row = out_row(r);
     if (OWN && cur.from > 0) {
       const long long token = static_cast<long long>(cur.b) * a.n + r / c.rep;
-      const PrefixAt at = prefix_at(c, token, cur.g);
+      const PrefixAt at = prefix_at(hd->pre[pq][r / c.rep]);
       float ref = mm - bias;
       x = make_float4(x.x * vs, x.y * vs, x.z * vs, x.w * vs);
       join_prefix(c, at, token, cur.g * c.rep + r % c.rep, d, x, ref, ll);
@@ -959,6 +972,10 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     if (cur.last) {
       end_item();
       if (!ok) break;
+      if constexpr (OWN) {
+        __syncwarp();
+        if (lane == 0) bar_arrive(&hd->q_empty[pq]);
+      }
     }
   }
 }

@@ -28,6 +28,7 @@
 #pragma once
 
 #include <algorithm>
+#include <type_traits>
 
 #include "tg_mma5.cuh"
 
@@ -55,7 +56,7 @@ struct Entry {
 constexpr int kSlotsMaxW = 10, kMetas = 8;
 struct WBars {
   unsigned long long q_full, q_empty, kv_full[kSlotsMaxW], kv_empty[kSlotsMaxW], raw_full[kSlotsMaxW], raw_empty[kSlotsMaxW],
-      s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
+      scales_full[8], scales_ready[8][2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
   unsigned tmem;
   int dead, last[2], first_b;
   Entry first;
@@ -66,23 +67,26 @@ struct WBars {
 };
 
 // Warps 0 to 7: softmax, one warpgroup per key head; 8: matrix instructions; 9:
-// items and copies; an 8-bit cache: 10 to 15 widen.
+// items and copies; an 8-bit cache: 12 to 15 widen, 10 and 11 prepare an i8
+// cache's scales, one key head each (by a widening warp, which its tiles wait for:
+// 32 sequences of 17 tokens 118 us, not %WIDEN%).
 // Registers of the softmax's two warpgroups, the third and the fourth: their
 // threads times these are what the block is launched with (8-bit: 128 each).
 template <int DP, int CK>
 struct WLay {
   static constexpr bool Q8 = CK != kC16;
   static constexpr int kThreads = Q8 ? 512 : 384;
-  static constexpr int kRegSoftmax = Q8 ? 192 : 208, kRegThird = Q8 ? 72 : 88, kRegFourth = 56;
-  static constexpr int kWideners = Q8 ? 6 : 0;
+  static constexpr int kRegSoftmax = Q8 ? 152 : 208, kRegThird = Q8 ? 104 : 88, kRegFourth = 104;
+  static constexpr int kWideners = 4, kScalers = CK == kI8 ? 2 : 0;
   static constexpr int kTileB = DP / 64 * kBlock;
   static constexpr int kSlots = Q8 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
   static constexpr int kRawB = kKeysW * DP;                       // a tile as the cache has it
   static constexpr int kRaw = Q8 ? (DP == 128 ? 3 : 6) : 0;
-  // A tile's scales are read until its products are done.  By then at most kRaw +
-  // kSlots pieces (keys or values of one key head, two a tile at least) are past it.
+  // A tile's scales are read until its products are done.  When a tile's are asked
+  // for, the pieces of the tiles before it (keys or values of one key head, two a tile
+  // at least) have their places, and all but the last kRaw + kSlots of those are done.
   static constexpr int kScaleTiles = DP == 128 ? 4 : 8;
-  static_assert(2 * kScaleTiles - kRaw - kSlots >= 1 && kScaleTiles <= kMetas, "");
+  static_assert(2 * kScaleTiles >= 2 + kRaw + kSlots && kMetas % kScaleTiles == 0, "");
   static constexpr int kScaleB = CK == kI8 ? kScaleTiles * 2 * 2 * kKeysW * 4 : 0;  // [tile][head][keys, values][128]
   static constexpr int kKv = 2 * kTileB, kRawAt = kKv + kSlots * kTileB, kScaleAt = kRawAt + kRaw * kRawB, kBars = kScaleAt + kScaleB;
   static constexpr int kSmem = kBars + static_cast<int>(sizeof(WBars)) + 1024;
@@ -108,6 +112,107 @@ __device__ __forceinline__ void widen16(const uint4& r, unsigned (&w)[8]) {
   }
 }
 
+// With an i8 cache's scales the f16 weights are multiplied by up to 4 (the values'
+// relative to about the largest): a bias of 6, so that none passes f16's end.
+template <bool F16, bool I8>
+constexpr float kBias = I8 ? 6.0f : kWeightBias<F16>;
+
+// softmax_tile over an 8-bit cache, from scores that stay in tensor memory, a few
+// columns at a time: the widening warps take registers that the whole row would
+// need (with them, spilled to a level 1 that shared memory has left no room, a
+// tile took 3,500 cycles).  f16 weights.  I8: scale, of each key, what its score is
+// multiplied by (else sc) and, behind those 128, what its weight is once it is summed;
+// shrink: what the sums so far are multiplied by first, the same for every row.
+// masked: rest keys from the tile's first are seen, except those in `bad`.
+template <bool I8>
+__device__ __forceinline__ void softmax_tile8(unsigned ts, unsigned to, int D, float sc, const float* scale, float shrink, bool masked,
+                                              int rest, const unsigned* bad, bool has_sums, float& m, float& l) {
+  constexpr float bias = kBias<true, I8>, most = I8 ? 255.0f * 64.0f : kMostSum<true>;
+  if (I8 && has_sums && shrink != 1.0f) {
+    scale_sums(to, D, shrink);
+    tm_wait_st();
+  }
+  const auto hidden = [&](int x) {  // of 32 keys
+    return bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
+  };
+  unsigned p[2][32];
+  bool search = __any_sync(~0u, m == -INFINITY);
+  float tile_sum;
+  for (;;) {
+    if (search) {
+      float top = -INFINITY;
+#pragma unroll 1
+      for (int x = 0; x < 8; ++x) {
+        unsigned v[16];
+        tm_ld16(v, ts + x * 16);
+        tm_wait_ld();
+        tm_pin(v);
+        const unsigned off = masked ? hidden(x >> 1) >> (16 * (x & 1)) : 0u;
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const float e = __uint_as_float(v[y]) * (I8 ? scale[x * 16 + y] : sc);
+          if (!((off >> y) & 1)) top = fmaxf(top, e);
+        }
+      }
+      const bool raise = top > m;
+      const float f = raise ? ex2(m - top) : 1.0f;
+      if (raise) m = top;
+      l *= f;
+      if (has_sums && __any_sync(~0u, raise)) scale_sums(to, D, f);
+    }
+    const float off = m == -INFINITY ? 0.0f : bias - m;
+    const unsigned long long sc2 = pair(sc, sc), off2 = pair(off, off);
+    unsigned long long sum[2] = {0ull, 0ull};
+    // 16 columns at a time, the next ones on their way
+    const auto weights = [&](auto mask) {
+      unsigned v[2][16];
+      tm_ld16(v[0], ts);
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        unsigned (&w)[16] = v[x & 1];
+        tm_wait_ld();
+        tm_pin(w);
+        if (x < 7) tm_ld16(v[(x + 1) & 1], ts + (x + 1) * 16);
+        const unsigned hid = decltype(mask)::value ? hidden(x >> 1) >> (16 * (x & 1)) : 0u;
+#pragma unroll
+        for (int y = 0; y < 16; y += 4) {
+          float4 k, f;
+          if constexpr (I8) {
+            k = *reinterpret_cast<const float4*>(scale + x * 16 + y);
+            f = *reinterpret_cast<const float4*>(scale + kKeysW + x * 16 + y);
+          }
+#pragma unroll
+          for (int z = 0; z < 4; z += 2) {
+            const unsigned long long ks = I8 ? (z ? pair(k.z, k.w) : pair(k.x, k.y)) : sc2;
+            float2 e = unpair(fma2(pair(__uint_as_float(w[y + z]), __uint_as_float(w[y + z + 1])), ks, off2));
+            if (decltype(mask)::value) {
+              if ((hid >> (y + z)) & 1) e.x = -INFINITY;
+              if ((hid >> (y + z + 1)) & 1) e.y = -INFINITY;
+            }
+            float p0 = ex2(e.x), p1 = ex2(e.y);
+            sum[(z >> 1) & 1] = add2(sum[(z >> 1) & 1], pair(p0, p1));
+            if constexpr (I8) {
+              const float2 q = unpair(mul2(pair(p0, p1), z ? pair(f.z, f.w) : pair(f.x, f.y)));
+              p0 = q.x;
+              p1 = q.y;
+            }
+            p[x >> 2][(x & 3) * 8 + ((y + z) >> 1)] = pack2<true>(p0, p1);
+          }
+        }
+      }
+    };
+    if (masked) weights(std::true_type());
+    else weights(std::false_type());
+    const float2 l2 = unpair(add2(sum[0], sum[1]));
+    tile_sum = l2.x + l2.y;
+    if (search || !__any_sync(~0u, tile_sum > most)) break;  // (a NaN stays one with any reference)
+    search = true;
+  }
+  tm_st32(ts, p[0]);
+  tm_st32(ts + 32, p[1]);
+  l += tile_sum;
+}
+
 // What a launch does: a step; a shared call's prefixes of groups; each sequence's own
 // keys behind them.
 enum Pass { kStepPass, kPrefixPass, kOwnPass };
@@ -130,13 +235,17 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     bar_init(&s->q_full, 1);
     bar_init(&s->q_empty, 1);
     for (int i = 0; i < L::kSlots; ++i) { bar_init(&s->kv_full[i], Q8 ? L::kWideners : 1); bar_init(&s->kv_empty[i], 1); }
+    for (int i = 0; i < L::kScaleTiles; ++i) {
+      bar_init(&s->scales_full[i], 32);
+      for (int t = 0; t < 2; ++t) bar_init(&s->scales_ready[i][t], 1);
+    }
     for (int i = 0; i < L::kRaw; ++i) { bar_init(&s->raw_full[i], 1); bar_init(&s->raw_empty[i], L::kWideners); }
     for (int t = 0; t < 2; ++t) {
       bar_init(&s->s_full[t], 1);
       bar_init(&s->p_full[t], 4);
       bar_init(&s->o_full[t], 1);
       bar_init(&s->item_full[t], 1);
-      bar_init(&s->item_empty[t], 9 + L::kWideners);
+      bar_init(&s->item_empty[t], 9 + (Q8 ? L::kWideners : 0) + L::kScalers);
       bar_init(&s->meet[t], 4);
     }
     bar_init(&s->drain, 1);
@@ -295,16 +404,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         return lane < per && key < e.len ? __ldg(table + (key >> c.page_shift)) : -1;
       };
       int id = page_of(it.t0);
-      ok = bar_wait(&s->dead, &s->q_empty, q_ph, c);
-      if (!ok) break;
-      q_ph ^= 1;
-      if (lane == 0) {
-        const int rows = (SHARED ? ws.tpt : min(a.n, ws.tpt)) * c.rep;
-        bar_expect(&s->q_full, it.nch * (DP / 64) * rows * 128);
-        for (int t = 0; t < it.nch; ++t)
-          for (int x = 0; x < DP / 64; ++x)
-            tma4(sptr(smem) + t * L::kTileB + x * kBlock, &mq, x * 64, 0, 2 * pr + t, it.tok0, &s->q_full);
-      }
       for (int j = it.t0; j < it.t1 && ok; ++j) {
         const int key = e.from + j * kKeysW + (lane << shift);
         const bool in = lane < per && key < e.len, bad = in && (id < 0 || id >= a.c.num_pages);
@@ -313,7 +412,35 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         const int copies = __popc(__ballot_sync(~0u, in && !bad));
         const int id_next = j + 1 < it.t1 ? page_of(j + 1) : -1;
         const int slot = key & (c.page_size - 1);
-        for (int w = 0; w < 2 && ok; ++w)
+        if constexpr (I8) {
+          // the scales, the values' too: four keys a lane, both key heads' at once (a bulk copy
+          // of a page's takes 0.2 us, one after the other)
+          const int k4 = e.from + j * kKeysW + 4 * lane, page = __shfl_sync(~0u, id, (4 * lane) >> shift);
+          const bool have = k4 < e.len && page >= 0 && page < a.c.num_pages;
+          const long long p0 = have ? page : 0;
+          const int mt = meta % L::kScaleTiles;
+          for (int t = 0; t < it.nch; ++t) {
+            const int at = c.scale_at + ((2 * pr + t) * c.page_size + (k4 & (c.page_size - 1))) * 4;
+            const unsigned to = sptr(smem + L::kScaleAt) + (mt * 2 + t) * (2 * kKeysW * 4) + lane * 16;
+            cp16(to, static_cast<const char*>(a.c.k) + p0 * a.c.k_page_stride + at, have);
+            cp16(to + kKeysW * 4, static_cast<const char*>(a.c.v) + p0 * a.c.v_page_stride + at, have);
+          }
+          bar_arrive_copied(&s->scales_full[mt]);
+        }
+        for (int w = 0; w < 2 && ok; ++w) {
+          if (w == 1 && j == it.t0) {
+            // the item's queries: its first keys are under way, the item before may still use the place
+            ok = bar_wait(&s->dead, &s->q_empty, q_ph, c);
+            if (!ok) break;
+            q_ph ^= 1;
+            if (lane == 0) {
+              const int rows = (SHARED ? ws.tpt : min(a.n, ws.tpt)) * c.rep;
+              bar_expect(&s->q_full, it.nch * (DP / 64) * rows * 128);
+              for (int t = 0; t < it.nch; ++t)
+                for (int x = 0; x < DP / 64; ++x)
+                  tma4(sptr(smem) + t * L::kTileB + x * kBlock, &mq, x * 64, 0, 2 * pr + t, it.tok0, &s->q_full);
+            }
+          }
           for (int t = 0; t < it.nch; ++t) {
             const int st = Q8 ? raw_of(pos) : slot_of(pos);
             unsigned long long* const full = Q8 ? &s->raw_full[st] : &s->kv_full[st];
@@ -327,19 +454,13 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
               s->bad[meta][lane] = bits;
             }
             __syncwarp();
-            if (lane == 0) bar_expect(full, copies * ws.box * (Q8 ? DP + (I8 && w == 0 ? 8 : 0) : (DP / 64) * 128));
+            if (lane == 0) bar_expect(full, copies * ws.box * (Q8 ? DP : (DP / 64) * 128));
             __syncwarp();
             if (in && !bad) {
               const int g = 2 * pr + t;
               const int y = c.token_major ? g : slot, z = c.token_major ? slot : g;
               if constexpr (Q8) {
                 tma4(kv0 + st * L::kRawB + (lane << shift) * DP, w ? &mv : &mk, 0, y, z, id, full);
-                if (I8 && w == 0) {  // the scales, the values' too, come with the keys
-                  const int at = c.scale_at + (g * c.page_size + slot) * 4;
-                  const unsigned to = sptr(smem + L::kScaleAt) + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4) + (lane << shift) * 4;
-                  bulk(to, static_cast<const char*>(a.c.k) + id * a.c.k_page_stride + at, ws.box * 4, full);
-                  bulk(to + kKeysW * 4, static_cast<const char*>(a.c.v) + id * a.c.v_page_stride + at, ws.box * 4, full);
-                }
               } else {
                 for (int x = 0; x < DP / 64; ++x)
                   tma4(kv0 + st * L::kTileB + x * kBlock + (lane << shift) * 128, w ? &mv : &mk, x * 64, y, z, id, full);
@@ -347,6 +468,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             }
             ++pos;
           }
+        }
         meta = (meta + 1) % kMetas;
         id = id_next;
       }
@@ -371,6 +493,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     for (unsigned k = pos > ring ? pos - ring : 0; k < pos; ++k)
       bar_drain(Q8 ? &s->raw_full[raw_of(k)] : &s->kv_full[slot_of(k)], Q8 ? raw_use(k) : use_of(k));
     bar_drain(&s->q_full, q_ph);
+    if (I8) cp_wait_all();
   } else if (warp == 8) {
     // ---- matrix instructions ----------------------------------------------
     registers_down<L::kRegThird>();
@@ -460,12 +583,11 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       if (!ok) break;
     }
     __syncwarp();
-  } else if (Q8 && warp >= 10) {
+  } else if (Q8 && warp >= 12) {
     // ---- 8-bit tiles to 16 bits --------------------------------------------
-    if (warp < 12) registers_down<L::kRegThird>();
-    else registers_down<L::kRegFourth>();
-    constexpr int CPR = DP / 16;  // vectors of a key's row
-    const int wt = tid - 320;     // of the widening warps' threads
+    registers_down<L::kRegFourth>();
+    constexpr int CPR = DP / 16, UN = kKeysW * CPR / (32 * L::kWideners);  // vectors of a key's row; of a tile, per thread
+    const int wt = tid - 384;
     unsigned pos = 0;
     int it_n = 0, meta = 0;
     bool ok = true;
@@ -478,72 +600,112 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       if (lane == 0) bar_arrive(&s->item_empty[is]);
       ++it_n;
       if (b < 0) break;
-      float vmax[2] = {0.0f, 0.0f};  // (warp 10)
+      // one piece: keys (KEYS) or values of one key head
+      const auto piece = [&](auto keys, int end, int stop) {
+        constexpr bool KEYS = decltype(keys)::value;
+        const int rs = raw_of(pos), st = slot_of(pos);
+        ok = bar_wait(&s->dead, &s->raw_full[rs], raw_use(pos), c);
+        if (!ok) return;
+        ok = bar_wait(&s->dead, &s->kv_empty[st], use_of(pos) ^ 1, c);
+        if (!ok) return;
+        const uint4* const src = reinterpret_cast<const uint4*>(smem + L::kRawAt + rs * L::kRawB);
+        unsigned char* const dst = smem + L::kKv + st * L::kTileB;
+        const unsigned* bad = s->bad[meta];
+        const bool all = KEYS || (end == kKeysW && !(bad[0] | bad[1] | bad[2] | bad[3]));
+        uint4 x[UN];
+#pragma unroll
+        for (int k = 0; k < UN; ++k) x[k] = src[wt + k * (32 * L::kWideners)];
+        // vector i of a row: chunks 2 i and 2 i + 1, in an order in which eight lanes meet different banks
+        const int r0 = wt / CPR, i = wt % CPR, ch = (2 * i) & 7, sw = (i >> 2) & 1;
+        unsigned char* const to = dst + (i >> 2) * kBlock + r0 * 128;
+        const unsigned a0 = ((ch + sw) ^ (r0 & 7)) << 4, a1 = ((ch + 1 - sw) ^ (r0 & 7)) << 4;  // (rows a multiple of 8 apart)
+        constexpr int RS = 32 * L::kWideners / CPR;  // rows between a thread's vectors
+        static_assert(RS % 8 == 0, "");
+#pragma unroll
+        for (int k = 0; k < UN; ++k) {
+          if (r0 + k * RS >= stop) break;
+          unsigned y[8];
+          widen16<CK, KEYS ? F16 : true>(x[k], y);
+          if (!all) {
+            const int r = r0 + k * RS;
+            if (r >= end || ((bad[r >> 5] >> (r & 31)) & 1)) {
+#pragma unroll
+              for (int z = 0; z < 8; ++z) y[z] = 0u;  // (0 x NaN is not 0)
+            }
+          }
+          const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+          *reinterpret_cast<uint4*>(to + k * RS * 128 + a0) = sw ? hi : lo;
+          *reinterpret_cast<uint4*>(to + k * RS * 128 + a1) = sw ? lo : hi;
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0) {
+          bar_arrive(&s->kv_full[st]);
+          bar_arrive(&s->raw_empty[rs]);
+        }
+        ++pos;
+      };
       for (int j = t0; j < t1 && ok; ++j) {
         const int end = max(0, min(kKeysW, len - j * kKeysW)), stop = max(16, (end + 15) & ~15);
-        for (int w = 0; w < 2 && ok; ++w)
-          for (int t = 0; t < nch; ++t) {
-            const int rs = raw_of(pos), st = slot_of(pos);
-            ok = bar_wait(&s->dead, &s->raw_full[rs], raw_use(pos), c);
-            if (!ok) break;
-            ok = bar_wait(&s->dead, &s->kv_empty[st], use_of(pos) ^ 1, c);
-            if (!ok) break;
-            const unsigned* bad = s->bad[meta];
-            const unsigned any_bad = bad[0] | bad[1] | bad[2] | bad[3];
-            if (I8 && w == 0 && warp == 10) {
-              // The values' scales relative to about the largest so far; those of keys
-              // that do not exist, which may be anything, 0.
-              float4* const vs = reinterpret_cast<float4*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4)) + kKeysW / 4 + lane;
-              const float4 x = *vs;
-              float f[4] = {x.x, x.y, x.z, x.w};
-              unsigned top = 0u;
-#pragma unroll
-              for (int k = 0; k < 4; ++k) {
-                const int key = 4 * lane + k;
-                if (key >= end || ((bad[key >> 5] >> (key & 31)) & 1)) f[k] = 0.0f;
-                const unsigned u = __float_as_uint(f[k]);
-                if (u < 0x7f800000u) top = max(top, u);
-              }
-              const float most = __uint_as_float(__reduce_max_sync(~0u, top));
-              float& vm = t ? vmax[1] : vmax[0];
-              float shrink = 1.0f;
-              if (most > 4.0f * vm || vm == 0.0f) {  // (rarely more than once: twice the largest leaves room for 8 times it)
-                const float now = fmaxf(2.0f * most, 0x1p-100f);
-                shrink = vm / now;
-                vm = now;
-              }
-              const float inv = 1.0f / vm;
-              *vs = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-              if (lane == 0) s->fac[meta][t] = make_float2(shrink, vm);
-            }
-            const uint4* const src = reinterpret_cast<const uint4*>(smem + L::kRawAt + rs * L::kRawB);
-            unsigned char* const dst = smem + L::kKv + st * L::kTileB;
-            // vector i of a row: chunks 2 i and 2 i + 1, in an order in which eight lanes meet different banks
-#pragma unroll 2
-            for (int u = wt; u < stop * CPR; u += 32 * L::kWideners) {
-              const int r = u / CPR, i = u % CPR;
-              unsigned y[8];
-              if (w == 0) widen16<CK, F16>(src[u], y);
-              else widen16<CK, true>(src[u], y);
-              if (w == 1 && (r >= end || (any_bad && ((bad[r >> 5] >> (r & 31)) & 1)))) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = 0u;  // (0 x NaN is not 0)
-              }
-              unsigned char* const to = dst + (i >> 2) * kBlock + r * 128;
-              const int ch = (2 * i) & 7, sw = (i >> 2) & 1;
-              const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-              *reinterpret_cast<uint4*>(to + (((ch + sw) ^ (r & 7)) << 4)) = sw ? hi : lo;
-              *reinterpret_cast<uint4*>(to + (((ch + 1 - sw) ^ (r & 7)) << 4)) = sw ? lo : hi;
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0) {
-              bar_arrive(&s->kv_full[st]);
-              bar_arrive(&s->raw_empty[rs]);
-            }
-            ++pos;
-          }
+        for (int t = 0; t < nch && ok; ++t) piece(std::true_type(), end, stop);
+        for (int t = 0; t < nch && ok; ++t) piece(std::false_type(), end, stop);
         meta = (meta + 1) % kMetas;
+      }
+      if (!ok) break;
+    }
+    __syncwarp();
+  } else if (I8 && (warp == 10 || warp == 11)) {
+    // ---- scales of an i8 cache ----------------------------------------------
+    registers_down<L::kRegThird>();
+    const int t = warp - 10;
+    unsigned tiles = 0;
+    int it_n = 0, meta = 0;
+    bool ok = true;
+    for (;;) {
+      const int is = it_n & 1;
+      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
+      if (!ok) break;
+      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len - s->item[is].from;
+      __syncwarp();
+      if (lane == 0) bar_arrive(&s->item_empty[is]);
+      ++it_n;
+      if (b < 0) break;
+      float vmax = 0.0f;
+      for (int j = t0; j < t1; ++j, ++tiles, meta = (meta + 1) % kMetas) {
+        const int mt = meta % L::kScaleTiles;
+        ok = bar_wait(&s->dead, &s->scales_full[mt], (tiles / L::kScaleTiles) & 1, c);
+        if (!ok) break;
+        if (t < nch) {
+          // Keys' scales times what makes scores powers of two; values' relative to about
+          // the largest so far, and 0 for keys that do not exist, whose may be anything.
+          // (Their weights are masked.)
+          float4* const kf = reinterpret_cast<float4*>(smem + L::kScaleAt + (mt * 2 + t) * (2 * kKeysW * 4)) + lane;
+          float4* const vs = kf + kKeysW / 4;
+          const float base2 = c.scale * kLog2E;
+          const float4 x = *vs, y = *kf;
+          float f[4] = {x.x, x.y, x.z, x.w};
+          const int key = 4 * lane, end = len - j * kKeysW;
+          unsigned top = 0u;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            if (key + k >= end) f[k] = 0.0f;  // (a page that does not exist: copied as 0)
+            const unsigned u = __float_as_uint(f[k]);
+            if (u < 0x7f800000u) top = max(top, u);
+          }
+          const float most = __uint_as_float(__reduce_max_sync(~0u, top));
+          float shrink = 1.0f;
+          if (most > 4.0f * vmax || vmax == 0.0f) {  // (rarely more than once: twice the largest leaves room for 8 times it)
+            const float now = fmaxf(2.0f * most, 0x1p-100f);
+            shrink = vmax / now;
+            vmax = now;
+          }
+          const float inv = 1.0f / vmax;
+          *kf = make_float4(y.x * base2, y.y * base2, y.z * base2, y.w * base2);
+          *vs = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
+          if (lane == 0) s->fac[meta][t] = make_float2(shrink, vmax);
+        }
+        __syncwarp();
+        if (lane == 0) bar_arrive(&s->scales_ready[mt][t]);
       }
       if (!ok) break;
     }
@@ -557,7 +719,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     constexpr float bias = kBias<PF16, I8>;
     const int tok = row / c.rep, head = row - tok * c.rep;
     int it_n = 0, meta = 0;
-    unsigned s_ph = 0, o_ph = 0, meet_ph = 0;
+    unsigned s_ph = 0, o_ph = 0, meet_ph = 0, tiles = 0;
     bool ok = true;
     const auto meet = [&]() {  // the four warps of this tile past this point
       __syncwarp();
@@ -577,6 +739,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       if (it.b < 0) break;
       if (t >= it.nch) {
         meta = (meta + it.t1 - it.t0) % kMetas;
+        tiles += it.t1 - it.t0;
         continue;
       }
       const int g = 2 * it.pair + t;
@@ -592,45 +755,41 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         if (!ok) break;
         s_ph ^= 1;
         fence_after();
-        unsigned v[4][32];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tm_ld32(v[x], ts + x * 32);
-        tm_wait_ld();
-#pragma unroll
-        for (int x = 0; x < 4; ++x) tm_pin(v[x]);
-        const float* const scales = reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4));
-        float shrink = 1.0f;
-        if constexpr (I8) {
-          const float2 f = s->fac[meta][t];
-          shrink = f.x;
-          vmax = f.y;
-#pragma unroll
-          for (int x = 0; x < 4; ++x)
-#pragma unroll
-            for (int y = 0; y < 32; y += 4) {
-              const float4 k = *reinterpret_cast<const float4*>(scales + x * 32 + y);
-              const float2 p = unpair(mul2(pair(__uint_as_float(v[x][y]), __uint_as_float(v[x][y + 1])), pair(k.x, k.y)));
-              const float2 q = unpair(mul2(pair(__uint_as_float(v[x][y + 2]), __uint_as_float(v[x][y + 3])), pair(k.z, k.w)));
-              v[x][y] = __float_as_uint(p.x);
-              v[x][y + 1] = __float_as_uint(p.y);
-              v[x][y + 2] = __float_as_uint(q.x);
-              v[x][y + 3] = __float_as_uint(q.y);
-            }
-        }
         const unsigned* bad = s->bad[meta];
         const unsigned any_bad = bad[0] | bad[1] | bad[2] | bad[3];
-        if ((j + 1) * kKeysW > lim_w || any_bad) {
-          const int rest = lim - j * kKeysW;
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const unsigned off = bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
-#pragma unroll
-            for (int y = 0; y < 32; ++y)
-              if (off & (1u << y)) v[x][y] = 0xff800000u;  // -infinity
+        const bool masked = (j + 1) * kKeysW > lim_w || any_bad;
+        const int rest = lim - j * kKeysW;
+        if constexpr (Q8) {
+          float shrink = 1.0f;
+          if constexpr (I8) {
+            ok = bar_wait(&s->dead, &s->scales_ready[meta % L::kScaleTiles][t], (tiles / L::kScaleTiles) & 1, c);
+            if (!ok) break;
+            ++tiles;
+            const float2 f = s->fac[meta][t];
+            shrink = f.x;
+            vmax = f.y;
           }
+          softmax_tile8<I8>(ts, to, c.D, sc, reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4)),
+                            shrink, masked, rest, bad, j > it.t0, m, l);
+        } else {
+          unsigned v[4][32];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tm_ld32(v[x], ts + x * 32);
+          tm_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 4; ++x) tm_pin(v[x]);
+          if (masked) {
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+              const unsigned off = bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
+#pragma unroll
+              for (int y = 0; y < 32; ++y)
+                if (off & (1u << y)) v[x][y] = 0xff800000u;  // -infinity
+            }
+          }
+          softmax_tile<F16>(v, ts, to, c.D, sc, j > it.t0, m, l);
         }
         meta = (meta + 1) % kMetas;
-        softmax_tile<PF16, I8>(v, ts, to, c.D, sc, j > it.t0, m, l, scales + kKeysW, shrink);
         tm_wait_st();
         fence_before();
         __syncwarp();
@@ -651,7 +810,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const float vs = I8 ? vmax : CK == kE4M3 && c.v_scale ? c.v_scale[g] : 1.0f;
       const bool to_out = !SHARED && whole;
       const float f = !to_out ? vs : l == 0.0f ? 0.0f : vs / l;
-      const PrefixAt pre = OWN && real && it.from > 0 ? prefix_at(c, token, g) : PrefixAt{0, 0, 0};
+      const PrefixAt pre = OWN && real && it.from > 0 ? prefix_at(__ldcg(prefix_entry(c, token, g))) : PrefixAt{0, 0, 0};
       float* const parts_to = !SHARED ? c.ws_o + mine_part * c.D : whole ? c.ws_pre_o + at * c.D : c.ws_part_o + mine_part * c.D;
       float ref = m - bias, sum = l;
 #pragma unroll 1
@@ -726,7 +885,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       // A thread keeps four columns and takes every step-th row, eight rows and
       // two parts at a time, because the join waits for reads (68 rows of three
       // parts: 14 us with four reads under way, 9 with sixteen).
-      constexpr int JP = 8;
+      constexpr int JP = Q8 ? 4 : 8;
       const int per_row = c.D >> 2, step = 128 / per_row, r_first = row / per_row, d = (row - r_first * per_row) * 4;
       const unsigned inv_rep = 65536u / c.rep + 1;  // r / rep for r < 128
       for (int r0 = r_first < step ? r_first : rows; r0 < rows; r0 += step * JP) {
@@ -786,7 +945,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           float ref = mm[y];
           if (OWN && it.from > 0) {
             ref -= bias;
-            const PrefixAt pre = prefix_at(c, it.tok0 + tk, g);
+            const PrefixAt pre = prefix_at(__ldcg(prefix_entry(c, it.tok0 + tk, g)));
             join_prefix(c, pre, it.tok0 + tk, g * c.rep + r - tk * c.rep, d, acc[y], ref, ll[y]);
             ref += bias;
           }
