@@ -21,7 +21,7 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libtg.so")
 BINDING = os.path.join(BUILD, "tg_binding.so")  # native argument marshalling of the attention calls
 BINDING_SOURCE = "tg_binding.cpp"
-SOURCES = ["tg_kernels.cu", "tg_api.cu", "tg_beam.cu", "tg_attn_api.cu", "tg_append.cu", "tg_read.cu", "tg_step.cu",
+SOURCES = ["tg_kernels.cu", "tg_api.cu", "tg_beam.cu", "tg_attn_api.cu", "tg_append.cu", "tg_read.cu", "tg_finish.cu", "tg_step.cu",
            "tg_step_e4m3.cu", "tg_step_i8.cu", "tg_wide.cu", "tg_wide_e4m3.cu", "tg_wide_i8.cu", "tg_prompt.cu"]
 HEADERS = ["tg_device.cuh", "tg_select_core.cuh", "tg_attn.cuh", "tg_tokens.cuh", "tg_step.cuh", "tg_wide.cuh", "tg_mma5.cuh", os.path.join("..", "..", "include", "tg.h")]
 

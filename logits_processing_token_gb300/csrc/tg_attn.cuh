@@ -43,12 +43,10 @@ struct AttnCfg {
   int step_slots;          // workspace slots (two per CTA)
   float* ws_o;             // [slots][step_rows][D]
   float2* ws_ml;           // [slots][step_rows]: running maximum (base 2) and sum
-  int* ws_start;           // [max_shared]: keys of a sequence that its group's prefix pass took
-  int4* ws_pre;            // [max_shared][pairs of key heads]: where that pass left a token's sums (PrefixAt)
-  float* ws_pre_o;         // [max_shared][H][D]: sums of prefixes that one CTA had whole
-  float2* ws_pre_ml;       // [max_shared][H]: reference (base 2) and sum
-  float* ws_part_o;        // [4 x CTAs][kPrefixRows][D]: parts of the others
-  float2* ws_part_ml;
+  int4* ws_pre;            // [max_shared][pairs of key heads]: the parts of a shared call's rows (PartsOf)
+  unsigned char* ws_alone; // [max_shared][H]: rows that came out infinite or not a number
+  float* ws_part_o;        // [4 x CTAs][kPartRows][D]: those parts
+  float2* ws_part_ml;      // reference (base 2) and sum
   unsigned* ws_count;      // [slots / 2]: parts of a split sequence that are done; zero between calls
   int nsm;
   int step_ctas[5];        // CTAs per SM of the step kernel's row variants
@@ -88,12 +86,10 @@ struct StepArgs {
   CacheView c;
   void* out;
   float* lse;
-  // a shared call's two passes: prefixes for whole groups (prefix), then each
-  // sequence's own keys (own), joined with its group's
-  int prefix, own;
+  // a shared call's
   const int64_t* goff;
   const int32_t* plens;
-  int groups;
+  int groups;  // < 0: no shared call
 };
 
 struct ReadArgs {
@@ -123,12 +119,13 @@ cudaError_t wide_i8(const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t launch_append(const AttnCfg& c, const AppendArgs& a, cudaStream_t s);
 cudaError_t launch_read(const AttnCfg& c, const ReadArgs& a, cudaStream_t s);
 cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
+cudaError_t launch_finish(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // what a shared call's items leave
 cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
 cudaError_t step_e4m3(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t step_i8(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, 16-bit cache
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
-constexpr int kPrefixRows = 128;  // of a part of a shared call's prefix
+constexpr int kPartRows = 128;  // of a part of a shared call
 // CTAs of the step kernel per SM at most (they size the handle's workspace).
 constexpr int kStepCtasPerSm = 4;
 
@@ -364,57 +361,16 @@ __device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, 
       "l"(m), "r"(x), "r"(y), "r"(z), "r"(w), "r"(sptr(bar)) : "memory");
 }
 
-// What a shared call's prefix pass left for one token and key head: the parts of
-// its group's item and the token's rows in it.
-struct PrefixAt {
-  int c0, parts, row;  // first CTA; how many (0: no prefix, 1: in ws_pre_o); the token's first row of the tile
-};
-__device__ __forceinline__ const int4* prefix_entry(const AttnCfg& c, long long token, int g) {
-  return c.ws_pre + token * ((c.G + 1) >> 1) + (g >> 1);
-}
-__device__ __forceinline__ PrefixAt prefix_at(const int4& x) { return PrefixAt{x.x, x.y, x.z}; }
-// A part's rows in the workspace of tg_wide.cuh: by CTA, whether the item began in
+// A part's rows in a workspace of tg_wide.cuh: by CTA, whether the item began in
 // it, and which of the two key heads.
 __device__ __forceinline__ long long wide_part(int slot_rows, long long cta, int begun, int t) {
   return ((2 * cta + begun) * 2 + t) * slot_rows;
 }
-// Joins a row's sums with its group's prefix: acc, four columns from d, weights'
-// reference ref (base 2; a weight is 2^(score - ref)) and sum l.
-__device__ __forceinline__ void join_prefix(const AttnCfg& c, const PrefixAt& at, long long token, int h, int d, float4& acc,
-                                            float& ref, float& l) {
-  constexpr int PB = 8;  // parts whose reads are in flight
-  const int g = h / c.rep;
-  for (int p0 = 0; p0 < at.parts; p0 += PB) {
-    float2 x[PB];
-    float4 v[PB];
-#pragma unroll
-    for (int p = 0; p < PB; ++p) {
-      const int q = min(p0 + p, at.parts - 1);
-      const long long sl = wide_part(kPrefixRows, at.c0 + q, q == 0, g & 1) + at.row + (h - g * c.rep);
-      const long long row = token * c.H + h;
-      x[p] = at.parts == 1 ? __ldcg(c.ws_pre_ml + row) : __ldcg(c.ws_part_ml + sl);
-      v[p] = __ldcg(reinterpret_cast<const float4*>((at.parts == 1 ? c.ws_pre_o + row * c.D : c.ws_part_o + sl * c.D) + d));
-    }
-    float top = l == 0.0f ? -INFINITY : ref;
-#pragma unroll
-    for (int p = 0; p < PB; ++p)
-      if (p0 + p < at.parts && x[p].y != 0.0f) top = fmaxf(top, x[p].x);
-    const float f = l == 0.0f ? 0.0f : ex2(ref - top);
-    l *= f;
-    acc = l == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(acc.x * f, acc.y * f, acc.z * f, acc.w * f);
-    ref = top;
-#pragma unroll
-    for (int p = 0; p < PB; ++p) {
-      if (p0 + p >= at.parts || x[p].y == 0.0f) continue;  // (a part in which the row saw no key)
-      const float e = ex2(x[p].x - top);
-      l += x[p].y * e;
-      acc.x += v[p].x * e;
-      acc.y += v[p].y * e;
-      acc.z += v[p].z * e;
-      acc.w += v[p].w * e;
-    }
-  }
-}
+// The parts of one token's rows of a key head in a shared call: the first CTA, how
+// many, and the token's first row of the tile.  One: the row is written.
+struct PartsOf {
+  int c0, parts, row;
+};
 
 // Weights exp2(s - m) of f16 products are stored times 2^8: a weight 2^-33 of
 // the row's largest is still a (subnormal) f16 number, and the largest, 256,

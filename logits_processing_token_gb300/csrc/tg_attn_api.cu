@@ -73,6 +73,7 @@ tg::StepArgs step_args(const void* q, int64_t q_stride, int32_t n, const tg_cach
   a.c = view_of(cache);
   a.out = out;
   a.lse = out_lse;
+  a.groups = -1;
   return a;
 }
 
@@ -177,11 +178,10 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   const size_t rows = static_cast<size_t>(d.step_slots) * d.step_rows;
   const auto up256 = [](size_t n) { return (n + 255) / 256 * 256; };  // 32-byte stores
   const size_t o_o = up256(o_ml + rows * sizeof(float2));
-  // a shared call's: where each sequence's own keys begin, where its prefix's sums are, and those
-  const size_t shared = d.max_shared, part_rows = shared ? static_cast<size_t>(4) * d.nsm * tg::kPrefixRows : 0;
-  const size_t o_start = up256(o_o + rows * d.D * 4), o_pre = up256(o_start + shared * 4),
-               o_pml = up256(o_pre + shared * ((d.G + 1) / 2) * sizeof(int4)), o_po = up256(o_pml + shared * d.H * sizeof(float2)),
-               o_tml = up256(o_po + shared * d.H * d.D * 4), o_to = up256(o_tml + part_rows * sizeof(float2)), bytes = o_to + part_rows * d.D * 4;
+  // a shared call's: where its rows' parts are, which come out infinite, and those parts
+  const size_t shared = d.max_shared, part_rows = shared ? static_cast<size_t>(4) * d.nsm * tg::kPartRows : 0;
+  const size_t o_pre = up256(o_o + rows * d.D * 4), o_alone = up256(o_pre + shared * ((d.G + 1) / 2) * sizeof(int4)),
+               o_tml = up256(o_alone + shared * d.H), o_to = up256(o_tml + part_rows * sizeof(float2)), bytes = o_to + part_rows * d.D * 4;
   unsigned char* host = new (std::nothrow) unsigned char[o_ml]();
   if (!host) { delete cfg; return TG_ERR_OUT_OF_MEMORY; }
   for (int i = 0; i < half; ++i) {
@@ -205,7 +205,7 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
     e = cudaMemcpyAsync(cfg->dmem, host, o_ml, cudaMemcpyHostToDevice, reinterpret_cast<cudaStream_t>(stream));
   // (what no pass has written yet names no part)
   if (e == cudaSuccess && shared)
-    e = cudaMemsetAsync(static_cast<unsigned char*>(cfg->dmem) + o_start, 0, o_pml - o_start, reinterpret_cast<cudaStream_t>(stream));
+    e = cudaMemsetAsync(static_cast<unsigned char*>(cfg->dmem) + o_pre, 0, o_tml - o_pre, reinterpret_cast<cudaStream_t>(stream));
   const cudaError_t e2 = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
   if (e == cudaSuccess) e = e2;
   delete[] host;
@@ -221,10 +221,8 @@ tg_status tg_attn_create(const tg_attn_params* p, tg_attn** out, tg_stream strea
   d.prompt_count = d.status + 1;
   d.ws_ml = reinterpret_cast<float2*>(m + o_ml);
   d.ws_o = reinterpret_cast<float*>(m + o_o);
-  d.ws_start = reinterpret_cast<int*>(m + o_start);
   d.ws_pre = reinterpret_cast<int4*>(m + o_pre);
-  d.ws_pre_ml = reinterpret_cast<float2*>(m + o_pml);
-  d.ws_pre_o = reinterpret_cast<float*>(m + o_po);
+  d.ws_alone = m + o_alone;
   d.ws_part_ml = reinterpret_cast<float2*>(m + o_tml);
   d.ws_part_o = reinterpret_cast<float*>(m + o_to);
   *out = cfg;

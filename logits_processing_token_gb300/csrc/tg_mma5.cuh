@@ -135,16 +135,17 @@ __device__ __forceinline__ void scale_sums(unsigned to, int D, float f) {
 // stores.  A row that is no token's of this sequence (it holds a neighbour's
 // query) comes with m = +infinity: its weights are 0, and it has no vote on
 // whether the warp's rows search their maximum, whose reference, and so whose
-// rounding, would else depend on the neighbour.
+// rounding, would else depend on the neighbour; nor has a row that sees no key of
+// the tile (sees).
 template <bool F16>
 __device__ __forceinline__ void softmax_tile(unsigned (&v)[4][32], unsigned ts, unsigned to, int D, float sc, bool has_sums,
-                                             float& m, float& l) {
+                                             float& m, float& l, bool sees = true) {
   constexpr float bias = kWeightBias<F16>;
   // The weights are taken against the row's reference as it stands; no
   // maximum is searched while their sum stays below 2^8, so none of them
   // can be too large.  (The first tile, and a tile that exceeds it, take
   // the maximum as the reference first.)
-  bool search = __any_sync(~0u, m == -INFINITY);
+  bool search = __any_sync(~0u, sees && m == -INFINITY);
   float tile_sum;
   for (;;) {
     if (search) {

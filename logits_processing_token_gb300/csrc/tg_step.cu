@@ -27,20 +27,22 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   return by_cache(nullptr, c, &a, s);
 }
 
-// tg_attend_shared: one pass over the groups' prefixes, whose rows are those of all of
-// a group's sequences, and one over each sequence's own keys, at whose ends its
-// rows are joined with what the first pass left.  (The rest of a shared call whose
-// shape the first pass does not take is a step.)
+// What a row tile's copies need in memory while the work is laid out: an int per
+// sequence, two per group.
+constexpr long long kMostShared = 36000;
+
+// tg_attend_shared: one launch over the groups' prefixes and each sequence's own keys
+// (tg_wide.cuh), one that joins what its CTAs split (tg_finish.cu).  Where nothing can be
+// shared, or the launch's shape does not fit, it is a step.
 cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   StepArgs b = a;
-  if (a.groups > 0 && wide_can(c)) {
-    b.prefix = 1;
-    const cudaError_t e = launch_wide(c, b, s);
-    if (e != cudaSuccess) return e;
-    b.prefix = 0;
-    b.own = 1;
-  }
-  return launch_step(c, b, s);
+  b.groups = -1;
+  const long long tiles = (static_cast<long long>(a.c.max_pages) << c.page_shift) / 128 + 5;
+  if (a.groups == 0 || a.c.batch < 2 || !wide_can(c) || a.c.batch + 2ll * a.groups >= kMostShared ||
+      tiles * a.c.batch * ((a.n * c.rep + 127) / 128 + 1) > 0x7fffffffll)
+    return launch_step(c, b, s);
+  const cudaError_t e = launch_wide(c, a, s);
+  return e != cudaSuccess ? e : launch_finish(c, a, s);
 }
 
 }  // namespace tg

@@ -40,7 +40,6 @@ namespace {
 // Everything about a unit that the computing warps need.
 struct Unit {
   int b, g, rt, key0, len;  // b < 0: no more units; key0: its first key
-  int from;                 // its sequence's first key: 0, or behind a shared prefix
   int any_bad;
   int first, last;          // of its item in this CTA
   long long base;           // the item's number of units before it
@@ -86,7 +85,7 @@ struct Shape {
   static constexpr int kMRow = DP + (kT ? 4 : Q8 ? 16 : 8);        // a row of sums, padded likewise
   static constexpr int kMergeBufs = kT ? 2 : 1;           // (two: no wait before the next item's)
   static constexpr int kMerge = WN > 1 ? kMergeBufs * WM * WN * 8 * kMRow * 4 : 0;
-  static constexpr int kHead = 1536;                      // barriers, metas, scan scratch
+  static constexpr int kHead = 1024;                      // barriers, metas, scan scratch
   static constexpr int kML = kMergeBufs * WN * kRows * 8;
   static constexpr int kFixed = kHead + 2 * kQ + kMerge + kML + 1024;
   // two CTAs on an SM where four warps compute, one where eight do
@@ -99,13 +98,12 @@ struct Shape {
 constexpr int kMaxStages = 8;
 struct Head {
   unsigned long long full[kMaxStages], empty[kMaxStages], q_full[2], q_empty[2], meet;
-  int dead, last, first_b, first_len, first_from;
+  int dead, last, first_b, first_len;
   long long first_in;
   long long wsum[16];
   UnitMeta meta[kMaxStages];
-  int4 pre[2][16];  // of an item's tokens: where the group's prefix left their sums
 };
-static_assert(sizeof(Head) <= 1536, "");
+static_assert(sizeof(Head) <= 1024, "");
 
 // Byte offset of 16-byte chunk c of key r in a tile: 128-byte rows (a 256-byte
 // row is two of them, one 64-element half behind the other) or 64-byte rows,
@@ -116,9 +114,7 @@ __device__ __forceinline__ unsigned key_at(int r, int c) {
   else return tile_at<RB>(r, c);
 }
 
-// OWN: the second pass of a shared call, over each sequence's keys behind its
-// group's prefix.
-template <int DP, bool MF16, bool QF16, int CK, int WMX, int WN, bool OWN>
+template <int DP, bool MF16, bool QF16, int CK, int WMX, int WN>
 __global__ void __launch_bounds__(32 * ((WMX ? WMX : 1) * WN + 1), WMX * WN > 4 ? 1 : 2)
 step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int box, const __grid_constant__ CUtensorMap mk,
             const __grid_constant__ CUtensorMap mv) {
@@ -141,9 +137,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   const int rows_all = a.n * c.rep;
   const int chunks = (c.D * (Q8 ? 1 : 2)) >> 4;  // chunks of a key's row that hold data
   const bool tensor_copies = box > 0;            // else the pages are too small for them
-  // copies that lanes make themselves: small ones.  (A bulk copy of a row of
-  // queries or a page's scales takes 0.2 us, one after the other: 32 sequences of
-  // 17 tokens over an i8 cache in pages of 16 took 123 us so.)
+  // copies that lanes make themselves: small ones
   const bool lane_copies = I8 || !tensor_copies;
 
   if (tid == 0) {
@@ -152,7 +146,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       bar_init(&hd->empty[i], NW);
     }
     for (int i = 0; i < 2; ++i) {
-      bar_init(&hd->q_full[i], 32);
+      bar_init(&hd->q_full[i], 1);
       bar_init(&hd->q_empty[i], NW);
     }
     bar_init(&hd->meet, NW);
@@ -174,19 +168,17 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   // ---- this CTA's units -------------------------------------------------
   const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
   const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
-  const auto from_of = [&](int b, int l) { return OWN ? min(c.ws_start[b], l) : 0; };  // keys of the group's prefix
-  const auto tiles_of = [](int keys) { return keys > 0 ? (keys + KT - 1) / KT : 1; };
-  const auto cost = [&](int keys) { return tiles_of(keys) + kItemCost; };
+  const auto tiles_of = [](int len) { return len > 0 ? (len + KT - 1) / KT : 1; };
+  const auto cost = [&](int len) { return tiles_of(len) + kItemCost; };
   const int per_tile = c.G * row_tiles;
   const int bper = (a.c.batch + NT - 1) / NT, b_first = tid * bper;
   long long mine = 0;
-  int len0 = 0, from0 = 0;  // of this thread's first sequence
+  int len0 = 0;  // of this thread's first sequence
   for (int b = b_first; b < min(a.c.batch, b_first + bper); ++b) {
     const int raw = a.c.lens[b], l = checked(raw);
     if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
-    const int f = from_of(b, l);
-    if (b == b_first) { len0 = l; from0 = f; }
-    mine += cost(l - f);
+    if (b == b_first) len0 = l;
+    mine += cost(l);
   }
   long long before = mine;
 #pragma unroll
@@ -209,38 +201,35 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   if (blockIdx.x >= N) return;
   const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
   if (mine > 0 && before * per_tile <= u0 && u0 < (before + mine) * per_tile) {
-    int b = b_first, l = len0, f = from0;
+    int b = b_first, l = len0;
     long long at = before;
     for (;;) {
-      const int t = cost(l - f);
+      const int t = cost(l);
       if ((at + t) * per_tile > u0) break;
       at += t;
       l = checked(a.c.lens[++b]);
-      f = from_of(b, l);
     }
     hd->first_b = b;
     hd->first_len = l;
-    hd->first_from = f;
     hd->first_in = u0 - at * per_tile;
   }
   __syncthreads();
   if (warp == NW) {
     // ---- pages and copies ---------------------------------------------------
-    int b = hd->first_b, len = hd->first_len, from = hd->first_from, nt = tiles_of(len - from);
-    const int skip = static_cast<int>(hd->first_in / cost(len - from));
+    int b = hd->first_b, len = hd->first_len, nt = tiles_of(len);
+    const int skip = static_cast<int>(hd->first_in / cost(len));
     int rt = skip % row_tiles, g = skip / row_tiles;
-    long long base = u0 - hd->first_in % cost(len - from);  // units before the item
+    long long base = u0 - hd->first_in % cost(len);  // units before the item
     // its tiles that are this CTA's: tile .. tend - 1
     int tile = static_cast<int>(max(0ll, u0 - base - kItemCost)), tend = static_cast<int>(min(static_cast<long long>(nt), u1 - base - kItemCost));
     int len_next = b + 1 < a.c.batch ? checked(a.c.lens[b + 1]) : 0;
-    int from_next = b + 1 < a.c.batch ? from_of(b + 1, len_next) : 0;
     const int R = tensor_copies ? box : 1;  // keys of one copy
     const int shift = R == 1 ? 0 : 31 - __clz(R);
     const auto entry = [&](int bb, int key, int ln) {  // the page of a key, -1 past the end
       return key < ln ? __ldg(a.c.table + bb * a.c.table_stride + (key >> c.page_shift)) : -1;
     };
     // lane i: the page of copy i of the tile (of key i, 32 apart, without tensor copies)
-    int id = tensor_copies && lane < (KT >> shift) ? entry(b, from + tile * KT + (lane << shift), len) : -1;
+    int id = tensor_copies && lane < (KT >> shift) ? entry(b, tile * KT + (lane << shift), len) : -1;
     int qs = 0;
     unsigned q_ph = 1;
     bool ok = true, first = true;
@@ -252,20 +241,22 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         // this item's queries: a row at a time into padded rows
         ok = bar_wait(&hd->dead, &hd->q_empty[qs], q_ph, c);
         if (!ok) break;
-        const int rows = min(S::kRows, rows_all - rt * S::kRows), vecs = c.D >> 3;
-        for (int y = lane; y < rows * vecs; y += 32) {
-          const int r = y / vecs, x = rt * S::kRows + r, j = x / c.rep;
+        const int rows = min(S::kRows, rows_all - rt * S::kRows);
+        if (lane == 0) bar_expect(&hd->q_full[qs], rows * c.D * 2);
+        __syncwarp();
+        for (int r = lane; r < rows; r += 32) {
+          const int x = rt * S::kRows + r, j = x / c.rep;
           const uint16_t* src = static_cast<const uint16_t*>(a.q) + (static_cast<long long>(b) * a.n + j) * a.qs +
-                                static_cast<long long>(g * c.rep + (x - j * c.rep)) * c.D + (y - r * vecs) * 8;
-          cp16(sptr(qbuf + qs * S::kQ + r * S::kQRow + (y - r * vecs) * 16), src, true);
+                                static_cast<long long>(g * c.rep + (x - j * c.rep)) * c.D;
+          asm volatile("cp.async.bulk.shared::cta.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                           sptr(qbuf + qs * S::kQ + r * S::kQRow)),
+                       "l"(src), "r"(c.D * 2), "r"(sptr(&hd->q_full[qs])) : "memory");
         }
-        if (OWN && from > 0 && lane < a.n) cp16(sptr(&hd->pre[qs][lane]), prefix_entry(c, static_cast<long long>(b) * a.n + lane, g), true);
-        bar_arrive_copied(&hd->q_full[qs]);
         if (++qs == 2) { qs = 0; q_ph ^= 1; }
       }
       // the following unit, and its pages while this one's stage is awaited
       const bool last = tile + 1 == tend;
-      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nfrom = from, nnt = nt, ntend = tend;
+      int nb = b, ng = g, nrt = rt, ntile = tile + 1, nlen = len, nnt = nt, ntend = tend;
       long long nbase = base;
       if (last) {
         ntile = 0;
@@ -276,20 +267,18 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             ng = 0;
             ++nb;
             nlen = len_next;
-            nfrom = from_next;
-            nnt = tiles_of(nlen - nfrom);
+            nnt = tiles_of(nlen);
             len_next = nb + 1 < a.c.batch ? checked(a.c.lens[nb + 1]) : 0;
-            from_next = nb + 1 < a.c.batch ? from_of(nb + 1, len_next) : 0;
           }
         }
         ntend = static_cast<int>(min(static_cast<long long>(nnt), u1 - nbase - kItemCost));
       }
-      const int id_next = tensor_copies && nbase + kItemCost < u1 && lane < (KT >> shift) ? entry(nb, nfrom + ntile * KT + (lane << shift), nlen) : -1;
+      const int id_next = tensor_copies && nbase + kItemCost < u1 && lane < (KT >> shift) ? entry(nb, ntile * KT + (lane << shift), nlen) : -1;
       ok = bar_wait(&hd->dead, &hd->empty[st], e_ph, c);
       if (!ok) break;
       const unsigned ks = sptr(stages + st * S::kStage), vs = ks + S::kMat;
       if (tensor_copies) {
-        const int key = from + tile * KT + (lane << shift);
+        const int key = tile * KT + (lane << shift);
         const bool in = lane < (KT >> shift) && key < len;
         const bool bad = in && (id < 0 || id >= a.c.num_pages);
         if (bad) atomicOr(c.status, kAttnBadPage);
@@ -304,14 +293,14 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           hd->meta[st].bad[lane] = w;
         }
         if (lane == 0) {
-          hd->meta[st].u = Unit{b, g, rt, from + tile * KT, len, from, badm != 0, first, last, base};
+          hd->meta[st].u = Unit{b, g, rt, tile * KT, len, badm != 0, first, last, base};
         }
         __syncwarp();
         if (lane == 0) bar_expect(&hd->full[st], copies * R * RB * 2);
         __syncwarp();
         if constexpr (I8) {
           // scales, four keys a lane (a copy's keys are 8 at least, so of one page)
-          const int k4 = tile * KT + 4 * lane + from, page = __shfl_sync(~0u, id, (4 * lane) >> shift);
+          const int k4 = tile * KT + 4 * lane, page = __shfl_sync(~0u, id, (4 * lane) >> shift);
           const bool have = k4 < len && page >= 0 && page < a.c.num_pages;
           const long long p0 = have ? page : 0;
           const int at = c.scale_at + (g * c.page_size + (k4 & (c.page_size - 1))) * 4;
@@ -334,7 +323,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
         const long long head = g * c.head_stride;
         unsigned any_bad = 0;
         for (int k0 = 0; k0 < KT; k0 += 32) {
-          const int key = from + tile * KT + k0 + lane;
+          const int key = tile * KT + k0 + lane;
           const int page = entry(b, key, len);
           const bool bad = key < len && (page < 0 || page >= a.c.num_pages);
           if (bad) atomicOr(c.status, kAttnBadPage);
@@ -353,19 +342,19 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             const int r = (k + lane) / CPR, cc = (k + lane) % CPR;
             const int pg = __shfl_sync(~0u, good, r);
             if (cc >= chunks) continue;
-            const long long in = head + ((from + tile * KT + k0 + r) & (c.page_size - 1)) * c.slot_stride;
+            const long long in = head + ((tile * KT + k0 + r) & (c.page_size - 1)) * c.slot_stride;
             const long long p0 = pg < 0 ? 0 : pg;
             const unsigned at = key_at<RB, KT>(k0 + r, cc);
             cp16(ks + at, static_cast<const char*>(a.c.k) + (p0 * a.c.k_page_stride + in) * ES + cc * 16, pg >= 0);
             cp16(vs + at, static_cast<const char*>(a.c.v) + (p0 * a.c.v_page_stride + in) * ES + cc * 16, pg >= 0);
           }
         }
-        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, from + tile * KT, len, from, any_bad != 0, first, last, base};
+        if (lane == 0) hd->meta[st].u = Unit{b, g, rt, tile * KT, len, any_bad != 0, first, last, base};
         bar_arrive_copied(&hd->full[st]);
         __syncwarp();
         if (lane == 0) bar_arrive(&hd->full[st]);
       }
-      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; from = nfrom; nt = nnt; tend = ntend; base = nbase; id = id_next;
+      b = nb; g = ng; rt = nrt; tile = ntile; len = nlen; nt = nnt; tend = ntend; base = nbase; id = id_next;
       first = last;
     }
     int used = i;  // stages used: the units, and the end
@@ -402,7 +391,6 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   Unit cur;
   int qs = 0;
   unsigned q_ph = 0, meet_ph = 0;
-  int pq = 0;  // the item's places of hd->pre
   int buf = 0;  // merge buffer of the next item (T)
   bool ok = true;
   // All computing warps past this point.
@@ -414,6 +402,11 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     return ok;
   };
 
+  // Column of accumulator (k, x) of this lane.
+  const auto col = [&](int k, int x) {
+    const int t = lane & 3;
+    return Q8 ? 16 * (k >> 1) + 4 * t + 2 * (x & 1) + (k & 1) : 8 * k + 2 * t + (x & 1);
+  };
   const auto begin_item = [&]() {
     const float sc = c.scale * kLog2E * (Q8 && c.k_scale ? c.k_scale[cur.g] : 1.0f);
     vmax = 0x1p-100f;
@@ -477,12 +470,8 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     for (int k = 0; k < NO; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i) o[k][i] = 0.0f;
-    if constexpr (OWN) {
-      pq = qs;  // (its queries' places are handed back when the item ends)
-    } else {
-      __syncwarp();
-      if (lane == 0) bar_arrive(&hd->q_empty[qs]);
-    }
+    __syncwarp();
+    if (lane == 0) bar_arrive(&hd->q_empty[qs]);
     if (++qs == 2) { qs = 0; q_ph ^= 1; }
   };
 
@@ -719,11 +708,6 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     }
   };
 
-  // Column of accumulator (k, x) of this lane.
-  const auto col = [&](int k, int x) {
-    const int t = lane & 3;
-    return Q8 ? 16 * (k >> 1) + 4 * t + 2 * (x & 1) + (k & 1) : 8 * k + 2 * t + (x & 1);
-  };
   const auto out_row = [&](int r) {  // index of row r of the current item in [batch, n, H]
     const int j = r / c.rep;
     return (static_cast<long long>(cur.b) * a.n + j) * c.H + cur.g * c.rep + (r - j * c.rep);
@@ -742,19 +726,8 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     return ll == 0.0f ? make_float4(0, 0, 0, 0) : make_float4(x.x * f, x.y * f, x.z * f, x.w * f);
   };
 
-  // A finished row's four columns from d: joined with the group's prefix, if there
-  // is one, divided, and written.
-  const auto put_row = [&](int r, int d, float4 x, float mm, float ll, float vs) {
+  const auto put_row = [&](int r, int d, float4 x, float mm, float ll, float vs) {  // a finished row's four columns from d
     const long long row = out_row(r);
-    if (OWN && cur.from > 0) {
-      const long long token = static_cast<long long>(cur.b) * a.n + r / c.rep;
-      const PrefixAt at = prefix_at(hd->pre[pq][r / c.rep]);
-      float ref = mm - bias;
-      x = make_float4(x.x * vs, x.y * vs, x.z * vs, x.w * vs);
-      join_prefix(c, at, token, cur.g * c.rep + r % c.rep, d, x, ref, ll);
-      mm = ref + bias;
-      vs = 1.0f;
-    }
     put4(row, d, divided(x, ll, vs));
     if (d == 0) put_lse(row, mm, ll);
   };
@@ -764,7 +737,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   const auto end_item = [&]() {
     // the CTAs with the item's first and last tile
     const long long tile0 = cur.base + kItemCost;
-    const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(cur.len - cur.from)) * N - 1) / U;
+    const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(cur.len)) * N - 1) / U;
     const bool whole = c0 == c1;
     const long long slot = 2ll * blockIdx.x + (tile0 < u0 ? 0 : 1);
     float* po = c.ws_o + slot * c.step_rows * c.D;
@@ -972,10 +945,6 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
     if (cur.last) {
       end_item();
       if (!ok) break;
-      if constexpr (OWN) {
-        __syncwarp();
-        if (lane == 0) bar_arrive(&hd->q_empty[pq]);
-      }
     }
   }
 }
@@ -988,12 +957,8 @@ int row_variant(int rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : rows <= 32 ?
 template <int DP, bool MF16, bool QF16, int CK, int WM, int WN>
 cudaError_t prepare_one(int* ctas) {
   using S = Shape<DP, CK, WM, WN>;
-  auto k = step_kernel<DP, MF16, QF16, CK, WM, WN, false>;
+  auto k = step_kernel<DP, MF16, QF16, CK, WM, WN>;
   cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  if constexpr (WM < 2) {
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(step_kernel<DP, MF16, QF16, CK, WM, WN, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
-  }
   if (e != cudaSuccess) return e;
   int occ = 0;
   e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&occ, k, S::kThreads, S::kSmem);
@@ -1038,10 +1003,7 @@ cudaError_t launch_one(const AttnCfg& c, const StepArgs& a, int variant, cudaStr
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if constexpr (WM < 2) {  // (more than 16 rows of a shared call: tg_wide.cuh)
-    if (a.own) return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, CK, WM, WN, true>, c, a, row_tiles, 2, box, mk, mv);
-  }
-  return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, CK, WM, WN, false>, c, a, row_tiles, 2, box, mk, mv);
+  return cudaLaunchKernelEx(&cfg, step_kernel<DP, MF16, QF16, CK, WM, WN>, c, a, row_tiles, 2, box, mk, mv);
 }
 
 template <int DP, bool MF16, bool QF16, int CK>

@@ -19,9 +19,16 @@
 // about the largest so far (a power of f16's range apart would be lost), by which
 // the sums are multiplied at the end.
 //
-// A prefix item is a (group, key head, row tile): the tokens of the group's
-// sequences are neighbours in q.  Its parts are not joined here but where each
-// sequence's own keys are (join_prefix): those rows are spread over the GPU.
+// A shared call's item is a pair of key heads and as many whole sequences of one
+// group as a row tile holds: its tiles are the group's prefix, then each of those
+// sequences' own keys, which the rows of the others do not see.  So a prefix is read
+// once for all of them, and no second pass joins it with the rest.  (Own keys on the
+// step kernel, after a pass over the prefixes, took 46 to 63 us where they are 67 MB:
+// items of a tile or two, each with its beginning, its end and a join.)  The idle
+// rows' products are free while the copies bound it.  The parts of split items are
+// joined by a kernel of their own (tg_finish.cu), spread over the GPU.
+// An infinity or a NaN among one sequence's values reaches the other rows of its tile
+// (0 x NaN): rows that come out so are computed again there, each alone.
 //
 // One translation unit per kind of cache (tg_wide.cu, tg_wide_e4m3.cu,
 // tg_wide_i8.cu); internal to the library.
@@ -39,18 +46,12 @@ constexpr int kKeysW = 128;
 constexpr int kItemCostW = 2;   // beginning and ending an item, in tiles
 
 struct WItem {
-  int b, pair, rt, len;  // b: sequence or group, < 0: no more; len: where its keys end
-  int from;              // and begin
+  int b, pair, rt, len;  // b: its (first) sequence, < 0: no more; len: keys of it, or of the prefix
   int tok0, toks;        // its first row's token in q, and the tokens from there on
+  int tiles;             // of all CTAs
   int t0, t1;            // its tiles that are this CTA's
   int nch;               // key heads side by side: 2, or 1 at the end of an odd number
   long long base;        // units before it
-};
-
-// An entry of the work, a sequence or a group: where its keys end and begin, its
-// tokens in q, its row tiles.
-struct Entry {
-  int len, from, tok, toks, row_tiles;
 };
 
 constexpr int kSlotsMaxW = 10, kMetas = 8;
@@ -58,11 +59,11 @@ struct WBars {
   unsigned long long q_full, q_empty, kv_full[kSlotsMaxW], kv_empty[kSlotsMaxW], raw_full[kSlotsMaxW], raw_empty[kSlotsMaxW],
       scales_full[8], scales_ready[8][2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
   unsigned tmem;
-  int dead, last[2], first_b;
-  Entry first;
+  int dead, last[2], first_b, first_len;
   long long first_in, wsum[16];
   WItem item[2];
   unsigned bad[kMetas][4];  // by tile, round the ring: keys on pages that do not exist
+  int4 tile[kMetas];        // a shared call's: its keys; whose (from the item's first sequence; -1: the prefix); the first one's place
   float2 fac[kMetas][2];    // i8, by tile and key head: what the sums shrink by first; the scale the values are relative to
 };
 
@@ -86,7 +87,7 @@ struct WLay {
   // for, the pieces of the tiles before it (keys or values of one key head, two a tile
   // at least) have their places, and all but the last kRaw + kSlots of those are done.
   static constexpr int kScaleTiles = DP == 128 ? 4 : 8;
-  static_assert(2 * kScaleTiles >= 2 + kRaw + kSlots && kMetas % kScaleTiles == 0, "");
+  static_assert((!Q8 || 2 * kScaleTiles >= 2 + kRaw + kSlots) && 2 * kMetas >= 2 + kRaw + kSlots && kMetas % kScaleTiles == 0, "");
   static constexpr int kScaleB = CK == kI8 ? kScaleTiles * 2 * 2 * kKeysW * 4 : 0;  // [tile][head][keys, values][128]
   static constexpr int kKv = 2 * kTileB, kRawAt = kKv + kSlots * kTileB, kScaleAt = kRawAt + kRaw * kRawB, kBars = kScaleAt + kScaleB;
   static constexpr int kSmem = kBars + static_cast<int>(sizeof(WBars)) + 1024;
@@ -95,7 +96,8 @@ struct WLay {
 
 struct WSetup {
   int tpt;        // tokens of a row tile
-  int row_tiles;  // (of a sequence; of a group: by its size)
+  int row_tiles;  // of a sequence
+  int members;    // sequences of a row tile (a shared call; else, and for longer ones, 1)
   int pairs;      // of key heads
   int box;        // keys of one copy
   int wide;       // outputs 32-byte aligned
@@ -117,6 +119,15 @@ __device__ __forceinline__ void widen16(const uint4& r, unsigned (&w)[8]) {
 template <bool F16, bool I8>
 constexpr float kBias = I8 ? 6.0f : kWeightBias<F16>;
 
+// Weights of a tile of which none of the warp's rows sees a key.
+__device__ __forceinline__ void no_weights(unsigned ts) {
+  unsigned z[32];
+#pragma unroll
+  for (int x = 0; x < 32; ++x) z[x] = 0u;
+  tm_st32(ts, z);
+  tm_st32(ts + 32, z);
+}
+
 // softmax_tile over an 8-bit cache, from scores that stay in tensor memory, a few
 // columns at a time: the widening warps take registers that the whole row would
 // need (with them, spilled to a level 1 that shared memory has left no room, a
@@ -126,7 +137,7 @@ constexpr float kBias = I8 ? 6.0f : kWeightBias<F16>;
 // masked: rest keys from the tile's first are seen, except those in `bad`.
 template <bool I8>
 __device__ __forceinline__ void softmax_tile8(unsigned ts, unsigned to, int D, float sc, const float* scale, float shrink, bool masked,
-                                              int rest, const unsigned* bad, bool has_sums, float& m, float& l) {
+                                              int rest, const unsigned* bad, bool has_sums, float& m, float& l, bool sees) {
   constexpr float bias = kBias<true, I8>, most = I8 ? 255.0f * 64.0f : kMostSum<true>;
   if (I8 && has_sums && shrink != 1.0f) {
     scale_sums(to, D, shrink);
@@ -136,7 +147,7 @@ __device__ __forceinline__ void softmax_tile8(unsigned ts, unsigned to, int D, f
     return bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
   };
   unsigned p[2][32];
-  bool search = __any_sync(~0u, m == -INFINITY);
+  bool search = __any_sync(~0u, sees && m == -INFINITY);
   float tile_sum;
   for (;;) {
     if (search) {
@@ -213,18 +224,14 @@ __device__ __forceinline__ void softmax_tile8(unsigned ts, unsigned to, int D, f
   l += tile_sum;
 }
 
-// What a launch does: a step; a shared call's prefixes of groups; each sequence's own
-// keys behind them.
-enum Pass { kStepPass, kPrefixPass, kOwnPass };
-
 // F16: the tensors' type is f16, else bf16.
-template <int DP, bool F16, int CK, Pass PASS>
+// SHARED: a shared call.
+template <int DP, bool F16, int CK, bool SHARED>
 __global__ void __launch_bounds__(WLay<DP, CK>::kThreads, 1)
 wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_constant__ CUtensorMap mq,
             const __grid_constant__ CUtensorMap mk, const __grid_constant__ CUtensorMap mv) {
   using L = WLay<DP, CK>;
   constexpr bool Q8 = L::Q8, I8 = CK == kI8;
-  constexpr bool SHARED = PASS == kPrefixPass, OWN = PASS == kOwnPass;
   constexpr bool PF16 = Q8 || F16;  // the weights' type, and the values'
   constexpr int NT = L::kThreads;
   extern __shared__ unsigned char smem_raw[];
@@ -236,7 +243,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     bar_init(&s->q_empty, 1);
     for (int i = 0; i < L::kSlots; ++i) { bar_init(&s->kv_full[i], Q8 ? L::kWideners : 1); bar_init(&s->kv_empty[i], 1); }
     for (int i = 0; i < L::kScaleTiles; ++i) {
-      bar_init(&s->scales_full[i], 32);
+      bar_init(&s->scales_full[i], 33);
       for (int t = 0; t < 2; ++t) bar_init(&s->scales_ready[i][t], 1);
     }
     for (int i = 0; i < L::kRaw; ++i) { bar_init(&s->raw_full[i], 1); bar_init(&s->raw_empty[i], L::kWideners); }
@@ -261,53 +268,69 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
   const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
   const auto tiles_of = [](int keys) { return keys > 0 ? (keys + kKeysW - 1) / kKeysW : 1; };
-  const auto entry_of = [&](int b) {
-    if constexpr (SHARED) {
-      const long long s0 = a.goff[b], s1 = a.goff[b + 1];
-      // a group of one shares nothing; a prefix is taken up to a whole copy
-      const int keys = s1 - s0 > 1 ? a.plens[b] & ~(ws.box - 1) : 0;
-      const int toks = static_cast<int>(s1 - s0) * a.n;
-      return Entry{keys, 0, static_cast<int>(s0) * a.n, toks, (toks + ws.tpt - 1) / ws.tpt};
-    } else {
-      const int l = checked(a.c.lens[b]);
-      return Entry{l, OWN ? min(c.ws_start[b], l) : 0, b * a.n, a.n, ws.row_tiles};
-    }
+  // of a sequence, where its keys behind a prefix of `keys` begin: at 0 if one of its tokens does not see all of it
+  const auto begin_of = [&](int len, int keys) { return len - a.n + 1 >= keys ? keys : 0; };
+  const int bper = (a.c.batch + NT - 1) / NT, b_first = tid * bper, b_end = min(a.c.batch, b_first + bper);
+  long long mine = 0;
+  int ng = 0;  // groups
+  int len0 = 0;
+  // The work of a pair of key heads is laid out in the sequences' order; at[b] is
+  // where sequence b's begins.  (In the memory of the copies, which come later.)
+  int* const gat = reinterpret_cast<int*>(smem + L::kKv);  // [groups + 1]: offsets
+  int* const gkeys = gat + a.groups + 1;                   // [groups]: keys of the prefix
+  unsigned* const at = reinterpret_cast<unsigned*>(gkeys + a.groups);
+  // the group of sequence b, looked for from group i on: its first sequence, the one behind it, its keys
+  const auto group_of = [&](int b, int& i, int& g0, int& g1, int& keys) {
+    while (i < ng && gat[i + 1] <= b) ++i;
+    g0 = i < ng ? gat[i] : b;
+    g1 = i < ng ? gat[i + 1] : b + 1;
+    keys = i < ng ? gkeys[i] : 0;
   };
-  // A sequence takes part in its group's prefix when all its tokens see all of it.
-  const auto takes_part = [&](int b, int keys) { return checked(a.c.lens[b]) - a.n + 1 >= keys; };
-  // its units
-  const auto cost = [&](const Entry& e) {
-    if (SHARED && e.len == 0) return 0ll;
-    return static_cast<long long>(tiles_of(e.len - e.from) + kItemCostW) * (ws.pairs * e.row_tiles);
-  };
-  const int entries = SHARED ? a.groups : a.c.batch;
-  const int bper = (entries + NT - 1) / NT, b_first = tid * bper, b_end = min(entries, b_first + bper);
+  int gi = 0, g0 = 0, g1 = 0, gk = 0;
   if constexpr (SHARED) {
-    // groups in order and inside the batch, prefixes inside the table; else none is shared
-    bool fine = tid > 0 || entries == 0 || a.goff[0] == 0;
-    for (int b = b_first; b < b_end; ++b) {
-      const long long s0 = a.goff[b], s1 = a.goff[b + 1];
-      fine = fine && s0 >= 0 && s0 <= s1 && s1 <= a.c.batch && a.plens[b] >= 0 && a.plens[b] <= max_len;
+    bool fine = true;
+    for (int i = tid; i <= a.groups; i += NT) {
+      const long long o = a.goff[i];
+      fine = fine && o >= 0 && o <= a.c.batch && (i > 0 || o == 0);
+      gat[i] = static_cast<int>(o);
+      if (i < a.groups) {
+        const int keys = a.plens[i];
+        fine = fine && keys >= 0 && keys <= max_len;
+        gkeys[i] = keys;
+      }
+    }
+    __syncthreads();
+    for (int i = tid; i < a.groups; i += NT) {
+      fine = fine && gat[i] <= gat[i + 1];
+      // a group of one shares nothing; a prefix is taken up to a whole copy
+      gkeys[i] = gat[i + 1] - gat[i] > 1 ? gkeys[i] & ~(ws.box - 1) : 0;
     }
     fine = __syncthreads_and(fine);
     if (!fine && blockIdx.x == 0 && tid == 0) atomicOr(c.status, kAttnBadRow);
-    // what is left to each sequence itself begins here
-    const long long behind = fine && entries > 0 ? a.goff[entries] : 0;
-    for (long long b = behind + blockIdx.x * NT + tid; b < a.c.batch; b += static_cast<long long>(gridDim.x) * NT) c.ws_start[b] = 0;
-    if (!fine) return;
-    for (int i = blockIdx.x; i < entries; i += gridDim.x) {
-      const Entry e = entry_of(i);
-      const int s0 = static_cast<int>(a.goff[i]), s1 = static_cast<int>(a.goff[i + 1]);
-      for (int b = s0 + tid; b < s1; b += NT) c.ws_start[b] = takes_part(b, e.len) ? e.len : 0;
+    ng = fine ? a.groups : 0;
+    if (b_first < b_end) {
+      int hi = ng;  // the last group that begins at or before b_first
+      while (hi - gi > 1) {
+        const int mid = (gi + hi) >> 1;
+        if (gat[mid] <= b_first) gi = mid; else hi = mid;
+      }
     }
-  }
-  long long mine = 0;
-  Entry e0{};
-  for (int b = b_first; b < b_end; ++b) {
-    const Entry e = entry_of(b);
-    if (!SHARED && blockIdx.x == 0 && checked(a.c.lens[b]) != a.c.lens[b]) atomicOr(c.status, kAttnBadRow);
-    if (b == b_first) e0 = e;
-    mine += cost(e);
+    for (int b = b_first; b < b_end; ++b) {
+      const int raw = a.c.lens[b], l = checked(raw);
+      if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
+      group_of(b, gi, g0, g1, gk);
+      const int pre = gk > 0 ? tiles_of(gk) : 0, own = tiles_of(l - begin_of(l, gk));
+      at[b] = static_cast<unsigned>(mine);
+      mine += ws.row_tiles > 1 ? static_cast<long long>(ws.row_tiles) * (kItemCostW + pre + own)
+                               : own + ((b - g0) % ws.members == 0 ? kItemCostW + pre : 0);
+    }
+  } else {
+    for (int b = b_first; b < b_end; ++b) {
+      const int raw = a.c.lens[b], l = checked(raw);
+      if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
+      if (b == b_first) len0 = l;
+      mine += tiles_of(l) + kItemCostW;
+    }
   }
   long long before = mine;
 #pragma unroll
@@ -317,35 +340,57 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   }
   if (lane == 31) s->wsum[warp] = before;
   __syncthreads();
-  long long U = 0;
+  long long total = 0;
 #pragma unroll
   for (int w = 0; w < NT / 32; ++w) {
     if (w < warp) before += s->wsum[w];
-    U += s->wsum[w];
+    total += s->wsum[w];
   }
   before -= mine;
-  const long long N = min(static_cast<long long>(gridDim.x), max(1ll, U / 2));
-  if (blockIdx.x >= N || U == 0) return;
+  const int per_tile = ws.pairs * (SHARED ? 1 : ws.row_tiles);
+  const long long U = total * per_tile, N = min(static_cast<long long>(gridDim.x), max(1ll, U / 2));
+  if (blockIdx.x >= N) return;
   const long long u0 = U * blockIdx.x / N, u1 = U * (blockIdx.x + 1) / N;
-  if (mine > 0 && before <= u0 && u0 < before + mine) {
-    int b = b_first;
-    Entry e = e0;
-    long long at = before;
-    for (;;) {
-      const long long t = cost(e);
-      if (at + t > u0) break;
-      at += t;
-      e = entry_of(++b);
+  if constexpr (SHARED) {
+    for (int b = b_first; b < b_end; ++b) at[b] += static_cast<unsigned>(before);
+    __syncthreads();
+    const long long in = u0 % total;
+    if (mine > 0 && before <= in && in < before + mine) {
+      int b = b_first;
+      while (b + 1 < b_end && at[b + 1] <= in) ++b;
+      gi = 0;
+      int hi = ng;
+      while (hi - gi > 1) {
+        const int mid = (gi + hi) >> 1;
+        if (gat[mid] <= b) gi = mid; else hi = mid;
+      }
+      group_of(b, gi, g0, g1, gk);
+      b -= (b - g0) % ws.members;  // the item's first
+      s->first_b = b;
+      s->first_len = gi;
+      s->first_in = in - at[b];
     }
-    s->first_b = b;
-    s->first = e;
-    s->first_in = u0 - at;
+  } else {
+    if (mine > 0 && before * per_tile <= u0 && u0 < (before + mine) * per_tile) {
+      int b = b_first, l = len0;
+      long long from = before;
+      for (;;) {
+        const int t = tiles_of(l) + kItemCostW;
+        if ((from + t) * per_tile > u0) break;
+        from += t;
+        l = checked(a.c.lens[++b]);
+      }
+      s->first_b = b;
+      s->first_len = l;
+      s->first_in = u0 - from * per_tile;
+    }
   }
   if (warp == 8) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(sptr(&s->tmem)) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     fence_before();
   }
+  if (SHARED) fence_async();  // (copies come where the work was laid out)
   __syncthreads();
   fence_after();
   const unsigned tmem = s->tmem;
@@ -360,14 +405,53 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   if (warp == 9) {
     // ---- items, pages and copies --------------------------------------------
     registers_down<L::kRegThird>();
-    int b = s->first_b;
-    Entry e = s->first;
-    int nt = tiles_of(e.len - e.from);
-    const long long in = s->first_in;
-    const int skip = static_cast<int>(in / (nt + kItemCostW));
-    int rt = skip % e.row_tiles, pr = skip / e.row_tiles;
-    long long base = u0 - in % (nt + kItemCostW);
     const int shift = 31 - __clz(ws.box), per = kKeysW >> shift;  // copies of a tile
+    int b = s->first_b, rt, pr, len;
+    long long base;  // units before the item
+    // a shared call's: the group, and of member lane + 32 i of the item its length and its last own tile's number + 1
+    int grp = 0, gs = 0, ge = 0, mlen[4] = {0, 0, 0, 0}, mend[4] = {0, 0, 0, 0};
+    int nt;
+    const auto members = [&]() {  // of the item that begins with sequence b: fills these in, gives its tiles
+      const int nm = min(ws.members, ge - b), pre = len > 0 ? tiles_of(len) : 0;
+      int sum = pre;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const bool is = lane + 32 * i < nm;
+        mlen[i] = is ? checked(a.c.lens[b + lane + 32 * i]) : 0;
+        int own = is ? tiles_of(mlen[i] - begin_of(mlen[i], len)) : 0;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+          const int v = __shfl_up_sync(~0u, own, d);
+          if (lane >= d) own += v;
+        }
+        mend[i] = sum + own;
+        sum = __shfl_sync(~0u, mend[i], 31);
+      }
+      return sum;
+    };
+    const auto enter_group = [&]() {  // the group of sequence b, from number grp on
+      while (grp < ng && a.goff[grp + 1] <= b) ++grp;
+      gs = grp < ng ? static_cast<int>(a.goff[grp]) : b;
+      ge = grp < ng ? static_cast<int>(a.goff[grp + 1]) : b + 1;
+      len = grp < ng && ge - gs > 1 ? a.plens[grp] & ~(ws.box - 1) : 0;
+    };
+    if constexpr (SHARED) {
+      grp = s->first_len;
+      enter_group();
+      nt = members();
+      pr = static_cast<int>(u0 / total);
+      const int skip = static_cast<int>(s->first_in / (nt + kItemCostW));
+      rt = ws.row_tiles > 1 ? skip : 0;
+      base = u0 - s->first_in + static_cast<long long>(rt) * (nt + kItemCostW);
+    } else {
+      len = s->first_len;
+      nt = tiles_of(len);
+      const long long in = s->first_in;
+      const int skip = static_cast<int>(in / (nt + kItemCostW));
+      rt = skip % ws.row_tiles;
+      pr = skip / ws.row_tiles;
+      base = u0 - in % (nt + kItemCostW);
+    }
     const unsigned kv0 = sptr(smem + (Q8 ? L::kRawAt : L::kKv));
     unsigned pos = 0, q_ph = 1;
     int it_n = 0, meta = 0;
@@ -382,10 +466,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         it.b = b;
         it.pair = pr;
         it.rt = rt;
-        it.len = e.len;
-        it.from = e.from;
-        it.tok0 = e.tok + rt * ws.tpt;
-        it.toks = e.toks - rt * ws.tpt;
+        it.len = len;
+        it.tok0 = b * a.n + rt * ws.tpt;
+        it.toks = SHARED && ws.row_tiles == 1 ? min(ws.members, ge - b) * a.n : a.n - rt * ws.tpt;
+        it.tiles = nt;
         it.t0 = static_cast<int>(max(0ll, u0 - base - kItemCostW));
         it.t1 = static_cast<int>(min(static_cast<long long>(nt), u1 - base - kItemCostW));
         it.nch = min(2, c.G - 2 * pr);
@@ -397,35 +481,68 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       ++it_n;
       if (!more) break;
-      // the row of the page table: the sequence's, or that of the group's first one
-      const int32_t* const table = a.c.table + (SHARED ? a.goff[b] : b) * a.c.table_stride;
-      const auto page_of = [&](int tile) {
-        const int key = e.from + tile * kKeysW + (lane << shift);
-        return lane < per && key < e.len ? __ldg(table + (key >> c.page_shift)) : -1;
+      // A tile's keys, whose they are, its first one's place, and the row of the page table.
+      struct Tile {
+        int keys, mem, key0, row;
       };
-      int id = page_of(it.t0);
+      const auto tile_at = [&](int j) {
+        if constexpr (!SHARED) return Tile{len - j * kKeysW, 0, j * kKeysW, b};
+        const int pre = len > 0 ? tiles_of(len) : 0;
+        if (j < pre) return Tile{len - j * kKeysW, -1, j * kKeysW, gs};
+        int mem = 0;  // members whose tiles end before this one
+#pragma unroll
+        for (int i = 0; i < 4; ++i) mem += __popc(__ballot_sync(~0u, lane + 32 * i < ws.members && mend[i] <= j));
+        const int i = mem >> 5;
+        const int l = __shfl_sync(~0u, i == 0 ? mlen[0] : i == 1 ? mlen[1] : i == 2 ? mlen[2] : mlen[3], mem & 31);
+        const int m1 = mem - 1, k = m1 >> 5;
+        const int e = __shfl_sync(~0u, k == 0 ? mend[0] : k == 1 ? mend[1] : k == 2 ? mend[2] : mend[3], m1 & 31);
+        const int key0 = begin_of(l, len) + (j - (mem > 0 ? e : pre)) * kKeysW;
+        return Tile{l - key0, mem, key0, b + mem};
+      };
+      const auto page_of = [&](const Tile& t) {
+        const int key = lane << shift;
+        return lane < per && key < t.keys ? __ldg(a.c.table + t.row * a.c.table_stride + ((t.key0 + key) >> c.page_shift)) : -1;
+      };
+      Tile tl = tile_at(it.t0);
+      int id = page_of(tl);
       for (int j = it.t0; j < it.t1 && ok; ++j) {
-        const int key = e.from + j * kKeysW + (lane << shift);
-        const bool in = lane < per && key < e.len, bad = in && (id < 0 || id >= a.c.num_pages);
+        const int key = lane << shift;
+        const bool in = lane < per && key < tl.keys, bad = in && (id < 0 || id >= a.c.num_pages);
         if (bad) atomicOr(c.status, kAttnBadPage);
         const unsigned badm = __ballot_sync(~0u, bad);
         const int copies = __popc(__ballot_sync(~0u, in && !bad));
-        const int id_next = j + 1 < it.t1 ? page_of(j + 1) : -1;
-        const int slot = key & (c.page_size - 1);
+        const int slot = (tl.key0 + key) & (c.page_size - 1);
+        Tile tn = tl;
+        int id_next = -1;
+        if (j + 1 < it.t1) {
+          tn = tile_at(j + 1);
+          id_next = page_of(tn);
+        }
+        // (the tile that had this place in the ring is done: see WLay)
+        if (SHARED && lane == 0) s->tile[meta] = make_int4(max(0, min(kKeysW, tl.keys)), tl.mem, tl.key0, 0);
+        if (lane < 4) {
+          unsigned bits = 0;
+          if (badm)
+            for (int k = 0; k < 32; ++k)
+              if ((badm >> ((lane * 32 + k) >> shift)) & 1) bits |= 1u << k;
+          s->bad[meta][lane] = bits;
+        }
+        __syncwarp();
         if constexpr (I8) {
           // the scales, the values' too: four keys a lane, both key heads' at once (a bulk copy
           // of a page's takes 0.2 us, one after the other)
-          const int k4 = e.from + j * kKeysW + 4 * lane, page = __shfl_sync(~0u, id, (4 * lane) >> shift);
-          const bool have = k4 < e.len && page >= 0 && page < a.c.num_pages;
+          const int page = __shfl_sync(~0u, id, (4 * lane) >> shift);
+          const bool have = 4 * lane < tl.keys && page >= 0 && page < a.c.num_pages;
           const long long p0 = have ? page : 0;
           const int mt = meta % L::kScaleTiles;
           for (int t = 0; t < it.nch; ++t) {
-            const int at = c.scale_at + ((2 * pr + t) * c.page_size + (k4 & (c.page_size - 1))) * 4;
+            const int at = c.scale_at + ((2 * pr + t) * c.page_size + ((tl.key0 + 4 * lane) & (c.page_size - 1))) * 4;
             const unsigned to = sptr(smem + L::kScaleAt) + (mt * 2 + t) * (2 * kKeysW * 4) + lane * 16;
             cp16(to, static_cast<const char*>(a.c.k) + p0 * a.c.k_page_stride + at, have);
             cp16(to + kKeysW * 4, static_cast<const char*>(a.c.v) + p0 * a.c.v_page_stride + at, have);
           }
           bar_arrive_copied(&s->scales_full[mt]);
+          if (lane == 0) bar_arrive(&s->scales_full[mt]);
         }
         for (int w = 0; w < 2 && ok; ++w) {
           if (w == 1 && j == it.t0) {
@@ -434,7 +551,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             if (!ok) break;
             q_ph ^= 1;
             if (lane == 0) {
-              const int rows = (SHARED ? ws.tpt : min(a.n, ws.tpt)) * c.rep;
+              const int rows = (SHARED ? ws.tpt : min(a.n, ws.tpt)) * c.rep;  // of the box
               bar_expect(&s->q_full, it.nch * (DP / 64) * rows * 128);
               for (int t = 0; t < it.nch; ++t)
                 for (int x = 0; x < DP / 64; ++x)
@@ -446,14 +563,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             unsigned long long* const full = Q8 ? &s->raw_full[st] : &s->kv_full[st];
             ok = bar_wait(&s->dead, Q8 ? &s->raw_empty[st] : &s->kv_empty[st], (Q8 ? raw_use(pos) : use_of(pos)) ^ 1, c);
             if (!ok) break;
-            if (w == 0 && t == 0 && lane < 4) {
-              unsigned bits = 0;
-              if (badm)
-                for (int k = 0; k < 32; ++k)
-                  if ((badm >> ((lane * 32 + k) >> shift)) & 1) bits |= 1u << k;
-              s->bad[meta][lane] = bits;
-            }
-            __syncwarp();
             if (lane == 0) bar_expect(full, copies * ws.box * (Q8 ? DP : (DP / 64) * 128));
             __syncwarp();
             if (in && !bad) {
@@ -470,20 +579,28 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           }
         }
         meta = (meta + 1) % kMetas;
+        tl = tn;
         id = id_next;
       }
       if (!ok) break;
       base += nt + kItemCostW;
-      if (++rt == e.row_tiles) {
+      if (++rt == ws.row_tiles) {
         rt = 0;
-        if (++pr == ws.pairs) {
-          pr = 0;
-          e = Entry{0, 0, 0, 0, 1};
-          while (++b < entries) {  // (groups that share nothing are no work)
-            e = entry_of(b);
-            if (!SHARED || e.len > 0) break;
+        if constexpr (SHARED) {
+          b = min(b + ws.members, ge);
+          if (b == a.c.batch) {
+            ++pr;
+            b = grp = ge = 0;
           }
-          nt = tiles_of(e.len - e.from);
+          if (pr < ws.pairs) {
+            if (b == ge) enter_group();
+            nt = members();
+          }
+        } else if (++pr == ws.pairs) {
+          pr = 0;
+          ++b;
+          len = b < a.c.batch ? checked(a.c.lens[b]) : 0;
+          nt = tiles_of(len);
         }
       }
     }
@@ -509,7 +626,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const int is = it_n & 1;
       ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
-      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len - s->item[is].from;
+      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len;
       __syncwarp();
       if (lane == 0) bar_arrive(&s->item_empty[is]);
       ++it_n;
@@ -517,8 +634,12 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       ok = bar_wait(&s->dead, &s->q_full, q_ph, c);
       if (!ok) break;
       q_ph ^= 1;
+      int now = t0;  // the tile that meta stands for
       // keys of a tile that there are, in steps of 16
-      const auto width = [&](int j) { return max(16, min(kKeysW, (len - j * kKeysW + 15) & ~15)); };
+      const auto keys_of = [&](int j) {  // (known once its first copy has landed)
+        return SHARED ? s->tile[(meta + j - now) % kMetas].x : max(0, min(kKeysW, len - j * kKeysW));
+      };
+      const auto width = [&](int j) { return max(16, (keys_of(j) + 15) & ~15); };
       const auto qk = [&](int t, int j, unsigned at) {
         ok = bar_wait(&s->dead, &s->kv_full[slot_of(at)], use_of(at), c);
         if (!ok) return;
@@ -548,7 +669,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           // Values of keys that do not exist are what the page or an earlier tile
           // holds; their weights are 0, but 0 x NaN is not: zero what is read.
           // (Of an 8-bit tile the widening warps do.)
-          const int end = max(0, len - j * kKeysW);
+          const int end = keys_of(j);
           const unsigned any_bad = Q8 ? 0u : s->bad[meta][0] | s->bad[meta][1] | s->bad[meta][2] | s->bad[meta][3];
           if (!Q8 && (end < kKeysW || any_bad)) {
             const int stop = width(j);
@@ -579,6 +700,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         }
         pos = next;
         meta = (meta + 1) % kMetas;
+        ++now;
       }
       if (!ok) break;
     }
@@ -595,17 +717,18 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const int is = it_n & 1;
       ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
-      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len - s->item[is].from;
+      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len;
       __syncwarp();
       if (lane == 0) bar_arrive(&s->item_empty[is]);
       ++it_n;
       if (b < 0) break;
       // one piece: keys (KEYS) or values of one key head
-      const auto piece = [&](auto keys, int end, int stop) {
+      const auto piece = [&](auto keys, int j) {
         constexpr bool KEYS = decltype(keys)::value;
         const int rs = raw_of(pos), st = slot_of(pos);
         ok = bar_wait(&s->dead, &s->raw_full[rs], raw_use(pos), c);
         if (!ok) return;
+        const int end = SHARED ? s->tile[meta].x : max(0, min(kKeysW, len - j * kKeysW)), stop = max(16, (end + 15) & ~15);
         ok = bar_wait(&s->dead, &s->kv_empty[st], use_of(pos) ^ 1, c);
         if (!ok) return;
         const uint4* const src = reinterpret_cast<const uint4*>(smem + L::kRawAt + rs * L::kRawB);
@@ -646,9 +769,8 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         ++pos;
       };
       for (int j = t0; j < t1 && ok; ++j) {
-        const int end = max(0, min(kKeysW, len - j * kKeysW)), stop = max(16, (end + 15) & ~15);
-        for (int t = 0; t < nch && ok; ++t) piece(std::true_type(), end, stop);
-        for (int t = 0; t < nch && ok; ++t) piece(std::false_type(), end, stop);
+        for (int t = 0; t < nch && ok; ++t) piece(std::true_type(), j);
+        for (int t = 0; t < nch && ok; ++t) piece(std::false_type(), j);
         meta = (meta + 1) % kMetas;
       }
       if (!ok) break;
@@ -665,7 +787,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const int is = it_n & 1;
       ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
       if (!ok) break;
-      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len - s->item[is].from;
+      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len;
       __syncwarp();
       if (lane == 0) bar_arrive(&s->item_empty[is]);
       ++it_n;
@@ -684,7 +806,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           const float base2 = c.scale * kLog2E;
           const float4 x = *vs, y = *kf;
           float f[4] = {x.x, x.y, x.z, x.w};
-          const int key = 4 * lane, end = len - j * kKeysW;
+          const int key = 4 * lane, end = SHARED ? s->tile[meta].x : len - j * kKeysW;
           unsigned top = 0u;
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
@@ -743,11 +865,20 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         continue;
       }
       const int g = 2 * it.pair + t;
-      const bool real = tok < ws.tpt && tok < it.toks && (!SHARED || takes_part((it.tok0 + tok) / a.n, it.len));
+      const bool real = tok < ws.tpt && tok < it.toks;
       const float sc = c.scale * kLog2E * (CK == kE4M3 && c.k_scale ? c.k_scale[g] : 1.0f);
-      // keys that the row sees, and the fewest that any does
-      const int lim_w = it.len - it.from - (SHARED ? 0 : a.n - 1);
-      const int lim = SHARED || !real ? it.len - it.from : lim_w + (a.n - it.toks + tok);
+      // keys that the row sees: of its sequence (a shared call: which of the item's) and the
+      // fewest that any row does
+      int lim, mem = 0, prefix = 0;  // prefix: keys of it that the row sees, all or none
+      const int lim_w = it.len - a.n + 1;
+      if constexpr (SHARED) {
+        const int at = it.tok0 + tok, b = real ? at / a.n : 0, l = checked(a.c.lens[b]);
+        mem = b - it.b;
+        lim = l - a.n + (at - b * a.n) + 1;
+        prefix = begin_of(l, it.len);
+      } else {
+        lim = real ? lim_w + (a.n - it.toks + tok) : it.len;
+      }
       float vmax = 1.0f;
       float m = real ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = it.t0; j < it.t1; ++j) {
@@ -757,8 +888,15 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         fence_after();
         const unsigned* bad = s->bad[meta];
         const unsigned any_bad = bad[0] | bad[1] | bad[2] | bad[3];
-        const bool masked = (j + 1) * kKeysW > lim_w || any_bad;
-        const int rest = lim - j * kKeysW;
+        // the first keys of the tile are seen; by none of a row of no token, by its own choice
+        int rest = lim - j * kKeysW;
+        bool masked = (j + 1) * kKeysW > lim_w || any_bad, sees = true;
+        if constexpr (SHARED) {
+          const int4 tl = s->tile[meta];
+          rest = !real ? kKeysW : tl.y < 0 ? (prefix > 0 ? tl.x : 0) : tl.y == mem ? lim - tl.z : 0;
+          sees = real && rest > 0;
+          masked = __any_sync(~0u, rest < kKeysW) || any_bad;
+        }
         if constexpr (Q8) {
           float shrink = 1.0f;
           if constexpr (I8) {
@@ -769,8 +907,13 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             shrink = f.x;
             vmax = f.y;
           }
-          softmax_tile8<I8>(ts, to, c.D, sc, reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4)),
-                            shrink, masked, rest, bad, j > it.t0, m, l);
+          if (SHARED && !__any_sync(~0u, sees)) {
+            if (I8 && j > it.t0 && shrink != 1.0f) scale_sums(to, c.D, shrink);
+            no_weights(ts);
+          } else softmax_tile8<I8>(ts, to, c.D, sc, reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4)),
+                            shrink, masked, rest, bad, j > it.t0, m, l, sees);
+        } else if (SHARED && !__any_sync(~0u, sees)) {
+          no_weights(ts);
         } else {
           unsigned v[4][32];
 #pragma unroll
@@ -787,7 +930,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
                 if (off & (1u << y)) v[x][y] = 0xff800000u;  // -infinity
             }
           }
-          softmax_tile<F16>(v, ts, to, c.D, sc, j > it.t0, m, l);
+          softmax_tile<F16>(v, ts, to, c.D, sc, j > it.t0, m, l, sees);
         }
         meta = (meta + 1) % kMetas;
         tm_wait_st();
@@ -802,42 +945,31 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       fence_after();
       // the CTAs with the item's first and last tile
       const long long tile0 = it.base + kItemCostW;
-      const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + tiles_of(it.len - it.from)) * N - 1) / U;
+      const long long c0 = ((tile0 + 1) * N - 1) / U, c1 = ((tile0 + (SHARED ? it.tiles : tiles_of(it.len))) * N - 1) / U;
       const bool whole = c0 == c1;
       const long long token = it.tok0 + tok, at = token * c.H + g * c.rep + head;
-      const long long mine_part = wide_part(SHARED ? kPrefixRows : c.step_rows, blockIdx.x, tile0 < u0 ? 0 : 1, t) + row;
+      const long long mine_part = wide_part(SHARED ? kPartRows : c.step_rows, blockIdx.x, tile0 < u0 ? 0 : 1, t) + row;
       // what the values' sums stand for
       const float vs = I8 ? vmax : CK == kE4M3 && c.v_scale ? c.v_scale[g] : 1.0f;
-      const bool to_out = !SHARED && whole;
-      const float f = !to_out ? vs : l == 0.0f ? 0.0f : vs / l;
-      const PrefixAt pre = OWN && real && it.from > 0 ? prefix_at(__ldcg(prefix_entry(c, token, g))) : PrefixAt{0, 0, 0};
-      float* const parts_to = !SHARED ? c.ws_o + mine_part * c.D : whole ? c.ws_pre_o + at * c.D : c.ws_part_o + mine_part * c.D;
-      float ref = m - bias, sum = l;
+      const float f = !whole ? vs : l == 0.0f ? 0.0f : vs / l;
+      float* const parts_to = (SHARED ? c.ws_part_o : c.ws_o) + mine_part * c.D;
+      float zero = 0.0f;  // or NaN, when the sums hold an infinity or one
 #pragma unroll 1
       for (int x = 0; x < c.D; x += 16) {
         unsigned o[16];
         tm_ld16(o, to + x);
         tm_wait_ld();
         tm_pin(o);
-        if (!real) continue;
-        if (to_out) {
+        if (!real || (SHARED && !whole && l == 0.0f)) continue;
+        if constexpr (SHARED) {
+#pragma unroll
+          for (int y = 0; y < 16; ++y) zero = fmaf(__uint_as_float(o[y]), 0.0f, zero);
+        }
+        if (whole) {
           unsigned w[8];
-          if (OWN && pre.parts > 0) {
 #pragma unroll
-            for (int y = 0; y < 4; ++y) {
-              float4 acc = make_float4(__uint_as_float(o[4 * y]) * vs, __uint_as_float(o[4 * y + 1]) * vs, __uint_as_float(o[4 * y + 2]) * vs, __uint_as_float(o[4 * y + 3]) * vs);
-              ref = m - bias;
-              sum = l;
-              join_prefix(c, pre, token, g * c.rep + head, x + 4 * y, acc, ref, sum);
-              const float e = sum == 0.0f ? 0.0f : 1.0f / sum;
-              w[2 * y] = sum == 0.0f ? 0u : pack2<F16>(acc.x * e, acc.y * e);
-              w[2 * y + 1] = sum == 0.0f ? 0u : pack2<F16>(acc.z * e, acc.w * e);
-            }
-          } else {
-#pragma unroll
-            for (int y = 0; y < 8; ++y)
-              w[y] = l == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
-          }
+          for (int y = 0; y < 8; ++y)
+            w[y] = l == 0.0f ? 0u : pack2<F16>(__uint_as_float(o[2 * y]) * f, __uint_as_float(o[2 * y + 1]) * f);
           uint16_t* dst = static_cast<uint16_t*>(a.out) + at * c.D + x;
           if (ws.wide) {
             asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), TG_I8(w, 0) : "memory");
@@ -860,16 +992,19 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       fence_before();  // the reads of O come before the next item's products
       if constexpr (SHARED) {
-        // joined with each sequence's own keys
+        // (what is left to do: tg_finish.cu)
         if (real) {
-          *(whole ? c.ws_pre_ml + at : c.ws_part_ml + mine_part) = make_float2(m - bias, l);
-          if (head == 0 && t == 0 && blockIdx.x == c0)
-            c.ws_pre[token * ws.pairs + it.pair] = make_int4(static_cast<int>(c0), static_cast<int>(c1 - c0) + 1, row, 0);  // PrefixAt
+          if (!whole) c.ws_part_ml[mine_part] = make_float2(m - bias, l);
+          else if (a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l) - bias) * kLn2;
+          if (blockIdx.x == c0) {
+            c.ws_alone[at] = whole && l != 0.0f && !(zero + l * 0.0f == 0.0f);
+            if (head == 0 && t == 0) c.ws_pre[token * ws.pairs + it.pair] = make_int4(static_cast<int>(c0), static_cast<int>(c1 - c0) + 1, row, 0);
+          }
         }
         continue;
       }
       if (whole) {
-        if (real && a.lse) a.lse[at] = sum == 0.0f ? -INFINITY : (OWN && pre.parts > 0 ? ref + log2f(sum) : m + log2f(l) - bias) * kLn2;
+        if (real && a.lse) a.lse[at] = l == 0.0f ? -INFINITY : (m + log2f(l) - bias) * kLn2;
         continue;
       }
       if (real) c.ws_ml[mine_part] = make_float2(m, l);
@@ -942,17 +1077,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           if (r >= rows) break;
           const int tk = (r * inv_rep) >> 16;
           const long long to_row = first + r + static_cast<long long>(tk) * (c.H - c.rep);
-          float ref = mm[y];
-          if (OWN && it.from > 0) {
-            ref -= bias;
-            const PrefixAt pre = prefix_at(__ldcg(prefix_entry(c, it.tok0 + tk, g)));
-            join_prefix(c, pre, it.tok0 + tk, g * c.rep + r - tk * c.rep, d, acc[y], ref, ll[y]);
-            ref += bias;
-          }
           const float e = ll[y] == 0.0f ? 0.0f : 1.0f / ll[y];
           *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + to_row * c.D + d) =
               make_uint2(pack2<F16>(acc[y].x * e, acc[y].y * e), pack2<F16>(acc[y].z * e, acc[y].w * e));
-          if (d == 0 && a.lse) a.lse[to_row] = ll[y] == 0.0f ? -INFINITY : (ref + log2f(ll[y]) - bias) * kLn2;
+          if (d == 0 && a.lse) a.lse[to_row] = ll[y] == 0.0f ? -INFINITY : (mm[y] + log2f(ll[y]) - bias) * kLn2;
         }
       }
     }
@@ -976,10 +1104,9 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   }
 }
 
-template <int DP, bool F16, int CK, Pass PASS>
+template <int DP, bool F16, int CK, bool SHARED>
 cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
-  constexpr bool SHARED = PASS == kPrefixPass;
-  auto k = wide_kernel<DP, F16, CK, PASS>;
+  auto k = wide_kernel<DP, F16, CK, SHARED>;
   using L = WLay<DP, CK>;
   if (!a) {
     // the warpgroups' registers come out of what the block is launched with
@@ -993,6 +1120,8 @@ cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
   WSetup ws{};
   ws.tpt = 128 / c.rep;
   ws.row_tiles = (a->n + ws.tpt - 1) / ws.tpt;
+  ws.members = SHARED && ws.row_tiles == 1 ? ws.tpt / a->n : 1;
+  if (SHARED && ws.row_tiles == 1) ws.tpt = ws.members * a->n;
   ws.pairs = (c.G + 1) / 2;
   ws.box = std::min(c.page_size, kKeysW);
   ws.wide = (reinterpret_cast<uintptr_t>(a->out) & 31) == 0;
@@ -1031,10 +1160,9 @@ cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
 
 template <int DP, bool F16, int CK>
 cudaError_t by_pass(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
-  if (a) return a->prefix ? go<DP, F16, CK, kPrefixPass>(c, a, s) : a->own ? go<DP, F16, CK, kOwnPass>(c, a, s) : go<DP, F16, CK, kStepPass>(c, a, s);
-  cudaError_t e = go<DP, F16, CK, kStepPass>(c, a, s);
-  if (e == cudaSuccess) e = go<DP, F16, CK, kPrefixPass>(c, a, s);
-  return e != cudaSuccess ? e : go<DP, F16, CK, kOwnPass>(c, a, s);
+  if (a) return a->groups >= 0 ? go<DP, F16, CK, true>(c, a, s) : go<DP, F16, CK, false>(c, a, s);
+  const cudaError_t e = go<DP, F16, CK, true>(c, a, s);
+  return e != cudaSuccess ? e : go<DP, F16, CK, false>(c, a, s);
 }
 
 template <int CK>

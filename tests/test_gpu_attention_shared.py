@@ -167,9 +167,46 @@ def test_numbers_behind_the_ends_and_neighbours_do_not_reach_a_row():
     own = c.table[2, 7:9]
     c.v[ids(own, np.int64)] = float("inf")
     o2, z2 = call()
-    for b in (0, 3, 4, 5):
+    # the group without them keeps its bits; a neighbour in the group may be computed another way
+    for b in (3, 4, 5):
         assert torch.equal(o2[b], out[b]) and torch.equal(z2[b], lse[b])
+    check_attention((o2[:1], z2[:1]), [x[:1] for x in want])
     assert o2[1].isnan().all() and not torch.isfinite(o2[2]).any()
+
+
+@pytest.mark.parametrize("kind, n", [("bf16", 1), ("f16", 5), ("e4m3", 1), ("i8", 1), ("i8", 6), ("bf16", 40)])
+def test_rows_beside_an_infinity_or_nan(kind, n):
+    # among one sequence's own values: the others of its group, which share products with it, are as before;
+    # in the prefix: all of the group's are not numbers
+    import torch
+    if n > 32:
+        n, H = 32, 20  # a sequence's rows fill several tiles
+    else:
+        H = 8
+    typ = "f16" if kind == "f16" else "bf16"
+    own = [n + 3, n + 40, n + 1, n + 200]
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(H, 2, 64, typ, kind, 16, "token", n, [4], [150], own, seed=13)
+    want = reference()
+    page, slot = int(c.table[1, 155 // 16]), 155 % 16  # a key of sequence 1's own that all its tokens see
+    if kind == "i8":
+        parts(c.v, 2, 64, 16, "token")[1][page, 1, slot] = float("nan")
+    elif kind == "e4m3":
+        c.v.view(torch.uint8)[page, slot, 1, 5] = 0x7f
+    else:
+        c.v[page, slot, 1, 5] = float("inf")
+    out, lse = call()
+    others = [0, 2, 3]
+    check_attention((out[others], lse[others]), [x[others] for x in want])
+    assert not torch.isfinite(out[1, :, H // 2:]).all(-1).any() and torch.isfinite(out[1, :, :H // 2]).all()
+    page, slot = int(c.table[0, 3]), 2
+    if kind == "i8":
+        parts(c.k, 2, 64, 16, "token")[1][page, 0, slot] = float("nan")
+    elif kind == "e4m3":
+        c.k.view(torch.uint8)[page, slot, 0, 0] = 0x7f
+    else:
+        c.k[page, slot, 0, 0] = float("nan")
+    out, lse = call()
+    assert out[:, :, :H // 2].isnan().all() and lse[:, :, :H // 2].isnan().all()
 
 
 def test_peaked_weights_of_prefix_or_own():
