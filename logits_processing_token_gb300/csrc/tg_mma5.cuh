@@ -115,9 +115,21 @@ __device__ __forceinline__ void registers_down() { asm volatile("setmaxnreg.dec.
 template <bool F16>
 constexpr float kMostSum = F16 ? 255.0f * 256.0f : 255.0f;
 
-// The row's sums times a factor.
+// The row's sums times a factor, 32 columns at a time: a read of tensor memory takes
+// hundreds of cycles, however much it reads.
 __device__ __forceinline__ void scale_sums(unsigned to, int D, float f) {
-  for (int x = 0; x < D; x += 16) {
+  int x = 0;
+#pragma unroll 1
+  for (; x + 32 <= D; x += 32) {
+    unsigned o[32];
+    tm_ld32(o, to + x);
+    tm_wait_ld();
+    tm_pin(o);
+#pragma unroll
+    for (int y = 0; y < 32; ++y) o[y] = __float_as_uint(__uint_as_float(o[y]) * f);
+    tm_st32(to + x, o);
+  }
+  if (x < D) {
     unsigned o[16];
     tm_ld16(o, to + x);
     tm_wait_ld();
@@ -135,17 +147,16 @@ __device__ __forceinline__ void scale_sums(unsigned to, int D, float f) {
 // stores.  A row that is no token's of this sequence (it holds a neighbour's
 // query) comes with m = +infinity: its weights are 0, and it has no vote on
 // whether the warp's rows search their maximum, whose reference, and so whose
-// rounding, would else depend on the neighbour; nor has a row that sees no key of
-// the tile (sees).
+// rounding, would else depend on the neighbour.
 template <bool F16>
 __device__ __forceinline__ void softmax_tile(unsigned (&v)[4][32], unsigned ts, unsigned to, int D, float sc, bool has_sums,
-                                             float& m, float& l, bool sees = true) {
+                                             float& m, float& l) {
   constexpr float bias = kWeightBias<F16>;
   // The weights are taken against the row's reference as it stands; no
   // maximum is searched while their sum stays below 2^8, so none of them
   // can be too large.  (The first tile, and a tile that exceeds it, take
   // the maximum as the reference first.)
-  bool search = __any_sync(~0u, sees && m == -INFINITY);
+  bool search = __any_sync(~0u, m == -INFINITY);
   float tile_sum;
   for (;;) {
     if (search) {

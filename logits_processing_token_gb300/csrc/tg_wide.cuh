@@ -71,13 +71,13 @@ struct WBars {
 // items and copies; an 8-bit cache: 12 to 15 widen, 10 and 11 prepare an i8
 // cache's scales, one key head each (by a widening warp, which its tiles wait for:
 // 32 sequences of 17 tokens 118 us, not %WIDEN%).
-// Registers of the softmax's two warpgroups, the third and the fourth: their
-// threads times these are what the block is launched with (8-bit: 128 each).
+// Registers of the softmax's two warpgroups and the third (8-bit: what the block is
+// launched with).
 template <int DP, int CK>
 struct WLay {
   static constexpr bool Q8 = CK != kC16;
   static constexpr int kThreads = Q8 ? 512 : 384;
-  static constexpr int kRegSoftmax = Q8 ? 152 : 208, kRegThird = Q8 ? 104 : 88, kRegFourth = 104;
+  static constexpr int kRegSoftmax = Q8 ? 128 : 208, kRegThird = Q8 ? 128 : 88;
   static constexpr int kWideners = 4, kScalers = CK == kI8 ? 2 : 0;
   static constexpr int kTileB = DP / 64 * kBlock;
   static constexpr int kSlots = Q8 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
@@ -114,8 +114,8 @@ __device__ __forceinline__ void widen16(const uint4& r, unsigned (&w)[8]) {
   }
 }
 
-// With an i8 cache's scales the f16 weights are multiplied by up to 4 (the values'
-// relative to about the largest): a bias of 6, so that none passes f16's end.
+// With an i8 cache's scales the f16 weights, up to 2^7, are multiplied by up to 4 (the
+// values' relative to about the largest): a bias of 6, so that none passes f16's end.
 template <bool F16, bool I8>
 constexpr float kBias = I8 ? 6.0f : kWeightBias<F16>;
 
@@ -128,100 +128,106 @@ __device__ __forceinline__ void no_weights(unsigned ts) {
   tm_st32(ts + 32, z);
 }
 
-// softmax_tile over an 8-bit cache, from scores that stay in tensor memory, a few
-// columns at a time: the widening warps take registers that the whole row would
-// need (with them, spilled to a level 1 that shared memory has left no room, a
-// tile took 3,500 cycles).  f16 weights.  I8: scale, of each key, what its score is
-// multiplied by (else sc) and, behind those 128, what its weight is once it is summed;
-// shrink: what the sums so far are multiplied by first, the same for every row.
-// masked: rest keys from the tile's first are seen, except those in `bad`.
-template <bool I8>
-__device__ __forceinline__ void softmax_tile8(unsigned ts, unsigned to, int D, float sc, const float* scale, float shrink, bool masked,
-                                              int rest, const unsigned* bad, bool has_sums, float& m, float& l, bool sees) {
-  constexpr float bias = kBias<true, I8>, most = I8 ? 255.0f * 64.0f : kMostSum<true>;
+// softmax_tile in a loop over 32 scores at a time, for 8-bit caches and shared calls:
+// little code, because several roles' code runs next to it and a shared call's own
+// tiles are one warp's alone (unrolled, 120 KB in all, a tile of theirs took 8 to 17
+// thousand cycles, most of them waits for instructions), and few registers, which the
+// widening warps have.  A row's reference is raised when a score is more than 2^7 above
+// it (or it has none), and what came before it, in the tile too, is scaled down.
+//
+// keys: of the tile, 128 at most; behind them the product reads up to the next 16, which
+// are masked.  rest: those from the tile's first that the row sees, except those in bad;
+// masked: some row of the warp does not see 128.  I8: ks, of each key, what its score is
+// multiplied by, else sc; part, what its weight is once it is summed; shrink: what the
+// sums so far are multiplied by first, the same for every row.
+template <bool F16, bool I8>
+__device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, float sc, const float* ks, const float* part, float shrink,
+                                             int keys, bool masked, int rest, const unsigned* bad, bool has_sums, float& m, float& l) {
+  constexpr float bias = kBias<F16, I8>;
   if (I8 && has_sums && shrink != 1.0f) {
     scale_sums(to, D, shrink);
     tm_wait_st();
   }
-  const auto hidden = [&](int x) {  // of 32 keys
-    return bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
-  };
-  unsigned p[2][32];
-  bool search = __any_sync(~0u, sees && m == -INFINITY);
-  float tile_sum;
-  for (;;) {
-    if (search) {
-      float top = -INFINITY;
+  unsigned next[32];
+  tm_ld32(next, ts);
 #pragma unroll 1
-      for (int x = 0; x < 8; ++x) {
-        unsigned v[16];
-        tm_ld16(v, ts + x * 16);
-        tm_wait_ld();
-        tm_pin(v);
-        const unsigned off = masked ? hidden(x >> 1) >> (16 * (x & 1)) : 0u;
+  for (int x = 0; 32 * x < max(1, keys); ++x) {
+    unsigned v[32];
+    tm_wait_ld();
+    tm_pin(next);
 #pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const float e = __uint_as_float(v[y]) * (I8 ? scale[x * 16 + y] : sc);
-          if (!((off >> y) & 1)) top = fmaxf(top, e);
-        }
+    for (int y = 0; y < 32; ++y) v[y] = next[y];
+    if (32 * x + 32 < keys) tm_ld32(next, ts + (x + 1) * 32);
+    if constexpr (I8) {  // (before the mask: a scale may be 0, or no number)
+#pragma unroll
+      for (int y = 0; y < 32; y += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(ks + x * 32 + y);
+        const float2 p = unpair(mul2(pair(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), pair(k.x, k.y)));
+        const float2 q = unpair(mul2(pair(__uint_as_float(v[y + 2]), __uint_as_float(v[y + 3])), pair(k.z, k.w)));
+        v[y] = __float_as_uint(p.x);
+        v[y + 1] = __float_as_uint(p.y);
+        v[y + 2] = __float_as_uint(q.x);
+        v[y + 3] = __float_as_uint(q.y);
       }
-      const bool raise = top > m;
+    }
+    if (masked) {
+      const unsigned off = bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
+#pragma unroll
+      for (int y = 0; y < 32; ++y)
+        if (off & (1u << y)) v[y] = 0xff800000u;  // -infinity
+    }
+    float top = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+#pragma unroll
+    for (int y = 2; y < 32; y += 2) top = max3(top, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
+    top *= sc;
+    const bool raise = top > m + 7.0f || (m == -INFINITY && top > m);
+    if (__any_sync(~0u, raise)) {
+      // (a row's first key: its sums are 0 whatever they are scaled by)
+      const bool some = __any_sync(~0u, raise && l != 0.0f);
       const float f = raise ? ex2(m - top) : 1.0f;
       if (raise) m = top;
       l *= f;
-      if (has_sums && __any_sync(~0u, raise)) scale_sums(to, D, f);
+      if (some && has_sums) scale_sums(to, D, f);
+#pragma unroll 1
+      for (int z = 0; some && z < x; ++z) {  // the tile's weights so far
+        unsigned w[16];
+        tm_ld16(w, ts + z * 16);
+        tm_wait_ld();
+        tm_pin(w);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const float2 e = unpack2<F16>(w[y]);
+          w[y] = pack2<F16>(e.x * f, e.y * f);
+        }
+        tm_st16(ts + z * 16, w);
+      }
+      if (some) tm_wait_st();
     }
     const float off = m == -INFINITY ? 0.0f : bias - m;
     const unsigned long long sc2 = pair(sc, sc), off2 = pair(off, off);
-    unsigned long long sum[2] = {0ull, 0ull};
-    // 16 columns at a time, the next ones on their way
-    const auto weights = [&](auto mask) {
-      unsigned v[2][16];
-      tm_ld16(v[0], ts);
+    unsigned long long sum = 0ull;
+    unsigned p[16];
 #pragma unroll
-      for (int x = 0; x < 8; ++x) {
-        unsigned (&w)[16] = v[x & 1];
-        tm_wait_ld();
-        tm_pin(w);
-        if (x < 7) tm_ld16(v[(x + 1) & 1], ts + (x + 1) * 16);
-        const unsigned hid = decltype(mask)::value ? hidden(x >> 1) >> (16 * (x & 1)) : 0u;
+    for (int y = 0; y < 32; y += 4) {
+      float4 w;
+      if constexpr (I8) w = *reinterpret_cast<const float4*>(part + x * 32 + y);
 #pragma unroll
-        for (int y = 0; y < 16; y += 4) {
-          float4 k, f;
-          if constexpr (I8) {
-            k = *reinterpret_cast<const float4*>(scale + x * 16 + y);
-            f = *reinterpret_cast<const float4*>(scale + kKeysW + x * 16 + y);
-          }
-#pragma unroll
-          for (int z = 0; z < 4; z += 2) {
-            const unsigned long long ks = I8 ? (z ? pair(k.z, k.w) : pair(k.x, k.y)) : sc2;
-            float2 e = unpair(fma2(pair(__uint_as_float(w[y + z]), __uint_as_float(w[y + z + 1])), ks, off2));
-            if (decltype(mask)::value) {
-              if ((hid >> (y + z)) & 1) e.x = -INFINITY;
-              if ((hid >> (y + z + 1)) & 1) e.y = -INFINITY;
-            }
-            float p0 = ex2(e.x), p1 = ex2(e.y);
-            sum[(z >> 1) & 1] = add2(sum[(z >> 1) & 1], pair(p0, p1));
-            if constexpr (I8) {
-              const float2 q = unpair(mul2(pair(p0, p1), z ? pair(f.z, f.w) : pair(f.x, f.y)));
-              p0 = q.x;
-              p1 = q.y;
-            }
-            p[x >> 2][(x & 3) * 8 + ((y + z) >> 1)] = pack2<true>(p0, p1);
-          }
+      for (int z = 0; z < 4; z += 2) {
+        const float2 e = unpair(fma2(pair(__uint_as_float(v[y + z]), __uint_as_float(v[y + z + 1])), sc2, off2));
+        float p0 = ex2(e.x), p1 = ex2(e.y);
+        sum = add2(sum, pair(p0, p1));
+        if constexpr (I8) {
+          const float2 q = unpair(mul2(pair(p0, p1), z ? pair(w.z, w.w) : pair(w.x, w.y)));
+          p0 = q.x;
+          p1 = q.y;
         }
+        p[(y + z) >> 1] = pack2<F16>(p0, p1);
       }
-    };
-    if (masked) weights(std::true_type());
-    else weights(std::false_type());
-    const float2 l2 = unpair(add2(sum[0], sum[1]));
-    tile_sum = l2.x + l2.y;
-    if (search || !__any_sync(~0u, tile_sum > most)) break;  // (a NaN stays one with any reference)
-    search = true;
+    }
+    const float2 l2 = unpair(sum);
+    l += l2.x + l2.y;
+    tm_st16(ts + x * 16, p);  // (scores of 16 x .. 16 x + 15 and before are in registers, or done with)
   }
-  tm_st32(ts, p[0]);
-  tm_st32(ts + 32, p[1]);
-  l += tile_sum;
 }
 
 // F16: the tensors' type is f16, else bf16.
@@ -404,7 +410,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
 
   if (warp == 9) {
     // ---- items, pages and copies --------------------------------------------
-    registers_down<L::kRegThird>();
+    if constexpr (!Q8) registers_down<L::kRegThird>();
     const int shift = 31 - __clz(ws.box), per = kKeysW >> shift;  // copies of a tile
     int b = s->first_b, rt, pr, len;
     long long base;  // units before the item
@@ -523,6 +529,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         if (lane < 4) {
           unsigned bits = 0;
           if (badm)
+#pragma unroll 1
             for (int k = 0; k < 32; ++k)
               if ((badm >> ((lane * 32 + k) >> shift)) & 1) bits |= 1u << k;
           s->bad[meta][lane] = bits;
@@ -544,6 +551,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           bar_arrive_copied(&s->scales_full[mt]);
           if (lane == 0) bar_arrive(&s->scales_full[mt]);
         }
+#pragma unroll 1
         for (int w = 0; w < 2 && ok; ++w) {
           if (w == 1 && j == it.t0) {
             // the item's queries: its first keys are under way, the item before may still use the place
@@ -558,6 +566,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
                   tma4(sptr(smem) + t * L::kTileB + x * kBlock, &mq, x * 64, 0, 2 * pr + t, it.tok0, &s->q_full);
             }
           }
+#pragma unroll 1
           for (int t = 0; t < it.nch; ++t) {
             const int st = Q8 ? raw_of(pos) : slot_of(pos);
             unsigned long long* const full = Q8 ? &s->raw_full[st] : &s->kv_full[st];
@@ -613,7 +622,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     if (I8) cp_wait_all();
   } else if (warp == 8) {
     // ---- matrix instructions ----------------------------------------------
-    registers_down<L::kRegThird>();
+    if constexpr (!Q8) registers_down<L::kRegThird>();
     const unsigned fmt = F16 ? 0u : 1u, fmt_pv = PF16 ? 0u : 1u;
     const unsigned id0 = (1u << 4) | (fmt << 7) | (fmt << 10) | (8u << 24);
     const unsigned id_pv = (1u << 4) | (fmt_pv << 7) | (fmt_pv << 10) | (8u << 24) | (1u << 16) | (static_cast<unsigned>(c.D >> 3) << 17);
@@ -707,7 +716,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     __syncwarp();
   } else if (Q8 && warp >= 12) {
     // ---- 8-bit tiles to 16 bits --------------------------------------------
-    registers_down<L::kRegFourth>();
     constexpr int CPR = DP / 16, UN = kKeysW * CPR / (32 * L::kWideners);  // vectors of a key's row; of a tile, per thread
     const int wt = tid - 384;
     unsigned pos = 0;
@@ -735,30 +743,31 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         unsigned char* const dst = smem + L::kKv + st * L::kTileB;
         const unsigned* bad = s->bad[meta];
         const bool all = KEYS || (end == kKeysW && !(bad[0] | bad[1] | bad[2] | bad[3]));
-        uint4 x[UN];
-#pragma unroll
-        for (int k = 0; k < UN; ++k) x[k] = src[wt + k * (32 * L::kWideners)];
         // vector i of a row: chunks 2 i and 2 i + 1, in an order in which eight lanes meet different banks
         const int r0 = wt / CPR, i = wt % CPR, ch = (2 * i) & 7, sw = (i >> 2) & 1;
         unsigned char* const to = dst + (i >> 2) * kBlock + r0 * 128;
         const unsigned a0 = ((ch + sw) ^ (r0 & 7)) << 4, a1 = ((ch + 1 - sw) ^ (r0 & 7)) << 4;  // (rows a multiple of 8 apart)
         constexpr int RS = 32 * L::kWideners / CPR;  // rows between a thread's vectors
         static_assert(RS % 8 == 0, "");
+#pragma unroll 1
+        for (int k0 = 0; k0 < UN; k0 += 4) {  // (in a loop: less code)
+          if (r0 + k0 * RS >= stop) break;
+          uint4 x[4];
 #pragma unroll
-        for (int k = 0; k < UN; ++k) {
-          if (r0 + k * RS >= stop) break;
-          unsigned y[8];
-          widen16<CK, KEYS ? F16 : true>(x[k], y);
-          if (!all) {
-            const int r = r0 + k * RS;
-            if (r >= end || ((bad[r >> 5] >> (r & 31)) & 1)) {
+          for (int k = 0; k < 4; ++k) x[k] = src[wt + (k0 + k) * (32 * L::kWideners)];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int r = r0 + (k0 + k) * RS;
+            unsigned y[8];
+            widen16<CK, KEYS ? F16 : true>(x[k], y);
+            if (!all && (r >= end || ((bad[r >> 5] >> (r & 31)) & 1))) {
 #pragma unroll
               for (int z = 0; z < 8; ++z) y[z] = 0u;  // (0 x NaN is not 0)
             }
+            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
+            *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a0) = sw ? hi : lo;
+            *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a1) = sw ? lo : hi;
           }
-          const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-          *reinterpret_cast<uint4*>(to + k * RS * 128 + a0) = sw ? hi : lo;
-          *reinterpret_cast<uint4*>(to + k * RS * 128 + a1) = sw ? lo : hi;
         }
         fence_async();
         __syncwarp();
@@ -769,7 +778,9 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         ++pos;
       };
       for (int j = t0; j < t1 && ok; ++j) {
+#pragma unroll 1
         for (int t = 0; t < nch && ok; ++t) piece(std::true_type(), j);
+#pragma unroll 1
         for (int t = 0; t < nch && ok; ++t) piece(std::false_type(), j);
         meta = (meta + 1) % kMetas;
       }
@@ -778,7 +789,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     __syncwarp();
   } else if (I8 && (warp == 10 || warp == 11)) {
     // ---- scales of an i8 cache ----------------------------------------------
-    registers_down<L::kRegThird>();
+    if constexpr (!Q8) registers_down<L::kRegThird>();
     const int t = warp - 10;
     unsigned tiles = 0;
     int it_n = 0, meta = 0;
@@ -834,7 +845,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: one thread per row --------------------------------------
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegSoftmax));
+    if constexpr (!Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegSoftmax));
     const int t = warp >> 2, row = tid & 127;
     const unsigned lanes = static_cast<unsigned>(warp & 3) << 21;  // this warp's lanes of tensor memory
     const unsigned ts = tmem + lanes + t * 128, to = tmem + lanes + 256 + t * 128;
@@ -890,30 +901,30 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         const unsigned any_bad = bad[0] | bad[1] | bad[2] | bad[3];
         // the first keys of the tile are seen; by none of a row of no token, by its own choice
         int rest = lim - j * kKeysW;
+        int keys = min(kKeysW, it.len - j * kKeysW);
         bool masked = (j + 1) * kKeysW > lim_w || any_bad, sees = true;
         if constexpr (SHARED) {
           const int4 tl = s->tile[meta];
           rest = !real ? kKeysW : tl.y < 0 ? (prefix > 0 ? tl.x : 0) : tl.y == mem ? lim - tl.z : 0;
+          keys = tl.x;
           sees = real && rest > 0;
           masked = __any_sync(~0u, rest < kKeysW) || any_bad;
         }
-        if constexpr (Q8) {
-          float shrink = 1.0f;
-          if constexpr (I8) {
-            ok = bar_wait(&s->dead, &s->scales_ready[meta % L::kScaleTiles][t], (tiles / L::kScaleTiles) & 1, c);
-            if (!ok) break;
-            ++tiles;
-            const float2 f = s->fac[meta][t];
-            shrink = f.x;
-            vmax = f.y;
-          }
-          if (SHARED && !__any_sync(~0u, sees)) {
-            if (I8 && j > it.t0 && shrink != 1.0f) scale_sums(to, c.D, shrink);
-            no_weights(ts);
-          } else softmax_tile8<I8>(ts, to, c.D, sc, reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4)),
-                            shrink, masked, rest, bad, j > it.t0, m, l, sees);
-        } else if (SHARED && !__any_sync(~0u, sees)) {
+        float shrink = 1.0f;
+        if constexpr (I8) {
+          ok = bar_wait(&s->dead, &s->scales_ready[meta % L::kScaleTiles][t], (tiles / L::kScaleTiles) & 1, c);
+          if (!ok) break;
+          ++tiles;
+          const float2 f = s->fac[meta][t];
+          shrink = f.x;
+          vmax = f.y;
+        }
+        if (SHARED && !__any_sync(~0u, sees)) {
+          if (I8 && j > it.t0 && shrink != 1.0f) scale_sums(to, c.D, shrink);
           no_weights(ts);
+        } else if constexpr (SHARED || Q8) {
+          const float* const scales = reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4));
+          softmax_loop<PF16, I8>(ts, to, c.D, I8 ? 1.0f : sc, scales, scales + kKeysW, shrink, keys, masked, rest, bad, j > it.t0, m, l);
         } else {
           unsigned v[4][32];
 #pragma unroll
@@ -930,7 +941,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
                 if (off & (1u << y)) v[x][y] = 0xff800000u;  // -infinity
             }
           }
-          softmax_tile<F16>(v, ts, to, c.D, sc, j > it.t0, m, l, sees);
+          softmax_tile<F16>(v, ts, to, c.D, sc, j > it.t0, m, l);
         }
         meta = (meta + 1) % kMetas;
         tm_wait_st();
@@ -1085,7 +1096,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
     }
   } else {
-    registers_down<L::kRegThird>();
+    if constexpr (!Q8) registers_down<L::kRegThird>();
   }
   fence_before();
   __syncthreads();
@@ -1113,7 +1124,7 @@ cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
     cudaFuncAttributes at{};
     const cudaError_t e = cudaFuncGetAttributes(&at, k);
     if (e != cudaSuccess) return e;
-    if ((at.numRegs + 7) / 8 * 8 * L::kThreads < 256 * L::kRegSoftmax + 128 * L::kRegThird + (L::Q8 ? 128 * L::kRegFourth : 0))
+    if (!L::Q8 && (at.numRegs + 7) / 8 * 8 * L::kThreads < 256 * L::kRegSoftmax + 128 * L::kRegThird)
       return cudaErrorInvalidConfiguration;
     return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, L::kSmem);
   }
