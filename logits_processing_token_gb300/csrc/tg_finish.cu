@@ -31,7 +31,7 @@ __device__ __forceinline__ float4 four(const char* p, long long at, float f) {
 }
 
 template <int CK, bool F16>
-__global__ void __launch_bounds__(32 * kFinishWarps) finish_kernel(const AttnCfg c, const StepArgs a) {
+__global__ void __launch_bounds__(32 * kFinishWarps, 5) finish_kernel(const AttnCfg c, const StepArgs a) {
   dep_wait();
   const int lane = threadIdx.x & 31, d = 4 * lane;
   const long long row = static_cast<long long>(blockIdx.x) * kFinishWarps + (threadIdx.x >> 5);
@@ -44,7 +44,7 @@ __global__ void __launch_bounds__(32 * kFinishWarps) finish_kernel(const AttnCfg
   float4 acc = make_float4(0, 0, 0, 0);
   float ref = -INFINITY, l = 0.0f;
   if (at.y > 1) {
-    constexpr int PB = 8;  // parts whose reads are under way
+    constexpr int PB = 4;  // parts whose reads are under way
     for (int p0 = 0; p0 < at.y; p0 += PB) {
       float2 x[PB];
       float4 v[PB];

@@ -27,9 +27,9 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   return by_cache(nullptr, c, &a, s);
 }
 
-// What a row tile's copies need in memory while the work is laid out: an int per
-// sequence, two per group.
-constexpr long long kMostShared = 36000;
+// What fits into the copies' memory while the work is laid out there: two ints per
+// sequence and per group.
+constexpr long long kMostShared = 18000;
 
 // tg_attend_shared: one launch over the groups' prefixes and each sequence's own keys
 // (tg_wide.cuh), one that joins what its CTAs split (tg_finish.cu).  Where nothing can be
@@ -38,7 +38,7 @@ cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   StepArgs b = a;
   b.groups = -1;
   const long long tiles = (static_cast<long long>(a.c.max_pages) << c.page_shift) / 128 + 5;
-  if (a.groups == 0 || a.c.batch < 2 || !wide_can(c) || a.c.batch + 2ll * a.groups >= kMostShared ||
+  if (a.groups == 0 || a.c.batch < 2 || !wide_can(c) || static_cast<long long>(a.c.batch) + a.groups >= kMostShared ||
       tiles * a.c.batch * ((a.n * c.rep + 127) / 128 + 1) > 0x7fffffffll)
     return launch_step(c, b, s);
   const cudaError_t e = launch_wide(c, a, s);

@@ -285,6 +285,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   int* const gat = reinterpret_cast<int*>(smem + L::kKv);  // [groups + 1]: offsets
   int* const gkeys = gat + a.groups + 1;                   // [groups]: keys of the prefix
   unsigned* const at = reinterpret_cast<unsigned*>(gkeys + a.groups);
+  int* const slen = reinterpret_cast<int*>(at + a.c.batch);  // [batch]: lengths
   // the group of sequence b, looked for from group i on: its first sequence, the one behind it, its keys
   const auto group_of = [&](int b, int& i, int& g0, int& g1, int& keys) {
     while (i < ng && gat[i + 1] <= b) ++i;
@@ -295,6 +296,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   int gi = 0, g0 = 0, g1 = 0, gk = 0;
   if constexpr (SHARED) {
     bool fine = true;
+    const int raw0 = b_first < b_end ? a.c.lens[b_first] : 0;
     for (int i = tid; i <= a.groups; i += NT) {
       const long long o = a.goff[i];
       fine = fine && o >= 0 && o <= a.c.batch && (i > 0 || o == 0);
@@ -322,8 +324,9 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
     }
     for (int b = b_first; b < b_end; ++b) {
-      const int raw = a.c.lens[b], l = checked(raw);
+      const int raw = b == b_first ? raw0 : a.c.lens[b], l = checked(raw);
       if (blockIdx.x == 0 && l != raw) atomicOr(c.status, kAttnBadRow);
+      slen[b] = l;
       group_of(b, gi, g0, g1, gk);
       const int pre = gk > 0 ? tiles_of(gk) : 0, own = tiles_of(l - begin_of(l, gk));
       at[b] = static_cast<unsigned>(mine);
@@ -417,13 +420,28 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     // a shared call's: the group, and of member lane + 32 i of the item its length and its last own tile's number + 1
     int grp = 0, gs = 0, ge = 0, mlen[4] = {0, 0, 0, 0}, mend[4] = {0, 0, 0, 0};
     int nt;
+    // What comes next is asked for an item ahead: lengths from a sequence on; the end and the keys of the next group.
+    int nlen[4] = {0, 0, 0, 0}, next_end = 0, next_keys = 0;
+    const auto fetch_lens = [&](int from) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = lane + 32 * i;
+        nlen[i] = m < ws.members && from + m < a.c.batch ? a.c.lens[from + m] : 0;
+      }
+    };
+    const auto fetch_group = [&]() {
+      if (grp + 1 < ng) {
+        next_end = static_cast<int>(a.goff[grp + 2]);
+        next_keys = a.plens[grp + 1];
+      }
+    };
     const auto members = [&]() {  // of the item that begins with sequence b: fills these in, gives its tiles
       const int nm = min(ws.members, ge - b), pre = len > 0 ? tiles_of(len) : 0;
       int sum = pre;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         const bool is = lane + 32 * i < nm;
-        mlen[i] = is ? checked(a.c.lens[b + lane + 32 * i]) : 0;
+        mlen[i] = is ? checked(nlen[i]) : 0;
         int own = is ? tiles_of(mlen[i] - begin_of(mlen[i], len)) : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -440,10 +458,30 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       gs = grp < ng ? static_cast<int>(a.goff[grp]) : b;
       ge = grp < ng ? static_cast<int>(a.goff[grp + 1]) : b + 1;
       len = grp < ng && ge - gs > 1 ? a.plens[grp] & ~(ws.box - 1) : 0;
+      fetch_group();
+    };
+    const auto next_group = [&]() {
+      if (grp + 1 >= ng || next_end <= ge) return enter_group();  // (none, or an empty one)
+      ++grp;
+      gs = ge;
+      ge = next_end;
+      len = ge - gs > 1 ? next_keys & ~(ws.box - 1) : 0;
+      fetch_group();
     };
     if constexpr (SHARED) {
+      // (from where the work was laid out: no copy is under way yet)
       grp = s->first_len;
-      enter_group();
+      gs = grp < ng ? gat[grp] : b;
+      ge = grp < ng ? gat[grp + 1] : b + 1;
+      len = grp < ng ? gkeys[grp] : 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int m = lane + 32 * i;
+        nlen[i] = m < ws.members && b + m < a.c.batch ? slen[b + m] : 0;
+      }
+      fence_async();
+      __syncwarp();
+      fetch_group();
       nt = members();
       pr = static_cast<int>(u0 / total);
       const int skip = static_cast<int>(s->first_in / (nt + kItemCostW));
@@ -487,6 +525,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       ++it_n;
       if (!more) break;
+      if (SHARED && rt + 1 == ws.row_tiles) {
+        const int after = min(b + ws.members, ge);
+        fetch_lens(after == a.c.batch ? 0 : after);
+      }
       // A tile's keys, whose they are, its first one's place, and the row of the page table.
       struct Tile {
         int keys, mem, key0, row;
@@ -599,10 +641,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           b = min(b + ws.members, ge);
           if (b == a.c.batch) {
             ++pr;
-            b = grp = ge = 0;
+            b = grp = ge = next_end = 0;  // (next_group: from the first one on)
           }
           if (pr < ws.pairs) {
-            if (b == ge) enter_group();
+            if (b == ge) next_group();
             nt = members();
           }
         } else if (++pr == ws.pairs) {
@@ -743,18 +785,21 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         unsigned char* const dst = smem + L::kKv + st * L::kTileB;
         const unsigned* bad = s->bad[meta];
         const bool all = KEYS || (end == kKeysW && !(bad[0] | bad[1] | bad[2] | bad[3]));
-        // vector i of a row: chunks 2 i and 2 i + 1, in an order in which eight lanes meet different banks
-        const int r0 = wt / CPR, i = wt % CPR, ch = (2 * i) & 7, sw = (i >> 2) & 1;
+        // Vector i of a row, chunks 2 i and 2 i + 1 of the widened one.  Those of the
+        // second 64 elements are taken from the row beside, so that eight lanes' chunks
+        // are in different banks.
+        const int i = wt % CPR, r0 = (wt / CPR) ^ (i >> 2), ch = (2 * i) & 7;
         unsigned char* const to = dst + (i >> 2) * kBlock + r0 * 128;
-        const unsigned a0 = ((ch + sw) ^ (r0 & 7)) << 4, a1 = ((ch + 1 - sw) ^ (r0 & 7)) << 4;  // (rows a multiple of 8 apart)
+        const unsigned a0 = (ch ^ (r0 & 7)) << 4, a1 = ((ch + 1) ^ (r0 & 7)) << 4;  // (rows a multiple of 8 apart)
         constexpr int RS = 32 * L::kWideners / CPR;  // rows between a thread's vectors
-        static_assert(RS % 8 == 0, "");
+        static_assert(RS % 8 == 0 && UN % 4 == 0, "");
+        const uint4* const from = src + r0 * CPR + i;
 #pragma unroll 1
         for (int k0 = 0; k0 < UN; k0 += 4) {  // (in a loop: less code)
-          if (r0 + k0 * RS >= stop) break;
+          if (wt / CPR + k0 * RS >= stop) break;  // (stop: a multiple of 16)
           uint4 x[4];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) x[k] = src[wt + (k0 + k) * (32 * L::kWideners)];
+          for (int k = 0; k < 4; ++k) x[k] = from[(k0 + k) * (32 * L::kWideners)];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
             const int r = r0 + (k0 + k) * RS;
@@ -764,9 +809,8 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
 #pragma unroll
               for (int z = 0; z < 8; ++z) y[z] = 0u;  // (0 x NaN is not 0)
             }
-            const uint4 lo = make_uint4(y[0], y[1], y[2], y[3]), hi = make_uint4(y[4], y[5], y[6], y[7]);
-            *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a0) = sw ? hi : lo;
-            *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a1) = sw ? lo : hi;
+            *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a0) = make_uint4(y[0], y[1], y[2], y[3]);
+            *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a1) = make_uint4(y[4], y[5], y[6], y[7]);
           }
         }
         fence_async();
