@@ -128,7 +128,7 @@ __device__ __forceinline__ void no_weights(unsigned ts) {
   tm_st32(ts + 32, z);
 }
 
-// softmax_tile in a loop over 32 scores at a time, for 8-bit caches and shared calls:
+// softmax_tile in a loop over 64 scores at a time, for 8-bit caches and shared calls:
 // little code, because several roles' code runs next to it and a shared call's own
 // tiles are one warp's alone (unrolled, 120 KB in all, a tile of theirs took 8 to 17
 // thousand cycles, most of them waits for instructions), and few registers, which the
@@ -148,38 +148,46 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
     scale_sums(to, D, shrink);
     tm_wait_st();
   }
-  unsigned next[32];
-  tm_ld32(next, ts);
 #pragma unroll 1
-  for (int x = 0; 32 * x < max(1, keys); ++x) {
-    unsigned v[32];
+  for (int x = 0; 64 * x < max(1, keys); ++x) {
+    unsigned v[2][32];
+    tm_ld32(v[0], ts + x * 64);
+    tm_ld32(v[1], ts + x * 64 + 32);
     tm_wait_ld();
-    tm_pin(next);
-#pragma unroll
-    for (int y = 0; y < 32; ++y) v[y] = next[y];
-    if (32 * x + 32 < keys) tm_ld32(next, ts + (x + 1) * 32);
+    tm_pin(v[0]);
+    tm_pin(v[1]);
     if constexpr (I8) {  // (before the mask: a scale may be 0, or no number)
 #pragma unroll
-      for (int y = 0; y < 32; y += 4) {
-        const float4 k = *reinterpret_cast<const float4*>(ks + x * 32 + y);
-        const float2 p = unpair(mul2(pair(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), pair(k.x, k.y)));
-        const float2 q = unpair(mul2(pair(__uint_as_float(v[y + 2]), __uint_as_float(v[y + 3])), pair(k.z, k.w)));
-        v[y] = __float_as_uint(p.x);
-        v[y + 1] = __float_as_uint(p.y);
-        v[y + 2] = __float_as_uint(q.x);
-        v[y + 3] = __float_as_uint(q.y);
+      for (int y = 0; y < 64; y += 4) {
+        unsigned* const w = &v[y >> 5][y & 31];
+        const float4 k = *reinterpret_cast<const float4*>(ks + x * 64 + y);
+        const float2 p = unpair(mul2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), pair(k.x, k.y)));
+        const float2 q = unpair(mul2(pair(__uint_as_float(w[2]), __uint_as_float(w[3])), pair(k.z, k.w)));
+        w[0] = __float_as_uint(p.x);
+        w[1] = __float_as_uint(p.y);
+        w[2] = __float_as_uint(q.x);
+        w[3] = __float_as_uint(q.y);
       }
     }
     if (masked) {
-      const unsigned off = bad[x] | (rest - 32 * x >= 32 ? 0u : rest <= 32 * x ? ~0u : ~0u << (rest - 32 * x));
 #pragma unroll
-      for (int y = 0; y < 32; ++y)
-        if (off & (1u << y)) v[y] = 0xff800000u;  // -infinity
+      for (int h = 0; h < 2; ++h) {
+        const int r = rest - 64 * x - 32 * h;
+        const unsigned off = bad[2 * x + h] | (r >= 32 ? 0u : r <= 0 ? ~0u : ~0u << r);
+#pragma unroll
+        for (int y = 0; y < 32; ++y)
+          if (off & (1u << y)) v[h][y] = 0xff800000u;  // -infinity
+      }
     }
-    float top = fmaxf(__uint_as_float(v[0]), __uint_as_float(v[1]));
+    float tops[4];
 #pragma unroll
-    for (int y = 2; y < 32; y += 2) top = max3(top, __uint_as_float(v[y]), __uint_as_float(v[y + 1]));
-    top *= sc;
+    for (int z = 0; z < 4; ++z) {
+      const unsigned* const w = &v[z >> 1][16 * (z & 1)];
+      tops[z] = fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+#pragma unroll
+      for (int y = 2; y < 16; y += 2) tops[z] = max3(tops[z], __uint_as_float(w[y]), __uint_as_float(w[y + 1]));
+    }
+    const float top = max3(tops[0], tops[1], fmaxf(tops[2], tops[3])) * sc;
     const bool raise = top > m + 7.0f || (m == -INFINITY && top > m);
     if (__any_sync(~0u, raise)) {
       // (a row's first key: its sums are 0 whatever they are scaled by)
@@ -189,7 +197,7 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
       l *= f;
       if (some && has_sums) scale_sums(to, D, f);
 #pragma unroll 1
-      for (int z = 0; some && z < x; ++z) {  // the tile's weights so far
+      for (int z = 0; some && z < 2 * x; ++z) {  // the tile's weights so far
         unsigned w[16];
         tm_ld16(w, ts + z * 16);
         tm_wait_ld();
@@ -205,28 +213,31 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
     }
     const float off = m == -INFINITY ? 0.0f : bias - m;
     const unsigned long long sc2 = pair(sc, sc), off2 = pair(off, off);
-    unsigned long long sum = 0ull;
-    unsigned p[16];
+    unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};
 #pragma unroll
-    for (int y = 0; y < 32; y += 4) {
-      float4 w;
-      if constexpr (I8) w = *reinterpret_cast<const float4*>(part + x * 32 + y);
+    for (int h = 0; h < 2; ++h) {
+      unsigned p[16];
 #pragma unroll
-      for (int z = 0; z < 4; z += 2) {
-        const float2 e = unpair(fma2(pair(__uint_as_float(v[y + z]), __uint_as_float(v[y + z + 1])), sc2, off2));
-        float p0 = ex2(e.x), p1 = ex2(e.y);
-        sum = add2(sum, pair(p0, p1));
-        if constexpr (I8) {
-          const float2 q = unpair(mul2(pair(p0, p1), z ? pair(w.z, w.w) : pair(w.x, w.y)));
-          p0 = q.x;
-          p1 = q.y;
+      for (int y = 0; y < 32; y += 4) {
+        float4 w;
+        if constexpr (I8) w = *reinterpret_cast<const float4*>(part + x * 64 + h * 32 + y);
+#pragma unroll
+        for (int z = 0; z < 4; z += 2) {
+          const float2 e = unpair(fma2(pair(__uint_as_float(v[h][y + z]), __uint_as_float(v[h][y + z + 1])), sc2, off2));
+          float p0 = ex2(e.x), p1 = ex2(e.y);
+          sum[((y >> 1) & 2) + (z >> 1)] = add2(sum[((y >> 1) & 2) + (z >> 1)], pair(p0, p1));
+          if constexpr (I8) {
+            const float2 q = unpair(mul2(pair(p0, p1), z ? pair(w.z, w.w) : pair(w.x, w.y)));
+            p0 = q.x;
+            p1 = q.y;
+          }
+          p[(y + z) >> 1] = pack2<F16>(p0, p1);
         }
-        p[(y + z) >> 1] = pack2<F16>(p0, p1);
       }
+      tm_st16(ts + x * 32 + h * 16, p);  // (the scores there are in registers, or done with)
     }
-    const float2 l2 = unpair(sum);
+    const float2 l2 = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
     l += l2.x + l2.y;
-    tm_st16(ts + x * 16, p);  // (scores of 16 x .. 16 x + 15 and before are in registers, or done with)
   }
 }
 
