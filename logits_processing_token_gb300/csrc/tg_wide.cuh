@@ -94,6 +94,9 @@ struct WLay {
   static_assert(kSmem <= 227 * 1024, "");
 };
 
+// Sequences of a row tile of a shared call: 32 to a register of the copying warp.
+constexpr int kMemberRegs = 2;
+
 struct WSetup {
   int tpt;        // tokens of a row tile
   int row_tiles;  // of a sequence
@@ -128,7 +131,7 @@ __device__ __forceinline__ void no_weights(unsigned ts) {
   tm_st32(ts + 32, z);
 }
 
-// softmax_tile in a loop over 64 scores at a time, for 8-bit caches and shared calls:
+// softmax_tile in a loop over 32 scores at a time, for 8-bit caches and shared calls:
 // little code, because several roles' code runs next to it and a shared call's own
 // tiles are one warp's alone (unrolled, 120 KB in all, a tile of theirs took 8 to 17
 // thousand cycles, most of them waits for instructions), and few registers, which the
@@ -149,43 +152,36 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
     tm_wait_st();
   }
 #pragma unroll 1
-  for (int x = 0; 64 * x < max(1, keys); ++x) {
-    unsigned v[2][32];
-    tm_ld32(v[0], ts + x * 64);
-    tm_ld32(v[1], ts + x * 64 + 32);
+  for (int x = 0; 32 * x < max(1, keys); ++x) {
+    unsigned v[32];
+    tm_ld32(v, ts + x * 32);
     tm_wait_ld();
-    tm_pin(v[0]);
-    tm_pin(v[1]);
+    tm_pin(v);
     if constexpr (I8) {  // (before the mask: a scale may be 0, or no number)
 #pragma unroll
-      for (int y = 0; y < 64; y += 4) {
-        unsigned* const w = &v[y >> 5][y & 31];
-        const float4 k = *reinterpret_cast<const float4*>(ks + x * 64 + y);
-        const float2 p = unpair(mul2(pair(__uint_as_float(w[0]), __uint_as_float(w[1])), pair(k.x, k.y)));
-        const float2 q = unpair(mul2(pair(__uint_as_float(w[2]), __uint_as_float(w[3])), pair(k.z, k.w)));
-        w[0] = __float_as_uint(p.x);
-        w[1] = __float_as_uint(p.y);
-        w[2] = __float_as_uint(q.x);
-        w[3] = __float_as_uint(q.y);
+      for (int y = 0; y < 32; y += 4) {
+        const float4 k = *reinterpret_cast<const float4*>(ks + x * 32 + y);
+        const float2 p = unpair(mul2(pair(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), pair(k.x, k.y)));
+        const float2 q = unpair(mul2(pair(__uint_as_float(v[y + 2]), __uint_as_float(v[y + 3])), pair(k.z, k.w)));
+        v[y] = __float_as_uint(p.x);
+        v[y + 1] = __float_as_uint(p.y);
+        v[y + 2] = __float_as_uint(q.x);
+        v[y + 3] = __float_as_uint(q.y);
       }
     }
     if (masked) {
+      const int r = rest - 32 * x;
+      const unsigned off = bad[x] | (r >= 32 ? 0u : r <= 0 ? ~0u : ~0u << r);
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int r = rest - 64 * x - 32 * h;
-        const unsigned off = bad[2 * x + h] | (r >= 32 ? 0u : r <= 0 ? ~0u : ~0u << r);
-#pragma unroll
-        for (int y = 0; y < 32; ++y)
-          if (off & (1u << y)) v[h][y] = 0xff800000u;  // -infinity
-      }
+      for (int y = 0; y < 32; ++y)
+        if (off & (1u << y)) v[y] = 0xff800000u;  // -infinity
     }
     float tops[4];
 #pragma unroll
     for (int z = 0; z < 4; ++z) {
-      const unsigned* const w = &v[z >> 1][16 * (z & 1)];
-      tops[z] = fmaxf(__uint_as_float(w[0]), __uint_as_float(w[1]));
+      tops[z] = fmaxf(__uint_as_float(v[8 * z]), __uint_as_float(v[8 * z + 1]));
 #pragma unroll
-      for (int y = 2; y < 16; y += 2) tops[z] = max3(tops[z], __uint_as_float(w[y]), __uint_as_float(w[y + 1]));
+      for (int y = 2; y < 8; y += 2) tops[z] = max3(tops[z], __uint_as_float(v[8 * z + y]), __uint_as_float(v[8 * z + y + 1]));
     }
     const float top = max3(tops[0], tops[1], fmaxf(tops[2], tops[3])) * sc;
     const bool raise = top > m + 7.0f || (m == -INFINITY && top > m);
@@ -197,7 +193,7 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
       l *= f;
       if (some && has_sums) scale_sums(to, D, f);
 #pragma unroll 1
-      for (int z = 0; some && z < 2 * x; ++z) {  // the tile's weights so far
+      for (int z = 0; some && z < x; ++z) {  // the tile's weights so far
         unsigned w[16];
         tm_ld16(w, ts + z * 16);
         tm_wait_ld();
@@ -214,28 +210,25 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
     const float off = m == -INFINITY ? 0.0f : bias - m;
     const unsigned long long sc2 = pair(sc, sc), off2 = pair(off, off);
     unsigned long long sum[4] = {0ull, 0ull, 0ull, 0ull};
+    unsigned p[16];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      unsigned p[16];
+    for (int y = 0; y < 32; y += 4) {
+      float4 w;
+      if constexpr (I8) w = *reinterpret_cast<const float4*>(part + x * 32 + y);
 #pragma unroll
-      for (int y = 0; y < 32; y += 4) {
-        float4 w;
-        if constexpr (I8) w = *reinterpret_cast<const float4*>(part + x * 64 + h * 32 + y);
-#pragma unroll
-        for (int z = 0; z < 4; z += 2) {
-          const float2 e = unpair(fma2(pair(__uint_as_float(v[h][y + z]), __uint_as_float(v[h][y + z + 1])), sc2, off2));
-          float p0 = ex2(e.x), p1 = ex2(e.y);
-          sum[((y >> 1) & 2) + (z >> 1)] = add2(sum[((y >> 1) & 2) + (z >> 1)], pair(p0, p1));
-          if constexpr (I8) {
-            const float2 q = unpair(mul2(pair(p0, p1), z ? pair(w.z, w.w) : pair(w.x, w.y)));
-            p0 = q.x;
-            p1 = q.y;
-          }
-          p[(y + z) >> 1] = pack2<F16>(p0, p1);
+      for (int z = 0; z < 4; z += 2) {
+        const float2 e = unpair(fma2(pair(__uint_as_float(v[y + z]), __uint_as_float(v[y + z + 1])), sc2, off2));
+        float p0 = ex2(e.x), p1 = ex2(e.y);
+        sum[((y >> 1) & 2) + (z >> 1)] = add2(sum[((y >> 1) & 2) + (z >> 1)], pair(p0, p1));
+        if constexpr (I8) {
+          const float2 q = unpair(mul2(pair(p0, p1), z ? pair(w.z, w.w) : pair(w.x, w.y)));
+          p0 = q.x;
+          p1 = q.y;
         }
+        p[(y + z) >> 1] = pack2<F16>(p0, p1);
       }
-      tm_st16(ts + x * 32 + h * 16, p);  // (the scores there are in registers, or done with)
     }
+    tm_st16(ts + x * 16, p);  // (the scores there are in registers, or done with)
     const float2 l2 = unpair(add2(add2(sum[0], sum[1]), add2(sum[2], sum[3])));
     l += l2.x + l2.y;
   }
@@ -429,13 +422,13 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     int b = s->first_b, rt, pr, len;
     long long base;  // units before the item
     // a shared call's: the group, and of member lane + 32 i of the item its length and its last own tile's number + 1
-    int grp = 0, gs = 0, ge = 0, mlen[4] = {0, 0, 0, 0}, mend[4] = {0, 0, 0, 0};
+    int grp = 0, gs = 0, ge = 0, mlen[kMemberRegs] = {}, mend[kMemberRegs] = {};
     int nt;
     // What comes next is asked for an item ahead: lengths from a sequence on; the end and the keys of the next group.
-    int nlen[4] = {0, 0, 0, 0}, next_end = 0, next_keys = 0;
+    int nlen[kMemberRegs] = {}, next_end = 0, next_keys = 0;
     const auto fetch_lens = [&](int from) {
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kMemberRegs; ++i) {
         const int m = lane + 32 * i;
         nlen[i] = m < ws.members && from + m < a.c.batch ? a.c.lens[from + m] : 0;
       }
@@ -450,7 +443,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const int nm = min(ws.members, ge - b), pre = len > 0 ? tiles_of(len) : 0;
       int sum = pre;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kMemberRegs; ++i) {
         const bool is = lane + 32 * i < nm;
         mlen[i] = is ? checked(nlen[i]) : 0;
         int own = is ? tiles_of(mlen[i] - begin_of(mlen[i], len)) : 0;
@@ -486,7 +479,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       ge = grp < ng ? gat[grp + 1] : b + 1;
       len = grp < ng ? gkeys[grp] : 0;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
+      for (int i = 0; i < kMemberRegs; ++i) {
         const int m = lane + 32 * i;
         nlen[i] = m < ws.members && b + m < a.c.batch ? slen[b + m] : 0;
       }
@@ -550,11 +543,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         if (j < pre) return Tile{len - j * kKeysW, -1, j * kKeysW, gs};
         int mem = 0;  // members whose tiles end before this one
 #pragma unroll
-        for (int i = 0; i < 4; ++i) mem += __popc(__ballot_sync(~0u, lane + 32 * i < ws.members && mend[i] <= j));
-        const int i = mem >> 5;
-        const int l = __shfl_sync(~0u, i == 0 ? mlen[0] : i == 1 ? mlen[1] : i == 2 ? mlen[2] : mlen[3], mem & 31);
-        const int m1 = mem - 1, k = m1 >> 5;
-        const int e = __shfl_sync(~0u, k == 0 ? mend[0] : k == 1 ? mend[1] : k == 2 ? mend[2] : mend[3], m1 & 31);
+        for (int i = 0; i < kMemberRegs; ++i) mem += __popc(__ballot_sync(~0u, lane + 32 * i < ws.members && mend[i] <= j));
+        static_assert(kMemberRegs == 2, "");
+        const int l = __shfl_sync(~0u, mem < 32 ? mlen[0] : mlen[1], mem & 31);
+        const int e = __shfl_sync(~0u, mem <= 32 ? mend[0] : mend[1], (mem - 1) & 31);
         const int key0 = begin_of(l, len) + (j - (mem > 0 ? e : pre)) * kKeysW;
         return Tile{l - key0, mem, key0, b + mem};
       };
@@ -1186,7 +1178,7 @@ cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
   WSetup ws{};
   ws.tpt = 128 / c.rep;
   ws.row_tiles = (a->n + ws.tpt - 1) / ws.tpt;
-  ws.members = SHARED && ws.row_tiles == 1 ? ws.tpt / a->n : 1;
+  ws.members = SHARED && ws.row_tiles == 1 ? std::min(ws.tpt / a->n, 32 * kMemberRegs) : 1;
   if (SHARED && ws.row_tiles == 1) ws.tpt = ws.members * a->n;
   ws.pairs = (c.G + 1) / 2;
   ws.box = std::min(c.page_size, kKeysW);
