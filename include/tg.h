@@ -608,10 +608,13 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
  * batch * n is at most max_shared_tokens.  Other arguments, outputs and numerics
  * as tg_attend_step, whose results these are up to the order of the sums.  A
  * sequence that is shorter than the prefix and its n tokens, or empty, takes no part
- * in the sharing; nor does any over pages of fewer than 8 tokens.  Offsets out of
- * order or a prefix_lens[i] outside [0, max_pages * page_size] raise
- * TG_FLAG_BAD_ROW, and nothing is shared in that call.  Calls that share a tg_attn
- * share its workspace: in stream order.
+ * in the sharing.  A call is a step, and reads neither group_offsets nor prefix_lens,
+ * where sharing would not pay (few rows, and a page table with room for few keys),
+ * over pages of fewer than 8 tokens, with more than 128 query heads to a key head,
+ * and for batch + groups of 18,000 and more; else offsets out of order or a
+ * prefix_lens[i] outside [0, max_pages * page_size] raise TG_FLAG_BAD_ROW, and
+ * nothing is shared in that call.  Calls that share a tg_attn share its workspace:
+ * in stream order.
  */
 tg_status tg_attend_shared(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const int64_t* group_offsets,
                            const int32_t* prefix_lens, int32_t groups, const tg_attn* cfg, void* out, float* out_lse,

@@ -31,14 +31,29 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
 // sequence and per group.
 constexpr long long kMostShared = 18000;
 
+// Up to 16 rows the step kernel reads every sequence's keys faster than the shared
+// launch the common ones once, where there are few of them: 8 heads of 128, groups x
+// sequences x keys, step and shared, us: bf16 1 x 4 x 4,000 (66 MB of keys) 15.8 and
+// 19.1, 4 x 4 x 2,000 (133) 24.4 and 21.7, 64 x 4 x 2,000 (2,130) 323 and 116; e4m3 4 x 4 x
+// 4,000 (132) 27.0 and 24.3, 1 x 32 x 1,000 (68) 18.4 and 20.4; i8 16 x 4 x 1,000 (136) 34.4 and
+// 36.1, 16 x 4 x 2,000 (267) 53.4 and 48.9.  Widening tiles of i8 keys for few rows costs
+// what two sequences' sharing saves: 64 x 2 x 2,000 105 and 115, 64 x 3 x 2,000 147 and
+// 126.  What the host knows is the longest that the sequences can be.
+static bool shared_pays(const AttnCfg& c, const StepArgs& a) {
+  if (a.n * c.rep > 16) return true;  // (4 x 4 x 1,000 keys, 5 tokens: bf16 26.6 and 18.6, i8 29.1 and 21.8)
+  const double key = 2.0 * c.G * (c.D * (c.ctype == c.dtype ? 2.0 : 1.0) + (c.ctype == TG_DTYPE_I8 ? 4.0 : 0.0));
+  const double keys = static_cast<double>(a.c.batch) * a.c.max_pages * c.page_size;
+  return keys * key >= 110e6 && (c.ctype != TG_DTYPE_I8 || a.c.batch >= 3ll * a.groups);
+}
+
 // tg_attend_shared: one launch over the groups' prefixes and each sequence's own keys
 // (tg_wide.cuh), one that joins what its CTAs split (tg_finish.cu).  Where nothing can be
-// shared, or the launch's shape does not fit, it is a step.
+// shared, it does not pay, or the launch's shape does not fit, it is a step.
 cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   StepArgs b = a;
   b.groups = -1;
   const long long tiles = (static_cast<long long>(a.c.max_pages) << c.page_shift) / 128 + 5;
-  if (a.groups == 0 || a.c.batch < 2 || !wide_can(c) || static_cast<long long>(a.c.batch) + a.groups >= kMostShared ||
+  if (a.groups == 0 || a.c.batch < 2 || !wide_can(c) || !shared_pays(c, a) || static_cast<long long>(a.c.batch) + a.groups >= kMostShared ||
       tiles * a.c.batch * ((a.n * c.rep + 127) / 128 + 1) > 0x7fffffffll)
     return launch_step(c, b, s);
   const cudaError_t e = launch_wide(c, a, s);

@@ -35,7 +35,18 @@ CASES = [
 ]
 
 
-def setup(H, G, D, typ, kind, page, layout, n, members, prefix, own, seed=0, copies=False, lens=None, spare=0, **more):
+def room(c, heads, dim):
+    """The page table with so many columns that the longest sequences it could name make sharing worth a launch."""
+    import torch
+    t = c.device_table()
+    key = 2 * heads * dim  # bytes of an 8-bit key and value
+    most = max(t.shape[1], -(-(120 << 20) // (key * c.page * t.shape[0])))
+    wide = torch.full((t.shape[0], most), -1, dtype=torch.int32, device="cuda")
+    wide[:, :t.shape[1]] = t
+    return wide
+
+
+def setup(H, G, D, typ, kind, page, layout, n, members, prefix, own, seed=0, copies=False, lens=None, spare=0, small=False, **more):
     import torch
     import logits_processing_token_gb300 as tg
     own = np.asarray(own)
@@ -49,6 +60,7 @@ def setup(H, G, D, typ, kind, page, layout, n, members, prefix, own, seed=0, cop
     t = torch_types()[typ]
     q = torch.from_numpy(rng.normal(0, 2, (len(lens), n, H, D)).astype(np.float32)).cuda().to(t)
     off, pl = ids(np.concatenate([[0], np.cumsum(members)]), np.int64), ids(prefix, np.int32)
+    c.table_now = lambda: c.device_table() if small else room(c, G, D)  # (small: too little to share)
 
     def reference(lens=None):
         if kind == "i8":
@@ -59,7 +71,7 @@ def setup(H, G, D, typ, kind, page, layout, n, members, prefix, own, seed=0, cop
         out = torch.full((len(lens), n, H, D), float("nan"), device="cuda", dtype=t) if out is None else out
         lse = torch.full((len(lens), n, H), float("nan"), device="cuda") if lse is None else lse
         kl = lens if isinstance(lens, torch.Tensor) else ids(lens, np.int32)
-        tg.tg_attend_shared(q, kl, c.device_table() if table is None else table, c.k, c.v, off, pl, cfg, out, lse, stream=stream)
+        tg.tg_attend_shared(q, kl, c.table_now() if table is None else table, c.k, c.v, off, pl, cfg, out, lse, stream=stream)
         return out, lse
 
     return tg, cfg, c, q, off, pl, lens, reference, call
@@ -75,6 +87,13 @@ def test_shared_matches_oracle(case):
     assert tg.tg_attn_status_word(cfg) == 0
     o2, z2 = call()  # equal bits
     assert torch.equal(o2, out) and torch.equal(z2, lse)
+
+
+@pytest.mark.parametrize("case", CASES[::3], ids=lambda c: "-".join(map(str, c[:8])))
+def test_calls_too_small_to_share(case):
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(*case, small=True)
+    check_attention(call(), reference())
+    assert tg.tg_attn_status_word(cfg) == 0
 
 
 @pytest.mark.parametrize("kind", ["bf16", "i8"])
@@ -108,7 +127,7 @@ def test_long_prefixes_and_many_groups(kind):
     import torch
     for args in ((4, 1, 128, "bf16", kind, 64, "token", 1, [3], [20_000], [3, 300, 1]),
                  (4, 2, 64, "bf16", kind, 16, "head", 1, [150], [700], [1 + i % 9 for i in range(150)]),
-                 (2, 1, 64, "bf16", kind, 16, "token", 1, [2] * 600, [17 + i % 40 for i in range(600)], [1 + i % 5 for i in range(1200)])):
+                 (2, 1, 64, "bf16", kind, 16, "token", 1, [3] * 600, [17 + i % 40 for i in range(600)], [1 + i % 5 for i in range(1800)])):
         tg, cfg, c, q, off, pl, lens, reference, call = setup(*args, seed=5)
         out, lse = call()
         check_attention((out, lse), reference())
@@ -118,18 +137,18 @@ def test_long_prefixes_and_many_groups(kind):
 @pytest.mark.parametrize("kind", ["bf16", "e4m3", "i8"])
 def test_offsets_out_of_order_share_nothing(kind):
     import torch
-    tg, cfg, c, q, off, pl, lens, reference, call = setup(4, 2, 64, "bf16", kind, 16, "token", 1, [3, 2], [70, 40], [1, 9, 30, 2, 2], seed=6)
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(4, 2, 64, "bf16", kind, 16, "token", 1, [3, 3], [70, 40], [1, 9, 30, 2, 2, 7], seed=6)
     want = reference()
     call()
-    for o, p in (([0, 4, 3], [70, 40]), ([0, 3, 6], [70, 40]), ([1, 3, 5], [70, 40]), ([-1, 3, 5], [70, 40]), ([0, 3, 5], [-1, 40]),
-                 ([0, 3, 5], [70, 10 ** 6]), ([0, 3, 2 ** 40], [70, 40])):
+    for o, p in (([0, 4, 3], [70, 40]), ([0, 3, 7], [70, 40]), ([1, 3, 6], [70, 40]), ([-1, 3, 6], [70, 40]), ([0, 3, 6], [-1, 40]),
+                 ([0, 3, 6], [70, 2 ** 30]), ([0, 3, 2 ** 40], [70, 40]), ([0, 3, 2 ** 32], [70, 40])):
         out, lse = call(off=ids(o, np.int64), pl=ids(p, np.int32))
         torch.cuda.synchronize()
         check_attention((out, lse), want)
         assert tg.tg_attn_status_word(cfg) == tg.TG_FLAG_BAD_ROW
         tg.tg_attn_clear_status(cfg)
     bad = lens.copy()
-    bad[4] = 10 ** 6  # a length past the table: an empty sequence, as in a step
+    bad[4] = 2 ** 30  # a length past the table: an empty sequence, as in a step
     out, lse = call(lens=bad)
     torch.cuda.synchronize()
     assert tg.tg_attn_status_word(cfg) == tg.TG_FLAG_BAD_ROW
@@ -143,7 +162,7 @@ def test_bad_pages_of_a_prefix(kind, n):
     import torch
     tg, cfg, c, q, off, pl, lens, reference, call = setup(4, 1, 64, "bf16", kind, 16, "token", n, [4, 2], [300, 90],
                                                           [n, n + 9, n + 30, n + 2, n, n + 8], seed=7)
-    table = c.device_table()
+    table = c.table_now()
     table[:4, 1] = 10 ** 6   # keys 16 .. 31 of the first group
     table[4:, 0] = -3        # keys 0 .. 15 of the second
     out, lse = call(table=table)
@@ -225,8 +244,8 @@ def test_peaked_weights_of_prefix_or_own():
 @pytest.mark.parametrize("kind, n", [("bf16", 1), ("i8", 1), ("bf16", 7)])
 def test_stream_and_graph_follow_the_lengths(kind, n):
     import torch
-    tg, cfg, c, q, off, pl, lens, reference, call = setup(8, 2, 128, "bf16", kind, 16, "head", n, [3, 2, 1], [300, 64, 9],
-                                                          [n, n + 50, n + 3, n + 1, n + 20, n + 30], seed=10)
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(8, 2, 128, "bf16", kind, 16, "head", n, [4, 4, 1], [300, 64, 9],
+                                                          [n, n + 50, n + 3, n, n + 1, n + 20, n + 9, n, n + 30], seed=10)
     want = reference()
     out, lse = call()
     side = torch.cuda.Stream()
@@ -234,11 +253,11 @@ def test_stream_and_graph_follow_the_lengths(kind, n):
     o2, z2 = call(stream=side)
     side.synchronize()
     assert torch.equal(o2, out) and torch.equal(z2, lse)
-    kl, table = ids(lens, np.int32), c.device_table()
+    kl, table = ids(lens, np.int32), c.table_now()
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         call(o2, z2, table=table, lens=kl)
-    for now, p in ((lens, [300, 64, 9]), ([300, 340, 20, 64, 70, 39], [299, 30, 0]), (lens, [0, 0, 0]), (lens, [300, 64, 9])):
+    for now, p in ((lens, [300, 64, 9]), ([300, 340, 20, 301, 64, 70, 70, 10, 39], [299, 30, 0]), (lens, [0, 0, 0]), (lens, [300, 64, 9])):
         now = np.minimum(now, lens)
         kl.copy_(ids(now, np.int32))
         pl.copy_(ids(p, np.int32))
@@ -255,7 +274,7 @@ def test_after_waits_ran_out(kind, n):
     from tests.test_gpu_attention_timeout import run_out
     tg, cfg, c, q, off, pl, lens, reference, call = setup(12, 3, 128, "bf16", kind, 16, "token", n, [5, 3], [2000, 300],
                                                           [n + 3 * i for i in range(8)], seed=11)
-    out, table, kl = torch.empty_like(q), c.device_table(), ids(lens, np.int32)
+    out, table, kl = torch.empty_like(q), c.table_now(), ids(lens, np.int32)
     lse = torch.empty(q.shape[:3], device="cuda")
     run_out(cfg, lambda: call(out, lse, table=table, lens=kl), out)
 
