@@ -125,6 +125,9 @@ cudaError_t step_e4m3(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaSt
 cudaError_t step_i8(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, 16-bit cache
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
+// What fits into the copies' memory while a shared call's work is laid out there: two
+// ints per sequence and per group.
+constexpr int kMostShared = 18000;
 constexpr int kPartRows = 128;  // of a part of a shared call
 // CTAs of the step kernel per SM at most (they size the handle's workspace).
 constexpr int kStepCtasPerSm = 4;

@@ -27,10 +27,6 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   return by_cache(nullptr, c, &a, s);
 }
 
-// What fits into the copies' memory while the work is laid out there: two ints per
-// sequence and per group.
-constexpr long long kMostShared = 18000;
-
 // Up to 16 rows the step kernel reads every sequence's keys faster than the shared
 // launch the common ones once, where there are few of them: 8 heads of 128, groups x
 // sequences x keys, step and shared, us: bf16 1 x 4 x 4,000 (66 MB of keys) 15.8 and

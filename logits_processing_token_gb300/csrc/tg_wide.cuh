@@ -12,12 +12,15 @@
 // copies bound the stream, 50 us of 74 (floor 42), and the look-ups at the
 // beginning (5) and the joins at the end (10) do the rest.
 //
-// An 8-bit cache is copied as it is into stages of its own, and six warps widen
+// An 8-bit cache is copied as it is into stages of its own, and four warps widen
 // each tile, exactly, into one that the matrix instructions read: keys to the
 // queries' type, values to f16, as the weights are.  The scales of an i8 cache enter
 // in the softmax: a score times its key's, a weight times its value's relative to
-// about the largest so far (a power of f16's range apart would be lost), by which
-// the sums are multiplied at the end.
+// about the largest so far, by which the sums are multiplied at the end (so a weight
+// stays in f16's range whatever the scales are).  32 sequences of 17 tokens take 77 us
+// (floor 23): chains of widening (1,200 cycles a tile and matrix), products and softmax,
+// and the joins.  On the warp-wide instructions, which widen each key once per 16
+// rows, they took 211.
 //
 // A shared call's item is a pair of key heads and as many whole sequences of one
 // group as a row tile holds: its tiles are the group's prefix, then each of those
@@ -25,7 +28,9 @@
 // once for all of them, and no second pass joins it with the rest.  (Own keys on the
 // step kernel, after a pass over the prefixes, took 46 to 63 us where they are 67 MB:
 // items of a tile or two, each with its beginning, its end and a join.)  The idle
-// rows' products are free while the copies bound it.  The parts of split items are
+// rows' products are free while the copies bound it: 64 prompts of up to 4,000 keys
+// with 4 beams each, bf16, 137 us (floor 103; every sequence's keys read, 323 us at
+// 2,000 keys a prompt).  The parts of split items are
 // joined by a kernel of their own (tg_finish.cu), spread over the GPU.
 // An infinity or a NaN among one sequence's values reaches the other rows of its tile
 // (0 x NaN): rows that come out so are computed again there, each alone.
@@ -57,9 +62,9 @@ struct WItem {
 constexpr int kSlotsMaxW = 10, kMetas = 8;
 struct WBars {
   unsigned long long q_full, q_empty, kv_full[kSlotsMaxW], kv_empty[kSlotsMaxW], raw_full[kSlotsMaxW], raw_empty[kSlotsMaxW],
-      scales_full[8], scales_ready[8][2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
+      scales_full[kMetas][2], scales_ready[kMetas][2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
   unsigned tmem;
-  int dead, last[2], first_b, first_len;
+  int dead, last[2], first_b, first_len;  // (of a shared call, first_len: the group)
   long long first_in, wsum[16];
   WItem item[2];
   unsigned bad[kMetas][4];  // by tile, round the ring: keys on pages that do not exist
@@ -69,8 +74,8 @@ struct WBars {
 
 // Warps 0 to 7: softmax, one warpgroup per key head; 8: matrix instructions; 9:
 // items and copies; an 8-bit cache: 12 to 15 widen, 10 and 11 prepare an i8
-// cache's scales, one key head each (by a widening warp, which its tiles wait for:
-// 32 sequences of 17 tokens 118 us, not %WIDEN%).
+// cache's scales, one key head each (a widening warp that also did held its tiles up:
+// 32 sequences of 17 tokens 118 us, 102 so; eight widening warps gained nothing).
 // Registers of the softmax's two warpgroups and the third (8-bit: what the block is
 // launched with).
 template <int DP, int CK>
@@ -91,7 +96,7 @@ struct WLay {
   static constexpr int kScaleB = CK == kI8 ? kScaleTiles * 2 * 2 * kKeysW * 4 : 0;  // [tile][head][keys, values][128]
   static constexpr int kKv = 2 * kTileB, kRawAt = kKv + kSlots * kTileB, kScaleAt = kRawAt + kRaw * kRawB, kBars = kScaleAt + kScaleB;
   static constexpr int kSmem = kBars + static_cast<int>(sizeof(WBars)) + 1024;
-  static_assert(kSmem <= 227 * 1024, "");
+  static_assert(kSmem <= 227 * 1024 && kBars - kKv >= 4 * (2 * kMostShared + 2), "");
 };
 
 // Sequences of a row tile of a shared call: 32 to a register of the copying warp.
@@ -191,6 +196,7 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
       const float f = raise ? ex2(m - top) : 1.0f;
       if (raise) m = top;
       l *= f;
+      if (some) tm_wait_st();
       if (some && has_sums) scale_sums(to, D, f);
 #pragma unroll 1
       for (int z = 0; some && z < x; ++z) {  // the tile's weights so far
@@ -252,10 +258,11 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     bar_init(&s->q_full, 1);
     bar_init(&s->q_empty, 1);
     for (int i = 0; i < L::kSlots; ++i) { bar_init(&s->kv_full[i], Q8 ? L::kWideners : 1); bar_init(&s->kv_empty[i], 1); }
-    for (int i = 0; i < L::kScaleTiles; ++i) {
-      bar_init(&s->scales_full[i], 33);
-      for (int t = 0; t < 2; ++t) bar_init(&s->scales_ready[i][t], 1);
-    }
+    for (int i = 0; i < L::kScaleTiles; ++i)
+      for (int t = 0; t < 2; ++t) {
+        bar_init(&s->scales_full[i][t], 33);
+        bar_init(&s->scales_ready[i][t], 1);
+      }
     for (int i = 0; i < L::kRaw; ++i) { bar_init(&s->raw_full[i], 1); bar_init(&s->raw_empty[i], L::kWideners); }
     for (int t = 0; t < 2; ++t) {
       bar_init(&s->s_full[t], 1);
@@ -581,8 +588,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         }
         __syncwarp();
         if constexpr (I8) {
-          // the scales, the values' too: four keys a lane, both key heads' at once (a bulk copy
-          // of a page's takes 0.2 us, one after the other)
+          // the scales, the values' too: four keys a lane (a copy's keys are 8 at least, so of one page)
           const int page = __shfl_sync(~0u, id, (4 * lane) >> shift);
           const bool have = 4 * lane < tl.keys && page >= 0 && page < a.c.num_pages;
           const long long p0 = have ? page : 0;
@@ -592,9 +598,9 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             const unsigned to = sptr(smem + L::kScaleAt) + (mt * 2 + t) * (2 * kKeysW * 4) + lane * 16;
             cp16(to, static_cast<const char*>(a.c.k) + p0 * a.c.k_page_stride + at, have);
             cp16(to + kKeysW * 4, static_cast<const char*>(a.c.v) + p0 * a.c.v_page_stride + at, have);
+            bar_arrive_copied(&s->scales_full[mt][t]);
+            if (lane == 0) bar_arrive(&s->scales_full[mt][t]);
           }
-          bar_arrive_copied(&s->scales_full[mt]);
-          if (lane == 0) bar_arrive(&s->scales_full[mt]);
         }
 #pragma unroll 1
         for (int w = 0; w < 2 && ok; ++w) {
@@ -838,7 +844,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     // ---- scales of an i8 cache ----------------------------------------------
     if constexpr (!Q8) registers_down<L::kRegThird>();
     const int t = warp - 10;
-    unsigned tiles = 0;
+    unsigned phases = 0;  // of the scales' places, a bit each (items with one key head pass the second's by)
     int it_n = 0, meta = 0;
     bool ok = true;
     for (;;) {
@@ -850,12 +856,17 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       if (lane == 0) bar_arrive(&s->item_empty[is]);
       ++it_n;
       if (b < 0) break;
+      if (t >= nch) {
+        meta = (meta + t1 - t0) % kMetas;
+        continue;
+      }
       float vmax = 0.0f;
-      for (int j = t0; j < t1; ++j, ++tiles, meta = (meta + 1) % kMetas) {
+      for (int j = t0; j < t1; ++j, meta = (meta + 1) % kMetas) {
         const int mt = meta % L::kScaleTiles;
-        ok = bar_wait(&s->dead, &s->scales_full[mt], (tiles / L::kScaleTiles) & 1, c);
+        ok = bar_wait(&s->dead, &s->scales_full[mt][t], (phases >> mt) & 1, c);
         if (!ok) break;
-        if (t < nch) {
+        phases ^= 1u << mt;
+        {
           // Keys' scales times what makes scores powers of two; values' relative to about
           // the largest so far, and 0 for keys that do not exist, whose may be anything.
           // (Their weights are masked.)
@@ -899,7 +910,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     constexpr float bias = kBias<PF16, I8>;
     const int tok = row / c.rep, head = row - tok * c.rep;
     int it_n = 0, meta = 0;
-    unsigned s_ph = 0, o_ph = 0, meet_ph = 0, tiles = 0;
+    unsigned s_ph = 0, o_ph = 0, meet_ph = 0, phases = 0;  // (phases: of the scales' places, a bit each)
     bool ok = true;
     const auto meet = [&]() {  // the four warps of this tile past this point
       __syncwarp();
@@ -919,7 +930,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       if (it.b < 0) break;
       if (t >= it.nch) {
         meta = (meta + it.t1 - it.t0) % kMetas;
-        tiles += it.t1 - it.t0;
         continue;
       }
       const int g = 2 * it.pair + t;
@@ -959,9 +969,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         }
         float shrink = 1.0f;
         if constexpr (I8) {
-          ok = bar_wait(&s->dead, &s->scales_ready[meta % L::kScaleTiles][t], (tiles / L::kScaleTiles) & 1, c);
+          const int mt = meta % L::kScaleTiles;
+          ok = bar_wait(&s->dead, &s->scales_ready[mt][t], (phases >> mt) & 1, c);
           if (!ok) break;
-          ++tiles;
+          phases ^= 1u << mt;
           const float2 f = s->fac[meta][t];
           shrink = f.x;
           vmax = f.y;
