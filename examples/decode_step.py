@@ -1,5 +1,6 @@
 """One attention layer and a vocabulary projection, decoded with the library:
-prompts, single tokens, and an assisted-generation step.
+prompts (whole or in chunks), single tokens, an assisted-generation step, and
+a beam search whose beams share their prompt's pages.
 
     python examples/decode_step.py            # needs the GPU
 
@@ -8,9 +9,12 @@ Every position runs the same path as in a serving loop:
   prompts   tg_cache_append (rotate, write the cache) -> tg_attend_prompt -> logits -> tg_select
   a token   tg_cache_append -> tg_attend_step (n = 1) -> logits -> tg_select
   K guesses tg_cache_append -> tg_attend_step (n = K + 1) -> logits -> tg_verify
+  a chunk   tg_cache_append -> tg_cache_read (all so far) -> tg_attend_prompt -> logits
+  beams     tg_cache_append -> tg_attend_shared -> logits -> tg_beam_step
 
-The weights are random; main() checks that verifying the tokens which single
-steps produced accepts all of them.
+The cache is 16-bit, or i8 with scales that are computed as it is written.  The
+weights are random; main() checks that verifying the tokens which single steps
+produced accepts all of them.
 """
 import os
 import sys
@@ -24,9 +28,9 @@ HEADS, KV_HEADS, DIM, HIDDEN, VOCAB, PAGE = 8, 2, 64, 256, 1000, 16
 
 
 class Layer:
-    """Embedding, one attention layer, vocabulary projection; its paged cache."""
+    """Embedding, one attention layer, vocabulary projection; its paged cache (cache_dtype None: 16-bit, or "i8")."""
 
-    def __init__(self, batch, max_len, seed=0):
+    def __init__(self, batch, max_len, seed=0, cache_dtype=None, shared_tokens=0):
         g = torch.Generator("cuda").manual_seed(seed)
 
         def weight(*shape):
@@ -37,9 +41,10 @@ class Layer:
         self.w_out, self.w_vocab = weight(HEADS * DIM, HIDDEN), weight(HIDDEN, VOCAB)
         inv_freq = 10000.0 ** (-torch.arange(0, DIM, 2) / DIM)
         self.attn = tg.AttnConfig(num_heads=HEADS, num_kv_heads=KV_HEADS, head_dim=DIM, page_size=PAGE, rotary_dim=DIM,
-                                  inv_freq=inv_freq.tolist())
+                                  inv_freq=inv_freq.tolist(), cache_dtype=cache_dtype, max_shared_tokens=shared_tokens)
         pages = -(-max_len // PAGE)
-        self.k_pages = torch.zeros(batch * pages, PAGE, KV_HEADS, DIM, dtype=torch.bfloat16, device="cuda")
+        page = (self.attn.page_bytes,) if cache_dtype == "i8" else self.attn.page_shape
+        self.k_pages = torch.zeros(batch * pages, *page, dtype=self.attn.cache_dtype, device="cuda")
         self.v_pages = torch.zeros_like(self.k_pages)
         order = torch.randperm(batch * pages, generator=g, device="cuda")
         self.table = order.view(batch, pages).to(torch.int32)
@@ -68,6 +73,45 @@ class Layer:
         tg.tg_attend_prompt(q, k, v, offsets, None, self.attn, out)
         last = offsets[1:] - 1
         return self._logits(x[last], out[last])
+
+    def chunk(self, ids, counts):
+        """prompts() for the next counts tokens of every prompt, after what the cache holds of it."""
+        x, q, _, _, offsets = self._append(ids, counts)
+        held = torch.zeros(self.batch + 1, dtype=torch.int64, device="cuda")
+        held[1:] = self.lens.cumsum(0)
+        k, v = (torch.empty(int(held[-1]), KV_HEADS, DIM, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        tg.tg_cache_read(held, self.lens, self.table, self.k_pages, self.v_pages, self.attn, k, v)
+        out = torch.empty_like(q)
+        tg.tg_attend_prompt(q, k, v, offsets, held, self.attn, out)
+        last = offsets[1:] - 1
+        return self._logits(x[last], out[last])
+
+    def fork(self, prompt_len):
+        """Every sequence begins with sequence 0's first prompt_len tokens: on the same pages as far as those are
+        whole, and a copy of the page in which they end."""
+        whole = prompt_len // PAGE
+        self.table[1:, :whole] = self.table[0, :whole]
+        if prompt_len % PAGE:
+            for pages in (self.k_pages, self.v_pages):
+                pages[self.table[1:, whole].long()] = pages[int(self.table[0, whole])].clone()
+        self.lens.fill_(prompt_len)
+        self.groups = torch.tensor([0, self.batch], device="cuda")
+        self.prefix = torch.tensor([prompt_len], dtype=torch.int32, device="cuda")
+
+    def reorder(self, prompt_len, parents):
+        """Sequence b continues what sequence parents[b] holds: its pages behind the prompt's whole ones are copied."""
+        own = slice(prompt_len // PAGE, None)
+        for pages in (self.k_pages, self.v_pages):
+            pages[self.table[:, own].long()] = pages[self.table[parents, own].long()].clone()
+
+    def beam_step(self, ids):
+        """ids [batch]: logits [batch, VOCAB] after one new token of every beam of one prompt (after fork())."""
+        counts = torch.ones(self.batch, dtype=torch.int64, device="cuda")
+        x, q, _, _, _ = self._append(ids, counts)
+        q = q.view(self.batch, 1, HEADS, DIM)
+        out = torch.empty_like(q)
+        tg.tg_attend_shared(q, self.lens, self.table, self.k_pages, self.v_pages, self.groups, self.prefix, self.attn, out)
+        return self._logits(x, out.flatten(0, 1).flatten(1).view(self.batch, HEADS, DIM))
 
     def step(self, ids):
         """ids [batch, n]: logits [batch, n, VOCAB] after each of the n new tokens."""
@@ -123,7 +167,40 @@ def run(batch=3, new_tokens=6, seed=0):
     return decoded, matches
 
 
+def beam_search(prompt, beams=4, new_tokens=6, seed=0, cache_dtype=None):
+    """Beam search over one prompt (ids int32 [n], longer than 8 tokens), written in two chunks.
+    Returns (tokens [beams, new_tokens], scores [beams]), best first."""
+    n = prompt.numel()
+    layer = Layer(beams, n + new_tokens, seed, cache_dtype, shared_tokens=beams)
+    cfg = tg.Config(vocab=VOCAB, mode="greedy", max_batch=beams)
+    keep = tg.tg_beam_keep(cfg, beams)
+    counts = torch.zeros(beams, dtype=torch.int64, device="cuda")
+    for part in (prompt[:8], prompt[8:]):  # (the other sequences have no tokens yet)
+        counts[0] = part.numel()
+        logits = layer.chunk(part, counts)[:1].expand(beams, VOCAB).contiguous()
+    layer.fork(n)
+    scores = torch.full((beams,), -1e9, device="cuda")
+    scores[0] = 0.0  # at the first step all beams are the same: one of them counts
+    tokens = torch.zeros(beams, 0, dtype=torch.int32, device="cuda")
+    plens = torch.full((beams,), n, dtype=torch.int32, device="cuda")
+    for i in range(new_tokens):
+        history = torch.cat([prompt.expand(beams, n), tokens], 1)
+        offsets = torch.arange(beams + 1, device="cuda") * history.shape[1]
+        best = torch.empty(1, keep, device="cuda")
+        ids, parents = (torch.empty(1, keep, dtype=torch.int32, device="cuda") for _ in range(2))
+        tg.tg_beam_step(logits, scores, history.reshape(-1).contiguous(), offsets, plens, cfg, beams, best, ids, parents)
+        chosen, parents, scores = ids[0, :beams].contiguous(), parents[0, :beams].long(), best[0, :beams].contiguous()
+        tokens = torch.cat([tokens[parents], chosen[:, None]], 1)
+        if i + 1 < new_tokens:
+            layer.reorder(n, parents)
+            logits = layer.beam_step(chosen)
+    return tokens, scores
+
+
 def main():
+    prompt = torch.arange(40, dtype=torch.int32, device="cuda") * 7 % VOCAB
+    for kind in (None, "i8"):
+        print("beams", kind or "bf16", beam_search(prompt, cache_dtype=kind)[0][0].tolist())
     decoded, matches = run()
     print("decoded", decoded.tolist())
     print("guesses accepted", matches.tolist(), "of", decoded.shape[1] - 1)

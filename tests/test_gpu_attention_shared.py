@@ -291,3 +291,62 @@ def test_refusals():
     for kw in (dict(off=off[:2].contiguous()), dict(off=off.int()), dict(pl=pl.long()), dict(pl=pl.cpu())):
         with pytest.raises((tg.TGError, ValueError)):
             call(**kw)
+
+
+@pytest.mark.parametrize("kind, n, typ", [("bf16", 1, "bf16"), ("f16", 1, "f16"), ("e4m3", 1, "f16"), ("i8", 1, "bf16"), ("i8", 9, "f16")])
+@pytest.mark.parametrize("rise", [0.5, 4.0])
+def test_scores_that_rise_inside_a_tile(kind, n, typ, rise):
+    # every key scores above the one before: references rise in each tile, what came before is scaled down
+    import torch
+    D, L, own = 64, 300, [n + 40, n + 3, n + 150]
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(8, 2, D, typ, kind, 16, "token", n, [3], [L], own, seed=14)
+    u = np.random.default_rng(1).choice([-1.0, 1.0], D)
+    q.copy_(torch.from_numpy(np.broadcast_to(u, q.shape).copy()).to(q))
+    for b in range(3):
+        for j in range(int(lens[b])):
+            if b and j < L:
+                continue  # (the shared pages, or copies of the first one's)
+            k = u * (j % 400) * rise / D
+            page, slot = int(c.table[b, j // 16]), j % 16
+            if kind == "i8":
+                codes, scales = parts(c.k, 2, D, 16, "token")
+                codes[page, slot] = torch.from_numpy((128 + 127 * u).astype(np.uint8)).cuda()
+                s = np.float32((j % 400) * rise / D / 127)
+                scales[page, :, slot] = float(s)
+                c.keys[b][j] = u * 127 * np.float64(s)
+            else:
+                row = torch.from_numpy(np.broadcast_to(k * (10 if kind == "e4m3" else 1), (2, D)).astype(np.float32)).cuda().to(c.k.dtype)
+                c.k.view(torch.uint8 if kind == "e4m3" else c.k.dtype)[page, slot] = row.view(torch.uint8) if kind == "e4m3" else row
+                c.keys[b][j] = f64(row)
+    for b in (1, 2):
+        whole = L // 16 * 16
+        c.keys[b][:L] = c.keys[0][:L]
+        for j in range(whole, L):  # (the page in which the prefix ends is each one's copy)
+            dst, src = int(c.table[b, j // 16]), int(c.table[0, j // 16])
+            if kind == "i8":
+                codes, scales = parts(c.k, 2, D, 16, "token")
+                codes[dst, j % 16] = codes[src, j % 16]
+                scales[dst, :, j % 16] = scales[src, :, j % 16]
+            else:
+                raw = c.k.view(torch.uint8) if kind == "e4m3" else c.k
+                raw[dst, j % 16] = raw[src, j % 16]
+    out, lse = call()
+    check_attention((out, lse), reference())
+    o2, z2 = torch.empty_like(out), torch.empty_like(lse)
+    tg.tg_attend_step(q, ids(lens, np.int32), c.device_table(), c.k, c.v, cfg, o2, z2)
+    check_attention((o2, z2), reference())
+
+
+def test_a_key_head_for_every_query_head_and_more_sequences_than_a_tile():
+    for kind in ("bf16", "i8"):
+        tg, cfg, c, q, off, pl, lens, reference, call = setup(3, 3, 64, "bf16", kind, 16, "head", 1, [100, 70], [200, 40],
+                                                              [i % 11 for i in range(170)], seed=15)
+        check_attention(call(), reference())
+
+
+def test_more_sequences_than_the_layout_holds():
+    # read one by one
+    B = 18000
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(2, 1, 16, "f16", "f16", 16, "token", 1, [B // 2, B // 2], [20, 16],
+                                                          [1 + i % 3 for i in range(B)], seed=16)
+    check_attention(call(), reference())
