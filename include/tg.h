@@ -464,8 +464,9 @@ typedef struct tg_attn_params {
   const float* k_scales;
   const float* v_scales;
   int32_t max_step_tokens; /* largest n of tg_attend_step, 1 .. TG_MAX_STEP_TOKENS; 0 = 17 */
-  /* Largest batch * n of tg_attend_shared (its workspace: num_heads *
-   * (head_dim + 2) f32 a token); 0 = the call is refused. */
+  /* Largest batch * n of tg_attend_shared; 0 = the call is refused.  (Its
+   * workspace: num_heads + 8 * (num_kv_heads + 1) bytes a token, and what the
+   * GPU's parts of split rows take, 40 MB at a head_dim of 128.) */
   int32_t max_shared_tokens;
 } tg_attn_params;
 
@@ -498,7 +499,7 @@ tg_status tg_attn_clear_status(const tg_attn* cfg);
  * A page of an i8 cache is its codes, laid out as page_layout says (a byte
  * holds code + 128), and behind them its scales, f32 [num_kv_heads, page_size]:
  * page_size * num_kv_heads * (head_dim + 4) bytes.  An element stands for code *
- * scale. */
+ * scale; no scale is negative. */
 typedef struct tg_cache {
   void* k_pages;            /* num_pages pages, each laid out as page_layout says */
   void* v_pages;

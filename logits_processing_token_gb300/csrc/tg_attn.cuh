@@ -1,5 +1,6 @@
-// Shared declarations of the attention kernels (tg_append.cu, tg_step.cu,
-// tg_prompt.cu) and their C ABI (tg_attn_api.cu); internal to the library.
+// Shared declarations of the attention kernels (tg_append.cu, tg_read.cu, tg_step.cuh,
+// tg_wide.cuh, tg_finish.cu, tg_prompt.cu) and their C ABI (tg_attn_api.cu); internal
+// to the library.
 #pragma once
 
 #include <cstdint>
@@ -43,7 +44,9 @@ struct AttnCfg {
   int step_slots;          // workspace slots (two per CTA)
   float* ws_o;             // [slots][step_rows][D]
   float2* ws_ml;           // [slots][step_rows]: running maximum (base 2) and sum
-  int4* ws_pre;            // [max_shared][pairs of key heads]: the parts of a shared call's rows (PartsOf)
+  // [max_shared][pairs of key heads]: of a token's rows in a shared call, the first CTA that has a part, how many
+  // have (one: it wrote the rows), the token's first row of the tile, -
+  int4* ws_pre;
   unsigned char* ws_alone; // [max_shared][H]: rows that came out infinite or not a number
   float* ws_part_o;        // [4 x CTAs][kPartRows][D]: those parts
   float2* ws_part_ml;      // reference (base 2) and sum
@@ -123,7 +126,7 @@ cudaError_t launch_finish(const AttnCfg& c, const StepArgs& a, cudaStream_t s); 
 cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s);
 cudaError_t step_e4m3(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
 cudaError_t step_i8(AttnCfg* prep, const AttnCfg& c, const StepArgs* a, cudaStream_t s);
-cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, 16-bit cache
+cudaError_t launch_wide(const AttnCfg& c, const StepArgs& a, cudaStream_t s);  // many rows, and shared calls
 cudaError_t launch_prompt(const AttnCfg& c, const PromptArgs& a, cudaStream_t s);
 // What fits into the copies' memory while a shared call's work is laid out there: two
 // ints per sequence and per group.
@@ -369,11 +372,6 @@ __device__ __forceinline__ void tma4(unsigned dst, const CUtensorMap* m, int x, 
 __device__ __forceinline__ long long wide_part(int slot_rows, long long cta, int begun, int t) {
   return ((2 * cta + begun) * 2 + t) * slot_rows;
 }
-// The parts of one token's rows of a key head in a shared call: the first CTA, how
-// many, and the token's first row of the tile.  One: the row is written.
-struct PartsOf {
-  int c0, parts, row;
-};
 
 // Weights exp2(s - m) of f16 products are stored times 2^8: a weight 2^-33 of
 // the row's largest is still a (subnormal) f16 number, and the largest, 256,

@@ -1,5 +1,5 @@
 // Fifth-generation tensor core helpers of the attention kernels (tg_prompt.cu,
-// tg_wide.cu): descriptors, matrix instructions, tensor memory, and the softmax
+// tg_wide.cuh): descriptors, matrix instructions, tensor memory, and the softmax
 // of a tile of 128 scores per row; internal to the library.
 #pragma once
 

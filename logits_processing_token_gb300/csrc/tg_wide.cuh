@@ -2,12 +2,12 @@
 // verify step), and the prefixes of tg_attend_shared, whose rows are those of all
 // of a group's sequences, on the fifth-generation tensor cores.
 //
-// The split over the GPU, the parts and their join are those of tg_step.cu, the
+// The split over the GPU, the parts and their join are those of tg_step.cuh, the
 // matrix instructions and the softmax those of tg_prompt.cu.  A tile is 128
 // keys of one (sequence, key head) against up to 128 rows, whole tokens times
 // the query heads that share the key head; two key heads of a sequence go side
 // by side, so that the softmax of one runs while the other's products do.
-// With 68 rows the warp-wide instructions of tg_step.cu take four times as long
+// With 68 rows the warp-wide instructions of tg_step.cuh take four times as long
 // as the copies (32 sequences of 256 to 4,096 keys, 17 tokens: 177 us); here the
 // copies bound the stream, 50 us of 74 (floor 42), and the look-ups at the
 // beginning (5) and the joins at the end (10) do the rest.
@@ -51,7 +51,7 @@ constexpr int kKeysW = 128;
 constexpr int kItemCostW = 2;   // beginning and ending an item, in tiles
 
 struct WItem {
-  int b, pair, rt, len;  // b: its (first) sequence, < 0: no more; len: keys of it, or of the prefix
+  int b, pair, len;      // b: its (first) sequence, < 0: no more; len: keys of it, or of the prefix
   int tok0, toks;        // its first row's token in q, and the tokens from there on
   int tiles;             // of all CTAs
   int t0, t1;            // its tiles that are this CTA's
@@ -281,7 +281,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
   fence_async();
   dep_wait();
 
-  // ---- this CTA's units, as in tg_step.cu --------------------------------
+  // ---- this CTA's units, as in tg_step.cuh -------------------------------
   const long long max_len = static_cast<long long>(a.c.max_pages) << c.page_shift;
   const auto checked = [&](int l) { return l >= 0 && l <= max_len ? l : 0; };
   const auto tiles_of = [](int keys) { return keys > 0 ? (keys + kKeysW - 1) / kKeysW : 1; };
@@ -516,11 +516,10 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const int is = it_n & 1;
       ok = bar_wait(&s->dead, &s->item_empty[is], ((it_n >> 1) & 1) ^ 1, c);
       if (!ok) break;
-      WItem it{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0};
+      WItem it{-1, 0, 0, 0, 0, 0, 0, 0, 0, 0};
       if (more) {
         it.b = b;
         it.pair = pr;
-        it.rt = rt;
         it.len = len;
         it.tok0 = b * a.n + rt * ws.tpt;
         it.toks = SHARED && ws.row_tiles == 1 ? min(ws.members, ge - b) * a.n : a.n - rt * ws.tpt;
