@@ -27,7 +27,7 @@ namespace tg {
 namespace {
 
 constexpr int kAppendThreads = 256;
-constexpr int kMaxTok = 4;  // tokens per CTA at most (7,300 into an e4m3 cache: 37.3 us, 42.6 at 8; 13,800 in bf16: 60.1, 60.6)
+constexpr int kMaxTok = 4;  // tokens per CTA at most, a warp each looks up (7,300 into an e4m3 cache: 37.3 us, 42.6 at 8; 13,800 in bf16: 60.1, 60.6)
 
 // W 16-bit elements of a head, in registers of two.
 template <int W>
@@ -77,23 +77,60 @@ __device__ __forceinline__ Vec8<W> narrow8(const float (&x)[W], const float4& d)
   return v;
 }
 
-// What quotient() takes of an i8 head's scale (0: every quotient 0).
+// An i8 head's codes: the quotients by the scale to the nearest whole numbers (ties to
+// even: 1.5 2^23 has an f32's last bit where ones are), plus 128, a byte each.
+constexpr float kOnes = 0x1.8p23f + 128.0f;
+__device__ __forceinline__ unsigned bytes4(float a, float b, float c, float d) {
+  return __byte_perm(__byte_perm(__float_as_uint(a), __float_as_uint(b), 0x0040), __byte_perm(__float_as_uint(c), __float_as_uint(d), 0x0040), 0x5410);
+}
+// Largest magnitudes from 2^-56 to below 2^64: the scale and its reciprocal are in the
+// middle of f32's range, no residual that matters is rounded, and no quotient passes
+// 127; so quotient()'s steps without what it needs at the ends, two elements at a time
+// (6,048 tokens of 32 + 2 x 8 heads of 128: 34.7 us with quotient(), 00 so).
+__device__ __forceinline__ bool middle(unsigned top) { return top - 0x23800000u < 0x3c000000u; }
+struct Divisor {
+  float scale, inv;
+};
+__device__ __forceinline__ Divisor divisor_middle(unsigned top) {
+  const float t = __uint_as_float(top), r = 1.0f / 127.0f, q = t * r;
+  const float scale = fmaf(fmaf(q, -127.0f, t), r, q);  // t / 127, rounded once
+  return Divisor{scale, __frcp_rn(scale)};
+}
+template <int W>
+__device__ __forceinline__ Vec8<W> narrow_middle(const float (&x)[W], const Divisor& d) {
+  const unsigned long long inv = pair(d.inv, d.inv), less = pair(-d.scale, -d.scale), ones = pair(kOnes, kOnes);
+  Vec8<W> v;
+  const auto two = [&](int i) {
+    const unsigned long long y = pair(x[i], x[i + 1]), q = mul2(y, inv);
+    return unpair(add2(fma2(fma2(q, less, y), inv, q), ones));
+  };
+#pragma unroll
+  for (int i = 0; i < W / 4; ++i) {
+    const float2 a = two(4 * i), b = two(4 * i + 2);
+    v.w[i] = bytes4(a.x, a.y, b.x, b.y);
+  }
+  return v;
+}
+// Of any scale.  (The smallest are rounded so far that quotients pass 127; of 0 and of a
+// NaN every code is 0.)
 __device__ __forceinline__ float4 divisor(float scale) {
   const float power = scale < 0x1p-64f ? 0x1p96f : scale > 0x1p64f ? 0x1p-96f : 1.0f, s = scale * power;
   return make_float4(s, s > 0.0f ? __frcp_rn(s) : 0.0f, power, 0.0f);
 }
-// As i8: the quotient by the scale to the nearest whole number (ties to even:
-// 1.5 2^23 has an f32's last bit where ones are), plus 128.
 template <int W>
-__device__ __forceinline__ Vec8<W> narrow_i8(const float (&x)[W], const float4& d, bool fine) {
+__device__ __forceinline__ Vec8<W> narrow_any(const float (&x)[W], const float4& d) {
+  const bool fine = d.y > 0.0f;
   Vec8<W> v;
-  const auto one = [&](int i) {
-    return __float_as_uint(fminf(fmaxf(fine ? quotient(x[i], d) : 0.0f, -127.0f), 127.0f) + (0x1.8p23f + 128.0f));
-  };
+  const auto one = [&](int i) { return fminf(fmaxf(fine ? quotient(x[i], d) : 0.0f, -127.0f), 127.0f) + kOnes; };
 #pragma unroll
-  for (int i = 0; i < W / 4; ++i)
-    v.w[i] = __byte_perm(__byte_perm(one(4 * i), one(4 * i + 1), 0x0040), __byte_perm(one(4 * i + 2), one(4 * i + 3), 0x0040), 0x5410);
+  for (int i = 0; i < W / 4; ++i) v.w[i] = bytes4(one(4 * i), one(4 * i + 1), one(4 * i + 2), one(4 * i + 3));
   return v;
+}
+// The largest magnitude of three; a NaN if one is.
+__device__ __forceinline__ float top3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
 }
 
 // One CTA: tpb tokens.  A unit of work is 2 W elements of one head: two vectors
@@ -109,7 +146,11 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
   dep_wait();
   const int t0 = blockIdx.x * tpb;
   const int nt = min(tpb, a.tokens - t0);
-  if (threadIdx.x < nt) meta[threadIdx.x] = look_up(c, a.c, a.off, t0 + threadIdx.x);
+  const int warp = threadIdx.x >> 5;
+  if (warp < nt) {
+    const TokMeta m = look_up(c, a.c, a.off, t0 + warp);
+    if ((threadIdx.x & 31) == 0) meta[warp] = m;
+  }
   __syncthreads();
   const int half = c.rotary >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kAppendThreads) {
@@ -185,21 +226,31 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
       *reinterpret_cast<Vec<W>*>(dst + e1) = n1;
     }
     if constexpr (I8) {
+      if (!__any_sync(~0u, on && kind > 0)) continue;
       // the largest magnitude, as bits: above every number's are infinity's and NaN's
-      unsigned top = 0u;
+      float most = 0.0f;
 #pragma unroll
-      for (int j = 0; j < W; ++j) top = max(top, max(__float_as_uint(x[j]) & 0x7fffffffu, __float_as_uint(y[j]) & 0x7fffffffu));
+      for (int j = 0; j < W; ++j) most = top3(most, x[j], y[j]);
+      unsigned top = __float_as_uint(most) & 0x7fffffffu;
       for (int d = 1; d < per_head; d <<= 1) top = max(top, __shfl_xor_sync(~0u, top, d));
       if (on && kind > 0 && m.page >= 0) {
-        const bool fine = top < 0x7f800000u;
-        const float scale = fine ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7fc00000u);
-        const float4 d = divisor(scale);
         const long long page = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride);
         uint8_t* dst = static_cast<uint8_t*>(kind == 1 ? a.c.k : a.c.v) + page;
-        if (part == 0) *reinterpret_cast<float*>(dst + c.scale_at + (head * c.page_size + m.slot) * 4) = scale;
+        float* const scale_to = reinterpret_cast<float*>(dst + c.scale_at + (head * c.page_size + m.slot) * 4);
         dst += m.slot * c.slot_stride + head * c.head_stride;
-        *reinterpret_cast<Vec8<W>*>(dst + e0) = narrow_i8<W>(x, d, fine);
-        *reinterpret_cast<Vec8<W>*>(dst + e1) = narrow_i8<W>(y, d, fine);
+        Vec8<W> *const to0 = reinterpret_cast<Vec8<W>*>(dst + e0), *const to1 = reinterpret_cast<Vec8<W>*>(dst + e1);
+        if (middle(top)) {
+          const Divisor d = divisor_middle(top);
+          if (part == 0) *scale_to = d.scale;
+          *to0 = narrow_middle<W>(x, d);
+          *to1 = narrow_middle<W>(y, d);
+        } else {
+          const float scale = top < 0x7f800000u ? __uint_as_float(top) / 127.0f : __uint_as_float(0x7fc00000u);
+          const float4 d = divisor(scale);
+          if (part == 0) *scale_to = scale;
+          *to0 = narrow_any<W>(x, d);
+          *to1 = narrow_any<W>(y, d);
+        }
       }
       continue;
     }

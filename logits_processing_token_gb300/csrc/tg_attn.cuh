@@ -196,6 +196,32 @@ __device__ __forceinline__ float2 unpack2(unsigned w) {
   if constexpr (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
   else return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w));
 }
+// Two f32 in one 64-bit register: one instruction for both.
+__device__ __forceinline__ unsigned long long pair(float a, float b) {
+  unsigned long long d;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+  return d;
+}
+__device__ __forceinline__ float2 unpair(unsigned long long a) {
+  float2 d;
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(a));
+  return d;
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+  unsigned long long d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ unsigned long long mul2(unsigned long long a, unsigned long long b) {
+  unsigned long long d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
 // What a cache's elements are: 16 bits, or 8 that are widened to f16, exactly.
 constexpr int kC16 = 0, kE4M3 = TG_DTYPE_E4M3, kI8 = TG_DTYPE_I8;
 

@@ -13,7 +13,7 @@ namespace tg {
 namespace {
 
 constexpr int kReadThreads = 256;
-constexpr int kReadTok = 8;  // tokens per CTA at most
+constexpr int kReadTok = 8;  // tokens per CTA at most, a warp each looks up
 constexpr int kFlight = 2;   // vectors of a thread whose reads are under way together
 // (120,000 tokens of 8 heads of 128 out of an i8 cache: 109 us; 16 tokens and 4 vectors 116)
 
@@ -23,7 +23,11 @@ __global__ void __launch_bounds__(kReadThreads) read_kernel(const AttnCfg c, con
   dep_wait();
   const long long t0 = static_cast<long long>(blockIdx.x) * tpb;
   const int nt = static_cast<int>(min(static_cast<long long>(tpb), a.tokens - t0));
-  if (threadIdx.x < nt) meta[threadIdx.x] = look_up(c, a.c, a.off, t0 + threadIdx.x);
+  const int warp = threadIdx.x >> 5;
+  if (warp < nt) {
+    const TokMeta m = look_up(c, a.c, a.off, t0 + warp);
+    if ((threadIdx.x & 31) == 0) meta[warp] = m;
+  }
   __syncthreads();
   const int per_head = c.D >> 4;
   const int side = c.G * per_head;  // vectors of a token's keys
