@@ -9,16 +9,16 @@
 // angle to 2^-32 of a turn and sincospi takes it from there.
 //
 // Bytes bound it: every element is read once and written once (13,787 tokens of
-// 32 + 2 x 8 heads of 128 in bf16: 60.9 us, 6.0 TB/s, 89 % of the measured copy
+// 32 + 2 x 8 heads of 128 in bf16: 59.0 us, 6.2 TB/s, 93 % of the measured copy
 // rate).  A few tokens are bound by the launch and one chain of dependent reads,
-// offsets, length, page (one token 3.4 us a pass, 256 tokens 4.8 us).
+// offsets, length, page (one token 3.4 us a pass, 256 tokens 4.5 us); a thread's first
+// elements are under way with it.
 //
 // Into an i8 cache a head's lanes exchange their largest magnitudes before they
-// round, so that a warp's chain of read, exchange, division and write is longer and
-// bytes no longer bound it: 6,040 tokens of 32 + 2 x 8 heads of 128 take 34.7 us where
-// their 136 MB would take 20 (profiled: a third of the DRAM's rate, half of the warps
-// resident).  The next vector's read ahead of the exchange, more tokens a CTA and fewer
-// registers changed nothing.
+// round, and instructions bound it: 6,048 tokens of 32 + 2 x 8 heads of 128 take 29.2 us
+// where their 136 MB would take 20 (profiled: an instruction in two of three cycles, the
+// DRAM at 41 %).  The next vectors' reads ahead of the exchange cost more registers than
+// they gained (35), more tokens a CTA 0.2 us.
 #include <type_traits>
 
 #include "tg_tokens.cuh"
@@ -86,7 +86,7 @@ __device__ __forceinline__ unsigned bytes4(float a, float b, float c, float d) {
 // Largest magnitudes from 2^-56 to below 2^64: the scale and its reciprocal are in the
 // middle of f32's range, no residual that matters is rounded, and no quotient passes
 // 127; so quotient()'s steps without what it needs at the ends, two elements at a time
-// (6,048 tokens of 32 + 2 x 8 heads of 128: 34.7 us with quotient(), 00 so).
+// (6,048 tokens of 32 + 2 x 8 heads of 128: 34.7 us with quotient() for all, 30.0 so, with the same memory accesses).
 __device__ __forceinline__ bool middle(unsigned top) { return top - 0x23800000u < 0x3c000000u; }
 struct Divisor {
   float scale, inv;
@@ -133,88 +133,122 @@ __device__ __forceinline__ float top3(float a, float b, float c) {
   return d;
 }
 
+// Where pair p's angle is: 16 bytes behind every eight of them, so that the lanes of a
+// head, eight pairs apart, read different banks.
+constexpr __host__ __device__ int angle_at(int p) { return p + (p >> 3) * 2; }
+
 // One CTA: tpb tokens.  A unit of work is 2 W elements of one head: two vectors
 // of W, which for rotated "halves" are the two partners.  W is 8, or 4 where
 // half the rotated width is no multiple of 8 and the partners would straddle
 // 16-byte boundaries.
 // CK: kC16, kE4M3, or kI8, where the lanes of a head (their number rounded up to a
 // power of two) find its largest magnitude together.
+// (registers: the compiler's choice; for I8 48, one more would cost a CTA)
 template <bool F16, int CK, int W>
-__global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c, const AppendArgs a, int tpb) {
+__global__ void __launch_bounds__(kAppendThreads, CK == kI8 ? 5 : 0) append_kernel(const AttnCfg c, const AppendArgs a, int tpb) {
   __shared__ TokMeta meta[kMaxTok];
-  __shared__ float2 cs[kMaxTok][TG_MAX_HEAD_DIM / 2];
+  __shared__ alignas(16) float2 cs[kMaxTok][angle_at(TG_MAX_HEAD_DIM / 2)];
   dep_wait();
   const int t0 = blockIdx.x * tpb;
   const int nt = min(tpb, a.tokens - t0);
+  constexpr bool I8 = CK == kI8;
+  const int parts = c.D / (2 * W);  // units of a head
+  const int per_head = I8 ? 1 << (32 - __clz(parts - 1)) : parts;
+  const int heads = (a.q ? c.H : 0) + 2 * c.G;
+  const int units = heads * per_head;
+  const int half = c.rotary >> 1, rot_units = half / W;  // units of a head that turn
+  const unsigned inv_head = (1u << 20) / per_head + 1;  // u / per_head for u < 2^20 / per_head
+  // A thread's unit: token t of the CTA, its u-th unit.  Where I8 a warp stays together,
+  // and u counts heads: the threads are whole heads, so a thread's part stays.
+  struct Place {
+    int t, u, kind, head, part, e0, e1;
+    Vec<W> w0, w1;
+  };
+  const int step = I8 ? kAppendThreads >> (32 - __clz(parts - 1)) : kAppendThreads, end = I8 ? heads : units;
+  const auto next = [&](Place& p) {
+    while (p.u >= end) { p.u -= end; ++p.t; }
+    int h = p.u;
+    if constexpr (!I8) {
+      h = static_cast<int>((p.u * inv_head) >> 20);
+      p.part = p.u - h * per_head;
+    }
+    if (!a.q) h += c.H;
+    const long long row = t0 + p.t;
+    const uint16_t* src;
+    // q heads, then key heads, then value heads
+    if (h < c.H) { p.kind = 0; p.head = h; src = static_cast<const uint16_t*>(a.q) + row * a.qs; }
+    else if (h < c.H + c.G) { p.kind = 1; p.head = h - c.H; src = static_cast<const uint16_t*>(a.k) + row * a.ks; }
+    else { p.kind = 2; p.head = h - c.H - c.G; src = static_cast<const uint16_t*>(a.v) + row * a.vs; }
+    src += p.head * c.D;
+    const bool turn = p.kind < 2 && p.part < rot_units;
+    p.e0 = turn && !c.inter ? p.part * W : p.part * 2 * W;
+    p.e1 = turn && !c.inter ? p.e0 + half : p.e0 + W;
+    p.w0 = Vec<W>{};
+    p.w1 = Vec<W>{};
+    if (p.t < nt && p.part < parts) {
+      p.w0 = *reinterpret_cast<const Vec<W>*>(src + p.e0);
+      p.w1 = *reinterpret_cast<const Vec<W>*>(src + p.e1);
+    }
+  };
+  Place pl;
+  pl.t = 0;
+  pl.u = I8 ? threadIdx.x >> (32 - __clz(parts - 1)) : threadIdx.x;
+  pl.part = threadIdx.x & (per_head - 1);
+  next(pl);
   const int warp = threadIdx.x >> 5;
   if (warp < nt) {
     const TokMeta m = look_up(c, a.c, a.off, t0 + warp);
     if ((threadIdx.x & 31) == 0) meta[warp] = m;
   }
   __syncthreads();
-  const int half = c.rotary >> 1;
   for (int i = threadIdx.x; i < nt * half; i += kAppendThreads) {
     const int t = i / half, p = i - t * half;
     const unsigned long long turn = c.turns[p] * meta[t].pos;
     float sn, cn;
     sincospif(static_cast<float>(static_cast<int>(turn >> 32)) * 0x1p-31f, &sn, &cn);
-    cs[t][p] = make_float2(cn, sn);
+    cs[t][angle_at(p)] = make_float2(cn, sn);
   }
   __syncthreads();
 
-  constexpr bool I8 = CK == kI8;
-  const int parts = c.D / (2 * W);  // units of a head
-  const int per_head = I8 ? 1 << (32 - __clz(parts - 1)) : parts;
-  const int heads = (a.q ? c.H : 0) + 2 * c.G;
-  const int units = heads * per_head;
-  const int rot_units = half / W;  // units of a head that turn
-  const unsigned inv_head = (1u << 20) / per_head + 1;  // u / per_head for u < 2^20 / per_head
-  for (int t = 0, u = threadIdx.x;; u += kAppendThreads) {
-    while (u >= units) { u -= units; ++t; }
-    if (I8 ? !__any_sync(~0u, t < nt) : t >= nt) break;  // (i8: a warp stays together)
+  for (;; next(pl)) {
+    const int t = pl.t, kind = pl.kind, head = pl.head, part = pl.part, e0 = pl.e0, e1 = pl.e1;
+    const Vec<W> w0 = pl.w0, w1 = pl.w1;
+    if (I8 ? !__any_sync(~0u, t < nt) : t >= nt) break;
+    pl.u += step;
     const TokMeta m = meta[min(t, nt - 1)];
-    if (!I8 && !m.ok) continue;
-    int h = static_cast<int>((u * inv_head) >> 20);
-    const int part = u - h * per_head;
-    const bool on = !I8 || (t < nt && m.ok && part < parts);
+    const bool on = t < nt && m.ok && part < parts;
     const long long row = t0 + t;
-    // q heads, then key heads, then value heads
-    const uint16_t* src;
-    int kind = 0, head = h;
-    if (!a.q) h += c.H;
-    if (h < c.H) { src = static_cast<const uint16_t*>(a.q) + row * a.qs + static_cast<long long>(h) * c.D; head = h; }
-    else if (h < c.H + c.G) { kind = 1; head = h - c.H; src = static_cast<const uint16_t*>(a.k) + row * a.ks + static_cast<long long>(head) * c.D; }
-    else { kind = 2; head = h - c.H - c.G; src = static_cast<const uint16_t*>(a.v) + row * a.vs + static_cast<long long>(head) * c.D; }
     const bool turn = on && kind < 2 && part < rot_units;
-    const int e0 = turn && !c.inter ? part * W : part * 2 * W;
-    const int e1 = turn && !c.inter ? e0 + half : e0 + W;
-    Vec<W> w0{}, w1{};
-    if (on) {
-      w0 = *reinterpret_cast<const Vec<W>*>(src + e0);
-      w1 = *reinterpret_cast<const Vec<W>*>(src + e1);
-    }
     float x[W], y[W];
     widen<F16, W>(w0, x);
     widen<F16, W>(w1, y);
     if (turn) {
       if (!c.inter) {
+        const float4* const r = reinterpret_cast<const float4*>(&cs[t][angle_at(e0)]);
 #pragma unroll
-        for (int j = 0; j < W; ++j) {
-          const float2 r = cs[t][e0 + j];
-          const float p = x[j], q = y[j];
-          x[j] = p * r.x - q * r.y;
-          y[j] = q * r.x + p * r.y;
+        for (int j = 0; j < W; j += 2) {
+          const float4 w = r[j >> 1];
+          const float p = x[j], q = y[j], p2 = x[j + 1], q2 = y[j + 1];
+          x[j] = p * w.x - q * w.y;
+          y[j] = q * w.x + p * w.y;
+          x[j + 1] = p2 * w.z - q2 * w.w;
+          y[j + 1] = q2 * w.z + p2 * w.w;
         }
       } else {
+        const auto two = [&](float (&z)[W], int e) {
+          const float4* const r = reinterpret_cast<const float4*>(&cs[t][angle_at(e >> 1)]);
 #pragma unroll
-        for (int j = 0; j < W / 2; ++j) {
-          const float2 r = cs[t][(e0 >> 1) + j], r2 = cs[t][((e0 + W) >> 1) + j];
-          const float p = x[2 * j], q = x[2 * j + 1], p2 = y[2 * j], q2 = y[2 * j + 1];
-          x[2 * j] = p * r.x - q * r.y;
-          x[2 * j + 1] = q * r.x + p * r.y;
-          y[2 * j] = p2 * r2.x - q2 * r2.y;
-          y[2 * j + 1] = q2 * r2.x + p2 * r2.y;
-        }
+          for (int j = 0; j < W; j += 4) {
+            const float4 w = r[j >> 2];
+            const float p = z[j], q = z[j + 1], p2 = z[j + 2], q2 = z[j + 3];
+            z[j] = p * w.x - q * w.y;
+            z[j + 1] = q * w.x + p * w.y;
+            z[j + 2] = p2 * w.z - q2 * w.w;
+            z[j + 3] = q2 * w.z + p2 * w.w;
+          }
+        };
+        two(x, e0);
+        two(y, e0 + W);
       }
     }
     Vec<W> n0 = w0, n1 = w1;
@@ -254,7 +288,7 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const AttnCfg c,
       }
       continue;
     }
-    if (kind > 0 && m.page >= 0) {
+    if (on && kind > 0 && m.page >= 0) {
       const long long at = m.page * (kind == 1 ? a.c.k_page_stride : a.c.v_page_stride) + m.slot * c.slot_stride +
                            head * c.head_stride;
       if constexpr (CK == kE4M3) {

@@ -4,7 +4,7 @@
 // A 16-bit cache is copied; an 8-bit one gives code * scale, one f32 product and
 // one rounding.  Bytes bound it: a token's heads lie together in the output, and
 // in a page of the token layout, so that a warp's vectors of 16 elements are
-// whole lines on both sides: 120,000 tokens of 8 heads of 128 out of an i8 cache
+// whole lines on both sides: 112,749 tokens of 8 heads of 128 out of an i8 cache
 // 108 us, 97 % of the measured copy rate; 517 tokens of one sequence 2.9 us, the launch
 // and the chain offsets, length, page, vector.
 #include "tg_tokens.cuh"
@@ -15,7 +15,7 @@ namespace {
 constexpr int kReadThreads = 256;
 constexpr int kReadTok = 8;  // tokens per CTA at most, a warp each looks up
 constexpr int kFlight = 2;   // vectors of a thread whose reads are under way together
-// (120,000 tokens of 8 heads of 128 out of an i8 cache: 109 us; 16 tokens and 4 vectors 116)
+// (112,749 tokens of 8 heads of 128 out of an i8 cache: 109 us; 16 tokens and 4 vectors 116)
 
 template <bool F16, int CK>
 __global__ void __launch_bounds__(kReadThreads) read_kernel(const AttnCfg c, const ReadArgs a, int tpb) {
