@@ -813,12 +813,18 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
             const int r = r0 + (k0 + k) * RS;
             unsigned y[8];
             widen16<CK, KEYS ? F16 : true>(x[k], y);
-            if (!all && (r >= end || ((bad[r >> 5] >> (r & 31)) & 1))) {
-#pragma unroll
-              for (int z = 0; z < 8; ++z) y[z] = 0u;  // (0 x NaN is not 0)
-            }
             *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a0) = make_uint4(y[0], y[1], y[2], y[3]);
             *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a1) = make_uint4(y[4], y[5], y[6], y[7]);
+          }
+        }
+        if (!all) {  // values that do not exist: 0 x NaN is not 0 (beside the loop above: less code in it)
+#pragma unroll 1
+          for (int k = 0; k < UN; ++k) {
+            const int r = r0 + k * RS;
+            if (r < stop && (r >= end || ((bad[r >> 5] >> (r & 31)) & 1))) {
+              *reinterpret_cast<uint4*>(to + k * RS * 128 + a0) = make_uint4(0, 0, 0, 0);
+              *reinterpret_cast<uint4*>(to + k * RS * 128 + a1) = make_uint4(0, 0, 0, 0);
+            }
           }
         }
         fence_async();
