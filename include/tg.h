@@ -602,9 +602,8 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
  *               share nothing.
  *  prefix_lens  device int32 [groups]: tokens 0 .. prefix_lens[i] - 1 are the same
  *               for all of the group's sequences.  Each sequence's row of the page
- *               table names them, on pages that they share or on copies, and the
- *               row of the group's first sequence does whatever its length; the
- *               call may read them through either.
+ *               table names them as far as it is long, on pages that they share or
+ *               on copies; the call may read them through any.
  *
  * batch * n is at most max_shared_tokens.  Other arguments, outputs and numerics
  * as tg_attend_step, whose results these are up to the order of the sums.  A

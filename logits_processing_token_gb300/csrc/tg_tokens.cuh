@@ -22,7 +22,7 @@ __device__ __forceinline__ int find_seq(const int64_t* off, int batch, long long
   const int lane = threadIdx.x & 31;
   int lo = 0;
   for (int left = batch; left > 1;) {  // it is in [lo, lo + left)
-    const int step = (left + 31) >> 5, at = lane * step;
+    const int step = ((left - 1) >> 5) + 1, at = lane * step;
     const unsigned under = __ballot_sync(~0u, at < left && off[lo + at] <= t);
     const int k = under ? (31 - __clz(under)) * step : 0;
     lo += k;

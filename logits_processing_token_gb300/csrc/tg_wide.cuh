@@ -430,7 +430,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     long long base;  // units before the item
     // a shared call's: the group, and of member lane + 32 i of the item its length and its last own tile's number + 1
     int grp = 0, gs = 0, ge = 0, mlen[kMemberRegs] = {}, mend[kMemberRegs] = {};
-    int nt;
+    int nt, pre_row = 0;  // (of the page table, for the prefix: the item's first sequence that sees it; < 0: none does)
     // What comes next is asked for an item ahead: lengths from a sequence on; the end and the keys of the next group.
     int nlen[kMemberRegs] = {}, next_end = 0, next_keys = 0;
     const auto fetch_lens = [&](int from) {
@@ -449,10 +449,13 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     const auto members = [&]() {  // of the item that begins with sequence b: fills these in, gives its tiles
       const int nm = min(ws.members, ge - b), pre = len > 0 ? tiles_of(len) : 0;
       int sum = pre;
+      pre_row = -1;
 #pragma unroll
       for (int i = 0; i < kMemberRegs; ++i) {
         const bool is = lane + 32 * i < nm;
         mlen[i] = is ? checked(nlen[i]) : 0;
+        const unsigned sees = __ballot_sync(~0u, is && begin_of(mlen[i], len) > 0);
+        if (pre_row < 0 && sees) pre_row = b + 32 * i + __ffs(sees) - 1;
         int own = is ? tiles_of(mlen[i] - begin_of(mlen[i], len)) : 0;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -546,7 +549,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const auto tile_at = [&](int j) {
         if constexpr (!SHARED) return Tile{len - j * kKeysW, 0, j * kKeysW, b};
         const int pre = len > 0 ? tiles_of(len) : 0;
-        if (j < pre) return Tile{len - j * kKeysW, -1, j * kKeysW, gs};
+        if (j < pre) return Tile{pre_row < 0 ? 0 : len - j * kKeysW, -1, j * kKeysW, pre_row};
         int mem = 0;  // members whose tiles end before this one
 #pragma unroll
         for (int i = 0; i < kMemberRegs; ++i) mem += __popc(__ballot_sync(~0u, lane + 32 * i < ws.members && mend[i] <= j));
@@ -810,7 +813,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           for (int k = 0; k < 4; ++k) x[k] = from[(k0 + k) * (32 * L::kWideners)];
 #pragma unroll
           for (int k = 0; k < 4; ++k) {
-            const int r = r0 + (k0 + k) * RS;
             unsigned y[8];
             widen16<CK, KEYS ? F16 : true>(x[k], y);
             *reinterpret_cast<uint4*>(to + (k0 + k) * RS * 128 + a0) = make_uint4(y[0], y[1], y[2], y[3]);

@@ -92,3 +92,19 @@ def test_two_handles_at_once():
         for o, z in g:
             assert torch.equal(o, w[0]) and torch.equal(z, w[1])
     assert all(m[0].tg_attn_status_word(m[1]) == 0 for m in made)
+
+
+@pytest.mark.parametrize("kind, n", [("bf16", 1), ("i8", 1), ("e4m3", 5), ("f16", 30)])
+def test_slots_that_name_no_page(kind, n):
+    # empty slots at a group's beginning, in it and at its end; sequences shorter than the prefix; a group of such ones
+    # alone; more sequences than a row tile holds: their rows of the table name the pages of their own lengths only
+    typ = "f16" if kind == "f16" else "bf16"
+    first = [0, 40, 0, 300 + n, 299 + n, 310, 0, 298 + n]
+    lens = first + [0, 20, 0] + ([0] * 70 + [200 + n, 260, 0] if n == 1 else [0])
+    members = [len(first), 3, len(lens) - len(first) - 3]
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(8, 2, 64, typ, kind, 16, "token", n, members, [300, 64, 200], [1] * len(lens), seed=47,
+                                                          lens=lens)
+    for b, m in enumerate(lens):
+        c.table[b, -(-int(m) // 16):] = -1
+    check_attention(call(), reference())
+    assert tg.tg_attn_status_word(cfg) == 0
