@@ -867,7 +867,8 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         meta = (meta + t1 - t0) % kMetas;
         continue;
       }
-      float vmax = 0.0f;
+      float vmax = 0.0f, vpre = 0.0f;  // (vpre: as the prefix left it)
+      int of = -1;                     // whose tile was the last one
       for (int j = t0; j < t1; ++j, meta = (meta + 1) % kMetas) {
         const int mt = meta % L::kScaleTiles;
         ok = bar_wait(&s->dead, &s->scales_full[mt][t], (phases >> mt) & 1, c);
@@ -892,11 +893,24 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           }
           const float most = __uint_as_float(__reduce_max_sync(~0u, top));
           float shrink = 1.0f;
+          if constexpr (SHARED) {
+            // Another sequence's own values: what the ones before them raised is not theirs.
+            // (Beyond 8 times, so that it is rare; sums that become infinite are a row's that
+            // tg_finish.cu computes again.)
+            const int mem = s->tile[meta].y;
+            const float low = fmaxf(vpre, fmaxf(2.0f * most, 0x1p-100f));
+            if (mem != of && most > 0.0f && vmax > 8.0f * low) {
+              shrink = vmax / low;
+              vmax = low;
+            }
+            of = mem;
+          }
           if (most > 4.0f * vmax || vmax == 0.0f) {  // (rarely more than once: twice the largest leaves room for 8 times it)
             const float now = fmaxf(2.0f * most, 0x1p-100f);
             shrink = vmax / now;
             vmax = now;
           }
+          if (SHARED && of < 0) vpre = vmax;
           const float inv = 1.0f / vmax;
           *kf = make_float4(y.x * base2, y.y * base2, y.z * base2, y.w * base2);
           *vs = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);

@@ -108,3 +108,29 @@ def test_slots_that_name_no_page(kind, n):
         c.table[b, -(-int(m) // 16):] = -1
     check_attention(call(), reference())
     assert tg.tg_attn_status_word(cfg) == 0
+
+
+@pytest.mark.parametrize("n, ratio", [(1, 2.0 ** 12), (1, 2.0 ** 30), (6, 2.0 ** 20), (1, 2.0 ** 110)])
+def test_i8_values_far_larger_in_another_sequence(n, ratio):
+    # every other sequence's own values are larger by a factor that f16 weights cannot hold: the others, whose rows
+    # share its tiles, are as exact as by themselves (their tolerances know their own values only)
+    import torch
+    from tests.quant_util import parts
+    H, G = (16, 8) if n == 1 else (8, 4)
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(H, G, 64, "bf16", "i8", 16, "token", n, [24, 6], [208, 64], [n + 5 * (i % 7) for i in range(30)],
+                                                          seed=48)
+    pre = np.repeat([208, 64], [24, 6])
+    scales = parts(c.v, G, 64, 16, "token")[1]
+    for b in range(1, 30, 2):
+        j = np.arange(pre[b], lens[b])
+        scales[ids(c.table[b, j // 16], np.int64), :, ids(j % 16, np.int64)] *= ratio
+        c.values[b] = c.values[b].copy()
+        c.values[b][pre[b]:] *= ratio
+    out, lse = call()
+    with np.errstate(over="ignore"):
+        want = reference()
+    even = list(range(0, 30, 2))
+    check_attention((out[even], lse[even]), [x[even] for x in want])
+    odd = list(range(1, 30, 2))
+    check_attention((out[odd], lse[odd]), [x[odd] for x in want])
+    assert tg.tg_attn_status_word(cfg) == 0
