@@ -17,7 +17,7 @@
 // queries' type, values to f16, as the weights are.  The scales of an i8 cache enter
 // in the softmax: a score times its key's, a weight times its value's relative to
 // about the largest so far, by which the sums are multiplied at the end (so a weight
-// stays in f16's range whatever the scales are).  32 sequences of 17 tokens take 77 us
+// stays in f16's range whatever the scales are).  32 sequences of 17 tokens take 78 us
 // (floor 23): chains of widening (1,200 cycles a tile and matrix), products and softmax,
 // and the joins.  On the warp-wide instructions, which widen each key once per 16
 // rows, they took 211.
