@@ -15,9 +15,10 @@
 // An 8-bit cache is copied as it is into stages of its own, and four warps widen
 // each tile, exactly, into one that the matrix instructions read: keys to the
 // queries' type, values to f16, as the weights are.  The scales of an i8 cache enter
-// in the softmax: a score times its key's, a weight times its value's relative to
-// about the largest so far, by which the sums are multiplied at the end (so a weight
-// stays in f16's range whatever the scales are).  32 sequences of 17 tokens take 78 us
+// in the softmax: a score times its key's, a weight times its value's and a factor of the
+// row's own, from the keys that it sees, by which the sums are divided at the end.  (One
+// factor for all the rows of a tile, from its largest scale, lost the weights of rows that
+// do not see that key.)  32 sequences of 17 tokens take 76 us
 // (floor 23): chains of widening (1,200 cycles a tile and matrix), products and softmax,
 // and the joins.  On the warp-wide instructions, which widen each key once per 16
 // rows, they took 211.
@@ -62,20 +63,17 @@ struct WItem {
 constexpr int kSlotsMaxW = 10, kMetas = 8;
 struct WBars {
   unsigned long long q_full, q_empty, kv_full[kSlotsMaxW], kv_empty[kSlotsMaxW], raw_full[kSlotsMaxW], raw_empty[kSlotsMaxW],
-      scales_full[kMetas][2], scales_ready[kMetas][2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
+      scales_full[kMetas][2], s_full[2], p_full[2], o_full[2], item_full[2], item_empty[2], meet[2], drain;
   unsigned tmem;
   int dead, last[2], first_b, first_len;  // (of a shared call, first_len: the group)
   long long first_in, wsum[16];
   WItem item[2];
   unsigned bad[kMetas][4];  // by tile, round the ring: keys on pages that do not exist
   int4 tile[kMetas];        // a shared call's: its keys; whose (from the item's first sequence; -1: the prefix); the first one's place
-  float2 fac[kMetas][2];    // i8, by tile and key head: what the sums shrink by first; the scale the values are relative to
 };
 
 // Warps 0 to 7: softmax, one warpgroup per key head; 8: matrix instructions; 9:
-// items and copies; an 8-bit cache: 12 to 15 widen, 10 and 11 prepare an i8
-// cache's scales, one key head each (a widening warp that also did held its tiles up:
-// 32 sequences of 17 tokens 118 us, 102 so; eight widening warps gained nothing).
+// items and copies; an 8-bit cache: 12 to 15 widen (eight gained nothing).
 // Registers of the softmax's two warpgroups and the third (8-bit: what the block is
 // launched with).
 template <int DP, int CK>
@@ -83,7 +81,7 @@ struct WLay {
   static constexpr bool Q8 = CK != kC16;
   static constexpr int kThreads = Q8 ? 512 : 384;
   static constexpr int kRegSoftmax = Q8 ? 128 : 208, kRegThird = Q8 ? 128 : 88;
-  static constexpr int kWideners = 4, kScalers = CK == kI8 ? 2 : 0;
+  static constexpr int kWideners = 4;
   static constexpr int kTileB = DP / 64 * kBlock;
   static constexpr int kSlots = Q8 ? (DP == 128 ? 3 : 6) : DP == 128 ? 5 : 10;
   static constexpr int kRawB = kKeysW * DP;                       // a tile as the cache has it
@@ -122,10 +120,14 @@ __device__ __forceinline__ void widen16(const uint4& r, unsigned (&w)[8]) {
   }
 }
 
-// With an i8 cache's scales the f16 weights, up to 2^7, are multiplied by up to 4 (the
-// values' relative to about the largest): a bias of 6, so that none passes f16's end.
+// How far a score may be above its row's reference before that is raised, and what the
+// exponents are raised by.  With an i8 cache's scales weights are 2^6 at most, so that no
+// product of a weight and a scale (below 2^122) leaves f32.
+template <bool I8>
+constexpr float kLag = I8 ? 9.0f : 7.0f;
 template <bool F16, bool I8>
-constexpr float kBias = I8 ? 6.0f : kWeightBias<F16>;
+constexpr float kBias = I8 ? -3.0f : kWeightBias<F16>;
+constexpr float kUpMost = 0x1p108f;  // largest factor of those products (smaller ones than 2^-100 lose bits)
 
 // Weights of a tile of which none of the warp's rows sees a key.
 __device__ __forceinline__ void no_weights(unsigned ts) {
@@ -140,24 +142,58 @@ __device__ __forceinline__ void no_weights(unsigned ts) {
 // little code, because several roles' code runs next to it and a shared call's own
 // tiles are one warp's alone (unrolled, 120 KB in all, a tile of theirs took 8 to 17
 // thousand cycles, most of them waits for instructions), and few registers, which the
-// widening warps have.  A row's reference is raised when a score is more than 2^7 above
-// it (or it has none), and what came before it, in the tile too, is scaled down.
+// widening warps have.  A row's reference is raised when a score is more than 2^7 (I8:
+// 2^9) above it (or it has none), and what came before it, in the tile too, is scaled
+// down; so the largest weight is in general rounded too, which costs f16 outputs over an
+// e4m3 cache 10 to 25 % of their distance from exact ones (raised with every larger
+// score, as in tg_step.cuh, most of a sequence's first 32 passes would rescale the sums).
+//
+// I8: what is stored are the products of weights and their values' scales, times the row's
+// factor up: 2^5 for the largest of the keys that it has seen, 2^15 at most, so that what
+// f16's smallest step loses is 2^-30 of the largest.  When the reference rises the factor
+// does too, and what is stored stays as it is.  Keys that the row does not see have no say
+// in it, and their products are 0 whatever their scale is.  The largest product is searched
+// only where a reference rises, where the row's largest weight and the tile's largest
+// scale (known before the scores are) could make one that is stored above 2^15, and in
+// tiles with a scale that is no number.  (32 sequences of 17 tokens, scores spread so far
+// that one pass in five rescales sums, 12 us in all: 88 us; the largest product searched
+// in every pass 96; one factor for all the rows of a tile, from its largest scale, 82.)
 //
 // keys: of the tile, 128 at most; behind them the product reads up to the next 16, which
 // are masked.  rest: those from the tile's first that the row sees, except those in bad;
-// masked: some row of the warp does not see 128.  I8: ks, of each key, what its score is
-// multiplied by, else sc; part, what its weight is once it is summed; shrink: what the
-// sums so far are multiplied by first, the same for every row.
+// masked: some row of the warp does not see 128.  I8: ks, vs: the scales of the tile's keys
+// and values; log_most: the logarithm of the largest of these, infinite with one that is
+// no number.
 template <bool F16, bool I8>
-__device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, float sc, const float* ks, const float* part, float shrink,
-                                             int keys, bool masked, int rest, const unsigned* bad, bool has_sums, float& m, float& l) {
+__device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, float sc, const float* ks, const float* vs, int keys, bool masked,
+                                             int rest, const unsigned* bad, float log_most, bool has_sums, float& m, float& l, float& up) {
   constexpr float bias = kBias<F16, I8>;
-  if (I8 && has_sums && shrink != 1.0f) {
-    scale_sums(to, D, shrink);
-    tm_wait_st();
-  }
+  const auto limit_of = [&]() {  // how far above the reference a score may be
+    float log_up;
+    asm("lg2.approx.f32 %0, %1;" : "=f"(log_up) : "f"(up));
+    return fminf(kLag<I8>, 14.9f - bias - log_up - log_most);
+  };
+  float limit = I8 ? limit_of() : kLag<I8>;
 #pragma unroll 1
   for (int x = 0; 32 * x < max(1, keys); ++x) {
+    const auto rescale = [&](float f) {  // what is stored so far: the sums, and the tile's weights
+      tm_wait_st();
+      if (has_sums) scale_sums(to, D, f);
+#pragma unroll 1
+      for (int z = 0; z < x; ++z) {
+        unsigned w[16];
+        tm_ld16(w, ts + z * 16);
+        tm_wait_ld();
+        tm_pin(w);
+#pragma unroll
+        for (int y = 0; y < 16; ++y) {
+          const float2 e = unpack2<F16>(w[y]);
+          w[y] = pack2<F16>(e.x * f, e.y * f);
+        }
+        tm_st16(ts + z * 16, w);
+      }
+      tm_wait_st();
+    };
     unsigned v[32];
     tm_ld32(v, ts + x * 32);
     tm_wait_ld();
@@ -174,12 +210,13 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
         v[y + 3] = __float_as_uint(q.y);
       }
     }
+    unsigned hidden = 0u;
     if (masked) {
       const int r = rest - 32 * x;
-      const unsigned off = bad[x] | (r >= 32 ? 0u : r <= 0 ? ~0u : ~0u << r);
+      hidden = bad[x] | (r >= 32 ? 0u : r <= 0 ? ~0u : ~0u << r);
 #pragma unroll
       for (int y = 0; y < 32; ++y)
-        if (off & (1u << y)) v[y] = 0xff800000u;  // -infinity
+        if (hidden & (1u << y)) v[y] = 0xff800000u;  // -infinity
     }
     float tops[4];
 #pragma unroll
@@ -189,29 +226,23 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
       for (int y = 2; y < 8; y += 2) tops[z] = max3(tops[z], __uint_as_float(v[8 * z + y]), __uint_as_float(v[8 * z + y + 1]));
     }
     const float top = max3(tops[0], tops[1], fmaxf(tops[2], tops[3])) * sc;
-    const bool raise = top > m + 7.0f || (m == -INFINITY && top > m);
-    if (__any_sync(~0u, raise)) {
-      // (a row's first key: its sums are 0 whatever they are scaled by)
-      const bool some = __any_sync(~0u, raise && l != 0.0f);
+    const bool first = m == -INFINITY && top > m;
+    const bool act = (I8 && log_most == INFINITY) || __any_sync(~0u, top > m + limit || first);
+    // (a row's first key: its sums are 0 whatever they are scaled by)
+    const bool some = l != 0.0f;
+    bool raise = false;
+    float grown = 1.0f;  // I8: what is stored so far is multiplied by
+    if (act) {
+      raise = top > m + kLag<I8> || first;
       const float f = raise ? ex2(m - top) : 1.0f;
+      if constexpr (I8) {
+        const float now = raise ? up * ex2(top - m) : up;
+        if (now > kUpMost) grown = __fdividef(f * kUpMost, up);
+        up = fminf(now, kUpMost);
+      }
       if (raise) m = top;
       l *= f;
-      if (some) tm_wait_st();
-      if (some && has_sums) scale_sums(to, D, f);
-#pragma unroll 1
-      for (int z = 0; some && z < x; ++z) {  // the tile's weights so far
-        unsigned w[16];
-        tm_ld16(w, ts + z * 16);
-        tm_wait_ld();
-        tm_pin(w);
-#pragma unroll
-        for (int y = 0; y < 16; ++y) {
-          const float2 e = unpack2<F16>(w[y]);
-          w[y] = pack2<F16>(e.x * f, e.y * f);
-        }
-        tm_st16(ts + z * 16, w);
-      }
-      if (some) tm_wait_st();
+      if (!I8 && __any_sync(~0u, raise && some)) rescale(f);
     }
     const float off = m == -INFINITY ? 0.0f : bias - m;
     const unsigned long long sc2 = pair(sc, sc), off2 = pair(off, off);
@@ -220,18 +251,48 @@ __device__ __forceinline__ void softmax_loop(unsigned ts, unsigned to, int D, fl
 #pragma unroll
     for (int y = 0; y < 32; y += 4) {
       float4 w;
-      if constexpr (I8) w = *reinterpret_cast<const float4*>(part + x * 32 + y);
+      if constexpr (I8) w = *reinterpret_cast<const float4*>(vs + x * 32 + y);
 #pragma unroll
       for (int z = 0; z < 4; z += 2) {
         const float2 e = unpair(fma2(pair(__uint_as_float(v[y + z]), __uint_as_float(v[y + z + 1])), sc2, off2));
-        float p0 = ex2(e.x), p1 = ex2(e.y);
+        const float p0 = ex2(e.x), p1 = ex2(e.y);
         sum[((y >> 1) & 2) + (z >> 1)] = add2(sum[((y >> 1) & 2) + (z >> 1)], pair(p0, p1));
         if constexpr (I8) {
           const float2 q = unpair(mul2(pair(p0, p1), z ? pair(w.z, w.w) : pair(w.x, w.y)));
-          p0 = q.x;
-          p1 = q.y;
+          v[y + z] = __float_as_uint(q.x);
+          v[y + z + 1] = __float_as_uint(q.y);
+        } else {
+          p[(y + z) >> 1] = pack2<F16>(p0, p1);
         }
-        p[(y + z) >> 1] = pack2<F16>(p0, p1);
+      }
+    }
+    if constexpr (I8) {
+      if (act) {
+        if (masked && log_most == INFINITY) {  // (0 times a scale that is no number is not 0)
+#pragma unroll
+          for (int y = 0; y < 32; ++y)
+            if (hidden & (1u << y)) v[y] = 0u;
+        }
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+          tops[z] = fmaxf(__uint_as_float(v[8 * z]), __uint_as_float(v[8 * z + 1]));
+#pragma unroll
+          for (int y = 2; y < 8; y += 2) tops[z] = max3(tops[z], __uint_as_float(v[8 * z + y]), __uint_as_float(v[8 * z + y + 1]));
+        }
+        const float most = max3(tops[0], tops[1], fmaxf(tops[2], tops[3]));
+        if (most * up > (raise ? 0x1p5f : 0x1p15f)) {
+          const float now = __fdividef(1.0f, most * 0x1p-5f);
+          grown *= __fdividef(now, up);
+          up = now;
+        }
+        if (__any_sync(~0u, some && grown != 1.0f)) rescale(grown);
+        limit = limit_of();
+      }
+      const unsigned long long up2 = pair(up, up);
+#pragma unroll
+      for (int y = 0; y < 32; y += 2) {
+        const float2 q = unpair(mul2(pair(__uint_as_float(v[y]), __uint_as_float(v[y + 1])), up2));
+        p[y >> 1] = pack2<F16>(q.x, q.y);
       }
     }
     tm_st16(ts + x * 16, p);  // (the scores there are in registers, or done with)
@@ -259,17 +320,14 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     bar_init(&s->q_empty, 1);
     for (int i = 0; i < L::kSlots; ++i) { bar_init(&s->kv_full[i], Q8 ? L::kWideners : 1); bar_init(&s->kv_empty[i], 1); }
     for (int i = 0; i < L::kScaleTiles; ++i)
-      for (int t = 0; t < 2; ++t) {
-        bar_init(&s->scales_full[i][t], 33);
-        bar_init(&s->scales_ready[i][t], 1);
-      }
+      for (int t = 0; t < 2; ++t) bar_init(&s->scales_full[i][t], 33);
     for (int i = 0; i < L::kRaw; ++i) { bar_init(&s->raw_full[i], 1); bar_init(&s->raw_empty[i], L::kWideners); }
     for (int t = 0; t < 2; ++t) {
       bar_init(&s->s_full[t], 1);
       bar_init(&s->p_full[t], 4);
       bar_init(&s->o_full[t], 1);
       bar_init(&s->item_full[t], 1);
-      bar_init(&s->item_empty[t], 9 + (Q8 ? L::kWideners : 0) + L::kScalers);
+      bar_init(&s->item_empty[t], 9 + (Q8 ? L::kWideners : 0));
       bar_init(&s->meet[t], 4);
     }
     bar_init(&s->drain, 1);
@@ -847,81 +905,6 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       if (!ok) break;
     }
     __syncwarp();
-  } else if (I8 && (warp == 10 || warp == 11)) {
-    // ---- scales of an i8 cache ----------------------------------------------
-    if constexpr (!Q8) registers_down<L::kRegThird>();
-    const int t = warp - 10;
-    unsigned phases = 0;  // of the scales' places, a bit each (items with one key head pass the second's by)
-    int it_n = 0, meta = 0;
-    bool ok = true;
-    for (;;) {
-      const int is = it_n & 1;
-      ok = bar_wait(&s->dead, &s->item_full[is], (it_n >> 1) & 1, c);
-      if (!ok) break;
-      const int b = s->item[is].b, t0 = s->item[is].t0, t1 = s->item[is].t1, nch = s->item[is].nch, len = s->item[is].len;
-      __syncwarp();
-      if (lane == 0) bar_arrive(&s->item_empty[is]);
-      ++it_n;
-      if (b < 0) break;
-      if (t >= nch) {
-        meta = (meta + t1 - t0) % kMetas;
-        continue;
-      }
-      float vmax = 0.0f, vpre = 0.0f;  // (vpre: as the prefix left it)
-      int of = -1;                     // whose tile was the last one
-      for (int j = t0; j < t1; ++j, meta = (meta + 1) % kMetas) {
-        const int mt = meta % L::kScaleTiles;
-        ok = bar_wait(&s->dead, &s->scales_full[mt][t], (phases >> mt) & 1, c);
-        if (!ok) break;
-        phases ^= 1u << mt;
-        {
-          // Keys' scales times what makes scores powers of two; values' relative to about
-          // the largest so far, and 0 for keys that do not exist, whose may be anything.
-          // (Their weights are masked.)
-          float4* const kf = reinterpret_cast<float4*>(smem + L::kScaleAt + (mt * 2 + t) * (2 * kKeysW * 4)) + lane;
-          float4* const vs = kf + kKeysW / 4;
-          const float base2 = c.scale * kLog2E;
-          const float4 x = *vs, y = *kf;
-          float f[4] = {x.x, x.y, x.z, x.w};
-          const int key = 4 * lane, end = SHARED ? s->tile[meta].x : len - j * kKeysW;
-          unsigned top = 0u;
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            if (key + k >= end) f[k] = 0.0f;  // (a page that does not exist: copied as 0)
-            const unsigned u = __float_as_uint(f[k]);
-            if (u < 0x7f800000u) top = max(top, u);
-          }
-          const float most = __uint_as_float(__reduce_max_sync(~0u, top));
-          float shrink = 1.0f;
-          if constexpr (SHARED) {
-            // Another sequence's own values: what the ones before them raised is not theirs.
-            // (Beyond 8 times, so that it is rare; sums that become infinite are a row's that
-            // tg_finish.cu computes again.)
-            const int mem = s->tile[meta].y;
-            const float low = fmaxf(vpre, fmaxf(2.0f * most, 0x1p-100f));
-            if (mem != of && most > 0.0f && vmax > 8.0f * low) {
-              shrink = vmax / low;
-              vmax = low;
-            }
-            of = mem;
-          }
-          if (most > 4.0f * vmax || vmax == 0.0f) {  // (rarely more than once: twice the largest leaves room for 8 times it)
-            const float now = fmaxf(2.0f * most, 0x1p-100f);
-            shrink = vmax / now;
-            vmax = now;
-          }
-          if (SHARED && of < 0) vpre = vmax;
-          const float inv = 1.0f / vmax;
-          *kf = make_float4(y.x * base2, y.y * base2, y.z * base2, y.w * base2);
-          *vs = make_float4(f[0] * inv, f[1] * inv, f[2] * inv, f[3] * inv);
-          if (lane == 0) s->fac[meta][t] = make_float2(shrink, vmax);
-        }
-        __syncwarp();
-        if (lane == 0) bar_arrive(&s->scales_ready[mt][t]);
-      }
-      if (!ok) break;
-    }
-    __syncwarp();
   } else if (warp < 8) {
     // ---- softmax: one thread per row --------------------------------------
     if constexpr (!Q8) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kRegSoftmax));
@@ -968,9 +951,19 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       } else {
         lim = real ? lim_w + (a.n - it.toks + tok) : it.len;
       }
-      float vmax = 1.0f;
+      float up = kUpMost;
       float m = real ? -INFINITY : INFINITY, l = 0.0f;
       for (int j = it.t0; j < it.t1; ++j) {
+        float log_most = 0.0f;
+        if constexpr (I8) {  // (there before the scores are)
+          const int mt = meta % L::kScaleTiles;
+          ok = bar_wait(&s->dead, &s->scales_full[mt][t], (phases >> mt) & 1, c);
+          if (!ok) break;
+          phases ^= 1u << mt;
+          const uint4 f = reinterpret_cast<const uint4*>(smem + L::kScaleAt + (mt * 2 + t) * (2 * kKeysW * 4) + kKeysW * 4)[lane];
+          const unsigned most = __reduce_max_sync(~0u, max(max(f.x, f.y), max(f.z, f.w)));
+          asm("lg2.approx.f32 %0, %1;" : "=f"(log_most) : "f"(__uint_as_float(min(most, 0x7f800000u))));
+        }
         ok = bar_wait(&s->dead, &s->s_full[t], s_ph, c);
         if (!ok) break;
         s_ph ^= 1;
@@ -988,22 +981,11 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
           sees = real && rest > 0;
           masked = __any_sync(~0u, rest < kKeysW) || any_bad;
         }
-        float shrink = 1.0f;
-        if constexpr (I8) {
-          const int mt = meta % L::kScaleTiles;
-          ok = bar_wait(&s->dead, &s->scales_ready[mt][t], (phases >> mt) & 1, c);
-          if (!ok) break;
-          phases ^= 1u << mt;
-          const float2 f = s->fac[meta][t];
-          shrink = f.x;
-          vmax = f.y;
-        }
         if (SHARED && !__any_sync(~0u, sees)) {
-          if (I8 && j > it.t0 && shrink != 1.0f) scale_sums(to, c.D, shrink);
           no_weights(ts);
         } else if constexpr (SHARED || Q8) {
           const float* const scales = reinterpret_cast<const float*>(smem + L::kScaleAt + ((meta % L::kScaleTiles) * 2 + t) * (2 * kKeysW * 4));
-          softmax_loop<PF16, I8>(ts, to, c.D, I8 ? 1.0f : sc, scales, scales + kKeysW, shrink, keys, masked, rest, bad, j > it.t0, m, l);
+          softmax_loop<PF16, I8>(ts, to, c.D, sc, scales, scales + kKeysW, keys, masked, rest, bad, log_most, j > it.t0, m, l, up);
         } else {
           unsigned v[4][32];
 #pragma unroll
@@ -1040,7 +1022,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       const long long token = it.tok0 + tok, at = token * c.H + g * c.rep + head;
       const long long mine_part = wide_part(SHARED ? kPartRows : c.step_rows, blockIdx.x, tile0 < u0 ? 0 : 1, t) + row;
       // what the values' sums stand for
-      const float vs = I8 ? vmax : CK == kE4M3 && c.v_scale ? c.v_scale[g] : 1.0f;
+      const float vs = I8 ? 1.0f / up : CK == kE4M3 && c.v_scale ? c.v_scale[g] : 1.0f;
       const float f = !whole ? vs : l == 0.0f ? 0.0f : vs / l;
       float* const parts_to = (SHARED ? c.ws_part_o : c.ws_o) + mine_part * c.D;
       float zero = 0.0f;  // or NaN, when the sums hold an infinity or one
