@@ -18,7 +18,7 @@
 //
 // The copies bound it: 64 sequences of 0 to 4,096 keys (32 heads over 8, D 128,
 // bf16) 91.5 us, 5.9 TB/s, 87 % of the measured copy rate; 256 of 1 to 2,048 keys
-// in e4m3 100 us, 84 %, in i8 107 us, 82 % (its scales come as copies of 16 bytes of four
+// in e4m3 100 us, 84 %, in i8 108 us, 81 % (its scales come as copies of 16 bytes of four
 // keys each, made by the lanes that ask for the pages); 5 of 20,000 to 40,000 keys of 16 heads of 64 113 us, 95 %.
 // One sequence of 4,001 keys takes 11.8 us: look-ups 3, two tiles 2, the part's
 // end 2, the join of 32 parts 3.
@@ -383,12 +383,13 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   constexpr int NO = T ? KS : KS * 2;
   unsigned qf[KS][T ? 2 : 4];
   float o[NO][4];
-  float vmax = 0.0f;  // i8: the largest scale of a value so far, which the weights are taken relative to
+  float unit[2];  // i8: the largest product of a weight and its value's scale so far, which they are taken relative to
   float m[2], l[2], rs[2];  // of two rows: lane / 4 and lane / 4 + 8 of this warp's 16, or 2 (lane % 4) and the next of 8
   int lim[2];               // keys that the row sees
   const int r0 = T ? 2 * (lane & 3) : wm * 16 + (lane >> 2);
   constexpr int RSTEP = T ? 1 : 8;
-  const float bias = kWeightBias<MF16>;
+  const float bias = I8 ? 0.0f : kWeightBias<MF16>;
+  constexpr float kUnit = 0x1p8f, kLeast = 0x1p-100f;  // i8: the f16 number that a unit is; the least of one
   Unit cur;
   int qs = 0;
   unsigned q_ph = 0, meet_ph = 0;
@@ -410,7 +411,6 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
   };
   const auto begin_item = [&]() {
     const float sc = c.scale * kLog2E * (Q8 && c.k_scale ? c.k_scale[cur.g] : 1.0f);
-    vmax = 0x1p-100f;
     const unsigned char* qb = qbuf + qs * S::kQ;
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
@@ -418,6 +418,7 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       lim[h] = r < rows_all ? cur.len - a.n + r / c.rep + 1 : 0;
       m[h] = -INFINITY;
       l[h] = 0.0f;
+      unit[h] = kLeast;
       rs[h] = sc;
     }
 #pragma unroll
@@ -567,26 +568,15 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
       }
       // element (h, y) of s[i]: row h of the two
       const auto el = [](int h, int y) { return T ? 2 * y + h : 2 * h + y; };
-      // i8: scores times their keys' scales, and what the weights will be
-      // multiplied by: their values' scales relative to the largest so far (at most
-      // 1, so that no f16 weight overflows)
-      float part[I8 ? NS : 1][2];
-      float grown = 1.0f;
+      // i8: scores times their keys' scales
+      float part[I8 ? NS : 1][2];  // the values'
       if constexpr (I8) {
-        static_assert(KC == 32, "a scale per lane");
-        const unsigned u = __float_as_uint(vscale[at + lane]);
-        const float top = __uint_as_float(__reduce_max_sync(~0u, u < 0x7f800000u ? u : 0u));
-        if (top > vmax) {
-          grown = __fdividef(vmax, top);
-          vmax = top;
-        }
-        const float inv = 1.0f / vmax;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
           for (int y = 0; y < 2; ++y) {
             const int key = at + (T ? i * 16 + (lane >> 2) + 8 * y : i * 8 + 2 * (lane & 3) + y);
-            part[i][y] = vscale[key] * inv;
+            part[i][y] = vscale[key];
 #pragma unroll
             for (int h = 0; h < 2; ++h) s[i][el(h, y)] *= kscale[key];
           }
@@ -602,22 +592,35 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             if (cur.key0 + at + in >= lim[T ? x & 1 : x >> 1] || ((bw >> in) & 1)) s[i][x] = -INFINITY;
           }
       }
+      // the largest of a row, over the lanes that have its keys
+      const auto over_row = [](float x) {
+        if constexpr (T) {
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 4));
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 8));
+          return fmaxf(x, __shfl_xor_sync(~0u, x, 16));
+        } else {
+          x = fmaxf(x, __shfl_xor_sync(~0u, x, 1));
+          return fmaxf(x, __shfl_xor_sync(~0u, x, 2));
+        }
+      };
       float sub[2];
-      bool moved = I8 && grown != 1.0f;
+      bool moved = false;
+      const auto scale_sums = [&]() {
+        if (__any_sync(~0u, moved)) {
+#pragma unroll
+          for (int k = 0; k < NO; ++k)
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+              for (int y = 0; y < 2; ++y) o[k][el(h, y)] *= sub[h];
+        }
+      };
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         float top = -INFINITY;
 #pragma unroll
         for (int i = 0; i < NS; ++i) top = fmaxf(top, fmaxf(s[i][el(h, 0)], s[i][el(h, 1)]));
-        if constexpr (T) {
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 4));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 8));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 16));
-        } else {
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 1));
-          top = fmaxf(top, __shfl_xor_sync(~0u, top, 2));
-        }
-        top *= rs[h];
+        top = over_row(top) * rs[h];
         sub[h] = 1.0f;
         if (top > m[h]) {
           sub[h] = ex2(m[h] - top);
@@ -625,19 +628,12 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
           m[h] = top;
           moved = true;
         }
-        if constexpr (I8) sub[h] *= grown;
       }
-      if (__any_sync(~0u, moved)) {
-#pragma unroll
-        for (int k = 0; k < NO; ++k)
-#pragma unroll
-          for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int y = 0; y < 2; ++y) o[k][el(h, y)] *= sub[h];
-      }
+      if constexpr (!I8) scale_sums();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const float off = m[h] == -INFINITY ? 0.0f : m[h] - bias;
+        float most = 0.0f;
 #pragma unroll
         for (int i = 0; i < NS; ++i)
 #pragma unroll
@@ -645,9 +641,28 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
             float& x = s[i][el(h, y)];
             x = ex2(fmaf(x, rs[h], -off));
             l[h] += x;
-            if constexpr (I8) x *= part[i][y];
+            if constexpr (I8) {
+              x *= part[i][y];
+              most = fmaxf(most, x);
+            }
           }
+        if constexpr (I8) {
+          // The unit goes down with the weights when their reference rises (the sums, in
+          // units, stay as they are), and up with a larger product than any so far.
+          // Each row has its own, from the keys that it sees: one from the keys of the pass,
+          // 1 us of 108 faster, lost rows whose later tokens have far larger values.
+          const float now = unit[h] * sub[h], next = fmaxf(fmaxf(now, kLeast), over_row(most));
+          sub[h] = next == now ? 1.0f : __fdividef(now, next);
+          moved = h == 0 ? sub[h] != 1.0f : moved || sub[h] != 1.0f;
+          unit[h] = next;
+          const float inv = __fdividef(kUnit, next);
+#pragma unroll
+          for (int i = 0; i < NS; ++i)
+#pragma unroll
+            for (int y = 0; y < 2; ++y) s[i][el(h, y)] *= inv;
+        }
       }
+      if constexpr (I8) scale_sums();
 #pragma unroll
       for (int kg = 0; kg < KC / 16; ++kg) {
         const int row = at + kg * 16 + (T ? ((lane >> 4) << 3) + (lane & 7) : lane & 15);
@@ -750,7 +765,9 @@ step_kernel(const AttnCfg c, const StepArgs a, int row_tiles, int min_units, int
 #pragma unroll
       for (int k = 0; k < NO; ++k)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) o[k][x] *= vmax;
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int y = 0; y < 2; ++y) o[k][T ? 2 * y + h : 2 * h + y] *= unit[h] * (1.0f / kUnit);
     }
 #pragma unroll
     for (int h = 0; h < 2; ++h) {

@@ -53,8 +53,10 @@ def enlarge(c, heads, dim, b, pos, factor):
 
 
 STEPS = [
-    # heads, key heads, dim, type, page, layout, n
-    (8, 2, 128, "bf16", 16, "token", 6), (8, 2, 64, "f16", 64, "head", 17), (16, 1, 128, "f16", 8, "token", 5),
+    # heads, key heads, dim, type, page, layout, n: up to 8 rows, 16, the tensor-memory kernel, rows over small pages
+    (8, 2, 128, "bf16", 16, "token", 2), (8, 2, 64, "f16", 32, "head", 4), (8, 2, 128, "bf16", 16, "token", 6),
+    (8, 2, 64, "f16", 64, "head", 17), (4, 1, 64, "f16", 4, "token", 9), (5, 5, 80, "bf16", 2, "head", 30),
+    (16, 1, 128, "f16", 8, "token", 5),
 ]
 
 
