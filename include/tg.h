@@ -605,16 +605,19 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
  *               table names them as far as it is long, on pages that they share or
  *               on copies; the call may read them through any.
  *
- * batch * n is at most max_shared_tokens.  Other arguments, outputs and numerics
- * as tg_attend_step, whose results these are up to the order of the sums.  A
- * sequence that is shorter than the prefix and its n tokens, or empty, takes no part
+ * batch * n is at most max_shared_tokens.  Other arguments and outputs as
+ * tg_attend_step, whose results these are up to the order of the sums and the
+ * rounding of the weights (below).  A prefix is read once for as many of a group's
+ * sequences as have 128 rows together (n * num_heads / num_kv_heads each), 64 at most.
+ * A sequence that is shorter than the prefix and its n tokens, or empty, takes no part
  * in the sharing.  A call is a step, and reads neither group_offsets nor prefix_lens,
- * where sharing would not pay (few rows, and a page table with room for few keys),
- * over pages of fewer than 8 tokens, with more than 128 query heads to a key head,
- * and for batch + groups of 18,000 and more; else offsets out of order or a
- * prefix_lens[i] outside [0, max_pages * page_size] raise TG_FLAG_BAD_ROW, and
- * nothing is shared in that call.  Calls that share a tg_attn share its workspace:
- * in stream order.
+ * where nothing can be shared (more than 64 rows a sequence, or groups >= batch) or
+ * sharing would not pay (few rows, and a page table with room for few keys: the room
+ * decides, not the lengths, so a table wider than its sequences need may be shared to
+ * no gain), over pages of fewer than 8 tokens, and for batch + groups of 18,000 and
+ * more; else offsets out of order or a prefix_lens[i] outside [0, max_pages *
+ * page_size] raise TG_FLAG_BAD_ROW, and nothing is shared in that call.  Calls that
+ * share a tg_attn share its workspace: in stream order.
  */
 tg_status tg_attend_shared(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const int64_t* group_offsets,
                            const int32_t* prefix_lens, int32_t groups, const tg_attn* cfg, void* out, float* out_lse,

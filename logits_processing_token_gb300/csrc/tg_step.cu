@@ -27,6 +27,16 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   return by_cache(nullptr, c, &a, s);
 }
 
+// Nothing is shared where a row tile holds one sequence (32 heads over 8 of 128, groups x
+// sequences x keys, step and shared, us: 17 tokens 4 x 8 x 2,000 bf16 66 and 69, i8 76 and
+// 82, 1 x 128 x 6,000 bf16 539 and 577, i8 574 and 618; 16 tokens, two sequences to a tile,
+// 64 and 46, 75 and 57, 537 and 318, 572 and 349), or every group (6 tokens, 32 x 1 x 2,000
+// bf16 62 and 62, i8 67 and 73; 8 tokens, 64 x 1 x 300 30 and 35, 37 and 46).  Groups may be
+// empty: what the host knows is that there are not more sequences than groups.
+static bool can_share(const AttnCfg& c, const StepArgs& a) {
+  return a.groups > 0 && a.groups < a.c.batch && a.n * c.rep <= 64;
+}
+
 // Up to 16 rows the step kernel reads every sequence's keys faster than the shared
 // launch the common ones once, where there are few of them: 8 heads of 128, groups x
 // sequences x keys, step and shared, us: bf16 1 x 4 x 4,000 (66 MB of keys) 15.8 and
@@ -34,7 +44,8 @@ cudaError_t launch_step(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
 // 4,000 (132) 27.0 and 24.3, 1 x 32 x 1,000 (68) 18.4 and 20.4; i8 16 x 4 x 1,000 (136) 34.4 and
 // 36.1, 16 x 4 x 2,000 (267) 53.4 and 48.9.  Widening tiles of i8 keys for few rows costs
 // what two sequences' sharing saves: 64 x 2 x 2,000 105 and 115, 64 x 3 x 2,000 147 and
-// 126.  What the host knows is the longest that the sequences can be.
+// 126.  What the host knows is the longest that the sequences can be: a page table with
+// room for many more keys than there are has few shared too (bf16 1 x 4 x 1,021: 10.5 and 16.4).
 static bool shared_pays(const AttnCfg& c, const StepArgs& a) {
   if (a.n * c.rep > 16) return true;  // (4 x 4 x 1,000 keys, 5 tokens: bf16 26.6 and 18.6, i8 29.1 and 21.8)
   const double key = 2.0 * c.G * (c.D * (c.ctype == c.dtype ? 2.0 : 1.0) + (c.ctype == TG_DTYPE_I8 ? 4.0 : 0.0));
@@ -49,8 +60,8 @@ cudaError_t launch_shared(const AttnCfg& c, const StepArgs& a, cudaStream_t s) {
   StepArgs b = a;
   b.groups = -1;
   const long long tiles = (static_cast<long long>(a.c.max_pages) << c.page_shift) / 128 + 5;
-  if (a.groups == 0 || a.c.batch < 2 || !wide_can(c) || !shared_pays(c, a) || static_cast<long long>(a.c.batch) + a.groups >= kMostShared ||
-      tiles * a.c.batch * ((a.n * c.rep + 127) / 128 + 1) > 0x7fffffffll)
+  if (!can_share(c, a) || !wide_can(c) || !shared_pays(c, a) || static_cast<long long>(a.c.batch) + a.groups >= kMostShared ||
+      tiles * a.c.batch > 0x7fffffffll)
     return launch_step(c, b, s);
   const cudaError_t e = launch_wide(c, a, s);
   return e != cudaSuccess ? e : launch_finish(c, a, s);

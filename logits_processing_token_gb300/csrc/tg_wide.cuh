@@ -102,8 +102,8 @@ constexpr int kMemberRegs = 2;
 
 struct WSetup {
   int tpt;        // tokens of a row tile
-  int row_tiles;  // of a sequence
-  int members;    // sequences of a row tile (a shared call; else, and for longer ones, 1)
+  int row_tiles;  // of a sequence (a shared call: 1)
+  int members;    // sequences of a row tile (a shared call: 2 to 64)
   int pairs;      // of key heads
   int box;        // keys of one copy
   int wide;       // outputs 32-byte aligned
@@ -399,8 +399,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       group_of(b, gi, g0, g1, gk);
       const int pre = gk > 0 ? tiles_of(gk) : 0, own = tiles_of(l - begin_of(l, gk));
       at[b] = static_cast<unsigned>(mine);
-      mine += ws.row_tiles > 1 ? static_cast<long long>(ws.row_tiles) * (kItemCostW + pre + own)
-                               : own + ((b - g0) % ws.members == 0 ? kItemCostW + pre : 0);
+      mine += own + ((b - g0) % ws.members == 0 ? kItemCostW + pre : 0);
     }
   } else {
     for (int b = b_first; b < b_end; ++b) {
@@ -484,7 +483,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
     // ---- items, pages and copies --------------------------------------------
     if constexpr (!Q8) registers_down<L::kRegThird>();
     const int shift = 31 - __clz(ws.box), per = kKeysW >> shift;  // copies of a tile
-    int b = s->first_b, rt, pr, len;
+    int b = s->first_b, rt = 0, pr, len;
     long long base;  // units before the item
     // a shared call's: the group, and of member lane + 32 i of the item its length and its last own tile's number + 1
     int grp = 0, gs = 0, ge = 0, mlen[kMemberRegs] = {}, mend[kMemberRegs] = {};
@@ -556,9 +555,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       fetch_group();
       nt = members();
       pr = static_cast<int>(u0 / total);
-      const int skip = static_cast<int>(s->first_in / (nt + kItemCostW));
-      rt = ws.row_tiles > 1 ? skip : 0;
-      base = u0 - s->first_in + static_cast<long long>(rt) * (nt + kItemCostW);
+      base = u0 - s->first_in;
     } else {
       len = s->first_len;
       nt = tiles_of(len);
@@ -583,7 +580,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
         it.pair = pr;
         it.len = len;
         it.tok0 = b * a.n + rt * ws.tpt;
-        it.toks = SHARED && ws.row_tiles == 1 ? min(ws.members, ge - b) * a.n : a.n - rt * ws.tpt;
+        it.toks = SHARED ? min(ws.members, ge - b) * a.n : a.n - rt * ws.tpt;
         it.tiles = nt;
         it.t0 = static_cast<int>(max(0ll, u0 - base - kItemCostW));
         it.t1 = static_cast<int>(min(static_cast<long long>(nt), u1 - base - kItemCostW));
@@ -596,7 +593,7 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       ++it_n;
       if (!more) break;
-      if (SHARED && rt + 1 == ws.row_tiles) {
+      if constexpr (SHARED) {
         const int after = min(b + ws.members, ge);
         fetch_lens(after == a.c.batch ? 0 : after);
       }
@@ -704,19 +701,19 @@ wide_kernel(const AttnCfg c, const StepArgs a, const WSetup ws, const __grid_con
       }
       if (!ok) break;
       base += nt + kItemCostW;
-      if (++rt == ws.row_tiles) {
+      if constexpr (SHARED) {
+        b = min(b + ws.members, ge);
+        if (b == a.c.batch) {
+          ++pr;
+          b = grp = ge = next_end = 0;  // (next_group: from the first one on)
+        }
+        if (pr < ws.pairs) {
+          if (b == ge) next_group();
+          nt = members();
+        }
+      } else if (++rt == ws.row_tiles) {
         rt = 0;
-        if constexpr (SHARED) {
-          b = min(b + ws.members, ge);
-          if (b == a.c.batch) {
-            ++pr;
-            b = grp = ge = next_end = 0;  // (next_group: from the first one on)
-          }
-          if (pr < ws.pairs) {
-            if (b == ge) next_group();
-            nt = members();
-          }
-        } else if (++pr == ws.pairs) {
+        if (++pr == ws.pairs) {
           pr = 0;
           ++b;
           len = b < a.c.batch ? checked(a.c.lens[b]) : 0;
@@ -1191,9 +1188,9 @@ cudaError_t go(const AttnCfg& c, const StepArgs* a, cudaStream_t s) {
   }
   WSetup ws{};
   ws.tpt = 128 / c.rep;
-  ws.row_tiles = (a->n + ws.tpt - 1) / ws.tpt;
-  ws.members = SHARED && ws.row_tiles == 1 ? std::min(ws.tpt / a->n, 32 * kMemberRegs) : 1;
-  if (SHARED && ws.row_tiles == 1) ws.tpt = ws.members * a->n;
+  ws.members = SHARED ? std::min(ws.tpt / a->n, 32 * kMemberRegs) : 1;
+  if (SHARED) ws.tpt = ws.members * a->n;
+  ws.row_tiles = SHARED ? 1 : (a->n + ws.tpt - 1) / ws.tpt;
   ws.pairs = (c.G + 1) / 2;
   ws.box = std::min(c.page_size, kKeysW);
   ws.wide = (reinterpret_cast<uintptr_t>(a->out) & 31) == 0;
