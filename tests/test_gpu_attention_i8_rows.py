@@ -172,3 +172,39 @@ def test_a_neighbours_nan_scales(n):
     keep = [0, 2, 3]
     check_attention((out[keep], lse[keep]), [x[keep] for x in want])
     assert out[[1, 4]].isnan().all() and lse[4].isnan().all() and torch.isfinite(lse[1]).all()
+
+
+@pytest.mark.parametrize("case", STEPS, ids=lambda c: "-".join(map(str, c)))
+def test_a_rows_bits_are_its_own_keys(case):
+    # with the last token's values and keys larger, the tokens before it keep their bits
+    import torch
+    import logits_processing_token_gb300 as tg
+    H, G, D, typ, page, layout, n = case
+    lens = [n, n + 130, 500, 1]
+    c = I8Cache(lens, G, D, page, layout, 23)
+    cfg = tg.AttnConfig(num_heads=H, num_kv_heads=G, head_dim=D, dtype=typ, cache_dtype="i8", page_size=page, page_layout=layout,
+                        max_step_tokens=32)
+    q = torch.from_numpy(np.random.default_rng(24).normal(0, 2, (len(lens), n, H, D)).astype(np.float32)).cuda().to(torch_types()[typ])
+    got = []
+    for factor in (1.0, 2.0 ** 90):
+        for b, L in enumerate(lens):
+            enlarge(c, G, D, b, [L - 1], factor)
+            parts(c.k, G, D, page, layout)[1][int(c.table[b, (L - 1) // page]), :, (L - 1) % page] *= min(factor, 64.0)
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:3], device="cuda")
+        tg.tg_attend_step(q, ids(lens, np.int32), c.device_table(), c.k, c.v, cfg, out, lse)
+        got.append((out[:, :-1], lse[:, :-1]))
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("n", [1, 6])
+def test_a_sequences_bits_are_its_own_keys_in_a_shared_call(n):
+    import torch
+    groups = 60
+    tg, cfg, c, q, off, pl, lens, reference, call = setup(16, 4, 64, "bf16", "i8", 16, "token", n, [4] * groups, [200] * groups,
+                                                          [n, n + 9, n + 130, n + 300] * groups, seed=56)
+    got = [call()]
+    for b in range(0, len(lens), 2):
+        enlarge(c, 4, 64, b, np.arange(200, lens[b]), 2.0 ** 50)
+    got.append(call())
+    odd = list(range(1, len(lens), 2))
+    assert torch.equal(got[0][0][odd], got[1][0][odd]) and torch.equal(got[0][1][odd], got[1][1][odd])
