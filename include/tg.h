@@ -584,9 +584,12 @@ tg_status tg_cache_read(const int64_t* offsets, int32_t tokens, const tg_cache* 
  * sequences' lengths decide where its keys are split, and so how its sums
  * round).  A non-finite value of one of the call's own n tokens may reach the
  * tokens before it (0 x NaN), but none that sees no key.
- * Softmax statistics and sums are f32; the weights are rounded to the 16-bit
- * type of the products.  The keys of one sequence are split over the GPU and
- * joined in a fixed order: equal inputs give equal bits.
+ * Softmax statistics and sums are f32.  The weights are rounded to the 16-bit type of
+ * the products (f16 over an 8-bit cache; over an i8 one the products of weights and their
+ * values' scales are): by half a step, and where that is less, in f16, by 2^-30 of the
+ * largest that the row has.  Rows, head_dim and the cache's type choose between two
+ * kernels, of which one does not round the largest weight.  The keys of one sequence are
+ * split over the GPU and joined in a fixed order: equal inputs give equal bits.
  */
 tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_cache* cache, const tg_attn* cfg,
                          void* out, float* out_lse, tg_stream stream);
@@ -607,8 +610,9 @@ tg_status tg_attend_step(const void* q, int64_t q_stride, int32_t n, const tg_ca
  *
  * batch * n is at most max_shared_tokens.  Other arguments and outputs as
  * tg_attend_step, whose results these are up to the order of the sums and the
- * rounding of the weights (below).  A prefix is read once for as many of a group's
- * sequences as have 128 rows together (n * num_heads / num_kv_heads each), 64 at most.
+ * rounding of the weights (the largest one's too).  A prefix is read once for as many
+ * of a group's sequences as have 128 rows together (n * num_heads / num_kv_heads each),
+ * 64 at most.
  * A sequence that is shorter than the prefix and its n tokens, or empty, takes no part
  * in the sharing.  A call is a step, and reads neither group_offsets nor prefix_lens,
  * where nothing can be shared (more than 64 rows a sequence, or groups >= batch) or

@@ -15,9 +15,10 @@
 // elements are under way with it.
 //
 // Into an i8 cache a head's lanes exchange their largest magnitudes before they
-// round, and instructions bound it: 6,048 tokens of 32 + 2 x 8 heads of 128 take 29.2 us
-// where their 136 MB would take 20 (profiled: an instruction in two of three cycles, the
-// DRAM at 41 %).  The next vectors' reads ahead of the exchange cost more registers than
+// round, and latency bounds it: 6,048 tokens of 32 + 2 x 8 heads of 128 take 29.2 us
+// where their 136 MB would take 20 and their instructions 17 (profiled: an instruction in
+// two of three cycles, the DRAM at 41 %), because a vector is asked for when the one before
+// is done.  The next vectors' reads ahead of the exchange cost more registers than
 // they gained (35), more tokens a CTA 0.2 us.
 #include <type_traits>
 

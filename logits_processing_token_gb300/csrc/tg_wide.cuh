@@ -19,8 +19,9 @@
 // row's own, from the keys that it sees, by which the sums are divided at the end.  (One
 // factor for all the rows of a tile, from its largest scale, lost the weights of rows that
 // do not see that key.)  32 sequences of 17 tokens take 76 us
-// (floor 23): chains of widening (1,200 cycles a tile and matrix), products and softmax,
-// and the joins.  On the warp-wide instructions, which widen each key once per 16
+// (floor 23): widening (1,000 of the 1,800 cycles of a tile and matrix; the rest are waits
+// for copies and places), products and softmax wait for one another; then the joins.  On
+// the warp-wide instructions, which widen each key once per 16
 // rows, they took 211.
 //
 // A shared call's item is a pair of key heads and as many whole sequences of one
